@@ -89,6 +89,7 @@ typedef enum qa_status {
 #define QA_DEVICE_BAD_SEGMENTS 0x4u /* cu_seqlens / cu_windows not monotonic, or
                                        not ending at total_tokens               */
 #define QA_DEVICE_TIMEOUT 0x8u      /* a bounded wait inside a kernel expired    */
+#define QA_DEVICE_BAD_POSITION 0x10u /* rotary position outside [0, 2^18)        */
 
 typedef struct qa_attn_params {
     int abi_version;       /* set by qa_attn_default_params()                    */
@@ -465,6 +466,154 @@ qa_status qa_linear(const void *x, int m, int k, const void *w, int n, const voi
  * Only params->stream and debug_checks are used. */
 qa_status qa_layer_norm(const void *x, int t, int d, const void *gain, const void *bias, float eps, void *y,
                         const qa_attn_params *params);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions with several axes, and a KV cache held in 4 bits.
+ *
+ * A prompt is rotated by qa_rope_rows, attended by qa_prefill_attn and
+ * quantised into its pages by qa_kvq_write.  A token then takes one
+ * qa_kvq_decode_step a layer (or qa_rope_rows, qa_kvq_write and
+ * qa_kvq_decode_attn).  qa_kvq_read gives cached rows back as bf16, for
+ * example as the cached part of a qa_prefill_chunk_attn.
+ * ------------------------------------------------------------------------ */
+
+/* Per-head norm and rotation of query and key vectors. */
+typedef struct qa_rope {
+    const float *q_gain;       /* device [head_dim]: per-head RMSNorm gains, both   */
+    const float *k_gain;       /* or neither; NULL: no norm                         */
+    float rms_eps;             /* > 0 (unused without gains)                        */
+    float theta;               /* > 0: frequency base                               */
+    int n_axes;                /* position axes, 1..4                               */
+    const int32_t *positions;  /* device [n_axes][rows]                             */
+    const uint8_t *pair_axis;  /* HOST [head_dim/2]: the axis of each rotation pair */
+                               /* (qa_rope_axes); NULL: axis 0 for all              */
+} qa_rope;
+
+/* The axis of each rotation pair (HOST helper).  sections[a] pairs turn with
+ * axis a; they add up to head_dim / 2.  interleaved 0: one section after
+ * another.  1: in turn -- pair i has axis i % n_axes while i < n_axes *
+ * sections[i % n_axes], and axis 0 after that (the form of decoders that
+ * spread time, height and width over all frequencies); sections that this
+ * rule does not reproduce are refused.  Returns 0, or -1 and sets
+ * qa_last_error(). */
+int qa_rope_axes(const int *sections, int n_axes, int interleaved, int head_dim, uint8_t *pair_axis);
+
+/* Per-head QK-norm and NEOX rotation of packed rows (prompt or decode rows):
+ *
+ *   y = x / sqrt(mean_d x[d]^2 + rms_eps) * gain     (y = x without gains)
+ *   a_i = positions[pair_axis[i]][t] * theta^(-2 i / D),     i in [0, D/2)
+ *   z[i] = y[i] cos a_i - y[i + D/2] sin a_i,  z[i + D/2] = y[i] sin a_i + y[i + D/2] cos a_i
+ *
+ * for every head of row t of q and of k, in fp32 with angles as in
+ * qa_decode_append, rounded to bf16 once.
+ *
+ *   q, q_out   bf16, row t's [n_q_heads][head_dim] at t * ldq, t * ldq_out
+ *   k, k_out   bf16, row t's [n_kv_heads][head_dim] at t * ldk, t * ldk_out;
+ *              k may be NULL (queries only; then k_out is not used)
+ *   ld*        row strides in elements, multiples of 8; 0 = packed.  q and k
+ *              may lie in the rows of one fused projection.  An output may be
+ *              its input (same pointer and stride); they may not overlap
+ *              otherwise, nor the outputs one another.
+ *
+ * A row with a position outside [0, 2^18) on any of the n_axes axes is not
+ * written and sets QA_DEVICE_BAD_POSITION.  rows = 0 does nothing.
+ * params: head counts (1..1024), head_dim 64 or 128, stream, debug_checks,
+ * stable_metadata (>= 1: positions and gains are not written by a kernel
+ * that may still be running; they are then read before the launch's wait). */
+qa_status qa_rope_rows(const void *q, long long ldq, const void *k, long long ldk, int rows, void *q_out,
+                       long long ldq_out, void *k_out, long long ldk_out, const qa_rope *rope,
+                       const qa_attn_params *params);
+
+/* The 4-bit pools.  A pool (one for K, one for V) is num_pages pages of
+ * qa_kvq_page_bytes() = n_kv_heads * 1280 bytes, a page 16 tokens: for each
+ * KV head 1024 bytes of codes, then 256 bytes of group parameters.  A group
+ * is 32 consecutive dims of one token's head.  It is held as a bf16 scale s,
+ * a bf16 minimum m and 32 codes n in 0..15, and stands for m + s n:
+ *
+ *   lo, hi = min, max of the group;  m = lo;  s = bf16((hi - lo) / 15)
+ *   n = rint((x - m) * r), r = 1 / s       each operation rounded to fp32
+ *
+ * s below the smallest normal number becomes 0, with codes 0 (a constant
+ * group reads back exactly).  A group whose range is not a finite fp32
+ * number (an infinity or NaN in it) reads back as NaN in all 32 dims; other
+ * groups and tokens are untouched by it.  The largest error of a value is
+ * about half of s, a thirtieth of the group's range.
+ *
+ * Bytes inside a head's part of a page, token t in 0..15, little-endian:
+ *   K codes   dim 32 g + 8 c + j: nibble j of the 4-byte word at
+ *             64 t + 16 c + 4 g
+ *   V codes   token t = 8 u + 2 p + e, dim 32 g + 4 r + i: nibble i of the
+ *             2-byte word at 512 u + 64 r + 16 p + 4 g + 2 e
+ *   params    s, m of group g at 1024 + 16 t + 4 g
+ * Returns 0 on bad params and sets qa_last_error(). */
+size_t qa_kvq_page_bytes(const qa_attn_params *params);
+
+/* Quantises packed K/V rows as it writes them to their pages.
+ *
+ *   k, v       bf16, row t's [n_kv_heads][128] at t * ldk and t * ldv
+ *              (elements, multiples of 8; 0 = packed)
+ *   cu_seqlens int32 [batch + 1], as in qa_prefill_attn
+ *   n_past     int32 [batch] (device) or NULL (all 0): row i of request r is
+ *              position n_past[r] + i
+ *   page_table int32 [batch][max_pages_per_seq]
+ *   k_pages, v_pages  4-bit pools, written in place; bytes of slots that no
+ *              row maps to are left as they were
+ *
+ * Device checks as in qa_prefill_chunk_attn's page write: n_past outside
+ * [0, max_pages_per_seq * 16] skips the request and rows past the page-table
+ * row are skipped (QA_DEVICE_BAD_LENGTH), as are pages outside
+ * [0, num_pages) (QA_DEVICE_BAD_PAGE) and requests whose cu_seqlens are
+ * malformed (QA_DEVICE_BAD_SEGMENTS).  Requests may not share a page that
+ * both write.  Supported: head_dim 128, page_size 16, n_kv_heads in [1, 8]
+ * (n_q_heads is checked as in the other calls, but not used).
+ * stable_metadata >= 1 covers cu_seqlens, n_past and page_table. */
+qa_status qa_kvq_write(const void *k, long long ldk, const void *v, long long ldv, const int32_t *cu_seqlens,
+                       const int32_t *n_past, int batch, int total_tokens, const int32_t *page_table,
+                       void *k_pages, void *v_pages, const qa_attn_params *params);
+
+/* Reads cached rows back: row cu_seqlens[r] + i of k_out and v_out (bf16
+ * [total_tokens][n_kv_heads][128], packed) receives position n_past[r] + i
+ * of request r, m + s n rounded to bf16.  Arguments and device checks as in
+ * qa_kvq_write; rows that are skipped stay as they were.  Slots that no
+ * token was written to read back as whatever bytes they hold, so with every
+ * cu_seqlens[r] a multiple of 16 the outputs are bf16 pools of whole pages
+ * (page cu_seqlens[r] / 16 + j holds positions [16 j, 16 j + 16) of request
+ * r) as qa_prefill_chunk_attn takes them. */
+qa_status qa_kvq_read(const void *k_pages, const void *v_pages, const int32_t *page_table,
+                      const int32_t *cu_seqlens, const int32_t *n_past, int batch, int total_tokens, void *k_out,
+                      void *v_out, const qa_attn_params *params);
+
+/* qa_decode_workspace_size and qa_decode_attn over 4-bit pools: the same
+ * arguments, workspace rules (its own size; zero-filled before the first
+ * use, ordered calls), stable_metadata levels, device checks and result,
+ *
+ *   out[b][h] = softmax_j(q[b][h] . K_b[j] * scale) V_b[j]
+ *
+ * with K and V rows m + s n as stored, never rounded to bf16.  Slots past
+ * seq_lens[b] may hold any bytes. */
+size_t qa_kvq_decode_workspace_size(int batch, int max_seq_len, const qa_attn_params *params);
+qa_status qa_kvq_decode_attn(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
+                             const int32_t *seq_lens, int batch, void *out, const qa_attn_params *params);
+
+/* One decode step of the 4-bit cache in one launch: qa_rope_rows on the new
+ * token's q and k, qa_kvq_write of its k (rounded to bf16 by the rotation)
+ * and v at position seq_lens[b] - 1, and qa_kvq_decode_attn, which reads the
+ * new row as quantised.
+ *
+ *   q          bf16, request b's [n_q_heads][128] at b * ldq
+ *   k, v       bf16, request b's [n_kv_heads][128] at b * ldkv (of k, of v)
+ *   ldq, ldkv  row strides in elements, multiples of 8; 0 = packed
+ *   rope       gains required; positions int32 [n_axes][batch], or NULL with
+ *              n_axes 1: seq_lens[b] - 1
+ *   other arguments as in qa_kvq_decode_attn; seq_lens[b] >= 1
+ *
+ * Device checks: those of the three calls.  A request with a bad length or a
+ * bad position has no new token written; its out row is zero.  A bad page
+ * among a request's pages is left out of its attention, as in
+ * qa_decode_attn.  stable_metadata >= 1 covers positions and gains too. */
+qa_status qa_kvq_decode_step(const void *q, long long ldq, const void *k, const void *v, long long ldkv,
+                             const qa_rope *rope, void *k_pages, void *v_pages, const int32_t *page_table,
+                             const int32_t *seq_lens, int batch, void *out, const qa_attn_params *params);
 
 /* Synchronises `stream` (cudaStream_t, NULL = legacy default), then reads and
  * clears the device status word of the current device.  Returns its bits

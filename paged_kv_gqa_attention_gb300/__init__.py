@@ -11,6 +11,15 @@ importing this package fails loudly when ``libqa.so`` has not been built.
     qa_prefill_attn   ragged causal prefill with the KV page write
     qa_window_attn    windowed bidirectional encoder attention
     qa_window_plan    cu_windows from per-request encoder token counts (host)
+
+Rotary positions with several axes, and a KV cache held in 4 bits:
+
+    qa_rope_rows         per-head QK-norm and rotation of packed rows
+    qa_rope_axes         the position axis of each rotation pair (host)
+    qa_kvq_write         K/V rows quantised into 4-bit pages
+    qa_kvq_read          cached rows back as bf16
+    qa_kvq_decode_attn   paged GQA decode over the 4-bit pages
+    qa_kvq_decode_step   norm, rotation, quantised append and decode of one token
 """
 from __future__ import annotations
 
@@ -25,12 +34,15 @@ __all__ = [
     "qa_window_workspace_size",
     "qa_device_status", "DEVICE_STATUS_BITS", "qa_decode_attn_noalloc", "qa_check_bounded_wait",
     "qa_encoder_workspace_size", "qa_encoder_layer", "qa_linear", "qa_layer_norm", "ENCODER_WEIGHT_NAMES",
+    "qa_rope_axes", "qa_rope_rows", "qa_kvq_page_bytes", "qa_kvq_write", "qa_kvq_read",
+    "qa_kvq_decode_workspace_size", "qa_kvq_decode_attn", "qa_kvq_decode_step",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_PKG, "libqa.so")
 
-DEVICE_STATUS_BITS = {0x1: "bad page id", 0x2: "bad length", 0x4: "bad segments", 0x8: "timeout"}
+DEVICE_STATUS_BITS = {0x1: "bad page id", 0x2: "bad length", 0x4: "bad segments", 0x8: "timeout",
+                      0x10: "bad position"}
 
 
 class QAError(RuntimeError):
@@ -61,6 +73,18 @@ class qa_attn_params(ctypes.Structure):
 
 ENCODER_WEIGHT_NAMES = ("ln1_g", "ln1_b", "w_qkv", "b_qkv", "w_o", "b_o", "ln2_g", "ln2_b", "w_fc1", "b_fc1",
                         "w_fc2", "b_fc2")
+
+
+class qa_rope(ctypes.Structure):
+    _fields_ = [
+        ("q_gain", ctypes.c_void_p),
+        ("k_gain", ctypes.c_void_p),
+        ("rms_eps", ctypes.c_float),
+        ("theta", ctypes.c_float),
+        ("n_axes", ctypes.c_int),
+        ("positions", ctypes.c_void_p),
+        ("pair_axis", ctypes.c_void_p),
+    ]
 
 
 class qa_encoder_weights(ctypes.Structure):
@@ -112,6 +136,23 @@ def _load():
     lib.qa_linear.argtypes = [P, I, I, P, I, P, I, P, P, PP]
     lib.qa_layer_norm.restype = I
     lib.qa_layer_norm.argtypes = [P, I, I, P, P, ctypes.c_float, P, PP]
+    L, PR, S = ctypes.c_longlong, ctypes.POINTER(qa_rope), ctypes.c_size_t
+    lib.qa_rope_axes.restype = I
+    lib.qa_rope_axes.argtypes = [P, I, I, I, P]
+    lib.qa_rope_rows.restype = I
+    lib.qa_rope_rows.argtypes = [P, L, P, L, I, P, L, P, L, PR, PP]
+    lib.qa_kvq_page_bytes.restype = S
+    lib.qa_kvq_page_bytes.argtypes = [PP]
+    lib.qa_kvq_write.restype = I
+    lib.qa_kvq_write.argtypes = [P, L, P, L, P, P, I, I, P, P, P, PP]
+    lib.qa_kvq_read.restype = I
+    lib.qa_kvq_read.argtypes = [P, P, P, P, P, I, I, P, P, PP]
+    lib.qa_kvq_decode_workspace_size.restype = S
+    lib.qa_kvq_decode_workspace_size.argtypes = [I, I, PP]
+    lib.qa_kvq_decode_attn.restype = I
+    lib.qa_kvq_decode_attn.argtypes = [P, P, P, P, P, I, P, PP]
+    lib.qa_kvq_decode_step.restype = I
+    lib.qa_kvq_decode_step.argtypes = [P, L, P, P, L, PR, P, P, P, P, I, P, PP]
     lib.qa_device_status.restype = I
     lib.qa_device_status.argtypes = [P]
     lib.qa_check_bounded_wait.restype = I
@@ -570,6 +611,269 @@ def qa_window_plan(token_counts, window_tokens: int = 0) -> np.ndarray:
     if n < 0:
         raise QAError("qa_window_plan", -1, qa_last_error())
     return cu[: n + 1]
+
+
+_KVQ_HEAD_BYTES = 1280  # one KV head of a 4-bit page (qa_kvq_page_bytes)
+
+
+def _same_device(*tensors):
+    """The calls launch on the current device, so their tensors must live there."""
+    torch = _torch()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+            current = torch.cuda.current_device()
+            raise ValueError(f"tensors must be on the current CUDA device ({current}), got {t.device}")
+
+
+def _on(stream):
+    """Buffers made inside a call are allocated (and zeroed, and later reused)
+    in the order of the stream that the call runs on."""
+    return _torch().cuda.stream(stream)  # None: no change
+
+
+def _rows(t, name):
+    """Device address and row stride of a bf16 [rows, heads, head_dim] tensor
+    whose rows are packed inside, but may lie apart (views into a fused
+    projection's rows)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
+    n, h, d = t.shape
+    s = t.stride()
+    if n > 0 and (s[2] != 1 or (h > 1 and s[1] != d)):
+        raise ValueError(f"{name} must be contiguous within each row")
+    return ctypes.c_void_p(t.data_ptr()), (s[0] if n > 1 else 0)
+
+
+def qa_rope_axes(sections, *, interleaved=False, head_dim=128):
+    """The axis of each rotation pair (uint8 numpy [head_dim / 2]): sections[a]
+    pairs turn with axis a, one section after another or interleaved."""
+    sec = np.ascontiguousarray(np.asarray(sections, dtype=np.int32))
+    out = np.zeros(max(1, int(head_dim) // 2), dtype=np.uint8)
+    if _lib.qa_rope_axes(sec.ctypes.data_as(ctypes.c_void_p), len(sec), int(bool(interleaved)), int(head_dim),
+                         out.ctypes.data_as(ctypes.c_void_p)) != 0:
+        raise QAError("qa_rope_axes", -1, qa_last_error())
+    return out
+
+
+def _rope(positions, rows, q_gain, k_gain, pair_axis, head_dim, rms_eps, rope_theta):
+    """The qa_rope struct and what must stay alive while a call reads it."""
+    torch = _torch()
+    r = qa_rope()
+    for name, gain in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if gain is not None:
+            if tuple(gain.shape) != (head_dim,):
+                raise ValueError("gains must be [head_dim]")
+            setattr(r, name, _dev(gain, name, torch.float32, 1).value)
+    r.rms_eps, r.theta, r.n_axes = float(rms_eps), float(rope_theta), 1
+    if positions is not None:
+        if positions.dim() not in (1, 2) or positions.shape[-1] != rows:
+            raise ValueError(f"positions must be [rows] or [n_axes, rows] with {rows} rows")
+        r.n_axes = positions.shape[0] if positions.dim() == 2 else 1
+        r.positions = _dev(positions, "positions", torch.int32).value
+    axes = None
+    if pair_axis is not None:
+        axes = bytes(pair_axis)
+        if len(axes) != head_dim // 2:
+            raise ValueError("pair_axis must have head_dim / 2 entries")
+        r.pair_axis = ctypes.cast(ctypes.c_char_p(axes), ctypes.c_void_p).value
+    return r, axes
+
+
+def qa_rope_rows(q, k, positions, q_out=None, k_out=None, *, q_gain=None, k_gain=None, rms_eps=1e-6, rope_theta=1e6,
+                 pair_axis=None, stream=None, debug_checks=False, stable_metadata=False):
+    """Per-head RMSNorm (gains float32 [D], both or neither) and NEOX rotation
+    of packed rows.  q bf16 [T,Hq,D]; k bf16 [T,Hkv,D] or None; positions
+    int32 [T] or [n_axes,T]; pair_axis: the axis of each rotation pair
+    (qa_rope_axes; default axis 0).  q, k and the outputs may be views whose
+    rows lie apart; q_out=q and k_out=k work in place.  Returns (q_out,
+    k_out)."""
+    torch = _torch()
+    T, Hq, D = q.shape
+    Hkv = k.shape[1] if k is not None else 1
+    if k is not None and (k.shape[0], k.shape[2]) != (T, D):
+        raise ValueError("inconsistent rope shapes")
+    if positions is None:
+        raise ValueError("positions are required")
+    with _on(stream):
+        if q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(T, Hkv, D, dtype=k.dtype, device=k.device)
+    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        raise ValueError("outputs must have their inputs' shapes")
+    _same_device(q, k, positions, q_out, k_out, q_gain, k_gain)
+    r, _axes = _rope(positions, T, q_gain, k_gain, pair_axis, D, rms_eps, rope_theta)
+    p = _params(n_q_heads=Hq, n_kv_heads=Hkv, head_dim=D, stream=stream, debug_checks=debug_checks,
+                stable_metadata=stable_metadata)
+    none = (None, 0)
+    st = _lib.qa_rope_rows(*_rows(q, "q"), *(none if k is None else _rows(k, "k")), T, *_rows(q_out, "q_out"),
+                           *(none if k is None else _rows(k_out, "k_out")), ctypes.byref(r), ctypes.byref(p))
+    _check("qa_rope_rows", st)
+    return q_out, k_out
+
+
+def qa_kvq_page_bytes(n_kv_heads=8) -> int:
+    """Bytes of one page (16 tokens) of one 4-bit pool."""
+    p = _lib.qa_attn_default_params()
+    p.n_kv_heads = n_kv_heads
+    n = _lib.qa_kvq_page_bytes(ctypes.byref(p))
+    if n == 0:
+        raise QAError("qa_kvq_page_bytes", -1, qa_last_error())
+    return int(n)
+
+
+def _kvq_heads(k_pages, v_pages):
+    if k_pages.dim() != 2 or k_pages.shape != v_pages.shape or k_pages.shape[1] % _KVQ_HEAD_BYTES:
+        raise ValueError("4-bit pools must be uint8 [num_pages, qa_kvq_page_bytes(n_kv_heads)], of one shape")
+    return k_pages.shape[1] // _KVQ_HEAD_BYTES
+
+
+def _kvq_rows_check(cu_seqlens, n_past, page_table):
+    B = cu_seqlens.shape[0] - 1
+    if page_table.dim() != 2 or page_table.shape[0] != B or (n_past is not None and tuple(n_past.shape) != (B,)):
+        raise ValueError("page_table must be [batch, max_pages] and n_past [batch]")
+    return B
+
+
+def qa_kvq_write(k, v, cu_seqlens, page_table, k_pages, v_pages, *, n_past=None, stream=None, debug_checks=False,
+                 stable_metadata=False):
+    """Quantises packed K/V rows into 4-bit pages.  k/v bf16 [T,Hkv,128] (rows
+    may lie apart); cu_seqlens int32 [B+1]; page_table int32 [B,max_pages];
+    pools uint8 [P, qa_kvq_page_bytes(Hkv)], written in place; n_past int32
+    [B]: request r's row i is position n_past[r] + i (default 0)."""
+    torch = _torch()
+    T, Hkv, D = k.shape
+    B = _kvq_rows_check(cu_seqlens, n_past, page_table)
+    if v.shape != k.shape or _kvq_heads(k_pages, v_pages) != Hkv:
+        raise ValueError("inconsistent 4-bit write shapes")
+    _same_device(k, v, cu_seqlens, page_table, k_pages, v_pages, n_past)
+    p = _params(n_q_heads=Hkv, n_kv_heads=Hkv, head_dim=D, num_pages=k_pages.shape[0],
+                max_pages_per_seq=page_table.shape[1], stream=stream, debug_checks=debug_checks,
+                stable_metadata=stable_metadata)
+    st = _lib.qa_kvq_write(*_rows(k, "k"), *_rows(v, "v"), _dev(cu_seqlens, "cu_seqlens", torch.int32, 1),
+                           None if n_past is None else _dev(n_past, "n_past", torch.int32, 1), B, T,
+                           _dev(page_table, "page_table", torch.int32, 2), _dev(k_pages, "k_pages", torch.uint8, 2),
+                           _dev(v_pages, "v_pages", torch.uint8, 2), ctypes.byref(p))
+    _check("qa_kvq_write", st)
+
+
+def qa_kvq_read(k_pages, v_pages, page_table, cu_seqlens, total_tokens, k_out=None, v_out=None, *, n_past=None,
+                stream=None, debug_checks=False, stable_metadata=False):
+    """Reads cached rows back as bf16 [total_tokens,Hkv,128]: row
+    cu_seqlens[r] + i is position n_past[r] + i of request r (arguments as
+    for qa_kvq_write).  Returns (k_out, v_out)."""
+    torch = _torch()
+    T, Hkv = int(total_tokens), _kvq_heads(k_pages, v_pages)
+    B = _kvq_rows_check(cu_seqlens, n_past, page_table)
+    with _on(stream):
+        if k_out is None:
+            k_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=k_pages.device)
+        if v_out is None:
+            v_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=k_pages.device)
+    if tuple(k_out.shape) != (T, Hkv, 128) or tuple(v_out.shape) != (T, Hkv, 128):
+        raise ValueError("k_out and v_out must be [total_tokens, n_kv_heads, 128]")
+    _same_device(k_pages, v_pages, page_table, cu_seqlens, k_out, v_out, n_past)
+    p = _params(n_q_heads=Hkv, n_kv_heads=Hkv, head_dim=128, num_pages=k_pages.shape[0],
+                max_pages_per_seq=page_table.shape[1], stream=stream, debug_checks=debug_checks,
+                stable_metadata=stable_metadata)
+    st = _lib.qa_kvq_read(_dev(k_pages, "k_pages", torch.uint8, 2), _dev(v_pages, "v_pages", torch.uint8, 2),
+                          _dev(page_table, "page_table", torch.int32, 2), _dev(cu_seqlens, "cu_seqlens", torch.int32, 1),
+                          None if n_past is None else _dev(n_past, "n_past", torch.int32, 1), B, T,
+                          _dev(k_out, "k_out", torch.bfloat16, 3), _dev(v_out, "v_out", torch.bfloat16, 3),
+                          ctypes.byref(p))
+    _check("qa_kvq_read", st)
+    return k_out, v_out
+
+
+def qa_kvq_decode_workspace_size(batch: int, max_seq_len: int, *, n_q_heads=16, n_kv_heads=8, head_dim=128,
+                                 page_size=16, num_pages=1, max_pages_per_seq=1) -> int:
+    """Bytes of 4-bit decode workspace for `batch` requests on the current device."""
+    p = _lib.qa_attn_default_params()
+    p.n_q_heads, p.n_kv_heads, p.head_dim = n_q_heads, n_kv_heads, head_dim
+    p.page_size, p.num_pages, p.max_pages_per_seq = page_size, num_pages, max_pages_per_seq
+    n = _lib.qa_kvq_decode_workspace_size(int(batch), int(max_seq_len), ctypes.byref(p))
+    if n == 0:
+        raise QAError("qa_kvq_decode_workspace_size", -1, qa_last_error())
+    return int(n)
+
+
+def _kvq_decode_params(q, k_pages, v_pages, page_table, seq_lens, out, workspace, **kw):
+    """Shape checks, output and workspace shared by the 4-bit decode calls."""
+    torch = _torch()
+    B, Hq, D = q.shape
+    Hkv = _kvq_heads(k_pages, v_pages)
+    if page_table.dim() != 2 or page_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("inconsistent decode shapes")
+    P, MP = k_pages.shape[0], page_table.shape[1]
+    with _on(kw["stream"]):
+        if out is None:
+            out = torch.empty(B, Hq, D, dtype=q.dtype, device=q.device)
+        if workspace is None:
+            nbytes = qa_kvq_decode_workspace_size(B, 0, n_q_heads=Hq, n_kv_heads=Hkv, head_dim=D, num_pages=P,
+                                                  max_pages_per_seq=MP)
+            workspace = torch.zeros(nbytes, dtype=torch.uint8, device=k_pages.device)
+    if tuple(out.shape) != (B, Hq, D):
+        raise ValueError("out must have q's shape")
+    _same_device(q, k_pages, v_pages, page_table, seq_lens, out, workspace)
+    return out, workspace, _params(n_q_heads=Hq, n_kv_heads=Hkv, head_dim=D, num_pages=P, max_pages_per_seq=MP,
+                                   workspace=workspace, **kw)
+
+
+def qa_kvq_decode_attn(q, k_pages, v_pages, page_table, seq_lens, out=None, *, workspace=None, scale=0.0, stream=None,
+                       debug_checks=False, stable_metadata=False):
+    """Paged GQA decode over 4-bit pools (uint8 [P, qa_kvq_page_bytes(Hkv)]).
+    q bf16 [B,Hq,128]; page_table int32 [B,max_pages]; seq_lens int32 [B]
+    (these and out may be page-locked CPU tensors; pass `out` then).
+    workspace: zero-filled uint8, qa_kvq_decode_workspace_size(B, ...) bytes
+    (allocated here if omitted), reusable across calls on one stream.
+    stable_metadata as for qa_decode_attn.  Returns out bf16 [B,Hq,128]."""
+    torch = _torch()
+    out, workspace, p = _kvq_decode_params(q, k_pages, v_pages, page_table, seq_lens, out, workspace, scale=scale,
+                                           stream=stream, debug_checks=debug_checks, stable_metadata=stable_metadata)
+    st = _lib.qa_kvq_decode_attn(_dev(q, "q", torch.bfloat16, 3, True), _dev(k_pages, "k_pages", torch.uint8, 2),
+                                 _dev(v_pages, "v_pages", torch.uint8, 2),
+                                 _dev(page_table, "page_table", torch.int32, 2, True),
+                                 _dev(seq_lens, "seq_lens", torch.int32, 1, True), q.shape[0],
+                                 _dev(out, "out", torch.bfloat16, 3, True), ctypes.byref(p))
+    _check("qa_kvq_decode_attn", st)
+    return out
+
+
+def qa_kvq_decode_step(q, k, v, q_gain, k_gain, page_table, seq_lens, k_pages, v_pages, out=None, *, positions=None,
+                       pair_axis=None, workspace=None, rms_eps=1e-6, rope_theta=1e6, scale=0.0, stream=None,
+                       debug_checks=False, stable_metadata=False):
+    """The decode step of the 4-bit cache in one launch: norm and rotation of
+    the new token's q and k, its k and v quantised into the pools at position
+    seq_lens[b] - 1, and attention over the cache.  q bf16 [B,Hq,128], k/v
+    bf16 [B,Hkv,128], pre-norm (rows may lie apart, k's and v's equally far);
+    gains float32 [128]; positions int32 [B] or [n_axes,B] (default
+    seq_lens - 1) with pair_axis as for qa_rope_rows; the rest as for
+    qa_kvq_decode_attn.  Returns out bf16 [B,Hq,128]."""
+    torch = _torch()
+    B, D = q.shape[0], q.shape[2]
+    if k.shape != v.shape or tuple(k.shape) != (B, _kvq_heads(k_pages, v_pages), D):
+        raise ValueError("inconsistent decode-step shapes")
+    _same_device(k, v, q_gain, k_gain, positions)
+    (qp, ldq), (kp, ldk), (vp, ldv) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    if ldk != ldv:
+        raise ValueError("k and v must have the same row stride")
+    out, workspace, p = _kvq_decode_params(q, k_pages, v_pages, page_table, seq_lens, out, workspace, scale=scale,
+                                           stream=stream, debug_checks=debug_checks, stable_metadata=stable_metadata)
+    r, _axes = _rope(positions, B, q_gain, k_gain, pair_axis, D, rms_eps, rope_theta)
+    st = _lib.qa_kvq_decode_step(qp, ldq, kp, vp, ldk, ctypes.byref(r), _dev(k_pages, "k_pages", torch.uint8, 2),
+                                 _dev(v_pages, "v_pages", torch.uint8, 2),
+                                 _dev(page_table, "page_table", torch.int32, 2),
+                                 _dev(seq_lens, "seq_lens", torch.int32, 1), B, _dev(out, "out", torch.bfloat16, 3),
+                                 ctypes.byref(p))
+    _check("qa_kvq_decode_step", st)
+    return out
 
 
 def qa_check_bounded_wait(limit_us=20000, stream=None) -> None:

@@ -1,0 +1,321 @@
+// Writing packed K/V rows into 4-bit pages (qa_kvq_write) and reading them
+// back (qa_kvq_read).
+//
+// One warp takes one KV head of one page: its 16 tokens x 128 dims of K and
+// of V.  Lane 4 r + c owns exactly the bytes of the page that it owns as a
+// tensor-core fragment in decode (kvq.cuh): of K, tokens r and r + 8, the 8
+// dims [8c, 8c + 8) of each group; of V, tokens 2c, 2c + 1 (+ 8), the 4 dims
+// [4r, 4r + 4) of each group.  So a group of K is spread over the 4 lanes of
+// equal r and one of V over the 8 of equal c, its range takes 2 or 3
+// shuffles, and every code a lane makes goes into its own words.
+//
+// Pages of a request are found without a prefix sum: request r's pages have
+// the ids S(r) + j with S(r) = cu[r] / 16 + 2 r.  S grows from r to r + 1 by
+// at least len / 16 + 2, the most pages that len rows touch at any n_past,
+// so ids never collide; the few ids left over end at once.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvq.cuh"
+#include "qa_internal.h"
+
+namespace qa {
+namespace {
+
+__device__ unsigned int g_status;
+
+struct PagesArgs {
+    const uint16_t *k_in, *v_in;  // write: packed rows
+    uint16_t *k_out, *v_out;      // read: packed rows
+    long long ldk, ldv;
+    const int32_t *cu, *n_past, *page_table;
+    uint8_t *k_pages, *v_pages;
+    int batch, total, hkv, max_pages, num_pages, early;
+};
+
+// What one warp works on: slots [t0, t1) of a page, whose slot t holds packed
+// row `row0 + t` (row0 may be negative: only rows of [t0, t1) exist).
+struct Job {
+    int t0, t1, page;
+    long long row0;
+};
+
+// The job of page id `id`; false when there is none.  Warp-collective.
+__device__ __forceinline__ bool find_job(const PagesArgs &a, int id, Job &j, bool report) {
+    const int lane = threadIdx.x & 31;
+    // the last request with S(r) <= id: 32 candidates a round
+    int lo = 0, n = a.batch;  // the answer is in [lo, lo + n), or there is none
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int r = lo + lane * step;
+        const bool le = lane * step < n && a.cu[r] / 16 + 2 * r <= id;
+        const unsigned votes = __ballot_sync(0xffffffffu, le);
+        const int last = votes ? 31 - __clz(votes) : 0;
+        n = min(step, n - last * step);
+        lo += last * step;
+    }
+    const int r = lo;
+    const int c0 = a.cu[r], c1 = a.cu[r + 1];
+    if (c0 < 0 || c1 > a.total || c1 < c0) {
+        if (report) atomicOr(&g_status, QA_DEVICE_BAD_SEGMENTS);
+        return false;
+    }
+    const int past = a.n_past ? a.n_past[r] : 0;
+    const long long cap = (long long)a.max_pages * kKvqTokens;
+    if (past < 0 || past > cap) {
+        if (report) atomicOr(&g_status, QA_DEVICE_BAD_LENGTH);
+        return false;
+    }
+    long long end = (long long)past + (c1 - c0);
+    if (end > cap) {
+        if (report) atomicOr(&g_status, QA_DEVICE_BAD_LENGTH);
+        end = cap;
+    }
+    const int k = id - (c0 / 16 + 2 * r);
+    if (k < 0) return false;
+    const long long pg = (long long)past / kKvqTokens + k;
+    const long long p0 = pg * kKvqTokens;
+    if (p0 >= end) return false;
+    j.t0 = (int)max(0LL, past - p0);
+    j.t1 = (int)min((long long)kKvqTokens, end - p0);
+    if (j.t1 <= j.t0) return false;
+    j.row0 = c0 + p0 - past;
+    j.page = a.page_table[(size_t)r * a.max_pages + pg];
+    if (j.page < 0 || j.page >= a.num_pages) {
+        if (report) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
+        return false;
+    }
+    return true;
+}
+
+// cu_seqlens as a whole, checked once a call.
+__device__ __forceinline__ void check_segments(const PagesArgs &a) {
+    if (blockIdx.x != 0) return;
+    bool bad = threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.batch] != a.total);
+    for (int r = threadIdx.x; r < a.batch; r += blockDim.x) bad |= a.cu[r] > a.cu[r + 1];
+    if (bad) atomicOr(&g_status, QA_DEVICE_BAD_SEGMENTS);
+}
+
+__device__ __forceinline__ void wait_dependency() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ float nan_min(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float nan_max(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__global__ void __launch_bounds__(256) kvq_write_kernel(const __grid_constant__ PagesArgs a) {
+    if (!a.early) wait_dependency();
+    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Job j;
+    const bool work = find_job(a, blockIdx.x, j, threadIdx.x == 0);
+    check_segments(a);
+    if (a.early) wait_dependency();
+    if (!work) return;
+    const int r = lane >> 2, c = lane & 3;
+    uint8_t *kp = a.k_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
+    uint8_t *vp = a.v_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
+
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // K: token r + 8 half
+        const int t = r + 8 * half;
+        const bool in = t >= j.t0 && t < j.t1;
+        uint32_t code[4], par[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (in) w = *reinterpret_cast<const uint4 *>(a.k_in + (j.row0 + t) * a.ldk + h * kKvqDim + 32 * g + 8 * c);
+            const float x[8] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y),
+                                bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)};
+            float lo = x[0], hi = x[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) lo = nan_min(lo, x[i]), hi = nan_max(hi, x[i]);
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                lo = nan_min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+                hi = nan_max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            }
+            const KvqGroup gr = kvq_group(lo, hi);
+            uint32_t word = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) word |= kvq_code(x[i], gr) << (4 * i);
+            code[g] = word;
+            par[g] = gr.sm;
+        }
+        if (in) {
+            *reinterpret_cast<uint4 *>(kp + t * 64 + c * 16) = make_uint4(code[0], code[1], code[2], code[3]);
+            if (c == 0) *reinterpret_cast<uint4 *>(kp + kvq_param_offset(t, 0)) = make_uint4(par[0], par[1], par[2], par[3]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // V: tokens 8 u + 2 c, + 1
+        uint32_t code[2][4];
+        bool in[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 8 * u + 2 * c + e;
+            in[e] = t >= j.t0 && t < j.t1;
+            uint32_t par[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint2 w = make_uint2(0u, 0u);
+                if (in[e]) w = *reinterpret_cast<const uint2 *>(a.v_in + (j.row0 + t) * a.ldv + h * kKvqDim + 32 * g + 4 * r);
+                const float x[4] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
+                float lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
+                float hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    lo = nan_min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+                    hi = nan_max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+                }
+                const KvqGroup gr = kvq_group(lo, hi);
+                uint32_t word = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) word |= kvq_code(x[i], gr) << (4 * i);
+                code[e][g] = word;
+                par[g] = gr.sm;
+            }
+            if (in[e] && r == 0)
+                *reinterpret_cast<uint4 *>(vp + kvq_param_offset(t, 0)) = make_uint4(par[0], par[1], par[2], par[3]);
+        }
+        uint8_t *dst = vp + u * 512 + lane * 16;
+        if (in[0] && in[1]) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(code[0][0] | code[1][0] << 16, code[0][1] | code[1][1] << 16,
+                                                         code[0][2] | code[1][2] << 16, code[0][3] | code[1][3] << 16);
+        } else {  // the neighbour's codes stay as they are
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (in[e])
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) *reinterpret_cast<uint16_t *>(dst + g * 4 + e * 2) = (uint16_t)code[e][g];
+        }
+    }
+}
+
+// Two values (codes in nibble positions 0 and 4 of `pair`) of a group.
+__device__ __forceinline__ float kvq_value(uint32_t n, float s, float m) { return fmaf(s, (float)n, m); }
+
+__global__ void __launch_bounds__(256) kvq_read_kernel(const __grid_constant__ PagesArgs a) {
+    if (!a.early) wait_dependency();
+    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Job j;
+    const bool work = find_job(a, blockIdx.x, j, threadIdx.x == 0);
+    check_segments(a);
+    if (a.early) wait_dependency();
+    if (!work) return;
+    const int r = lane >> 2, c = lane & 3;
+    const uint8_t *kp = a.k_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
+    const uint8_t *vp = a.v_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int t = r + 8 * half;
+        if (t < j.t0 || t >= j.t1) continue;
+        const uint4 w4 = *reinterpret_cast<const uint4 *>(kp + t * 64 + c * 16);
+        const uint4 p4 = *reinterpret_cast<const uint4 *>(kp + kvq_param_offset(t, 0));
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w}, p[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float s = bf16lo(p[g]), m = bf16hi(p[g]);
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = pack_bf16x2(kvq_value((w[g] >> (8 * i)) & 15u, s, m), kvq_value((w[g] >> (8 * i + 4)) & 15u, s, m));
+            *reinterpret_cast<uint4 *>(a.k_out + ((j.row0 + t) * a.hkv + h) * kKvqDim + 32 * g + 8 * c) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const uint4 w4 = *reinterpret_cast<const uint4 *>(vp + u * 512 + lane * 16);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 8 * u + 2 * c + e;
+            if (t < j.t0 || t >= j.t1) continue;
+            const uint4 p4 = *reinterpret_cast<const uint4 *>(vp + kvq_param_offset(t, 0));
+            const uint32_t p[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float s = bf16lo(p[g]), m = bf16hi(p[g]);
+                const uint32_t n = w[g] >> (16 * e);
+                *reinterpret_cast<uint2 *>(a.v_out + ((j.row0 + t) * a.hkv + h) * kKvqDim + 32 * g + 4 * r) =
+                    make_uint2(pack_bf16x2(kvq_value(n & 15u, s, m), kvq_value((n >> 4) & 15u, s, m)),
+                               pack_bf16x2(kvq_value((n >> 8) & 15u, s, m), kvq_value((n >> 12) & 15u, s, m)));
+            }
+        }
+    }
+}
+
+cudaError_t launch_pages(const PagesArgs &a, bool write, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.total / kKvqTokens + 2 * a.batch));
+    cfg.blockDim = dim3((unsigned)(a.hkv * 32));
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, write ? kvq_write_kernel : kvq_read_kernel, a);
+}
+
+PagesArgs pages_args(const int32_t *cu, const int32_t *n_past, int batch, int total, const int32_t *page_table,
+                     const qa_attn_params &p) {
+    PagesArgs a = {};
+    a.cu = cu;
+    a.n_past = n_past;
+    a.page_table = page_table;
+    a.batch = batch;
+    a.total = total;
+    a.hkv = p.n_kv_heads;
+    a.max_pages = p.max_pages_per_seq;
+    a.num_pages = p.num_pages;
+    a.early = (p.abi_version >= 2 && p.stable_metadata >= 1) ? 1 : 0;
+    return a;
+}
+
+}  // namespace
+
+cudaError_t launch_kvq_write(const void *k, long long ldk, const void *v, long long ldv, const int32_t *cu_seqlens,
+                             const int32_t *n_past, int batch, int total_tokens, const int32_t *page_table,
+                             void *k_pages, void *v_pages, const qa_attn_params &p, cudaStream_t stream) {
+    PagesArgs a = pages_args(cu_seqlens, n_past, batch, total_tokens, page_table, p);
+    a.k_in = static_cast<const uint16_t *>(k);
+    a.v_in = static_cast<const uint16_t *>(v);
+    a.ldk = ldk ? ldk : (long long)p.n_kv_heads * kKvqDim;
+    a.ldv = ldv ? ldv : (long long)p.n_kv_heads * kKvqDim;
+    a.k_pages = static_cast<uint8_t *>(k_pages);
+    a.v_pages = static_cast<uint8_t *>(v_pages);
+    return launch_pages(a, true, stream);
+}
+
+cudaError_t launch_kvq_read(const void *k_pages, const void *v_pages, const int32_t *page_table,
+                            const int32_t *cu_seqlens, const int32_t *n_past, int batch, int total_tokens, void *k_out,
+                            void *v_out, const qa_attn_params &p, cudaStream_t stream) {
+    PagesArgs a = pages_args(cu_seqlens, n_past, batch, total_tokens, page_table, p);
+    a.k_out = static_cast<uint16_t *>(k_out);
+    a.v_out = static_cast<uint16_t *>(v_out);
+    a.k_pages = const_cast<uint8_t *>(static_cast<const uint8_t *>(k_pages));
+    a.v_pages = const_cast<uint8_t *>(static_cast<const uint8_t *>(v_pages));
+    return launch_pages(a, false, stream);
+}
+
+unsigned int status_read_clear_kvq_pages(cudaStream_t stream, cudaError_t *err) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status, sizeof v, 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && v) e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (err) *err = e;
+    return v;
+}
+
+}  // namespace qa

@@ -76,9 +76,10 @@ qa_status launch_result(cudaError_t e, const char *fn) {
 qa_status debug_status(unsigned int bits, cudaError_t e, const char *fn) {
     if (e != cudaSuccess) return fail(QA_STATUS_LAUNCH_FAILED, "%s: CUDA error %s", fn, cudaGetErrorString(e));
     if (bits)
-        return fail(QA_STATUS_DEVICE_ERROR, "%s: device status 0x%x (%s%s%s%s)", fn, bits,
+        return fail(QA_STATUS_DEVICE_ERROR, "%s: device status 0x%x (%s%s%s%s%s)", fn, bits,
                     bits & QA_DEVICE_BAD_PAGE ? "bad page id " : "", bits & QA_DEVICE_BAD_LENGTH ? "bad length " : "",
-                    bits & QA_DEVICE_BAD_SEGMENTS ? "bad segments " : "", bits & QA_DEVICE_TIMEOUT ? "timeout" : "");
+                    bits & QA_DEVICE_BAD_SEGMENTS ? "bad segments " : "",
+                    bits & QA_DEVICE_BAD_POSITION ? "bad position " : "", bits & QA_DEVICE_TIMEOUT ? "timeout" : "");
     return QA_STATUS_OK;
 }
 
@@ -454,10 +455,11 @@ QA_API qa_status qa_layer_norm(const void *x, int t, int d, const void *gain, co
 QA_API int qa_device_status(void *stream) {
     clear_error();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e[5];
+    cudaError_t e[8];
     const unsigned int bits = qa::status_read_clear_decode(s, &e[0]) | qa::status_read_clear_prefill(s, &e[1]) |
                               qa::status_read_clear_window(s, &e[2]) | qa::status_read_clear_append(s, &e[3]) |
-                              qa::status_read_clear_gemm(s, &e[4]);
+                              qa::status_read_clear_gemm(s, &e[4]) | qa::status_read_clear_rope(s, &e[5]) |
+                              qa::status_read_clear_kvq_pages(s, &e[6]) | qa::status_read_clear_kvq_decode(s, &e[7]);
     for (cudaError_t ei : e)
         if (ei != cudaSuccess) {
             fail(QA_STATUS_LAUNCH_FAILED, "qa_device_status: CUDA error %s", cudaGetErrorString(ei));
@@ -485,6 +487,11 @@ QA_API const char *qa_version(void) {
 }
 
 namespace qa {
+
+qa_status check_params(const qa_attn_params *p, const char *fn) { return check_common(p, fn); }
+qa_status check_gqa_params(const qa_attn_params *p, const char *fn) { return check_gqa(p, fn); }
+qa_status report_device_status(unsigned int bits, cudaError_t e, const char *fn) { return debug_status(bits, e, fn); }
+
 // Lets entry points defined in other translation units report through the
 // same thread-local qa_last_error() slot.
 void set_last_error(const char *msg) { snprintf(t_last_error, sizeof t_last_error, "%s", msg); }

@@ -79,7 +79,43 @@ cudaError_t launch_encoder_layer(const void *x, const int32_t *cu_windows, int n
                                  int d_ffn, const qa_encoder_weights &w, float eps, void *workspace, void *out,
                                  const qa_attn_params &p, cudaStream_t stream);
 
+// ---- rotary positions of packed rows (rope.cu)
+cudaError_t launch_rope_rows(const void *q, long long ldq, const void *k, long long ldk, int rows, void *q_out,
+                             long long ldq_out, void *k_out, long long ldk_out, const qa_rope &rope,
+                             const qa_attn_params &p, cudaStream_t stream);
+// theta^(-2i/D) of the D/2 pairs, computed in fp64, as fp32 hi + lo parts
+void rope_frequencies(float theta, int head_dim, float *hi, float *lo);
+unsigned int status_read_clear_rope(cudaStream_t stream, cudaError_t *err);
+
+// ---- 4-bit pools: rows quantised into pages and read back (kvq_pages.cu)
+cudaError_t launch_kvq_write(const void *k, long long ldk, const void *v, long long ldv, const int32_t *cu_seqlens,
+                             const int32_t *n_past, int batch, int total_tokens, const int32_t *page_table,
+                             void *k_pages, void *v_pages, const qa_attn_params &p, cudaStream_t stream);
+cudaError_t launch_kvq_read(const void *k_pages, const void *v_pages, const int32_t *page_table,
+                            const int32_t *cu_seqlens, const int32_t *n_past, int batch, int total_tokens, void *k_out,
+                            void *v_out, const qa_attn_params &p, cudaStream_t stream);
+unsigned int status_read_clear_kvq_pages(cudaStream_t stream, cudaError_t *err);
+
+// ---- decode over 4-bit pools (kvq_decode.cu); app: the fused step's new token
+struct KvqAppend {
+    const void *k_new, *v_new;
+    long long ldkv;
+    const qa_rope *rope;
+};
+size_t kvq_decode_workspace_bytes(int batch, int n_q_heads, int ctas);
+cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void *v_pages, const int32_t *page_table,
+                              const int32_t *seq_lens, int batch, void *out, const qa_attn_params &p, float scale,
+                              int ctas, cudaStream_t stream, const KvqAppend *app);
+unsigned int status_read_clear_kvq_decode(cudaStream_t stream, cudaError_t *err);
+
 // ---- qa_api.cu
+// The checks every call makes of its params (ABI range, scale,
+// stable_metadata), and those of the paged GQA calls (head counts, page size,
+// pool and table sizes); set qa_last_error().
+qa_status check_params(const qa_attn_params *p, const char *fn);
+qa_status check_gqa_params(const qa_attn_params *p, const char *fn);
+// QA_STATUS_OK for no bits and no error, else the status and its message.
+qa_status report_device_status(unsigned int bits, cudaError_t e, const char *fn);
 // Writes the thread-local qa_last_error() message.
 void set_last_error(const char *msg);
 // CTAs of the decode grid on the current device (0 when there is none).
