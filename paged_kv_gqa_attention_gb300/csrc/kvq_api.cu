@@ -89,7 +89,7 @@ qa_status decode_entry(const char *fn, const void *q, long long ldq, const void 
     if (ok != QA_STATUS_OK) return ok;
     const int ctas = qa::current_decode_ctas();
     if (ctas <= 0) return reject(QA_STATUS_LAUNCH_FAILED, "%s: no CUDA device", fn);
-    const size_t need = qa::kvq_decode_workspace_bytes(batch, p->n_q_heads, ctas);
+    const size_t need = qa::kvq_decode_workspace_bytes(batch, p->n_q_heads, p->n_kv_heads, ctas);
     if (!p->workspace || p->workspace_bytes < need || !aligned(p->workspace, 256))
         return reject(QA_STATUS_INVALID_PARAMS, "%s: workspace must be >= %zu bytes and 256-byte aligned (got %zu)", fn, need,
                       p->workspace_bytes);
@@ -242,7 +242,7 @@ QA_API size_t qa_kvq_decode_workspace_size(int batch, int max_seq_len, const qa_
         reject(QA_STATUS_LAUNCH_FAILED, "%s: no CUDA device", fn);
         return 0;
     }
-    return qa::kvq_decode_workspace_bytes(batch, p->n_q_heads, ctas);
+    return qa::kvq_decode_workspace_bytes(batch, p->n_q_heads, p->n_kv_heads, ctas);
 }
 
 QA_API qa_status qa_kvq_decode_attn(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,

@@ -5,8 +5,32 @@
 //   score_j = scale sum_g (m_jg sum_{d in g} q_d + s_jg sum_{d in g} q_d n_jd)
 //   out = sum_j p_j (m_j + s_j n_j) / sum_j p_j,  p = exp(score - max)
 //
-// One warp takes one request's KV head and its query heads.  Lane l holds
-// dims [4l, 4l + 4); running maximum, sum and outputs are fp32.
+// Work split.  The pages of all requests form one flat list (request-major),
+// cut into equal contiguous ranges, one a worker.  A worker is one warp for
+// each KV head; a CTA (one an SM) holds S = 16 / Hkv workers, so its warps
+// hide one another's latency without meeting: each worker has its own
+// softmax state and its own requests.  A producer warp streams the workers'
+// pages in turn into one ring of shared memory with the bulk-copy engine,
+// the K page and the V page of a stage on separate mbarriers.
+//
+// A request that lies in one worker's range is finished there.  Otherwise
+// each worker writes an fp32 partial (maximum, sum, outputs) to slot v + b
+// (worker v, request b: unique, since both ranges are ordered), and after its
+// last page counts itself in the arrival counter of (request, KV head); the
+// warp that arrives last merges the partials and resets the counter, so
+// nothing waits on another CTA.
+//
+// Arithmetic of one page and KV head (16 tokens, mma.m16n8k16, fp32 sums).
+// Codes become bf16 by masking a nibble of both halves of a word and ORing
+// the bits of 128: 128 + n, exact.  The 8 columns are (group g, query head
+// h): B of the scores holds head h's dims of group g and zeros elsewhere, so
+// one product gives sum_{d in g} q_d (128 + n_jd) for each group apart, to
+// which its s and m are applied in fp32.  B of the outputs holds p_jh s_jg,
+// rounded to bf16, and the columns of a dim's own group are kept.  Offsets
+// are taken back in fp32: 128 sum q from the scores; from the outputs 136
+// times the same rounded p s, with m + 8 s in place of m, so the rounding
+// acts on n - 8.  The maximum is a reference that is only moved once a score
+// passes it by 2^10, which leaves the reduction over tokens out of most pages.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -30,8 +54,12 @@ struct KvqArgs {
     const int32_t *page_table, *seq_lens;
     uint16_t *out;
     long long ldq, ldkv;
+    float *part_acc;  // [slots][Hq][D]
+    float *part_ml;   // [slots][Hq][2]
+    int *arrivals;    // [kDecodeMaxBatch][kMaxHkv], zero between calls
     int batch, hkv, max_pages, num_pages;
     float scale_log2;
+    int early, early_pools;  // stable_metadata >= 1, >= 2
     // step only
     const uint16_t *k_new, *v_new;
     const float *q_gain, *k_gain;
@@ -85,112 +113,585 @@ __device__ __forceinline__ uint32_t quantise_row(uint2 w, int lane, uint32_t &sm
     return word;
 }
 
-template <int GROUP, bool APPEND>
-__global__ void __launch_bounds__(32) kvq_decode_kernel(const __grid_constant__ KvqArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.x / a.hkv, g = blockIdx.x % a.hkv, lane = threadIdx.x;
-    int len = a.seq_lens[b];
-    if (len < (APPEND ? 1 : 0) || len > a.max_pages * kPS) {
-        if (lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_LENGTH);
-        len = 0;
+constexpr int kMaxHkv = 8;
+constexpr int kMaxWorkers = 16;       // warps that compute, in a CTA
+constexpr int kMaxStages = 32;
+constexpr float kRefSlack = 10.f;     // log2 units a score may pass the reference by
+
+// Workers of a CTA: as many as fill 16 warps.
+__host__ __device__ constexpr int workers_of(int hkv) { return kMaxWorkers / hkv; }
+
+struct SmemLayout {
+    uint32_t page_bytes, stage_bytes, stages, off_bar, off_ok, off_scan, off_prefix, total;
+};
+
+__host__ __device__ inline SmemLayout smem_layout(int hkv, int batch) {
+    SmemLayout s;
+    s.page_bytes = hkv * kKvqHeadBytes;
+    s.stage_bytes = 2 * s.page_bytes;
+    s.stages = 204800u / s.stage_bytes;
+    if (s.stages > kMaxStages) s.stages = kMaxStages;
+    uint32_t o = s.stages * s.stage_bytes;
+    s.off_bar = o;  // full K, full V, empty, for each stage
+    o += 3 * s.stages * 8;
+    s.off_ok = o;  // the stage's page id, -1 if bad
+    o += s.stages * 4;
+    s.off_scan = o;  // warp sums of the prefix scan
+    o += 32 * 4;
+    s.off_prefix = o;
+    o += (batch + 1) * 4;
+    s.total = (o + 15) & ~15u;
+    return s;
+}
+
+// Workspace: arrival counters in a region of fixed size, zero between calls,
+// then the partials.
+struct WorkspaceLayout {
+    size_t arrivals, acc, ml, total;
+};
+
+__host__ __device__ inline WorkspaceLayout workspace_layout(int batch, int hq, int workers) {
+    const size_t slots = (size_t)workers + (size_t)batch;
+    WorkspaceLayout w;
+    w.arrivals = 0;
+    w.acc = ((size_t)kDecodeMaxBatch * kMaxHkv * sizeof(int) + 255) & ~(size_t)255;
+    w.ml = w.acc + ((slots * hq * kD * sizeof(float) + 255) & ~(size_t)255);
+    w.total = w.ml + ((slots * hq * 2 * sizeof(float) + 255) & ~(size_t)255);
+    return w;
+}
+
+// How the flat page list is cut: worker v has pages [total v / nv, total
+// (v + 1) / nv), none empty.  With pages for every worker a CTA has
+// neighbouring ones, so CTAs differ by one page at most; with fewer, each
+// page has a worker of its own, spread over the CTAs.
+struct Split {
+    int total, nv;
+    bool spread;
+    __device__ __forceinline__ Split(int total_, int ctas, int s) {
+        total = total_;
+        spread = total_ < ctas * s;
+        nv = spread ? total_ : ctas * s;
     }
-    float cs[4], sn[4];
-    if (APPEND && len > 0) {
+    __device__ __forceinline__ int worker(int cta, int ctas, int e, int s) const { return spread ? e * ctas + cta : cta * s + e; }
+    __device__ __forceinline__ int lo(int v) const {
+        return v >= nv ? total : (int)((long long)total * v / nv);
+    }
+    __device__ __forceinline__ int of_page(int x) const { return (int)((((long long)x + 1) * nv - 1) / total); }
+};
+
+// Pages request b contributes; invalid lengths and positions contribute none
+// (and are reported once, by CTA 0).
+template <bool APPEND>
+__device__ __forceinline__ int pages_of(const KvqArgs &a, int b, bool report) {
+    const int len = a.seq_lens[b];
+    if (len < (APPEND ? 1 : 0) || len > a.max_pages * kPS) {
+        if (report) atomicOr(&g_status, QA_DEVICE_BAD_LENGTH);
+        return 0;
+    }
+    if (APPEND && a.positions) {
         bool ok = true;
         for (int x = 0; x < a.n_axes; ++x) {
-            const int pos = a.positions ? a.positions[(size_t)x * a.batch + b] : len - 1;
+            const int pos = a.positions[(size_t)x * a.batch + b];
             ok &= pos >= 0 && pos < kMaxRopePos;
         }
         if (!ok) {
-            if (lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_POSITION);
-            len = 0;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int i = 4 * (lane & 15) + c;
-            const int pos = a.positions ? a.positions[(size_t)a.pair_axis[i] * a.batch + b] : len - 1;
-            sincos_pos_freq(pos, a.freq_hi[i], a.freq_lo[i], &sn[c], &cs[c]);
+            if (report) atomicOr(&g_status, QA_DEVICE_BAD_POSITION);
+            return 0;
         }
     }
-    const int32_t *row = a.page_table + (size_t)b * a.max_pages;
-    if (APPEND && len > 0) {
-        const int t = (len - 1) % kPS, page = row[(len - 1) / kPS];
-        const size_t o = b * a.ldkv + g * kD + 4 * lane;
-        const uint2 kw = norm_rope(*reinterpret_cast<const uint2 *>(a.k_new + o), a.k_gain, a.eps, cs, sn, lane);
-        uint32_t ksm, vsm;
-        const uint32_t kc = quantise_row(kw, lane, ksm);
-        const uint32_t vc = quantise_row(*reinterpret_cast<const uint2 *>(a.v_new + o), lane, vsm);
-        if (page >= 0 && page < a.num_pages) {
-            uint8_t *kp = a.k_pages + ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-            uint8_t *vp = a.v_pages + ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-            *reinterpret_cast<uint16_t *>(kp + kvq_k_quad_offset(t, lane)) = (uint16_t)kc;
-            *reinterpret_cast<uint16_t *>(vp + kvq_v_quad_offset(t, lane)) = (uint16_t)vc;
-            if ((lane & 7) == 0) {
-                *reinterpret_cast<uint32_t *>(kp + kvq_param_offset(t, lane >> 3)) = ksm;
-                *reinterpret_cast<uint32_t *>(vp + kvq_param_offset(t, lane >> 3)) = vsm;
+    return (len + kPS - 1) / kPS;
+}
+
+// First request b whose pages reach past page x (prefix[b + 1] > x).
+__device__ __forceinline__ int request_of(const int *prefix, int batch, int x) {
+    int l = 0, r = batch - 1;
+    while (l < r) {
+        const int mid = (l + r) >> 1;
+        if (prefix[mid + 1] > x) r = mid; else l = mid + 1;
+    }
+    return l;
+}
+
+__device__ __forceinline__ void grid_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 transpose of 16-bit values over the warp: lane 4 i + j gives and gets
+// row i, columns 2j and 2j + 1.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// bf16 pair 128 + n of nibble I of both halves of a code word.
+template <int I>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+    return ((w >> (4 * I)) & 0x000f000fu) | 0x43004300u;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+template <int GROUP, bool APPEND>
+__global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(const __grid_constant__ KvqArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const SmemLayout L = smem_layout(a.hkv, a.batch);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = workers_of(a.hkv);
+    const int n_consumers = a.hkv * S;
+    const int hq = a.hkv * GROUP;
+    const int n_stages = (int)L.stages;
+
+    int *prefix = reinterpret_cast<int *>(smem + L.off_prefix);
+    int *scan = reinterpret_cast<int *>(smem + L.off_scan);
+    volatile int *page_ok = reinterpret_cast<int *>(smem + L.off_ok);
+    const uint32_t bar_full_k = smem_u32(smem + L.off_bar);
+    const uint32_t bar_full_v = bar_full_k + n_stages * 8;
+    const uint32_t bar_empty = bar_full_v + n_stages * 8;
+
+    if (!a.early) grid_wait();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < n_stages; ++s) {
+            mbar_init(bar_full_k + 8 * s, 1);
+            mbar_init(bar_full_v + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, a.hkv);
+        }
+        fence_mbar_init();
+        prefix[0] = 0;
+    }
+    // prefix sums of the page counts, one request a thread
+    for (int base = 0, carry = 0; base < a.batch; base += blockDim.x) {
+        const int b = base + threadIdx.x;
+        int v = b < a.batch ? pages_of<APPEND>(a, b, blockIdx.x == 0) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) scan[warp] = v;
+        __syncthreads();
+        int before = carry;
+        for (int w = 0; w <= n_consumers; ++w) {
+            const int x = scan[w];
+            before += w < warp ? x : 0;
+            carry += x;
+        }
+        if (b < a.batch) prefix[b + 1] = before + v;
+        __syncthreads();
+    }
+    __syncthreads();
+    const int total = prefix[a.batch];
+    const Split split(total, gridDim.x, S);
+
+    // With the pools vouched for (early_pools) the producer streams before it waits.
+    const bool producer = warp == n_consumers;
+    const bool producer_first = a.early && a.early_pools && producer;
+    if (a.early && !producer_first) grid_wait();
+
+    if (blockIdx.x == 0 && !producer) {  // zero rows of requests with nothing to attend over
+        const int chunks = hq * kD * 2 / 16;
+        for (int b = warp; b < a.batch; b += n_consumers) {
+            if (prefix[b + 1] != prefix[b]) continue;
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)b * hq * kD);
+            for (int c = lane; c < chunks; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+
+    if (producer) {
+        // ---------------- producer: lanes find 32 page ids, lane 0 issues the copies
+        const uint64_t policy = policy_evict_first();
+        int rounds = 0;  // pages of the longest worker
+        for (int e = 0; e < S; ++e) {
+            const int v = split.worker(blockIdx.x, gridDim.x, e, S);
+            rounds = max(rounds, split.lo(v + 1) - split.lo(v));
+        }
+        const int n_it = total > 0 ? rounds * S : 0;
+        // the page of ring position `it`: worker it % S's page it / S; -2: it has no such page
+        auto find = [&](int it) -> int {
+            if (it >= n_it) return -2;
+            const int v = split.worker(blockIdx.x, gridDim.x, it % S, S);
+            const int x = split.lo(v) + it / S;
+            if (x >= split.lo(v + 1)) return -2;
+            const int b = request_of(prefix, a.batch, x);
+            const int page = a.page_table[(size_t)b * a.max_pages + (x - prefix[b])];
+            return page < 0 || page >= a.num_pages ? -1 : page;
+        };
+        bool waited = !producer_first;
+        int next = find(lane);
+        for (int base = 0; base < n_it; base += 32) {
+            const int mine = next;
+            next = find(base + 32 + lane);
+            const int cnt = min(32, n_it - base);
+            for (int u = 0; u < cnt; ++u) {
+                const int page = __shfl_sync(0xffffffffu, mine, u);
+                const int it = base + u;
+                if (page == -2) continue;
+                if (!waited && it >= n_stages) {
+                    grid_wait();
+                    waited = true;
+                }
+                if (lane == 0) {
+                    const int s = it % n_stages;
+                    if (it >= n_stages) mbar_wait(bar_empty + 8 * s, ((it / n_stages) & 1) ^ 1, &g_status);
+                    uint8_t *dst = smem + s * L.stage_bytes;
+                    page_ok[s] = page;
+                    if (page < 0) {
+                        atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
+                        mbar_arrive(bar_full_k + 8 * s);
+                        mbar_arrive(bar_full_v + 8 * s);
+                    } else {
+                        const size_t off = (size_t)page * L.page_bytes;
+                        mbar_arrive_expect_tx(bar_full_k + 8 * s, L.page_bytes);
+                        bulk_g2s_hint(smem_u32(dst), a.k_pages + off, L.page_bytes, bar_full_k + 8 * s, policy);
+                        mbar_arrive_expect_tx(bar_full_v + 8 * s, L.page_bytes);
+                        bulk_g2s_hint(smem_u32(dst + L.page_bytes), a.v_pages + off, L.page_bytes, bar_full_v + 8 * s, policy);
+                    }
+                }
+                __syncwarp();
             }
         }
-        __syncwarp();
+        if (!waited) grid_wait();
+        return;
     }
-    float q[GROUP][4], acc[GROUP][4], m[GROUP], l[GROUP];
+
+    // ---------------- a worker's warp of KV head g
+    const int g = warp % a.hkv, e = warp / a.hkv;
+    const int v = split.worker(blockIdx.x, gridDim.x, e, S);
+    if (total == 0 || v >= split.nv) return;
+    const int lo = split.lo(v), hi = split.lo(v + 1);
+    const int r = lane >> 2, c = lane & 3;
+
+    auto load_q = [&](int b, uint2 (&w)[GROUP]) {
 #pragma unroll
-    for (int i = 0; i < GROUP; ++i) {
-        uint2 w = *reinterpret_cast<const uint2 *>(a.q + b * a.ldq + (g * GROUP + i) * kD + 4 * lane);
-        if (APPEND && len > 0) w = norm_rope(w, a.q_gain, a.eps, cs, sn, lane);
-        q[i][0] = bf16lo(w.x) * a.scale_log2, q[i][1] = bf16hi(w.x) * a.scale_log2;
-        q[i][2] = bf16lo(w.y) * a.scale_log2, q[i][3] = bf16hi(w.y) * a.scale_log2;
-        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        m[i] = -INFINITY, l[i] = 0.f;
-    }
-    for (int j = 0; j < len; ++j) {
-        const int page = row[j / kPS], t = j % kPS;
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
-            continue;
-        }
-        const uint8_t *kp = a.k_pages + ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-        const uint8_t *vp = a.v_pages + ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-        const uint32_t kc = *reinterpret_cast<const uint16_t *>(kp + kvq_k_quad_offset(t, lane));
-        const uint32_t vc = *reinterpret_cast<const uint16_t *>(vp + kvq_v_quad_offset(t, lane));
-        const uint32_t ksm = *reinterpret_cast<const uint32_t *>(kp + kvq_param_offset(t, lane >> 3));
-        const uint32_t vsm = *reinterpret_cast<const uint32_t *>(vp + kvq_param_offset(t, lane >> 3));
-        float k[4], v[4];
+        for (int i = 0; i < GROUP; ++i)
+            w[i] = *reinterpret_cast<const uint2 *>(a.q + b * a.ldq + (g * GROUP + i) * kD + 4 * lane);
+    };
+    int b = request_of(prefix, a.batch, lo);
+    uint2 q_next[GROUP];
+    load_q(b, q_next);
+    int split_b[2] = {-1, -1};  // requests whose partials this worker wrote: its first and last at most
+    int it = e;                 // ring position of the worker's next page
+
+    for (int x = lo; x < hi;) {
+        const int p0 = prefix[b], p1 = prefix[b + 1];
+        const int j0 = x - p0, j1 = min(hi, p1) - p0;
+        const int seq_len = a.seq_lens[b];
+        uint2 qw[GROUP];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            k[c] = fmaf(bf16lo(ksm), (float)((kc >> (4 * c)) & 15u), bf16hi(ksm));
-            v[c] = fmaf(bf16lo(vsm), (float)((vc >> (4 * c)) & 15u), bf16hi(vsm));
+        for (int i = 0; i < GROUP; ++i) qw[i] = q_next[i];
+        // the next request, whose q is loaded a segment ahead
+        int b_next = b + 1;
+        if (p1 < hi) {
+            while (prefix[b_next + 1] == prefix[b_next]) ++b_next;
+            load_q(b_next, q_next);
         }
+        const bool has_new = APPEND && j1 == p1 - p0;
+        uint32_t new_k = 0, new_v = 0, new_ksm = 0, new_vsm = 0;
+        if (APPEND) {
+            float cs[4], sn[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = 4 * (lane & 15) + u;
+                const int pos = a.positions ? a.positions[(size_t)a.pair_axis[i] * a.batch + b] : seq_len - 1;
+                sincos_pos_freq(pos, a.freq_hi[i], a.freq_lo[i], &sn[u], &cs[u]);
+            }
+            if (has_new) {
+                const size_t o = b * a.ldkv + g * kD + 4 * lane;
+                const uint2 kw = norm_rope(*reinterpret_cast<const uint2 *>(a.k_new + o), a.k_gain, a.eps, cs, sn, lane);
+                new_k = quantise_row(kw, lane, new_ksm);
+                new_v = quantise_row(*reinterpret_cast<const uint2 *>(a.v_new + o), lane, new_vsm);
+            }
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) qw[i] = norm_rope(qw[i], a.q_gain, a.eps, cs, sn, lane);
+        }
+        // B of the scores: lane (n, c), n = (group n / 2, head n % 2), holds head n % 2's dims [32 g + 8 c, + 8) of its
+        // own group, as the pairs (j, j + 4) that the code words hold
+        uint32_t bq[16];
+        float qsum[GROUP];  // 128 sum of the head's q over group c
+        {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            const int src = 8 * (r >> 1) + 2 * c;
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) {
+                const uint32_t x0 = __shfl_sync(0xffffffffu, qw[i].x, src), x1 = __shfl_sync(0xffffffffu, qw[i].y, src);
+                const uint32_t x2 = __shfl_sync(0xffffffffu, qw[i].x, src + 1), x3 = __shfl_sync(0xffffffffu, qw[i].y, src + 1);
+                if ((r & 1) == i) w[0] = x0, w[1] = x1, w[2] = x2, w[3] = x3;
+                float s = (bf16lo(qw[i].x) + bf16hi(qw[i].x)) + (bf16lo(qw[i].y) + bf16hi(qw[i].y));
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                qsum[i] = __shfl_sync(0xffffffffu, s, 8 * c);
+            }
+            const uint32_t pr[4] = {__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
+                                    __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632)};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) bq[k] = (k >> 2) == (r >> 1) ? pr[k & 3] : 0u;
+        }
+        float o[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float ref[GROUP], l[GROUP], corr[GROUP];
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) ref[i] = -INFINITY, l[i] = 0.f, corr[i] = 0.f;
+
+        for (int j = j0; j < j1; ++j, it += S) {
+            const int s = it % n_stages;
+            const uint32_t phase = (it / n_stages) & 1;
+            const uint32_t ks = smem_u32(smem) + s * L.stage_bytes + g * kKvqHeadBytes;
+            const uint32_t vs = ks + L.page_bytes;
+            mbar_wait(bar_full_k + 8 * s, phase, &g_status);
+            const int nt = min(kPS, seq_len - j * kPS);
+            const int page = page_ok[s];
+            const bool patch = has_new && j == j1 - 1 && page >= 0;
+            if (page >= 0) {
+                if (patch) {
+                    // the new token's row, in the stage and in the pool
+                    const int t = nt - 1;
+                    uint8_t *dst = smem + (ks - smem_u32(smem));
+                    uint8_t *pool = a.k_pages + ((size_t)page * a.hkv + g) * kKvqHeadBytes;
+                    *reinterpret_cast<uint16_t *>(dst + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
+                    *reinterpret_cast<uint16_t *>(pool + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
+                    if ((lane & 7) == 0) {
+                        *reinterpret_cast<uint32_t *>(dst + kvq_param_offset(t, lane >> 3)) = new_ksm;
+                        *reinterpret_cast<uint32_t *>(pool + kvq_param_offset(t, lane >> 3)) = new_ksm;
+                    }
+                    __syncwarp();
+                }
+                // scores: A rows are tokens r and r + 8
+                const uint4 k0 = lds128(ks + r * 64 + c * 16), k1 = lds128(ks + 512 + r * 64 + c * 16);
+                const uint32_t kp0 = lds32(ks + kKvqCodeBytes + lane * 4), kp1 = lds32(ks + kKvqCodeBytes + 128 + lane * 4);
+                float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma16816(d0, code_pair<0>(w0[u]), code_pair<0>(w1[u]), code_pair<1>(w0[u]), code_pair<1>(w1[u]), bq[4 * u],
+                             bq[4 * u + 1]);
+                    mma16816(d1, code_pair<0>(w0[u + 2]), code_pair<0>(w1[u + 2]), code_pair<1>(w0[u + 2]),
+                             code_pair<1>(w1[u + 2]), bq[4 * u + 8], bq[4 * u + 9]);
+                    mma16816(d0, code_pair<2>(w0[u]), code_pair<2>(w1[u]), code_pair<3>(w0[u]), code_pair<3>(w1[u]),
+                             bq[4 * u + 2], bq[4 * u + 3]);
+                    mma16816(d1, code_pair<2>(w0[u + 2]), code_pair<2>(w1[u + 2]), code_pair<3>(w0[u + 2]),
+                             code_pair<3>(w1[u + 2]), bq[4 * u + 10], bq[4 * u + 11]);
+                }
+                // s and m of (token, group c), then the sum over groups (the 4 lanes of a token)
+                float sc[GROUP][2];
+                const float s0 = bf16lo(kp0), m0 = bf16hi(kp0), s1 = bf16lo(kp1), m1 = bf16hi(kp1);
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i) {
+                    sc[i][0] = fmaf(s0, fmaf(-128.f, qsum[i], d0[i] + d1[i]), m0 * qsum[i]);
+                    sc[i][1] = fmaf(s1, fmaf(-128.f, qsum[i], d0[2 + i] + d1[2 + i]), m1 * qsum[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        sc[i][y] += __shfl_xor_sync(0xffffffffu, sc[i][y], 1);
+                        sc[i][y] += __shfl_xor_sync(0xffffffffu, sc[i][y], 2);
+                        sc[i][y] *= a.scale_log2;
+                    }
+                if (nt < kPS) {
+#pragma unroll
+                    for (int i = 0; i < GROUP; ++i) {
+                        if (r >= nt) sc[i][0] = -INFINITY;
+                        if (r + 8 >= nt) sc[i][1] = -INFINITY;
+                    }
+                }
+                bool past = false;
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i) past |= fmaxf(sc[i][0], sc[i][1]) > ref[i] + kRefSlack;
+                if (__any_sync(0xffffffffu, past)) {  // move the references to the maxima so far
+                    float alpha[2] = {1.f, 1.f};
+#pragma unroll
+                    for (int i = 0; i < GROUP; ++i) {
+                        float m = fmaxf(sc[i][0], sc[i][1]);
+#pragma unroll
+                        for (int y = 4; y < 32; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+                        m = fmaxf(m, ref[i]);
+                        alpha[i] = m > ref[i] ? exp2_approx(ref[i] - m) : 1.f;
+                        ref[i] = m;
+                        l[i] *= alpha[i];
+                        corr[i] *= alpha[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i][0] *= alpha[0], o[i][1] *= alpha[1], o[i][2] *= alpha[0], o[i][3] *= alpha[1];
+                }
+                mbar_wait(bar_full_v + 8 * s, phase, &g_status);
+                if (patch) {
+                    const int t = nt - 1;
+                    uint8_t *dst = smem + (vs - smem_u32(smem));
+                    uint8_t *pool = a.v_pages + ((size_t)page * a.hkv + g) * kKvqHeadBytes;
+                    *reinterpret_cast<uint16_t *>(dst + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
+                    *reinterpret_cast<uint16_t *>(pool + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
+                    if ((lane & 7) == 0) {
+                        *reinterpret_cast<uint32_t *>(dst + kvq_param_offset(t, lane >> 3)) = new_vsm;
+                        *reinterpret_cast<uint32_t *>(pool + kvq_param_offset(t, lane >> 3)) = new_vsm;
+                    }
+                    __syncwarp();
+                }
+                const uint4 v0 = lds128(vs + lane * 16), v1 = lds128(vs + 512 + lane * 16);
+                uint32_t vp0 = lds32(vs + kKvqCodeBytes + lane * 4), vp1 = lds32(vs + kKvqCodeBytes + 128 + lane * 4);
+                if (nt < kPS) {  // slots past the length may hold anything
+                    if (r >= nt) vp0 = 0u;
+                    if (r + 8 >= nt) vp1 = 0u;
+                }
+                // p s of (token, group c) for both heads, rounded to bf16, transposed into B
+                const float t0 = bf16lo(vp0), t1 = bf16lo(vp1);
+                const float c0 = fmaf(8.f, t0, bf16hi(vp0)), c1 = fmaf(8.f, t1, bf16hi(vp1));
+                float ps[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i) {
+                    const float pa = exp2_approx(sc[i][0] - ref[i]), pb = exp2_approx(sc[i][1] - ref[i]);
+                    l[i] += pa + pb;
+                    ps[0][i] = pa * t0;
+                    ps[1][i] = pb * t1;
+                    corr[i] = fmaf(pa, c0, fmaf(pb, c1, corr[i]));
+                }
+                const uint32_t pk0 = pack_bf16x2(ps[0][0], ps[0][1]), pk1 = pack_bf16x2(ps[1][0], ps[1][1]);
+                corr[0] = fmaf(-136.f, bf16lo(pk0) + bf16lo(pk1), corr[0]);
+                if (GROUP == 2) corr[GROUP - 1] = fmaf(-136.f, bf16hi(pk0) + bf16hi(pk1), corr[GROUP - 1]);
+                const uint32_t b0 = transpose8x8(pk0), b1 = transpose8x8(pk1);
+                const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    mma16816(o[2 * u], code_pair<0>(x0[u]), code_pair<1>(x0[u]), code_pair<0>(x1[u]), code_pair<1>(x1[u]), b0, b1);
+                    mma16816(o[2 * u + 1], code_pair<2>(x0[u]), code_pair<3>(x0[u]), code_pair<2>(x1[u]), code_pair<3>(x1[u]), b0,
+                             b1);
+                }
+            } else {
+                mbar_wait(bar_full_v + 8 * s, phase, &g_status);
+            }
+            // the patch's generic stores come before the next bulk copy into the stage
+            if (patch) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+        }
+
+        // sums over the tokens (lanes of equal c); the lane keeps dims [32 c + 4 r, + 4) of both heads
+        float acc[GROUP][4];
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
-            const float s = warp_sum(q[i][0] * k[0] + q[i][1] * k[1] + q[i][2] * k[2] + q[i][3] * k[3]);
-            const float m_new = fmaxf(m[i], s);
-            const float alpha = exp2_approx(m[i] - m_new), p = exp2_approx(s - m_new);
-            m[i] = m_new;
-            l[i] = l[i] * alpha + p;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[i][c] = acc[i][c] * alpha + p * v[c];
+            for (int y = 4; y < 32; y <<= 1) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], y);
+                corr[i] += __shfl_xor_sync(0xffffffffu, corr[i], y);
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int k = (d & 1) * 2 + i, t = d >> 1;
+                const float lo2 = c & 1 ? o[2 + t][k] : o[t][k], hi2 = c & 1 ? o[6 + t][k] : o[4 + t][k];
+                acc[i][d] = (c & 2 ? hi2 : lo2) + corr[i];
+            }
         }
+        if (j0 == 0 && j1 == p1 - p0) {
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) {
+                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+                *reinterpret_cast<uint2 *>(a.out + ((size_t)b * hq + g * GROUP + i) * kD + 32 * c + 4 * r) =
+                    make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
+            }
+        } else {
+            const size_t slot = (size_t)v + b;
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) {
+                const int h = g * GROUP + i;
+                *reinterpret_cast<float4 *>(a.part_acc + (slot * hq + h) * kD + 4 * lane) =
+                    make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * hq + h) * 2) = make_float2(ref[i], l[i]);
+            }
+            split_b[x == lo ? 0 : 1] = b;
+        }
+        x = p0 + j1;
+        b = b_next;
+    }
+
+    // Split requests: count in, and merge where this warp is the last.
+    if (split_b[0] < 0 && split_b[1] < 0) return;
+    __syncwarp();
+    int prev[2] = {0, 0};
+    if (lane == 0) {
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+            if (split_b[d] >= 0)
+                asm volatile("atom.add.relaxed.gpu.s32 %0, [%1], 1;"
+                             : "=r"(prev[d])
+                             : "l"(a.arrivals + (size_t)split_b[d] * kMaxHkv + g)
+                             : "memory");
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
     }
 #pragma unroll
-    for (int i = 0; i < GROUP; ++i) {
-        const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
-        *reinterpret_cast<uint2 *>(a.out + ((size_t)b * a.hkv * GROUP + g * GROUP + i) * kD + 4 * lane) =
-            make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
+    for (int d = 0; d < 2; ++d) {
+        const int bb = split_b[d];
+        if (bb < 0) continue;
+        const int v0 = split.of_page(prefix[bb]), v1 = split.of_page(prefix[bb + 1] - 1);
+        if (__shfl_sync(0xffffffffu, prev[d], 0) != v1 - v0) continue;
+        constexpr int kBatch = 8;  // partials in flight together
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) {
+            const int h = g * GROUP + i;
+            float m = -INFINITY, ls = 0.f, z[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int w0 = v0; w0 <= v1; w0 += kBatch) {
+                float2 ml[kBatch];
+                float4 pv[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const size_t row = ((size_t)min(w0 + u, v1) + bb) * hq + h;
+                    ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + row * 2));
+                    pv[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_acc + row * kD + 4 * lane));
+                }
+                float mb = m;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) mb = fmaxf(mb, ml[u].x);
+                const float at = mb == -INFINITY ? 0.f : mb;  // nothing attended so far: weights 2^-inf
+                const float alpha = exp2_approx(m - at);
+                ls *= alpha;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) z[k] *= alpha;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    if (w0 + u > v1) continue;
+                    const float w = exp2_approx(ml[u].x - at);
+                    ls = fmaf(w, ml[u].y, ls);
+                    z[0] = fmaf(w, pv[u].x, z[0]);
+                    z[1] = fmaf(w, pv[u].y, z[1]);
+                    z[2] = fmaf(w, pv[u].z, z[2]);
+                    z[3] = fmaf(w, pv[u].w, z[3]);
+                }
+                m = mb;
+            }
+            const float inv = ls == 0.f ? 0.f : 1.f / ls;
+            *reinterpret_cast<uint2 *>(a.out + ((size_t)bb * hq + h) * kD + 32 * c + 4 * r) =
+                make_uint2(pack_bf16x2(z[0] * inv, z[1] * inv), pack_bf16x2(z[2] * inv, z[3] * inv));
+        }
+        if (lane == 0) a.arrivals[(size_t)bb * kMaxHkv + g] = 0;
     }
 }
 
 }  // namespace
 
-size_t kvq_decode_workspace_bytes(int batch, int n_q_heads, int ctas) {
-    (void)batch, (void)n_q_heads, (void)ctas;
-    return 256;
+size_t kvq_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int ctas) {
+    return workspace_layout(batch, n_q_heads, ctas * workers_of(n_kv_heads)).total;
 }
 
 cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void *v_pages, const int32_t *page_table,
                               const int32_t *seq_lens, int batch, void *out, const qa_attn_params &p, float scale,
                               int ctas, cudaStream_t stream, const KvqAppend *app) {
-    (void)ctas;
     KvqArgs a = {};
     const int group = p.n_q_heads / p.n_kv_heads;
     a.q = static_cast<const uint16_t *>(q);
@@ -205,6 +706,13 @@ cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void 
     a.max_pages = p.max_pages_per_seq;
     a.num_pages = p.num_pages;
     a.scale_log2 = scale * kLog2e;
+    a.early = (p.abi_version >= 2 && p.stable_metadata >= 1) ? 1 : 0;
+    a.early_pools = (p.abi_version >= 2 && p.stable_metadata >= 2) ? 1 : 0;
+    const WorkspaceLayout w = workspace_layout(batch, p.n_q_heads, ctas * workers_of(p.n_kv_heads));
+    uint8_t *ws = static_cast<uint8_t *>(p.workspace);
+    a.part_acc = reinterpret_cast<float *>(ws + w.acc);
+    a.part_ml = reinterpret_cast<float *>(ws + w.ml);
+    a.arrivals = reinterpret_cast<int *>(ws + w.arrivals);
     if (app) {
         const qa_rope &rope = *app->rope;
         a.k_new = static_cast<const uint16_t *>(app->k_new);
@@ -222,13 +730,16 @@ cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(batch * p.n_kv_heads));
-    cfg.blockDim = dim3(32);
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)((workers_of(p.n_kv_heads) * p.n_kv_heads + 1) * 32));
+    cfg.dynamicSmemBytes = smem_layout(p.n_kv_heads, batch).total;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     auto kernel = app ? (group == 2 ? kvq_decode_kernel<2, true> : kvq_decode_kernel<1, true>)
                       : (group == 2 ? kvq_decode_kernel<2, false> : kvq_decode_kernel<1, false>);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 

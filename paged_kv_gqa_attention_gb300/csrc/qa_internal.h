@@ -102,7 +102,7 @@ struct KvqAppend {
     long long ldkv;
     const qa_rope *rope;
 };
-size_t kvq_decode_workspace_bytes(int batch, int n_q_heads, int ctas);
+size_t kvq_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int ctas);
 cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void *v_pages, const int32_t *page_table,
                               const int32_t *seq_lens, int batch, void *out, const qa_attn_params &p, float scale,
                               int ctas, cudaStream_t stream, const KvqAppend *app);

@@ -40,7 +40,7 @@ def check(got, w, what, scale=None, q=None):
     g = f64(got)
     assert np.isfinite(g).all(), f"{what}: non-finite"
     over = np.abs(g - ref) > bound
-    assert not over.any(), f"{what}: {int(over.sum())} of {over.size} past the bound, worst {np.max(np.abs(g - ref) / np.maximum(bound, 1e-30)):.3g} times it"
+    assert not over.any(), f"{what}: {int(over.sum())} of {over.size} past the bound, worst {np.max(np.abs(g - ref) / np.maximum(bound, 1e-30)):.3g} times it, error {np.max(np.abs(g - ref)[over]):.3g}"
     assert np.linalg.norm(g - ref) <= 5e-3 * np.linalg.norm(ref), what
 
 
