@@ -20,17 +20,23 @@
 // warp that arrives last merges the partials and resets the counter, so
 // nothing waits on another CTA.
 //
-// Arithmetic of one page and KV head (16 tokens, mma.m16n8k16, fp32 sums).
-// Codes become bf16 by masking a nibble of both halves of a word and ORing
-// the bits of 128: 128 + n, exact.  The 8 columns are (group g, query head
-// h): B of the scores holds head h's dims of group g and zeros elsewhere, so
-// one product gives sum_{d in g} q_d (128 + n_jd) for each group apart, to
-// which its s and m are applied in fp32.  B of the outputs holds p_jh s_jg,
-// rounded to bf16, and the columns of a dim's own group are kept.  Offsets
-// are taken back in fp32: 128 sum q from the scores; from the outputs 136
-// times the same rounded p s, with m + 8 s in place of m, so the rounding
-// acts on n - 8.  The maximum is a reference that is only moved once a score
-// passes it by 2^10, which leaves the reduction over tokens out of most pages.
+// Arithmetic of one page and KV head (16 tokens, mma.m16n8k16 on fp16, fp32
+// sums).  A masked nibble of both halves of a code word is a pair of fp16
+// subnormals, n 2^-24 or 16 n 2^-24: the codes are multiplied as they lie,
+// exactly and without an offset to take back (a word of 8 codes costs one
+// shift and four ANDs; as 128 + n in bf16 it cost seven, the ALU pipe was the
+// busiest, and 136 times the sums had to cancel).  q is scaled by a power of
+// two to a maximum below 2^15, where bf16's 8 bits are exact in fp16 down to
+// 2^-22 of the largest.  The 8 columns are (group g, query head h): B of the
+// scores holds head h's dims of group g and zeros elsewhere, so one product
+// gives sum_{d in g} q_d n_jd for each group apart, to which its s and m are
+// applied in fp32.  B of the outputs holds p_jh s_jg, rounded to fp16 (2^-12
+// of itself), and the columns of a dim's own group are kept; sum p m is kept
+// in fp32 beside it.  fp16's range: p is taken against a reference maximum
+// that is moved when a score passes it by 2^4, s against a power of two that
+// is moved when an s passes 16 times its target, so p s stays below 2^14 and
+// is a normal number down to 2^-20 of the largest; most pages move neither,
+// which leaves the reductions over tokens out.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -116,7 +122,8 @@ __device__ __forceinline__ uint32_t quantise_row(uint2 w, int lane, uint32_t &sm
 constexpr int kMaxHkv = 8;
 constexpr int kMaxWorkers = 16;       // warps that compute, in a CTA
 constexpr int kMaxStages = 32;
-constexpr float kRefSlack = 10.f;     // log2 units a score may pass the reference by
+constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
+constexpr float kScaleMost = 1024.f;  // s times its factor: set to [32, 64), moved past this
 
 // Workers of a CTA: as many as fill 16 warps.
 __host__ __device__ constexpr int workers_of(int hkv) { return kMaxWorkers / hkv; }
@@ -132,8 +139,8 @@ __host__ __device__ inline SmemLayout smem_layout(int hkv, int batch) {
     s.stages = 204800u / s.stage_bytes;
     if (s.stages > kMaxStages) s.stages = kMaxStages;
     uint32_t o = s.stages * s.stage_bytes;
-    s.off_bar = o;  // full K, full V, empty, for each stage
-    o += 3 * s.stages * 8;
+    s.off_bar = o;  // full, empty, for each stage
+    o += 2 * s.stages * 8;
     s.off_ok = o;  // the stage's page id, -1 if bad
     o += s.stages * 4;
     s.off_scan = o;  // warp sums of the prefix scan
@@ -219,7 +226,7 @@ __device__ __forceinline__ void grid_wait() {
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -232,11 +239,22 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-// bf16 pair 128 + n of nibble I of both halves of a code word.
+// fp16 pair of nibble I of both halves of a code word: n 2^-24 (I even) or
+// 16 n 2^-24 (I odd).
 template <int I>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-    return ((w >> (4 * I)) & 0x000f000fu) | 0x43004300u;
+    return (I < 2 ? w : w >> 8) & (I & 1 ? 0x00f000f0u : 0x000f000fu);
 }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// The power of two 2^e (e in [-126, 127]).
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int exponent_of(float x) { return (__float_as_int(x) >> 23 & 255) - 127; }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
@@ -258,19 +276,18 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
     const int n_consumers = a.hkv * S;
     const int hq = a.hkv * GROUP;
     const int n_stages = (int)L.stages;
+    const uint32_t smem_base = smem_u32(smem);
 
     int *prefix = reinterpret_cast<int *>(smem + L.off_prefix);
     int *scan = reinterpret_cast<int *>(smem + L.off_scan);
     volatile int *page_ok = reinterpret_cast<int *>(smem + L.off_ok);
-    const uint32_t bar_full_k = smem_u32(smem + L.off_bar);
-    const uint32_t bar_full_v = bar_full_k + n_stages * 8;
-    const uint32_t bar_empty = bar_full_v + n_stages * 8;
+    const uint32_t bar_full = smem_u32(smem + L.off_bar);
+    const uint32_t bar_empty = bar_full + n_stages * 8;
 
     if (!a.early) grid_wait();
     if (threadIdx.x == 0) {
         for (int s = 0; s < n_stages; ++s) {
-            mbar_init(bar_full_k + 8 * s, 1);
-            mbar_init(bar_full_v + 8 * s, 1);
+            mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, a.hkv);
         }
         fence_mbar_init();
@@ -335,33 +352,34 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
         };
         bool waited = !producer_first;
         int next = find(lane);
+        int st = 0;               // stage of ring position `it`, and how often the ring has been full
+        uint32_t turn = 0;
         for (int base = 0; base < n_it; base += 32) {
             const int mine = next;
             next = find(base + 32 + lane);
             const int cnt = min(32, n_it - base);
             for (int u = 0; u < cnt; ++u) {
                 const int page = __shfl_sync(0xffffffffu, mine, u);
-                const int it = base + u;
+                const int s = st;
+                const uint32_t now = turn;
+                if (++st == n_stages) st = 0, ++turn;
                 if (page == -2) continue;
-                if (!waited && it >= n_stages) {
+                if (!waited && now > 0) {
                     grid_wait();
                     waited = true;
                 }
                 if (lane == 0) {
-                    const int s = it % n_stages;
-                    if (it >= n_stages) mbar_wait(bar_empty + 8 * s, ((it / n_stages) & 1) ^ 1, &g_status);
+                    if (now > 0) mbar_wait(bar_empty + 8 * s, (now & 1) ^ 1, &g_status);
                     uint8_t *dst = smem + s * L.stage_bytes;
                     page_ok[s] = page;
                     if (page < 0) {
                         atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
-                        mbar_arrive(bar_full_k + 8 * s);
-                        mbar_arrive(bar_full_v + 8 * s);
+                        mbar_arrive(bar_full + 8 * s);
                     } else {
                         const size_t off = (size_t)page * L.page_bytes;
-                        mbar_arrive_expect_tx(bar_full_k + 8 * s, L.page_bytes);
-                        bulk_g2s_hint(smem_u32(dst), a.k_pages + off, L.page_bytes, bar_full_k + 8 * s, policy);
-                        mbar_arrive_expect_tx(bar_full_v + 8 * s, L.page_bytes);
-                        bulk_g2s_hint(smem_u32(dst + L.page_bytes), a.v_pages + off, L.page_bytes, bar_full_v + 8 * s, policy);
+                        mbar_arrive_expect_tx(bar_full + 8 * s, L.stage_bytes);
+                        bulk_g2s_hint(smem_u32(dst), a.k_pages + off, L.page_bytes, bar_full + 8 * s, policy);
+                        bulk_g2s_hint(smem_u32(dst + L.page_bytes), a.v_pages + off, L.page_bytes, bar_full + 8 * s, policy);
                     }
                 }
                 __syncwarp();
@@ -387,7 +405,8 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
     uint2 q_next[GROUP];
     load_q(b, q_next);
     int split_b[2] = {-1, -1};  // requests whose partials this worker wrote: its first and last at most
-    int it = e;                 // ring position of the worker's next page
+    int st = e;                 // stage of the worker's next page, and its barrier's phase
+    uint32_t phase = 0;
 
     for (int x = lo; x < hi;) {
         const int p0 = prefix[b], p1 = prefix[b + 1];
@@ -422,60 +441,77 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
             for (int i = 0; i < GROUP; ++i) qw[i] = norm_rope(qw[i], a.q_gain, a.eps, cs, sn, lane);
         }
         // B of the scores: lane (n, c), n = (group n / 2, head n % 2), holds head n % 2's dims [32 g + 8 c, + 8) of its
-        // own group, as the pairs (j, j + 4) that the code words hold
+        // own group, as the pairs (j, j + 4) that the code words hold, a 16th of the pairs whose codes come 16-fold
         uint32_t bq[16];
-        float qsum[GROUP];  // 128 sum of the head's q over group c
+        float qsum[GROUP], qback[GROUP];  // sum of the head's q over group c; 2^12 / q's scale
         {
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const int src = 8 * (r >> 1) + 2 * c;
 #pragma unroll
             for (int i = 0; i < GROUP; ++i) {
-                const uint32_t x0 = __shfl_sync(0xffffffffu, qw[i].x, src), x1 = __shfl_sync(0xffffffffu, qw[i].y, src);
-                const uint32_t x2 = __shfl_sync(0xffffffffu, qw[i].x, src + 1), x3 = __shfl_sync(0xffffffffu, qw[i].y, src + 1);
-                if ((r & 1) == i) w[0] = x0, w[1] = x1, w[2] = x2, w[3] = x3;
-                float s = (bf16lo(qw[i].x) + bf16hi(qw[i].x)) + (bf16lo(qw[i].y) + bf16hi(qw[i].y));
+                const float x[4] = {bf16lo(qw[i].x), bf16hi(qw[i].x), bf16lo(qw[i].y), bf16hi(qw[i].y)};
+                float s = (x[0] + x[1]) + (x[2] + x[3]);
+                float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 qsum[i] = __shfl_sync(0xffffffffu, s, 8 * c);
+                const int k = min(14 - exponent_of(m), 126);  // 126: q is zero or nearly
+                qback[i] = pow2i(12 - k);
+                const float up = pow2i(k);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const float y0 = __shfl_sync(0xffffffffu, x[d] * up, src), y1 = __shfl_sync(0xffffffffu, x[d] * up, src + 1);
+                    if ((r & 1) == i) w[d] = y0, w[4 + d] = y1;
+                }
             }
-            const uint32_t pr[4] = {__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
-                                    __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632)};
+            const uint32_t pr[4] = {pack_f16x2(w[0], w[4]), pack_f16x2(w[1] * 0.0625f, w[5] * 0.0625f), pack_f16x2(w[2], w[6]),
+                                    pack_f16x2(w[3] * 0.0625f, w[7] * 0.0625f)};
 #pragma unroll
             for (int k = 0; k < 16; ++k) bq[k] = (k >> 2) == (r >> 1) ? pr[k & 3] : 0u;
         }
         float o[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float ref[GROUP], l[GROUP], corr[GROUP];
+        float ref[GROUP], l[GROUP], corr[GROUP];  // reference, sum of p, sum of p m (log2 units, this lane's tokens)
+        float s_up = pow2i(126);                  // factor of s: moved by the first page
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) ref[i] = -INFINITY, l[i] = 0.f, corr[i] = 0.f;
 
-        for (int j = j0; j < j1; ++j, it += S) {
-            const int s = it % n_stages;
-            const uint32_t phase = (it / n_stages) & 1;
-            const uint32_t ks = smem_u32(smem) + s * L.stage_bytes + g * kKvqHeadBytes;
+        for (int j = j0; j < j1; ++j) {
+            const int s = st;
+            mbar_wait(bar_full + 8 * s, phase, &g_status);
+            st += S;
+            if (st >= n_stages) st -= n_stages, phase ^= 1;
+            const uint32_t ks = smem_base + s * L.stage_bytes + g * kKvqHeadBytes;
             const uint32_t vs = ks + L.page_bytes;
-            mbar_wait(bar_full_k + 8 * s, phase, &g_status);
             const int nt = min(kPS, seq_len - j * kPS);
             const int page = page_ok[s];
             const bool patch = has_new && j == j1 - 1 && page >= 0;
-            if (page >= 0) {
-                if (patch) {
-                    // the new token's row, in the stage and in the pool
-                    const int t = nt - 1;
-                    uint8_t *dst = smem + (ks - smem_u32(smem));
-                    uint8_t *pool = a.k_pages + ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-                    *reinterpret_cast<uint16_t *>(dst + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
-                    *reinterpret_cast<uint16_t *>(pool + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
-                    if ((lane & 7) == 0) {
-                        *reinterpret_cast<uint32_t *>(dst + kvq_param_offset(t, lane >> 3)) = new_ksm;
-                        *reinterpret_cast<uint32_t *>(pool + kvq_param_offset(t, lane >> 3)) = new_ksm;
-                    }
-                    __syncwarp();
+            if (patch) {
+                // the new token's row, in the stage and in the pools
+                const int t = nt - 1;
+                uint8_t *kd = smem + (ks - smem_base), *vd = smem + (vs - smem_base);
+                const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
+                *reinterpret_cast<uint16_t *>(kd + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
+                *reinterpret_cast<uint16_t *>(vd + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
+                *reinterpret_cast<uint16_t *>(a.k_pages + off + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
+                *reinterpret_cast<uint16_t *>(a.v_pages + off + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
+                if ((lane & 7) == 0) {
+                    const int at = kvq_param_offset(t, lane >> 3);
+                    *reinterpret_cast<uint32_t *>(kd + at) = new_ksm;
+                    *reinterpret_cast<uint32_t *>(vd + at) = new_vsm;
+                    *reinterpret_cast<uint32_t *>(a.k_pages + off + at) = new_ksm;
+                    *reinterpret_cast<uint32_t *>(a.v_pages + off + at) = new_vsm;
                 }
+                __syncwarp();
+            }
+            if (page >= 0) {
                 // scores: A rows are tokens r and r + 8
                 const uint4 k0 = lds128(ks + r * 64 + c * 16), k1 = lds128(ks + 512 + r * 64 + c * 16);
                 const uint32_t kp0 = lds32(ks + kKvqCodeBytes + lane * 4), kp1 = lds32(ks + kKvqCodeBytes + 128 + lane * 4);
+                uint32_t vp0 = lds32(vs + kKvqCodeBytes + lane * 4), vp1 = lds32(vs + kKvqCodeBytes + 128 + lane * 4);
                 float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
                 const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -491,11 +527,11 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
                 }
                 // s and m of (token, group c), then the sum over groups (the 4 lanes of a token)
                 float sc[GROUP][2];
-                const float s0 = bf16lo(kp0), m0 = bf16hi(kp0), s1 = bf16lo(kp1), m1 = bf16hi(kp1);
+                const float s0 = bf16lo(kp0) * 4096.f, m0 = bf16hi(kp0), s1 = bf16lo(kp1) * 4096.f, m1 = bf16hi(kp1);
 #pragma unroll
                 for (int i = 0; i < GROUP; ++i) {
-                    sc[i][0] = fmaf(s0, fmaf(-128.f, qsum[i], d0[i] + d1[i]), m0 * qsum[i]);
-                    sc[i][1] = fmaf(s1, fmaf(-128.f, qsum[i], d0[2 + i] + d1[2 + i]), m1 * qsum[i]);
+                    sc[i][0] = fmaf(s0, (d0[i] + d1[i]) * qback[i], m0 * qsum[i]);
+                    sc[i][1] = fmaf(s1, (d0[2 + i] + d1[2 + i]) * qback[i], m1 * qsum[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < GROUP; ++i)
@@ -505,67 +541,58 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
                         sc[i][y] += __shfl_xor_sync(0xffffffffu, sc[i][y], 2);
                         sc[i][y] *= a.scale_log2;
                     }
-                if (nt < kPS) {
+                if (nt < kPS) {  // slots past the length may hold anything
 #pragma unroll
                     for (int i = 0; i < GROUP; ++i) {
                         if (r >= nt) sc[i][0] = -INFINITY;
                         if (r + 8 >= nt) sc[i][1] = -INFINITY;
                     }
+                    if (r >= nt) vp0 = 0u;
+                    if (r + 8 >= nt) vp1 = 0u;
                 }
-                bool past = false;
+                const float t0 = bf16lo(vp0), t1 = bf16lo(vp1);
+                bool past = fmaxf(fabsf(t0), fabsf(t1)) * s_up > kScaleMost;
 #pragma unroll
                 for (int i = 0; i < GROUP; ++i) past |= fmaxf(sc[i][0], sc[i][1]) > ref[i] + kRefSlack;
                 if (__any_sync(0xffffffffu, past)) {  // move the references to the maxima so far
+                    float t = fmaxf(fabsf(t0), fabsf(t1));
+#pragma unroll
+                    for (int y = 1; y < 32; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, y));
                     float alpha[2] = {1.f, 1.f};
+                    if (t * s_up > kScaleMost) {
+                        const float up = pow2i(min(5 - exponent_of(t), 126));
+                        alpha[0] = alpha[1] = up / s_up;
+                        s_up = up;
+                    }
 #pragma unroll
                     for (int i = 0; i < GROUP; ++i) {
                         float m = fmaxf(sc[i][0], sc[i][1]);
 #pragma unroll
                         for (int y = 4; y < 32; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-                        m = fmaxf(m, ref[i]);
-                        alpha[i] = m > ref[i] ? exp2_approx(ref[i] - m) : 1.f;
-                        ref[i] = m;
-                        l[i] *= alpha[i];
-                        corr[i] *= alpha[i];
+                        if (m > ref[i]) {
+                            const float f = exp2_approx(ref[i] - m);
+                            ref[i] = m;
+                            alpha[i] *= f;
+                            l[i] *= f;
+                            corr[i] *= f;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) o[i][0] *= alpha[0], o[i][1] *= alpha[1], o[i][2] *= alpha[0], o[i][3] *= alpha[1];
                 }
-                mbar_wait(bar_full_v + 8 * s, phase, &g_status);
-                if (patch) {
-                    const int t = nt - 1;
-                    uint8_t *dst = smem + (vs - smem_u32(smem));
-                    uint8_t *pool = a.v_pages + ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-                    *reinterpret_cast<uint16_t *>(dst + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
-                    *reinterpret_cast<uint16_t *>(pool + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
-                    if ((lane & 7) == 0) {
-                        *reinterpret_cast<uint32_t *>(dst + kvq_param_offset(t, lane >> 3)) = new_vsm;
-                        *reinterpret_cast<uint32_t *>(pool + kvq_param_offset(t, lane >> 3)) = new_vsm;
-                    }
-                    __syncwarp();
-                }
-                const uint4 v0 = lds128(vs + lane * 16), v1 = lds128(vs + 512 + lane * 16);
-                uint32_t vp0 = lds32(vs + kKvqCodeBytes + lane * 4), vp1 = lds32(vs + kKvqCodeBytes + 128 + lane * 4);
-                if (nt < kPS) {  // slots past the length may hold anything
-                    if (r >= nt) vp0 = 0u;
-                    if (r + 8 >= nt) vp1 = 0u;
-                }
-                // p s of (token, group c) for both heads, rounded to bf16, transposed into B
-                const float t0 = bf16lo(vp0), t1 = bf16lo(vp1);
-                const float c0 = fmaf(8.f, t0, bf16hi(vp0)), c1 = fmaf(8.f, t1, bf16hi(vp1));
+                // p s of (token, group c) for both heads, rounded to fp16, transposed into B
+                const float u0 = t0 * s_up, u1 = t1 * s_up, c0 = bf16hi(vp0), c1 = bf16hi(vp1);
                 float ps[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
                 for (int i = 0; i < GROUP; ++i) {
                     const float pa = exp2_approx(sc[i][0] - ref[i]), pb = exp2_approx(sc[i][1] - ref[i]);
                     l[i] += pa + pb;
-                    ps[0][i] = pa * t0;
-                    ps[1][i] = pb * t1;
+                    ps[0][i] = pa * u0;
+                    ps[1][i] = pb * u1;
                     corr[i] = fmaf(pa, c0, fmaf(pb, c1, corr[i]));
                 }
-                const uint32_t pk0 = pack_bf16x2(ps[0][0], ps[0][1]), pk1 = pack_bf16x2(ps[1][0], ps[1][1]);
-                corr[0] = fmaf(-136.f, bf16lo(pk0) + bf16lo(pk1), corr[0]);
-                if (GROUP == 2) corr[GROUP - 1] = fmaf(-136.f, bf16hi(pk0) + bf16hi(pk1), corr[GROUP - 1]);
-                const uint32_t b0 = transpose8x8(pk0), b1 = transpose8x8(pk1);
+                const uint32_t b0 = transpose8x8(pack_f16x2(ps[0][0], ps[0][1])), b1 = transpose8x8(pack_f16x2(ps[1][0], ps[1][1]));
+                const uint4 v0 = lds128(vs + lane * 16), v1 = lds128(vs + 512 + lane * 16);
                 const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -573,8 +600,6 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
                     mma16816(o[2 * u + 1], code_pair<2>(x0[u]), code_pair<3>(x0[u]), code_pair<2>(x1[u]), code_pair<3>(x1[u]), b0,
                              b1);
                 }
-            } else {
-                mbar_wait(bar_full_v + 8 * s, phase, &g_status);
             }
             // the patch's generic stores come before the next bulk copy into the stage
             if (patch) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -584,6 +609,7 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
 
         // sums over the tokens (lanes of equal c); the lane keeps dims [32 c + 4 r, + 4) of both heads
         float acc[GROUP][4];
+        const float s_back = 1.f / s_up;
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
 #pragma unroll
@@ -595,7 +621,7 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
             for (int d = 0; d < 4; ++d) {
                 const int k = (d & 1) * 2 + i, t = d >> 1;
                 const float lo2 = c & 1 ? o[2 + t][k] : o[t][k], hi2 = c & 1 ? o[6 + t][k] : o[4 + t][k];
-                acc[i][d] = (c & 2 ? hi2 : lo2) + corr[i];
+                acc[i][d] = fmaf((c & 2 ? hi2 : lo2) * (d & 1 ? 1048576.f : 16777216.f), s_back, corr[i]);
             }
         }
         if (j0 == 0 && j1 == p1 - p0) {

@@ -93,17 +93,13 @@ def decode(q, k_pool, v_pool, table, lens, scale=None):
     """Attention in 64 bits over the 4-bit cache, and a bound on a kernel's
     error.  q float64 [B, Hq, 128]; returns out, bound [B, Hq, 128].
 
-    The bound: probabilities times scales are rounded to bf16 for the product
-    with the codes (taken about their middle 8), half a step of 2^-8 relative
-    each; the result is rounded once more, 2^-8 of itself; and 2^-10 of the
-    weighted values for the fp32 scores, whose sums carry the codes' offset
-    of 128: 128 dims x 2^-23 x 136 s |q| x 1/sqrt(128) is 2^-13 x (s |q| / 0.3)
-    for each of a few roundings, and moves p by that much relatively.  Where
-    all of these vanish (a value near 0 whose code is 8) the offsets remain:
-    codes are multiplied as 128 + n <= 143 and 136 is taken back in fp32, so
-    running sums reach 143 sum p s, and each page adds at most 4 roundings or
-    truncations of 2^-23 of that, 2^-21 x 143 sum p s a page (the terms are
-    positive, so no partial sum is larger)."""
+    The bound: probabilities times scales are rounded to fp16 for the product
+    with the codes, 2^-11 of themselves (half a step), and act on n; the
+    result is rounded once to bf16, 2^-8 of itself; and 2^-10 of the weighted
+    values for the fp32 scores: sums over 128 dims of |q| (|m| + 15 s), about
+    128 x 1.5 x 9 for these inputs, times 1/sqrt(128) and a few roundings of
+    2^-23 each, are 2^-15 to 2^-13 absolute (up to 2^-10 for queries of 12),
+    and move p by that much relatively."""
     B, Hq, D = q.shape
     H = k_pool.shape[1] // HEAD_BYTES
     scale = D ** -0.5 if scale is None else scale
@@ -120,9 +116,8 @@ def decode(q, k_pool, v_pool, table, lens, scale=None):
         v = vm + vs * vn
         o = np.einsum("hgt,htd->hgd", p, v)
         out[b] = o.reshape(Hq, D)
-        bound[b] = (2.0 ** -8 * (np.einsum("hgt,htd->hgd", p, vs * np.abs(vn - 8)) + np.abs(o))
-                    + 2.0 ** -10 * np.einsum("hgt,htd->hgd", p, np.abs(v))
-                    + 2.0 ** -21 * 143 * -(-n // PAGE) * np.einsum("hgt,htd->hgd", p, vs)).reshape(Hq, D)
+        bound[b] = (2.0 ** -11 * np.einsum("hgt,htd->hgd", p, vs * vn) + 2.0 ** -8 * np.abs(o)
+                    + 2.0 ** -10 * np.einsum("hgt,htd->hgd", p, np.abs(v))).reshape(Hq, D)
     return out, bound
 
 
