@@ -7,11 +7,11 @@
 //
 // Work split.  The pages of all requests form one flat list (request-major),
 // cut into equal contiguous ranges, one a worker.  A worker is one warp for
-// each KV head; a CTA (one an SM) holds S = 16 / Hkv workers, so its warps
-// hide one another's latency without meeting: each worker has its own
-// softmax state and its own requests.  A producer warp streams the workers'
-// pages in turn into one ring of shared memory with the bulk-copy engine,
-// the K page and the V page of a stage on separate mbarriers.
+// each KV head, and a CTA of 8 warps holds 8 / Hkv workers, two CTAs an SM.
+// Every warp streams the part of its own head (1280 contiguous bytes of a K
+// page and of a V page) through its own ring of shared memory with the
+// bulk-copy engine, so the warps of a CTA never meet after the prologue:
+// there is no producer warp to feed and no barrier to release a stage.
 //
 // A request that lies in one worker's range is finished there.  Otherwise
 // each worker writes an fp32 partial (maximum, sum, outputs) to slot v + b
@@ -41,6 +41,7 @@
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
+#include <type_traits>
 
 #include "kvq.cuh"
 #include "qa_internal.h"
@@ -120,31 +121,30 @@ __device__ __forceinline__ uint32_t quantise_row(uint2 w, int lane, uint32_t &sm
 }
 
 constexpr int kMaxHkv = 8;
-constexpr int kMaxWorkers = 16;       // warps that compute, in a CTA
-constexpr int kMaxStages = 32;
+constexpr int kWarps = 8;             // of a CTA
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxStages = 5;         // pages in a warp's ring
+constexpr int kStageBytes = 2 * kKvqHeadBytes;
 constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
 constexpr float kScaleMost = 1024.f;  // s times its factor: set to [32, 64), moved past this
 
-// Workers of a CTA: as many as fill 16 warps.
-__host__ __device__ constexpr int workers_of(int hkv) { return kMaxWorkers / hkv; }
+// Workers of a CTA.
+__host__ __device__ constexpr int workers_of(int hkv) { return kWarps / hkv; }
 
 struct SmemLayout {
-    uint32_t page_bytes, stage_bytes, stages, off_bar, off_ok, off_scan, off_prefix, total;
+    uint32_t stages, off_bar, off_scan, off_prefix, total;
 };
 
-__host__ __device__ inline SmemLayout smem_layout(int hkv, int batch) {
+// Two CTAs share an SM's 227 KB; the prefix sums of a large batch cost one
+// stage of every ring.
+__host__ __device__ inline SmemLayout smem_layout(int batch) {
     SmemLayout s;
-    s.page_bytes = hkv * kKvqHeadBytes;
-    s.stage_bytes = 2 * s.page_bytes;
-    s.stages = 204800u / s.stage_bytes;
-    if (s.stages > kMaxStages) s.stages = kMaxStages;
-    uint32_t o = s.stages * s.stage_bytes;
-    s.off_bar = o;  // full, empty, for each stage
-    o += 2 * s.stages * 8;
-    s.off_ok = o;  // the stage's page id, -1 if bad
-    o += s.stages * 4;
+    s.stages = batch <= 2048 ? kMaxStages : kMaxStages - 1;
+    uint32_t o = s.stages * kStageBytes * kWarps;
+    s.off_bar = o;  // a barrier for each stage of each warp
+    o += s.stages * 8 * kWarps;
     s.off_scan = o;  // warp sums of the prefix scan
-    o += 32 * 4;
+    o += kWarps * 4;
     s.off_prefix = o;
     o += (batch + 1) * 4;
     s.total = (o + 15) & ~15u;
@@ -268,33 +268,27 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 }
 
 template <int GROUP, bool APPEND>
-__global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(const __grid_constant__ KvqArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(const __grid_constant__ KvqArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
-    const SmemLayout L = smem_layout(a.hkv, a.batch);
+    const SmemLayout L = smem_layout(a.batch);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = workers_of(a.hkv);
-    const int n_consumers = a.hkv * S;
     const int hq = a.hkv * GROUP;
     const int n_stages = (int)L.stages;
-    const uint32_t smem_base = smem_u32(smem);
-
     int *prefix = reinterpret_cast<int *>(smem + L.off_prefix);
     int *scan = reinterpret_cast<int *>(smem + L.off_scan);
-    volatile int *page_ok = reinterpret_cast<int *>(smem + L.off_ok);
-    const uint32_t bar_full = smem_u32(smem + L.off_bar);
-    const uint32_t bar_empty = bar_full + n_stages * 8;
+    uint8_t *ring = smem + warp * n_stages * kStageBytes;
+    const uint32_t ring_base = smem_u32(ring);
+    const uint32_t bars = smem_u32(smem + L.off_bar) + warp * n_stages * 8;
 
     if (!a.early) grid_wait();
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < n_stages; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, a.hkv);
-        }
+    if (lane == 0) {
+        for (int s = 0; s < n_stages; ++s) mbar_init(bars + 8 * s, 1);
         fence_mbar_init();
-        prefix[0] = 0;
     }
+    if (threadIdx.x == 0) prefix[0] = 0;
     // prefix sums of the page counts, one request a thread
-    for (int base = 0, carry = 0; base < a.batch; base += blockDim.x) {
+    for (int base = 0, carry = 0; base < a.batch; base += kWarps * 32) {
         const int b = base + threadIdx.x;
         int v = b < a.batch ? pages_of<APPEND>(a, b, blockIdx.x == 0) : 0;
 #pragma unroll
@@ -305,7 +299,8 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
         if (lane == 31) scan[warp] = v;
         __syncthreads();
         int before = carry;
-        for (int w = 0; w <= n_consumers; ++w) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
             const int x = scan[w];
             before += w < warp ? x : 0;
             carry += x;
@@ -313,87 +308,59 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
         if (b < a.batch) prefix[b + 1] = before + v;
         __syncthreads();
     }
-    __syncthreads();
     const int total = prefix[a.batch];
     const Split split(total, gridDim.x, S);
 
-    // With the pools vouched for (early_pools) the producer streams before it waits.
-    const bool producer = warp == n_consumers;
-    const bool producer_first = a.early && a.early_pools && producer;
-    if (a.early && !producer_first) grid_wait();
+    // this warp: KV head g of worker v, pages [lo, hi) of the flat list
+    const int g = warp % a.hkv, e = warp / a.hkv;
+    const int v = split.worker(blockIdx.x, gridDim.x, e, S);
+    const bool working = e < S && v < split.nv;
+    const int lo = working ? split.lo(v) : 0, hi = working ? split.lo(v + 1) : 0;
+    // page ids, 32 at a time, one a lane: bad ones are -1
+    auto find = [&](int x) -> int {
+        if (x >= hi) return -1;
+        const int b = request_of(prefix, a.batch, x);
+        const int page = a.page_table[(size_t)b * a.max_pages + (x - prefix[b])];
+        return page < 0 || page >= a.num_pages ? -1 : page;
+    };
+    int ids = find(lo + lane), ids_next = -1;
+    int slot_page = -1;        // lane s: the page in stage s
+    int issued = lo;           // next page to copy
+    const uint64_t policy = policy_evict_first();
+    auto issue = [&](int s) {  // copies page `issued` into stage s
+        const int page = __shfl_sync(0xffffffffu, ids, (issued - lo) & 31);
+        if (lane == s) slot_page = page;
+        if (lane == 0) {
+            if (page < 0) {
+                atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
+                mbar_arrive(bars + 8 * s);
+            } else {
+                const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
+                const uint32_t dst = ring_base + s * kStageBytes;
+                mbar_arrive_expect_tx(bars + 8 * s, kStageBytes);
+                bulk_g2s_hint(dst, a.k_pages + off, kKvqHeadBytes, bars + 8 * s, policy);
+                bulk_g2s_hint(dst + kKvqHeadBytes, a.v_pages + off, kKvqHeadBytes, bars + 8 * s, policy);
+            }
+        }
+        ++issued;
+        if (((issued - lo) & 31) == 16) ids_next = find(issued + 16 + lane);
+        if (((issued - lo) & 31) == 0) ids = ids_next;
+    };
 
-    if (blockIdx.x == 0 && !producer) {  // zero rows of requests with nothing to attend over
+    // With the pools vouched for (early_pools) the rings fill before the wait.
+    if (a.early && !a.early_pools) grid_wait();
+    for (int s = 0; s < n_stages && issued < hi; ++s) issue(s);
+    if (a.early && a.early_pools) grid_wait();
+
+    if (blockIdx.x == 0) {  // zero rows of requests with nothing to attend over
         const int chunks = hq * kD * 2 / 16;
-        for (int b = warp; b < a.batch; b += n_consumers) {
+        for (int b = warp; b < a.batch; b += kWarps) {
             if (prefix[b + 1] != prefix[b]) continue;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)b * hq * kD);
             for (int c = lane; c < chunks; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-
-    if (producer) {
-        // ---------------- producer: lanes find 32 page ids, lane 0 issues the copies
-        const uint64_t policy = policy_evict_first();
-        int rounds = 0;  // pages of the longest worker
-        for (int e = 0; e < S; ++e) {
-            const int v = split.worker(blockIdx.x, gridDim.x, e, S);
-            rounds = max(rounds, split.lo(v + 1) - split.lo(v));
-        }
-        const int n_it = total > 0 ? rounds * S : 0;
-        // the page of ring position `it`: worker it % S's page it / S; -2: it has no such page
-        auto find = [&](int it) -> int {
-            if (it >= n_it) return -2;
-            const int v = split.worker(blockIdx.x, gridDim.x, it % S, S);
-            const int x = split.lo(v) + it / S;
-            if (x >= split.lo(v + 1)) return -2;
-            const int b = request_of(prefix, a.batch, x);
-            const int page = a.page_table[(size_t)b * a.max_pages + (x - prefix[b])];
-            return page < 0 || page >= a.num_pages ? -1 : page;
-        };
-        bool waited = !producer_first;
-        int next = find(lane);
-        int st = 0;               // stage of ring position `it`, and how often the ring has been full
-        uint32_t turn = 0;
-        for (int base = 0; base < n_it; base += 32) {
-            const int mine = next;
-            next = find(base + 32 + lane);
-            const int cnt = min(32, n_it - base);
-            for (int u = 0; u < cnt; ++u) {
-                const int page = __shfl_sync(0xffffffffu, mine, u);
-                const int s = st;
-                const uint32_t now = turn;
-                if (++st == n_stages) st = 0, ++turn;
-                if (page == -2) continue;
-                if (!waited && now > 0) {
-                    grid_wait();
-                    waited = true;
-                }
-                if (lane == 0) {
-                    if (now > 0) mbar_wait(bar_empty + 8 * s, (now & 1) ^ 1, &g_status);
-                    uint8_t *dst = smem + s * L.stage_bytes;
-                    page_ok[s] = page;
-                    if (page < 0) {
-                        atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
-                        mbar_arrive(bar_full + 8 * s);
-                    } else {
-                        const size_t off = (size_t)page * L.page_bytes;
-                        mbar_arrive_expect_tx(bar_full + 8 * s, L.stage_bytes);
-                        bulk_g2s_hint(smem_u32(dst), a.k_pages + off, L.page_bytes, bar_full + 8 * s, policy);
-                        bulk_g2s_hint(smem_u32(dst + L.page_bytes), a.v_pages + off, L.page_bytes, bar_full + 8 * s, policy);
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        if (!waited) grid_wait();
-        return;
-    }
-
-    // ---------------- a worker's warp of KV head g
-    const int g = warp % a.hkv, e = warp / a.hkv;
-    const int v = split.worker(blockIdx.x, gridDim.x, e, S);
-    if (total == 0 || v >= split.nv) return;
-    const int lo = split.lo(v), hi = split.lo(v + 1);
+    if (lo >= hi) return;
     const int r = lane >> 2, c = lane & 3;
 
     auto load_q = [&](int b, uint2 (&w)[GROUP]) {
@@ -405,7 +372,7 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
     uint2 q_next[GROUP];
     load_q(b, q_next);
     int split_b[2] = {-1, -1};  // requests whose partials this worker wrote: its first and last at most
-    int st = e;                 // stage of the worker's next page, and its barrier's phase
+    int st = 0;                 // stage of the next page, and its barrier's phase
     uint32_t phase = 0;
 
     for (int x = lo; x < hi;) {
@@ -443,7 +410,7 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
         // B of the scores: lane (n, c), n = (group n / 2, head n % 2), holds head n % 2's dims [32 g + 8 c, + 8) of its
         // own group, as the pairs (j, j + 4) that the code words hold, a 16th of the pairs whose codes come 16-fold
         uint32_t bq[16];
-        float qsum[GROUP], qback[GROUP];  // sum of the head's q over group c; 2^12 / q's scale
+        float qsum[GROUP], qback[GROUP];  // softmax scale times: sum of the head's q over group c; 2^12 / q's scale
         {
             float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const int src = 8 * (r >> 1) + 2 * c;
@@ -456,9 +423,9 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
                 for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                qsum[i] = __shfl_sync(0xffffffffu, s, 8 * c);
+                qsum[i] = __shfl_sync(0xffffffffu, s, 8 * c) * a.scale_log2;
                 const int k = min(14 - exponent_of(m), 126);  // 126: q is zero or nearly
-                qback[i] = pow2i(12 - k);
+                qback[i] = pow2i(12 - k) * a.scale_log2;
                 const float up = pow2i(k);
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
@@ -479,21 +446,27 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) ref[i] = -INFINITY, l[i] = 0.f, corr[i] = 0.f;
 
-        for (int j = j0; j < j1; ++j) {
-            const int s = st;
-            mbar_wait(bar_full + 8 * s, phase, &g_status);
-            st += S;
-            if (st >= n_stages) st -= n_stages, phase ^= 1;
-            const uint32_t ks = smem_base + s * L.stage_bytes + g * kKvqHeadBytes;
-            const uint32_t vs = ks + L.page_bytes;
-            const int nt = min(kPS, seq_len - j * kPS);
-            const int page = page_ok[s];
-            const bool patch = has_new && j == j1 - 1 && page >= 0;
-            if (patch) {
+        // NP neighbouring pages at once: their chains of products, shuffles and exponentials are independent
+        auto pages = [&](auto np, int j) {
+            constexpr int NP = decltype(np)::value;
+            int stage[NP], page[NP], nt[NP];
+            uint32_t ks[NP], vp0[NP], vp1[NP];
+            bool patch = false;
+#pragma unroll
+            for (int y = 0; y < NP; ++y) {
+                stage[y] = st;
+                mbar_wait(bars + 8 * st, phase, &g_status);
+                if (++st == n_stages) st = 0, phase ^= 1;
+                ks[y] = ring_base + stage[y] * kStageBytes;
+                page[y] = __shfl_sync(0xffffffffu, slot_page, stage[y]);
+                nt[y] = page[y] >= 0 ? min(kPS, seq_len - (j + y) * kPS) : 0;  // nothing of a bad page
+            }
+            if (has_new && j + NP == j1 && page[NP - 1] >= 0) {
                 // the new token's row, in the stage and in the pools
-                const int t = nt - 1;
-                uint8_t *kd = smem + (ks - smem_base), *vd = smem + (vs - smem_base);
-                const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
+                patch = true;
+                const int t = nt[NP - 1] - 1;
+                uint8_t *kd = ring + stage[NP - 1] * kStageBytes, *vd = kd + kKvqHeadBytes;
+                const size_t off = ((size_t)page[NP - 1] * a.hkv + g) * kKvqHeadBytes;
                 *reinterpret_cast<uint16_t *>(kd + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
                 *reinterpret_cast<uint16_t *>(vd + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
                 *reinterpret_cast<uint16_t *>(a.k_pages + off + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
@@ -507,92 +480,111 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
                 }
                 __syncwarp();
             }
-            if (page >= 0) {
-                // scores: A rows are tokens r and r + 8
-                const uint4 k0 = lds128(ks + r * 64 + c * 16), k1 = lds128(ks + 512 + r * 64 + c * 16);
-                const uint32_t kp0 = lds32(ks + kKvqCodeBytes + lane * 4), kp1 = lds32(ks + kKvqCodeBytes + 128 + lane * 4);
-                uint32_t vp0 = lds32(vs + kKvqCodeBytes + lane * 4), vp1 = lds32(vs + kKvqCodeBytes + 128 + lane * 4);
-                float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+            // scores: A rows are tokens r and r + 8
+            float d[NP][4], sc[NP][GROUP][2];
+            uint32_t kp0[NP], kp1[NP];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    mma16816(d0, code_pair<0>(w0[u]), code_pair<0>(w1[u]), code_pair<1>(w0[u]), code_pair<1>(w1[u]), bq[4 * u],
+            for (int y = 0; y < NP; ++y) {
+                kp0[y] = lds32(ks[y] + kKvqCodeBytes + lane * 4);
+                kp1[y] = lds32(ks[y] + kKvqCodeBytes + 128 + lane * 4);
+                const uint4 k0 = lds128(ks[y] + r * 64 + c * 16), k1 = lds128(ks[y] + 512 + r * 64 + c * 16);
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+                d[y][0] = d[y][1] = d[y][2] = d[y][3] = 0.f;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    mma16816(d[y], code_pair<0>(w0[u]), code_pair<0>(w1[u]), code_pair<1>(w0[u]), code_pair<1>(w1[u]), bq[4 * u],
                              bq[4 * u + 1]);
-                    mma16816(d1, code_pair<0>(w0[u + 2]), code_pair<0>(w1[u + 2]), code_pair<1>(w0[u + 2]),
-                             code_pair<1>(w1[u + 2]), bq[4 * u + 8], bq[4 * u + 9]);
-                    mma16816(d0, code_pair<2>(w0[u]), code_pair<2>(w1[u]), code_pair<3>(w0[u]), code_pair<3>(w1[u]),
+                    mma16816(d[y], code_pair<2>(w0[u]), code_pair<2>(w1[u]), code_pair<3>(w0[u]), code_pair<3>(w1[u]),
                              bq[4 * u + 2], bq[4 * u + 3]);
-                    mma16816(d1, code_pair<2>(w0[u + 2]), code_pair<2>(w1[u + 2]), code_pair<3>(w0[u + 2]),
-                             code_pair<3>(w1[u + 2]), bq[4 * u + 10], bq[4 * u + 11]);
                 }
-                // s and m of (token, group c), then the sum over groups (the 4 lanes of a token)
-                float sc[GROUP][2];
-                const float s0 = bf16lo(kp0) * 4096.f, m0 = bf16hi(kp0), s1 = bf16lo(kp1) * 4096.f, m1 = bf16hi(kp1);
+            }
+            // s and m of (token, group c), then the sum over groups (the 4 lanes of a token)
+            bool past = false;
+            float t_max = 0.f;
+#pragma unroll
+            for (int y = 0; y < NP; ++y) {
+                const float s0 = bf16lo(kp0[y]) * 4096.f, m0 = bf16hi(kp0[y]), s1 = bf16lo(kp1[y]) * 4096.f, m1 = bf16hi(kp1[y]);
+                vp0[y] = lds32(ks[y] + kKvqHeadBytes + kKvqCodeBytes + lane * 4);
+                vp1[y] = lds32(ks[y] + kKvqHeadBytes + kKvqCodeBytes + 128 + lane * 4);
 #pragma unroll
                 for (int i = 0; i < GROUP; ++i) {
-                    sc[i][0] = fmaf(s0, (d0[i] + d1[i]) * qback[i], m0 * qsum[i]);
-                    sc[i][1] = fmaf(s1, (d0[2 + i] + d1[2 + i]) * qback[i], m1 * qsum[i]);
+                    sc[y][i][0] = fmaf(s0, d[y][i] * qback[i], m0 * qsum[i]);
+                    sc[y][i][1] = fmaf(s1, d[y][2 + i] * qback[i], m1 * qsum[i]);
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < GROUP; ++i)
+            for (int x = 1; x < 4; x <<= 1)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        sc[i][y] += __shfl_xor_sync(0xffffffffu, sc[i][y], 1);
-                        sc[i][y] += __shfl_xor_sync(0xffffffffu, sc[i][y], 2);
-                        sc[i][y] *= a.scale_log2;
-                    }
-                if (nt < kPS) {  // slots past the length may hold anything
+                for (int y = 0; y < NP; ++y)
 #pragma unroll
                     for (int i = 0; i < GROUP; ++i) {
-                        if (r >= nt) sc[i][0] = -INFINITY;
-                        if (r + 8 >= nt) sc[i][1] = -INFINITY;
+                        sc[y][i][0] += __shfl_xor_sync(0xffffffffu, sc[y][i][0], x);
+                        sc[y][i][1] += __shfl_xor_sync(0xffffffffu, sc[y][i][1], x);
                     }
-                    if (r >= nt) vp0 = 0u;
-                    if (r + 8 >= nt) vp1 = 0u;
-                }
-                const float t0 = bf16lo(vp0), t1 = bf16lo(vp1);
-                bool past = fmaxf(fabsf(t0), fabsf(t1)) * s_up > kScaleMost;
+            // slots past the length may hold anything
 #pragma unroll
-                for (int i = 0; i < GROUP; ++i) past |= fmaxf(sc[i][0], sc[i][1]) > ref[i] + kRefSlack;
-                if (__any_sync(0xffffffffu, past)) {  // move the references to the maxima so far
-                    float t = fmaxf(fabsf(t0), fabsf(t1));
-#pragma unroll
-                    for (int y = 1; y < 32; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, y));
-                    float alpha[2] = {1.f, 1.f};
-                    if (t * s_up > kScaleMost) {
-                        const float up = pow2i(min(5 - exponent_of(t), 126));
-                        alpha[0] = alpha[1] = up / s_up;
-                        s_up = up;
-                    }
+            for (int y = 0; y < NP; ++y) {
+                if (nt[y] < kPS) {
 #pragma unroll
                     for (int i = 0; i < GROUP; ++i) {
-                        float m = fmaxf(sc[i][0], sc[i][1]);
-#pragma unroll
-                        for (int y = 4; y < 32; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-                        if (m > ref[i]) {
-                            const float f = exp2_approx(ref[i] - m);
-                            ref[i] = m;
-                            alpha[i] *= f;
-                            l[i] *= f;
-                            corr[i] *= f;
-                        }
+                        if (r >= nt[y]) sc[y][i][0] = -INFINITY;
+                        if (r + 8 >= nt[y]) sc[y][i][1] = -INFINITY;
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i][0] *= alpha[0], o[i][1] *= alpha[1], o[i][2] *= alpha[0], o[i][3] *= alpha[1];
+                    if (r >= nt[y]) vp0[y] = 0u;
+                    if (r + 8 >= nt[y]) vp1[y] = 0u;
                 }
+                t_max = fmaxf(t_max, fmaxf(fabsf(bf16lo(vp0[y])), fabsf(bf16lo(vp1[y]))));
+            }
+            past = t_max * s_up > kScaleMost;
+            float x_max[GROUP];
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) {
+                x_max[i] = fmaxf(sc[0][i][0], sc[0][i][1]);
+#pragma unroll
+                for (int y = 1; y < NP; ++y) x_max[i] = fmaxf(x_max[i], fmaxf(sc[y][i][0], sc[y][i][1]));
+                past |= x_max[i] > ref[i] + kRefSlack;
+            }
+            if (__any_sync(0xffffffffu, past)) {  // move the references to the maxima so far
+#pragma unroll
+                for (int y = 1; y < 32; y <<= 1) t_max = fmaxf(t_max, __shfl_xor_sync(0xffffffffu, t_max, y));
+                float alpha[2] = {1.f, 1.f};
+                if (t_max * s_up > kScaleMost) {
+                    const float up = pow2i(min(5 - exponent_of(t_max), 126));
+                    alpha[0] = alpha[1] = up / s_up;
+                    s_up = up;
+                }
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i) {
+                    float m = x_max[i];
+#pragma unroll
+                    for (int y = 4; y < 32; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+                    if (m > ref[i]) {
+                        const float f = exp2_approx(ref[i] - m);
+                        ref[i] = m;
+                        alpha[i] *= f;
+                        l[i] *= f;
+                        corr[i] *= f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i][0] *= alpha[0], o[i][1] *= alpha[1], o[i][2] *= alpha[0], o[i][3] *= alpha[1];
+            }
+#pragma unroll
+            for (int y = 0; y < NP; ++y) {
+                if ((nt[0] | nt[NP - 1]) == 0) continue;  // bad pages alone: there may be no reference yet
                 // p s of (token, group c) for both heads, rounded to fp16, transposed into B
-                const float u0 = t0 * s_up, u1 = t1 * s_up, c0 = bf16hi(vp0), c1 = bf16hi(vp1);
+                const float u0 = bf16lo(vp0[y]) * s_up, u1 = bf16lo(vp1[y]) * s_up, c0 = bf16hi(vp0[y]), c1 = bf16hi(vp1[y]);
                 float ps[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
                 for (int i = 0; i < GROUP; ++i) {
-                    const float pa = exp2_approx(sc[i][0] - ref[i]), pb = exp2_approx(sc[i][1] - ref[i]);
+                    const float pa = exp2_approx(sc[y][i][0] - ref[i]), pb = exp2_approx(sc[y][i][1] - ref[i]);
                     l[i] += pa + pb;
                     ps[0][i] = pa * u0;
                     ps[1][i] = pb * u1;
                     corr[i] = fmaf(pa, c0, fmaf(pb, c1, corr[i]));
                 }
                 const uint32_t b0 = transpose8x8(pack_f16x2(ps[0][0], ps[0][1])), b1 = transpose8x8(pack_f16x2(ps[1][0], ps[1][1]));
-                const uint4 v0 = lds128(vs + lane * 16), v1 = lds128(vs + 512 + lane * 16);
+                const uint4 v0 = lds128(ks[y] + kKvqHeadBytes + lane * 16), v1 = lds128(ks[y] + kKvqHeadBytes + 512 + lane * 16);
                 const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -604,8 +596,13 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
             // the patch's generic stores come before the next bulk copy into the stage
             if (patch) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
-        }
+#pragma unroll
+            for (int y = 0; y < NP; ++y)
+                if (issued < hi) issue(stage[y]);
+        };
+        int j = j0;
+        for (; j + 2 <= j1; j += 2) pages(std::integral_constant<int, 2>(), j);
+        if (j < j1) pages(std::integral_constant<int, 1>(), j);
 
         // sums over the tokens (lanes of equal c); the lane keeps dims [32 c + 4 r, + 4) of both heads
         float acc[GROUP][4];
@@ -712,7 +709,7 @@ __global__ void __launch_bounds__((kMaxWorkers + 1) * 32, 1) kvq_decode_kernel(c
 }  // namespace
 
 size_t kvq_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int ctas) {
-    return workspace_layout(batch, n_q_heads, ctas * workers_of(n_kv_heads)).total;
+    return workspace_layout(batch, n_q_heads, ctas * kCtasPerSm * workers_of(n_kv_heads)).total;
 }
 
 cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void *v_pages, const int32_t *page_table,
@@ -734,7 +731,7 @@ cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void 
     a.scale_log2 = scale * kLog2e;
     a.early = (p.abi_version >= 2 && p.stable_metadata >= 1) ? 1 : 0;
     a.early_pools = (p.abi_version >= 2 && p.stable_metadata >= 2) ? 1 : 0;
-    const WorkspaceLayout w = workspace_layout(batch, p.n_q_heads, ctas * workers_of(p.n_kv_heads));
+    const WorkspaceLayout w = workspace_layout(batch, p.n_q_heads, ctas * kCtasPerSm * workers_of(p.n_kv_heads));
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     a.part_acc = reinterpret_cast<float *>(ws + w.acc);
     a.part_ml = reinterpret_cast<float *>(ws + w.ml);
@@ -756,9 +753,9 @@ cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3((unsigned)((workers_of(p.n_kv_heads) * p.n_kv_heads + 1) * 32));
-    cfg.dynamicSmemBytes = smem_layout(p.n_kv_heads, batch).total;
+    cfg.gridDim = dim3((unsigned)(ctas * kCtasPerSm));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem_layout(batch).total;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
