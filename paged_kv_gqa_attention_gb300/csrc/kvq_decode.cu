@@ -9,9 +9,12 @@
 // cut into equal contiguous ranges, one a worker.  A worker is one warp for
 // each KV head, and a CTA of 8 warps holds 8 / Hkv workers, two CTAs an SM.
 // Every warp streams the part of its own head (1280 contiguous bytes of a K
-// page and of a V page) through its own ring of shared memory with the
-// bulk-copy engine, so the warps of a CTA never meet after the prologue:
-// there is no producer warp to feed and no barrier to release a stage.
+// page and of a V page) through its own ring of shared memory with 16-byte
+// asynchronous copies, five a lane and page, so the warps of a CTA never
+// meet after the prologue: there is no producer warp to feed, no barrier to
+// poll and none to release a stage (a producer warp with bulk copies into a
+// ring shared by the heads, and bulk copies issued by each warp, took more
+// instructions a page).
 //
 // A request that lies in one worker's range is finished there.  Otherwise
 // each worker writes an fp32 partial (maximum, sum, outputs) to slot v + b
@@ -124,7 +127,10 @@ constexpr int kMaxHkv = 8;
 constexpr int kWarps = 8;             // of a CTA
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxStages = 5;         // pages in a warp's ring
+// A stage: K codes, V codes, K parameters, V parameters, so that lane l copies
+// 16 bytes at 16 l of each 512.
 constexpr int kStageBytes = 2 * kKvqHeadBytes;
+constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;
 constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
 constexpr float kScaleMost = 1024.f;  // s times its factor: set to [32, 64), moved past this
 
@@ -132,7 +138,7 @@ constexpr float kScaleMost = 1024.f;  // s times its factor: set to [32, 64), mo
 __host__ __device__ constexpr int workers_of(int hkv) { return kWarps / hkv; }
 
 struct SmemLayout {
-    uint32_t stages, off_bar, off_scan, off_prefix, total;
+    uint32_t stages, off_scan, off_prefix, total;
 };
 
 // Two CTAs share an SM's 227 KB; the prefix sums of a large batch cost one
@@ -141,8 +147,6 @@ __host__ __device__ inline SmemLayout smem_layout(int batch) {
     SmemLayout s;
     s.stages = batch <= 2048 ? kMaxStages : kMaxStages - 1;
     uint32_t o = s.stages * kStageBytes * kWarps;
-    s.off_bar = o;  // a barrier for each stage of each warp
-    o += s.stages * 8 * kWarps;
     s.off_scan = o;  // warp sums of the prefix scan
     o += kWarps * 4;
     s.off_prefix = o;
@@ -256,6 +260,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 __device__ __forceinline__ int exponent_of(float x) { return (__float_as_int(x) >> 23 & 255) - 127; }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -278,14 +289,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     int *prefix = reinterpret_cast<int *>(smem + L.off_prefix);
     int *scan = reinterpret_cast<int *>(smem + L.off_scan);
     uint8_t *ring = smem + warp * n_stages * kStageBytes;
-    const uint32_t ring_base = smem_u32(ring);
-    const uint32_t bars = smem_u32(smem + L.off_bar) + warp * n_stages * 8;
+    const uint32_t ring_base = smem_u32(ring), ring_end = ring_base + n_stages * kStageBytes;
 
     if (!a.early) grid_wait();
-    if (lane == 0) {
-        for (int s = 0; s < n_stages; ++s) mbar_init(bars + 8 * s, 1);
-        fence_mbar_init();
-    }
     if (threadIdx.x == 0) prefix[0] = 0;
     // prefix sums of the page counts, one request a thread
     for (int base = 0, carry = 0; base < a.batch; base += kWarps * 32) {
@@ -324,32 +330,42 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         return page < 0 || page >= a.num_pages ? -1 : page;
     };
     int ids = find(lo + lane), ids_next = -1;
-    int slot_page = -1;        // lane s: the page in stage s
-    int issued = lo;           // next page to copy
+    int issued = 0;                  // pages copied so far
+    uint32_t fill = ring_base;       // the stage that the next one goes to
+    uint32_t bad = 0;                // bit i: the page copied i pages before the last one is bad
     const uint64_t policy = policy_evict_first();
-    auto issue = [&](int s) {  // copies page `issued` into stage s
-        const int page = __shfl_sync(0xffffffffu, ids, (issued - lo) & 31);
-        if (lane == s) slot_page = page;
-        if (lane == 0) {
-            if (page < 0) {
+    const size_t head_at = (size_t)g * kKvqHeadBytes + 16 * lane;
+    const uint8_t *k_src = a.k_pages + head_at, *v_src = a.v_pages + head_at;
+    const uint8_t *p_src = (lane < 16 ? a.k_pages : a.v_pages - 256) + kKvqCodeBytes + head_at;
+    const uint32_t page_stride = (uint32_t)a.hkv * kKvqHeadBytes;
+    auto issue = [&]() {  // the next page, or nothing after the last: a group either way
+        if (issued < hi - lo) {
+            const int page = __shfl_sync(0xffffffffu, ids, issued & 31);
+            bad = bad << 1 | (page < 0);
+            if (page >= 0) {
+                const size_t off = (size_t)(uint32_t)page * page_stride;
+                const uint32_t dst = fill + 16 * lane;
+                copy16(dst, k_src + off, policy);
+                copy16(dst + 512, k_src + off + 512, policy);
+                copy16(dst + kAtV, v_src + off, policy);
+                copy16(dst + kAtV + 512, v_src + off + 512, policy);
+                copy16(dst + kAtKp, p_src + off, policy);
+            } else if (lane == 0) {
                 atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
-                mbar_arrive(bars + 8 * s);
-            } else {
-                const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-                const uint32_t dst = ring_base + s * kStageBytes;
-                mbar_arrive_expect_tx(bars + 8 * s, kStageBytes);
-                bulk_g2s_hint(dst, a.k_pages + off, kKvqHeadBytes, bars + 8 * s, policy);
-                bulk_g2s_hint(dst + kKvqHeadBytes, a.v_pages + off, kKvqHeadBytes, bars + 8 * s, policy);
             }
+            ++issued;
+            if ((issued & 31) == 16) ids_next = find(lo + issued + 16 + lane);
+            if ((issued & 31) == 0) ids = ids_next;
+            fill = fill + kStageBytes == ring_end ? ring_base : fill + kStageBytes;
         }
-        ++issued;
-        if (((issued - lo) & 31) == 16) ids_next = find(issued + 16 + lane);
-        if (((issued - lo) & 31) == 0) ids = ids_next;
+        copy_commit();
     };
 
     // With the pools vouched for (early_pools) the rings fill before the wait.
     if (a.early && !a.early_pools) grid_wait();
-    for (int s = 0; s < n_stages && issued < hi; ++s) issue(s);
+#pragma unroll 1
+    for (int s = 0; s < kMaxStages; ++s)
+        if (s < n_stages) issue();
     if (a.early && a.early_pools) grid_wait();
 
     if (blockIdx.x == 0) {  // zero rows of requests with nothing to attend over
@@ -372,8 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     uint2 q_next[GROUP];
     load_q(b, q_next);
     int split_b[2] = {-1, -1};  // requests whose partials this worker wrote: its first and last at most
-    int st = 0;                 // stage of the next page, and its barrier's phase
-    uint32_t phase = 0;
+    uint32_t at = ring_base;    // stage of the next page
 
     for (int x = lo; x < hi;) {
         const int p0 = prefix[b], p1 = prefix[b + 1];
@@ -410,23 +425,29 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         // B of the scores: lane (n, c), n = (group n / 2, head n % 2), holds head n % 2's dims [32 g + 8 c, + 8) of its
         // own group, as the pairs (j, j + 4) that the code words hold, a 16th of the pairs whose codes come 16-fold
         uint32_t bq[16];
-        float qsum[GROUP], qback[GROUP];  // softmax scale times: sum of the head's q over group c; 2^12 / q's scale
+        float2 qsum = make_float2(0.f, 0.f);  // softmax scale times the sum of the heads' q over group c
+        float qback;                          // softmax scale times 2^24 / q's scale
         {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i)
+                m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16lo(qw[i].x)), fabsf(bf16hi(qw[i].x))),
+                                   fmaxf(fabsf(bf16lo(qw[i].y)), fabsf(bf16hi(qw[i].y)))));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int k = max(min(14 - exponent_of(m), 126), -100);  // 126: q is zero or nearly; -100: it is past 2^114
+            const float up = pow2i(k);
+            qback = pow2i(24 - k) * a.scale_log2;
             float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const int src = 8 * (r >> 1) + 2 * c;
 #pragma unroll
             for (int i = 0; i < GROUP; ++i) {
                 const float x[4] = {bf16lo(qw[i].x), bf16hi(qw[i].x), bf16lo(qw[i].y), bf16hi(qw[i].y)};
                 float s = (x[0] + x[1]) + (x[2] + x[3]);
-                float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                qsum[i] = __shfl_sync(0xffffffffu, s, 8 * c) * a.scale_log2;
-                const int k = min(14 - exponent_of(m), 126);  // 126: q is zero or nearly
-                qback[i] = pow2i(12 - k) * a.scale_log2;
-                const float up = pow2i(k);
+                s = __shfl_sync(0xffffffffu, s, 8 * c) * a.scale_log2;
+                if (i == 0) qsum.x = s; else qsum.y = s;
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     const float y0 = __shfl_sync(0xffffffffu, x[d] * up, src), y1 = __shfl_sync(0xffffffffu, x[d] * up, src + 1);
@@ -436,58 +457,56 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             const uint32_t pr[4] = {pack_f16x2(w[0], w[4]), pack_f16x2(w[1] * 0.0625f, w[5] * 0.0625f), pack_f16x2(w[2], w[6]),
                                     pack_f16x2(w[3] * 0.0625f, w[7] * 0.0625f)};
 #pragma unroll
-            for (int k = 0; k < 16; ++k) bq[k] = (k >> 2) == (r >> 1) ? pr[k & 3] : 0u;
+            for (int k2 = 0; k2 < 16; ++k2) bq[k2] = (k2 >> 2) == (r >> 1) ? pr[k2 & 3] : 0u;
         }
+        // outputs, and of both heads (x, y): the reference (log2), sum of p and sum of p m over this lane's tokens
         float o[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float ref[GROUP], l[GROUP], corr[GROUP];  // reference, sum of p, sum of p m (log2 units, this lane's tokens)
-        float s_up = pow2i(126);                  // factor of s: moved by the first page
-#pragma unroll
-        for (int i = 0; i < GROUP; ++i) ref[i] = -INFINITY, l[i] = 0.f, corr[i] = 0.f;
+        float2 ref = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f), corr = make_float2(0.f, 0.f);
+        float s_up = 0.f, s_most = -1.f;  // factor of s, and the largest s it serves: the first page sets them
 
         // NP neighbouring pages at once: their chains of products, shuffles and exponentials are independent
         auto pages = [&](auto np, int j) {
             constexpr int NP = decltype(np)::value;
-            int stage[NP], page[NP], nt[NP];
+            if (n_stages == kMaxStages) copy_wait<kMaxStages - NP>(); else copy_wait<kMaxStages - 1 - NP>();
+            __syncwarp();
             uint32_t ks[NP], vp0[NP], vp1[NP];
-            bool patch = false;
+            int nt[NP];
 #pragma unroll
             for (int y = 0; y < NP; ++y) {
-                stage[y] = st;
-                mbar_wait(bars + 8 * st, phase, &g_status);
-                if (++st == n_stages) st = 0, phase ^= 1;
-                ks[y] = ring_base + stage[y] * kStageBytes;
-                page[y] = __shfl_sync(0xffffffffu, slot_page, stage[y]);
-                nt[y] = page[y] >= 0 ? min(kPS, seq_len - (j + y) * kPS) : 0;  // nothing of a bad page
+                ks[y] = at;
+                at = at + kStageBytes == ring_end ? ring_base : at + kStageBytes;
+                nt[y] = min(kPS, seq_len - (j + y) * kPS);
+                if (bad && (bad >> (issued - 1 - (x - lo + j + y - j0)) & 1)) nt[y] = 0;  // nothing of a bad page
             }
-            if (has_new && j + NP == j1 && page[NP - 1] >= 0) {
+            if (has_new && j + NP == j1 && nt[NP - 1] > 0) {
                 // the new token's row, in the stage and in the pools
-                patch = true;
-                const int t = nt[NP - 1] - 1;
-                uint8_t *kd = ring + stage[NP - 1] * kStageBytes, *vd = kd + kKvqHeadBytes;
-                const size_t off = ((size_t)page[NP - 1] * a.hkv + g) * kKvqHeadBytes;
-                *reinterpret_cast<uint16_t *>(kd + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
-                *reinterpret_cast<uint16_t *>(vd + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
+                const int t = nt[NP - 1] - 1, page = a.page_table[(size_t)b * a.max_pages + j1 - 1];
+                uint8_t *stage = ring + (ks[NP - 1] - ring_base);
+                const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
+                *reinterpret_cast<uint16_t *>(stage + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
+                *reinterpret_cast<uint16_t *>(stage + kAtV + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
                 *reinterpret_cast<uint16_t *>(a.k_pages + off + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
                 *reinterpret_cast<uint16_t *>(a.v_pages + off + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
                 if ((lane & 7) == 0) {
-                    const int at = kvq_param_offset(t, lane >> 3);
-                    *reinterpret_cast<uint32_t *>(kd + at) = new_ksm;
-                    *reinterpret_cast<uint32_t *>(vd + at) = new_vsm;
-                    *reinterpret_cast<uint32_t *>(a.k_pages + off + at) = new_ksm;
-                    *reinterpret_cast<uint32_t *>(a.v_pages + off + at) = new_vsm;
+                    const int p = kvq_param_offset(t, lane >> 3);
+                    *reinterpret_cast<uint32_t *>(stage + kAtKp - kKvqCodeBytes + p) = new_ksm;
+                    *reinterpret_cast<uint32_t *>(stage + kAtVp - kKvqCodeBytes + p) = new_vsm;
+                    *reinterpret_cast<uint32_t *>(a.k_pages + off + p) = new_ksm;
+                    *reinterpret_cast<uint32_t *>(a.v_pages + off + p) = new_vsm;
                 }
                 __syncwarp();
             }
             // scores: A rows are tokens r and r + 8
-            float d[NP][4], sc[NP][GROUP][2];
+            float d[NP][4];
+            float2 sc[NP][2];
             uint32_t kp0[NP], kp1[NP];
 #pragma unroll
             for (int y = 0; y < NP; ++y) {
-                kp0[y] = lds32(ks[y] + kKvqCodeBytes + lane * 4);
-                kp1[y] = lds32(ks[y] + kKvqCodeBytes + 128 + lane * 4);
-                const uint4 k0 = lds128(ks[y] + r * 64 + c * 16), k1 = lds128(ks[y] + 512 + r * 64 + c * 16);
+                const uint4 k0 = lds128(ks[y] + 16 * lane), k1 = lds128(ks[y] + 512 + 16 * lane);
+                kp0[y] = lds32(ks[y] + kAtKp + 4 * lane), kp1[y] = lds32(ks[y] + kAtKp + 128 + 4 * lane);
+                vp0[y] = lds32(ks[y] + kAtVp + 4 * lane), vp1[y] = lds32(ks[y] + kAtVp + 128 + 4 * lane);
                 const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
                 d[y][0] = d[y][1] = d[y][2] = d[y][3] = 0.f;
 #pragma unroll
@@ -499,92 +518,84 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                 }
             }
             // s and m of (token, group c), then the sum over groups (the 4 lanes of a token)
-            bool past = false;
-            float t_max = 0.f;
 #pragma unroll
             for (int y = 0; y < NP; ++y) {
-                const float s0 = bf16lo(kp0[y]) * 4096.f, m0 = bf16hi(kp0[y]), s1 = bf16lo(kp1[y]) * 4096.f, m1 = bf16hi(kp1[y]);
-                vp0[y] = lds32(ks[y] + kKvqHeadBytes + kKvqCodeBytes + lane * 4);
-                vp1[y] = lds32(ks[y] + kKvqHeadBytes + kKvqCodeBytes + 128 + lane * 4);
-#pragma unroll
-                for (int i = 0; i < GROUP; ++i) {
-                    sc[y][i][0] = fmaf(s0, d[y][i] * qback[i], m0 * qsum[i]);
-                    sc[y][i][1] = fmaf(s1, d[y][2 + i] * qback[i], m1 * qsum[i]);
-                }
+                const float s0 = bf16lo(kp0[y]) * qback, m0 = bf16hi(kp0[y]), s1 = bf16lo(kp1[y]) * qback, m1 = bf16hi(kp1[y]);
+                sc[y][0] = ffma2(make_float2(d[y][0], d[y][1]), make_float2(s0, s0), fmul2(make_float2(m0, m0), qsum));
+                sc[y][1] = ffma2(make_float2(d[y][2], d[y][3]), make_float2(s1, s1), fmul2(make_float2(m1, m1), qsum));
             }
 #pragma unroll
-            for (int x = 1; x < 4; x <<= 1)
+            for (int z = 1; z < 4; z <<= 1)
 #pragma unroll
                 for (int y = 0; y < NP; ++y)
 #pragma unroll
-                    for (int i = 0; i < GROUP; ++i) {
-                        sc[y][i][0] += __shfl_xor_sync(0xffffffffu, sc[y][i][0], x);
-                        sc[y][i][1] += __shfl_xor_sync(0xffffffffu, sc[y][i][1], x);
+                    for (int h = 0; h < 2; ++h) {
+                        float2 w = make_float2(__shfl_xor_sync(0xffffffffu, sc[y][h].x, z), 0.f);
+                        if (GROUP == 2) w.y = __shfl_xor_sync(0xffffffffu, sc[y][h].y, z);
+                        sc[y][h] = fadd2(sc[y][h], w);
                     }
-            // slots past the length may hold anything
+            float t_max = 0.f;
 #pragma unroll
             for (int y = 0; y < NP; ++y) {
-                if (nt[y] < kPS) {
-#pragma unroll
-                    for (int i = 0; i < GROUP; ++i) {
-                        if (r >= nt[y]) sc[y][i][0] = -INFINITY;
-                        if (r + 8 >= nt[y]) sc[y][i][1] = -INFINITY;
-                    }
-                    if (r >= nt[y]) vp0[y] = 0u;
-                    if (r + 8 >= nt[y]) vp1[y] = 0u;
+                if (nt[y] < kPS) {  // slots past the length may hold anything
+                    if (r >= nt[y]) sc[y][0] = make_float2(-INFINITY, -INFINITY), vp0[y] = 0u;
+                    if (r + 8 >= nt[y]) sc[y][1] = make_float2(-INFINITY, -INFINITY), vp1[y] = 0u;
                 }
-                t_max = fmaxf(t_max, fmaxf(fabsf(bf16lo(vp0[y])), fabsf(bf16lo(vp1[y]))));
+                t_max = fmax3(t_max, fabsf(bf16lo(vp0[y])), fabsf(bf16lo(vp1[y])));
             }
-            past = t_max * s_up > kScaleMost;
-            float x_max[GROUP];
+            float2 e[NP][2];  // log2 p
+            float e_max = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < GROUP; ++i) {
-                x_max[i] = fmaxf(sc[0][i][0], sc[0][i][1]);
+            for (int y = 0; y < NP; ++y)
 #pragma unroll
-                for (int y = 1; y < NP; ++y) x_max[i] = fmaxf(x_max[i], fmaxf(sc[y][i][0], sc[y][i][1]));
-                past |= x_max[i] > ref[i] + kRefSlack;
-            }
-            if (__any_sync(0xffffffffu, past)) {  // move the references to the maxima so far
+                for (int h = 0; h < 2; ++h) {
+                    e[y][h] = fsub2(sc[y][h], ref);
+                    e_max = GROUP == 2 ? fmax3(e_max, e[y][h].x, e[y][h].y) : fmaxf(e_max, e[y][h].x);
+                }
+            if (__any_sync(0xffffffffu, e_max > kRefSlack || t_max > s_most)) {  // move the references to the maxima so far
 #pragma unroll
-                for (int y = 1; y < 32; y <<= 1) t_max = fmaxf(t_max, __shfl_xor_sync(0xffffffffu, t_max, y));
+                for (int z = 1; z < 32; z <<= 1) t_max = fmaxf(t_max, __shfl_xor_sync(0xffffffffu, t_max, z));
                 float alpha[2] = {1.f, 1.f};
-                if (t_max * s_up > kScaleMost) {
+                if (t_max > s_most) {
                     const float up = pow2i(min(5 - exponent_of(t_max), 126));
-                    alpha[0] = alpha[1] = up / s_up;
+                    if (s_up > 0.f) alpha[0] = alpha[1] = up / s_up;
                     s_up = up;
+                    s_most = kScaleMost / up;
                 }
 #pragma unroll
                 for (int i = 0; i < GROUP; ++i) {
-                    float m = x_max[i];
+                    float m = -INFINITY;
 #pragma unroll
-                    for (int y = 4; y < 32; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-                    if (m > ref[i]) {
-                        const float f = exp2_approx(ref[i] - m);
-                        ref[i] = m;
+                    for (int y = 0; y < NP; ++y) m = i == 0 ? fmax3(m, sc[y][0].x, sc[y][1].x) : fmax3(m, sc[y][0].y, sc[y][1].y);
+#pragma unroll
+                    for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+                    float &rf = i == 0 ? ref.x : ref.y, &li = i == 0 ? l.x : l.y, &ci = i == 0 ? corr.x : corr.y;
+                    if (m > rf) {
+                        const float f = exp2_approx(rf - m);
+                        rf = m;
                         alpha[i] *= f;
-                        l[i] *= f;
-                        corr[i] *= f;
+                        li *= f;
+                        ci *= f;
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i][0] *= alpha[0], o[i][1] *= alpha[1], o[i][2] *= alpha[0], o[i][3] *= alpha[1];
+#pragma unroll
+                for (int y = 0; y < NP; ++y) e[y][0] = fsub2(sc[y][0], ref), e[y][1] = fsub2(sc[y][1], ref);
             }
 #pragma unroll
             for (int y = 0; y < NP; ++y) {
                 if ((nt[0] | nt[NP - 1]) == 0) continue;  // bad pages alone: there may be no reference yet
                 // p s of (token, group c) for both heads, rounded to fp16, transposed into B
                 const float u0 = bf16lo(vp0[y]) * s_up, u1 = bf16lo(vp1[y]) * s_up, c0 = bf16hi(vp0[y]), c1 = bf16hi(vp1[y]);
-                float ps[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-                for (int i = 0; i < GROUP; ++i) {
-                    const float pa = exp2_approx(sc[y][i][0] - ref[i]), pb = exp2_approx(sc[y][i][1] - ref[i]);
-                    l[i] += pa + pb;
-                    ps[0][i] = pa * u0;
-                    ps[1][i] = pb * u1;
-                    corr[i] = fmaf(pa, c0, fmaf(pb, c1, corr[i]));
-                }
-                const uint32_t b0 = transpose8x8(pack_f16x2(ps[0][0], ps[0][1])), b1 = transpose8x8(pack_f16x2(ps[1][0], ps[1][1]));
-                const uint4 v0 = lds128(ks[y] + kKvqHeadBytes + lane * 16), v1 = lds128(ks[y] + kKvqHeadBytes + 512 + lane * 16);
+                float2 pa = make_float2(exp2_approx(e[y][0].x), 0.f), pb = make_float2(exp2_approx(e[y][1].x), 0.f);
+                if (GROUP == 2) pa.y = exp2_approx(e[y][0].y), pb.y = exp2_approx(e[y][1].y);
+                l = fadd2(l, fadd2(pa, pb));
+                corr = ffma2(pa, make_float2(c0, c0), ffma2(pb, make_float2(c1, c1), corr));
+                pa = fmul2(pa, make_float2(u0, u0));
+                pb = fmul2(pb, make_float2(u1, u1));
+                const uint32_t b0 = transpose8x8(pack_f16x2(pa.x, pa.y)), b1 = transpose8x8(pack_f16x2(pb.x, pb.y));
+                const uint4 v0 = lds128(ks[y] + kAtV + 16 * lane), v1 = lds128(ks[y] + kAtV + 512 + 16 * lane);
                 const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -593,38 +604,38 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                              b1);
                 }
             }
-            // the patch's generic stores come before the next bulk copy into the stage
-            if (patch) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
 #pragma unroll
-            for (int y = 0; y < NP; ++y)
-                if (issued < hi) issue(stage[y]);
+            for (int y = 0; y < NP; ++y) issue();
         };
         int j = j0;
         for (; j + 2 <= j1; j += 2) pages(std::integral_constant<int, 2>(), j);
         if (j < j1) pages(std::integral_constant<int, 1>(), j);
 
         // sums over the tokens (lanes of equal c); the lane keeps dims [32 c + 4 r, + 4) of both heads
-        float acc[GROUP][4];
-        const float s_back = 1.f / s_up;
+        float acc[GROUP][4], l_sum[GROUP], ref_of[GROUP];
+        const float s_back = s_up > 0.f ? 1.f / s_up : 0.f;
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
+            float ls = i == 0 ? l.x : l.y, cr = i == 0 ? corr.x : corr.y;
 #pragma unroll
-            for (int y = 4; y < 32; y <<= 1) {
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], y);
-                corr[i] += __shfl_xor_sync(0xffffffffu, corr[i], y);
+            for (int z = 4; z < 32; z <<= 1) {
+                ls += __shfl_xor_sync(0xffffffffu, ls, z);
+                cr += __shfl_xor_sync(0xffffffffu, cr, z);
             }
+            l_sum[i] = ls;
+            ref_of[i] = i == 0 ? ref.x : ref.y;
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 const int k = (d & 1) * 2 + i, t = d >> 1;
                 const float lo2 = c & 1 ? o[2 + t][k] : o[t][k], hi2 = c & 1 ? o[6 + t][k] : o[4 + t][k];
-                acc[i][d] = fmaf((c & 2 ? hi2 : lo2) * (d & 1 ? 1048576.f : 16777216.f), s_back, corr[i]);
+                acc[i][d] = fmaf((c & 2 ? hi2 : lo2) * (d & 1 ? 1048576.f : 16777216.f), s_back, cr);
             }
         }
         if (j0 == 0 && j1 == p1 - p0) {
 #pragma unroll
             for (int i = 0; i < GROUP; ++i) {
-                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+                const float inv = l_sum[i] == 0.f ? 0.f : 1.f / l_sum[i];
                 *reinterpret_cast<uint2 *>(a.out + ((size_t)b * hq + g * GROUP + i) * kD + 32 * c + 4 * r) =
                     make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
             }
@@ -635,7 +646,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                 const int h = g * GROUP + i;
                 *reinterpret_cast<float4 *>(a.part_acc + (slot * hq + h) * kD + 4 * lane) =
                     make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-                if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * hq + h) * 2) = make_float2(ref[i], l[i]);
+                if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * hq + h) * 2) = make_float2(ref_of[i], l_sum[i]);
             }
             split_b[x == lo ? 0 : 1] = b;
         }
