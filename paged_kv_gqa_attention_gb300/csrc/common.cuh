@@ -83,7 +83,7 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // C1 + C2 + C3 with C1 = 6.28125 (8 significant bits), so n * C1 is exact for
 // n < 2^16 and the first subtraction is exact.  The reduced angle is within a
 // few fp32 ulps of the true one, then an fp32 sincos.
-__device__ __forceinline__ void sincos_pos_freq(int pos, float f_hi, float f_lo, float *s, float *c) {
+__device__ __forceinline__ float reduced_angle(int pos, float f_hi, float f_lo) {
     constexpr double kTwoPiD = 6.283185307179586476925286766559;
     constexpr float kC1 = 6.28125f;
     constexpr float kC2 = (float)(kTwoPiD - 6.28125);
@@ -96,7 +96,20 @@ __device__ __forceinline__ void sincos_pos_freq(int pos, float f_hi, float f_lo,
     float r = fmaf(-n, kC1, a_hi);
     r = fmaf(-n, kC2, r);
     r = fmaf(-n, kC3, r);
-    sincosf(r + a_lo, s, c);
+    return r + a_lo;
+}
+
+__device__ __forceinline__ void sincos_pos_freq(int pos, float f_hi, float f_lo, float *s, float *c) {
+    sincosf(reduced_angle(pos, f_hi, f_lo), s, c);
+}
+
+// The same angle with the hardware sine and cosine (sin.approx, cos.approx:
+// within 2^-20.5 absolute, the reduced angle being within [-pi, pi]), for
+// results that are rounded to bf16, whose half step is 2^-9 or more.
+__device__ __forceinline__ void sincos_pos_freq_fast(int pos, float f_hi, float f_lo, float *s, float *c) {
+    const float r = reduced_angle(pos, f_hi, f_lo);
+    *s = __sinf(r);
+    *c = __cosf(r);
 }
 
 __device__ __forceinline__ void prefetch_l2(const void *p) {

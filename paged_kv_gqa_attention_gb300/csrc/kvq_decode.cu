@@ -21,7 +21,7 @@
 // (worker v, request b: unique, since both ranges are ordered), and after its
 // last page counts itself in the arrival counter of (request, KV head); the
 // warp that arrives last merges the partials and resets the counter, so
-// nothing waits on another CTA.
+// nothing waits on another CTA.  Many partials are merged in two levels.
 //
 // Arithmetic of one page and KV head (16 tokens, mma.m16n8k16 on fp16, fp32
 // sums).  A masked nibble of both halves of a code word is a pair of fp16
@@ -64,9 +64,9 @@ struct KvqArgs {
     const int32_t *page_table, *seq_lens;
     uint16_t *out;
     long long ldq, ldkv;
-    float *part_acc;  // [slots][Hq][D]
-    float *part_ml;   // [slots][Hq][2]
-    int *arrivals;    // [kDecodeMaxBatch][kMaxHkv], zero between calls
+    float *part_acc, *group_acc;    // [slots][Hq][D]
+    float *part_ml, *group_ml;      // [slots][Hq][2]
+    int *arrivals, *group_arrivals; // [request or slot][kMaxHkv], zero between calls
     int batch, hkv, max_pages, num_pages;
     float scale_log2;
     int early, early_pools;  // stable_metadata >= 1, >= 2
@@ -82,11 +82,10 @@ struct KvqArgs {
 
 // Norm and rotation of a head vector over a warp; lane l holds dims
 // [4l, 4l + 4), whose rotation partners are on lane l ^ 16.  Rounded to bf16.
-__device__ __forceinline__ uint2 norm_rope(uint2 w, const float *gain, float eps, const float *cs, const float *sn, int lane) {
+__device__ __forceinline__ uint2 norm_rope(uint2 w, float4 g, float eps, const float (&cs)[4], const float (&sn)[4], int lane) {
     const float x[4] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
     const float ss = warp_sum(x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3]);
     const float r = 1.0f / sqrtf(ss * (1.0f / kD) + eps);
-    const float4 g = *reinterpret_cast<const float4 *>(gain + 4 * lane);
     const float y[4] = {x[0] * r * g.x, x[1] * r * g.y, x[2] * r * g.z, x[3] * r * g.w};
     float z[4];
 #pragma unroll
@@ -130,6 +129,9 @@ constexpr int kMaxStages = 5;         // pages in a warp's ring
 // A stage: K codes, V codes, K parameters, V parameters, so that lane l copies
 // 16 bytes at 16 l of each 512.
 constexpr int kStageBytes = 2 * kKvqHeadBytes;
+constexpr int kMinPages = 2;          // of a worker
+constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group
+constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 384 SMs
 constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;
 constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
 constexpr float kScaleMost = 1024.f;  // s times its factor: set to [32, 64), moved past this
@@ -138,7 +140,7 @@ constexpr float kScaleMost = 1024.f;  // s times its factor: set to [32, 64), mo
 __host__ __device__ constexpr int workers_of(int hkv) { return kWarps / hkv; }
 
 struct SmemLayout {
-    uint32_t stages, off_scan, off_prefix, total;
+    uint32_t stages, off_scan, off_freq, off_prefix, total;
 };
 
 // Two CTAs share an SM's 227 KB; the prefix sums of a large batch cost one
@@ -149,45 +151,67 @@ __host__ __device__ inline SmemLayout smem_layout(int batch) {
     uint32_t o = s.stages * kStageBytes * kWarps;
     s.off_scan = o;  // warp sums of the prefix scan
     o += kWarps * 4;
+    s.off_freq = o;  // rotation frequencies (hi, lo) and axes of the 64 pairs
+    o += kD / 2 * 8 + kD / 2;
     s.off_prefix = o;
     o += (batch + 1) * 4;
     s.total = (o + 15) & ~15u;
     return s;
 }
 
-// Workspace: arrival counters in a region of fixed size, zero between calls,
-// then the partials.
+// Workspace: arrival counters in regions of fixed size, zero between calls
+// (one a request, one a request's group of workers), then the partials of
+// workers and of groups.
 struct WorkspaceLayout {
-    size_t arrivals, acc, ml, total;
+    size_t arrivals, group_arrivals, acc, ml, group_acc, group_ml, total;
 };
 
 __host__ __device__ inline WorkspaceLayout workspace_layout(int batch, int hq, int workers) {
     const size_t slots = (size_t)workers + (size_t)batch;
+    const size_t group_slots = (size_t)workers / kMergeMost + 1 + (size_t)batch;
+    const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     WorkspaceLayout w;
     w.arrivals = 0;
-    w.acc = ((size_t)kDecodeMaxBatch * kMaxHkv * sizeof(int) + 255) & ~(size_t)255;
-    w.ml = w.acc + ((slots * hq * kD * sizeof(float) + 255) & ~(size_t)255);
-    w.total = w.ml + ((slots * hq * 2 * sizeof(float) + 255) & ~(size_t)255);
+    w.group_arrivals = up((size_t)kDecodeMaxBatch * kMaxHkv * sizeof(int));
+    w.acc = w.group_arrivals + up((size_t)(kDecodeMaxBatch + kMaxGroups) * kMaxHkv * sizeof(int));
+    w.ml = w.acc + up(slots * hq * kD * sizeof(float));
+    w.group_acc = w.ml + up(slots * hq * 2 * sizeof(float));
+    w.group_ml = w.group_acc + up(group_slots * hq * kD * sizeof(float));
+    w.total = w.group_ml + up(group_slots * hq * 2 * sizeof(float));
     return w;
 }
 
 // How the flat page list is cut: worker v has pages [total v / nv, total
-// (v + 1) / nv), none empty.  With pages for every worker a CTA has
-// neighbouring ones, so CTAs differ by one page at most; with fewer, each
-// page has a worker of its own, spread over the CTAs.
+// (v + 1) / nv), none empty.  With kMinPages or more for every worker a CTA
+// has neighbouring ones, so CTAs differ by one page at most.  With fewer
+// there are as many workers as have kMinPages, spread over the CTAs (the
+// first ones of a grid lie on different SMs): a worker more would save less
+// than its partial costs to merge.
 struct Split {
     int total, nv;
     bool spread;
     __device__ __forceinline__ Split(int total_, int ctas, int s) {
         total = total_;
-        spread = total_ < ctas * s;
-        nv = spread ? total_ : ctas * s;
+        spread = total_ < ctas * s * kMinPages;
+        nv = ctas * s;
+        if (spread) {
+            nv = max(1, total_ / kMinPages);
+            if (nv > ctas / kCtasPerSm * s) nv = ctas / kCtasPerSm * s;  // not two on some SMs and one on others
+            if (nv > total_) nv = total_;
+        }
     }
-    __device__ __forceinline__ int worker(int cta, int ctas, int e, int s) const { return spread ? e * ctas + cta : cta * s + e; }
+    __device__ __forceinline__ int worker(int cta, int ctas, int e, int s) const {
+        return !spread ? cta * s + e : e * (ctas / kCtasPerSm) + (cta < ctas / kCtasPerSm ? cta : ctas * s);
+    }
+    // 64-bit divisions cost ten times 32-bit ones, which serve up to 2^19 pages (nv is below 2^13)
     __device__ __forceinline__ int lo(int v) const {
-        return v >= nv ? total : (int)((long long)total * v / nv);
+        if (v >= nv) return total;
+        return total < 1 << 19 ? (int)((uint32_t)total * (uint32_t)v / (uint32_t)nv) : (int)((long long)total * v / nv);
     }
-    __device__ __forceinline__ int of_page(int x) const { return (int)((((long long)x + 1) * nv - 1) / total); }
+    __device__ __forceinline__ int of_page(int x) const {
+        return total < 1 << 19 ? (int)(((uint32_t)(x + 1) * (uint32_t)nv - 1u) / (uint32_t)total)
+                               : (int)((((long long)x + 1) * nv - 1) / total);
+    }
 };
 
 // Pages request b contributes; invalid lengths and positions contribute none
@@ -278,6 +302,100 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     return v;
 }
 
+// Merges the partials at slots [s0, s0 + n) of both heads of KV head g: the
+// lane's dims, maximum and sum.  A round loads kMergeMost partials at once;
+// lane 16 i + u holds the maximum and sum of the round's partial u of head i.
+template <int GROUP>
+__device__ __forceinline__ void merge(const float *acc, const float *ml, size_t s0, int n, int hq, int g, int lane,
+                                      float (&z)[GROUP][4], float (&m)[GROUP], float (&ls)[GROUP]) {
+    static_assert(kMergeMost <= 16, "a head's partials of a round lie on 16 lanes");
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
+    float m_own = -INFINITY, l_own = 0.f;  // of this lane's head: maximum (of both lanes' halves alike), sum over its partials
+    for (int w0 = 0; w0 < n; w0 += kMergeMost) {
+        const int cnt = min(kMergeMost, n - w0);
+        const int hi = GROUP == 2 ? lane >> 4 : 0, u_own = lane & 15;
+        float2 mine = make_float2(-INFINITY, 0.f);
+        if (u_own < cnt) mine = __ldcg(reinterpret_cast<const float2 *>(ml + ((s0 + w0 + u_own) * hq + g * GROUP + hi) * 2));
+        float4 pv[GROUP][kMergeMost];
+#pragma unroll
+        for (int u = 0; u < kMergeMost; ++u)
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i)
+                pv[i][u] = __ldcg(reinterpret_cast<const float4 *>(acc + ((s0 + w0 + min(u, cnt - 1)) * hq + g * GROUP + i) * kD + 4 * lane));
+        float mb = fmaxf(m_own, mine.x);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+        const float at = mb == -INFINITY ? 0.f : mb;  // nothing attended so far: weights 2^-inf
+        const float alpha = exp2_approx(m_own - at);
+        const float w_own = u_own < cnt ? exp2_approx(mine.x - at) : 0.f;
+        l_own = fmaf(w_own, mine.y, l_own * alpha);
+        m_own = mb;
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) {
+            const float al = __shfl_sync(0xffffffffu, alpha, 16 * i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[i][k] *= al;
+#pragma unroll
+            for (int u = 0; u < kMergeMost; ++u) {
+                const float w = __shfl_sync(0xffffffffu, w_own, 16 * i + u);
+                if (u < cnt) {
+                    z[i][0] = fmaf(w, pv[i][u].x, z[i][0]);
+                    z[i][1] = fmaf(w, pv[i][u].y, z[i][1]);
+                    z[i][2] = fmaf(w, pv[i][u].z, z[i][2]);
+                    z[i][3] = fmaf(w, pv[i][u].w, z[i][3]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) l_own += __shfl_xor_sync(0xffffffffu, l_own, o);
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+        m[i] = __shfl_sync(0xffffffffu, m_own, 16 * i);
+        ls[i] = __shfl_sync(0xffffffffu, l_own, 16 * i);
+    }
+}
+
+template <int GROUP>
+__device__ __forceinline__ void write_partial(float *acc, float *ml, size_t slot, int hq, int g, int lane, const float (&z)[GROUP][4],
+                                              const float (&m)[GROUP], const float (&l)[GROUP]) {
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+        const size_t row = slot * hq + g * GROUP + i;
+        *reinterpret_cast<float4 *>(acc + row * kD + 4 * lane) = make_float4(z[i][0], z[i][1], z[i][2], z[i][3]);
+        if (lane == 0) *reinterpret_cast<float2 *>(ml + row * 2) = make_float2(m[i], l[i]);
+    }
+}
+
+// Lane 4 r + c holds dims [32 c + 4 r, + 4) of an output row.
+template <int GROUP>
+__device__ __forceinline__ void write_out(uint16_t *out, int hq, int b, int g, int lane, const float (&z)[GROUP][4],
+                                          const float (&l)[GROUP]) {
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        *reinterpret_cast<uint2 *>(out + ((size_t)b * hq + g * GROUP + i) * kD + 32 * (lane & 3) + 4 * (lane >> 2)) =
+            make_uint2(pack_bf16x2(z[i][0] * inv, z[i][1] * inv), pack_bf16x2(z[i][2] * inv, z[i][3] * inv));
+    }
+}
+
+// Counts this warp in on up to two counters, after all its writes; lane 0's
+// fences order the partials before the counts and the reads after them.
+// Returns (to every lane) how many were there before.
+__device__ __forceinline__ int2 count_in(int *c0, int *c1, int lane) {
+    __syncwarp();
+    int2 prev = make_int2(0, 0);
+    if (lane == 0) {
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+        if (c0) asm volatile("atom.add.relaxed.gpu.s32 %0, [%1], 1;" : "=r"(prev.x) : "l"(c0) : "memory");
+        if (c1) asm volatile("atom.add.relaxed.gpu.s32 %0, [%1], 1;" : "=r"(prev.y) : "l"(c1) : "memory");
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    }
+    __syncwarp();
+    return make_int2(__shfl_sync(0xffffffffu, prev.x, 0), __shfl_sync(0xffffffffu, prev.y, 0));
+}
+
 template <int GROUP, bool APPEND>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(const __grid_constant__ KvqArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -293,6 +411,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
 
     if (!a.early) grid_wait();
     if (threadIdx.x == 0) prefix[0] = 0;
+    float2 *freq = reinterpret_cast<float2 *>(smem + L.off_freq);
+    uint8_t *axis = smem + L.off_freq + kD / 2 * 8;
+    if (APPEND && threadIdx.x < kD / 2) {
+        freq[threadIdx.x] = make_float2(a.freq_hi[threadIdx.x], a.freq_lo[threadIdx.x]);
+        axis[threadIdx.x] = a.pair_axis[threadIdx.x];
+    }
     // prefix sums of the page counts, one request a thread
     for (int base = 0, carry = 0; base < a.batch; base += kWarps * 32) {
         const int b = base + threadIdx.x;
@@ -364,8 +488,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     // With the pools vouched for (early_pools) the rings fill before the wait.
     if (a.early && !a.early_pools) grid_wait();
 #pragma unroll 1
-    for (int s = 0; s < kMaxStages; ++s)
-        if (s < n_stages) issue();
+    for (int s = 0; s < n_stages; ++s) issue();
     if (a.early && a.early_pools) grid_wait();
 
     if (blockIdx.x == 0) {  // zero rows of requests with nothing to attend over
@@ -379,48 +502,64 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     if (lo >= hi) return;
     const int r = lane >> 2, c = lane & 3;
 
-    auto load_q = [&](int b, uint2 (&w)[GROUP]) {
+    // what a segment reads of its request, loaded a segment ahead: q, the length and the positions (lane x: axis x)
+    uint2 q_next[GROUP];
+    int len_next, pos_next = 0;
+    auto load_ahead = [&](int b) {
 #pragma unroll
         for (int i = 0; i < GROUP; ++i)
-            w[i] = *reinterpret_cast<const uint2 *>(a.q + b * a.ldq + (g * GROUP + i) * kD + 4 * lane);
+            q_next[i] = *reinterpret_cast<const uint2 *>(a.q + b * a.ldq + (g * GROUP + i) * kD + 4 * lane);
+        len_next = a.seq_lens[b];
+        if (APPEND && a.positions && lane < a.n_axes) pos_next = a.positions[(size_t)lane * a.batch + b];
     };
     int b = request_of(prefix, a.batch, lo);
-    uint2 q_next[GROUP];
-    load_q(b, q_next);
+    load_ahead(b);
     int split_b[2] = {-1, -1};  // requests whose partials this worker wrote: its first and last at most
     uint32_t at = ring_base;    // stage of the next page
 
     for (int x = lo; x < hi;) {
         const int p0 = prefix[b], p1 = prefix[b + 1];
         const int j0 = x - p0, j1 = min(hi, p1) - p0;
-        const int seq_len = a.seq_lens[b];
-        uint2 qw[GROUP];
+        const int seq_len = len_next;
+        const bool has_new = APPEND && j1 == p1 - p0;
+        uint2 qw[GROUP], kw = make_uint2(0u, 0u), vw = kw;
+        float4 gq, gk;
+        if (APPEND) {
+            gq = *reinterpret_cast<const float4 *>(a.q_gain + 4 * lane);
+            if (has_new) {
+                const size_t o = b * a.ldkv + g * kD + 4 * lane;
+                kw = *reinterpret_cast<const uint2 *>(a.k_new + o);
+                vw = *reinterpret_cast<const uint2 *>(a.v_new + o);
+                gk = *reinterpret_cast<const float4 *>(a.k_gain + 4 * lane);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) qw[i] = q_next[i];
-        // the next request, whose q is loaded a segment ahead
+        uint32_t new_k = 0, new_v = 0, new_ksm = 0, new_vsm = 0;
+        if (APPEND) {
+            // angles of pairs 4 (l mod 16) + u: each of two lanes takes half of them
+            float cs[4], sn[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = 4 * (lane & 15) + (lane >> 4) * 2 + u;
+                const int pos = a.positions ? __shfl_sync(0xffffffffu, pos_next, axis[i]) : seq_len - 1;
+                float s1, c1;
+                sincos_pos_freq_fast(pos, freq[i].x, freq[i].y, &s1, &c1);
+                const float s2 = __shfl_xor_sync(0xffffffffu, s1, 16), c2 = __shfl_xor_sync(0xffffffffu, c1, 16);
+                sn[u] = lane < 16 ? s1 : s2, sn[2 + u] = lane < 16 ? s2 : s1;
+                cs[u] = lane < 16 ? c1 : c2, cs[2 + u] = lane < 16 ? c2 : c1;
+            }
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) qw[i] = norm_rope(qw[i], gq, a.eps, cs, sn, lane);
+            if (has_new) {
+                new_k = quantise_row(norm_rope(kw, gk, a.eps, cs, sn, lane), lane, new_ksm);
+                new_v = quantise_row(vw, lane, new_vsm);
+            }
+        }
         int b_next = b + 1;
         if (p1 < hi) {
             while (prefix[b_next + 1] == prefix[b_next]) ++b_next;
-            load_q(b_next, q_next);
-        }
-        const bool has_new = APPEND && j1 == p1 - p0;
-        uint32_t new_k = 0, new_v = 0, new_ksm = 0, new_vsm = 0;
-        if (APPEND) {
-            float cs[4], sn[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = 4 * (lane & 15) + u;
-                const int pos = a.positions ? a.positions[(size_t)a.pair_axis[i] * a.batch + b] : seq_len - 1;
-                sincos_pos_freq(pos, a.freq_hi[i], a.freq_lo[i], &sn[u], &cs[u]);
-            }
-            if (has_new) {
-                const size_t o = b * a.ldkv + g * kD + 4 * lane;
-                const uint2 kw = norm_rope(*reinterpret_cast<const uint2 *>(a.k_new + o), a.k_gain, a.eps, cs, sn, lane);
-                new_k = quantise_row(kw, lane, new_ksm);
-                new_v = quantise_row(*reinterpret_cast<const uint2 *>(a.v_new + o), lane, new_vsm);
-            }
-#pragma unroll
-            for (int i = 0; i < GROUP; ++i) qw[i] = norm_rope(qw[i], a.q_gain, a.eps, cs, sn, lane);
+            load_ahead(b_next);
         }
         // B of the scores: lane (n, c), n = (group n / 2, head n % 2), holds head n % 2's dims [32 g + 8 c, + 8) of its
         // own group, as the pairs (j, j + 4) that the code words hold, a 16th of the pairs whose codes come 16-fold
@@ -633,86 +772,53 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             }
         }
         if (j0 == 0 && j1 == p1 - p0) {
-#pragma unroll
-            for (int i = 0; i < GROUP; ++i) {
-                const float inv = l_sum[i] == 0.f ? 0.f : 1.f / l_sum[i];
-                *reinterpret_cast<uint2 *>(a.out + ((size_t)b * hq + g * GROUP + i) * kD + 32 * c + 4 * r) =
-                    make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
-            }
+            write_out<GROUP>(a.out, hq, b, g, lane, acc, l_sum);
         } else {
-            const size_t slot = (size_t)v + b;
-#pragma unroll
-            for (int i = 0; i < GROUP; ++i) {
-                const int h = g * GROUP + i;
-                *reinterpret_cast<float4 *>(a.part_acc + (slot * hq + h) * kD + 4 * lane) =
-                    make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-                if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * hq + h) * 2) = make_float2(ref_of[i], l_sum[i]);
-            }
+            write_partial<GROUP>(a.part_acc, a.part_ml, (size_t)v + b, hq, g, lane, acc, ref_of, l_sum);
             split_b[x == lo ? 0 : 1] = b;
         }
         x = p0 + j1;
         b = b_next;
     }
 
-    // Split requests: count in, and merge where this warp is the last.
+    // Split requests: count in, and merge where this warp is the last.  A request over more workers than two rounds of
+    // loads take is merged by groups of neighbouring workers first, each by the last of its group.
     if (split_b[0] < 0 && split_b[1] < 0) return;
-    __syncwarp();
-    int prev[2] = {0, 0};
-    if (lane == 0) {
-        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    int v0[2], v1[2];
+    int *counter[2];
+    bool grouped[2];
 #pragma unroll
-        for (int d = 0; d < 2; ++d)
-            if (split_b[d] >= 0)
-                asm volatile("atom.add.relaxed.gpu.s32 %0, [%1], 1;"
-                             : "=r"(prev[d])
-                             : "l"(a.arrivals + (size_t)split_b[d] * kMaxHkv + g)
-                             : "memory");
-        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    for (int d = 0; d < 2; ++d) {
+        const int bb = max(split_b[d], 0);
+        v0[d] = split.of_page(prefix[bb]), v1[d] = split.of_page(prefix[bb + 1] - 1);
+        grouped[d] = v1[d] - v0[d] >= 2 * kMergeMost;
+        counter[d] = split_b[d] < 0 ? nullptr
+                     : grouped[d]   ? a.group_arrivals + (size_t)(v / kMergeMost + bb) * kMaxHkv + g
+                                    : a.arrivals + (size_t)bb * kMaxHkv + g;
     }
+    const int2 prev = count_in(counter[0], counter[1], lane);
 #pragma unroll
     for (int d = 0; d < 2; ++d) {
         const int bb = split_b[d];
         if (bb < 0) continue;
-        const int v0 = split.of_page(prefix[bb]), v1 = split.of_page(prefix[bb + 1] - 1);
-        if (__shfl_sync(0xffffffffu, prev[d], 0) != v1 - v0) continue;
-        constexpr int kBatch = 8;  // partials in flight together
-#pragma unroll
-        for (int i = 0; i < GROUP; ++i) {
-            const int h = g * GROUP + i;
-            float m = -INFINITY, ls = 0.f, z[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int w0 = v0; w0 <= v1; w0 += kBatch) {
-                float2 ml[kBatch];
-                float4 pv[kBatch];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const size_t row = ((size_t)min(w0 + u, v1) + bb) * hq + h;
-                    ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + row * 2));
-                    pv[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_acc + row * kD + 4 * lane));
-                }
-                float mb = m;
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) mb = fmaxf(mb, ml[u].x);
-                const float at = mb == -INFINITY ? 0.f : mb;  // nothing attended so far: weights 2^-inf
-                const float alpha = exp2_approx(m - at);
-                ls *= alpha;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) z[k] *= alpha;
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    if (w0 + u > v1) continue;
-                    const float w = exp2_approx(ml[u].x - at);
-                    ls = fmaf(w, ml[u].y, ls);
-                    z[0] = fmaf(w, pv[u].x, z[0]);
-                    z[1] = fmaf(w, pv[u].y, z[1]);
-                    z[2] = fmaf(w, pv[u].z, z[2]);
-                    z[3] = fmaf(w, pv[u].w, z[3]);
-                }
-                m = mb;
-            }
-            const float inv = ls == 0.f ? 0.f : 1.f / ls;
-            *reinterpret_cast<uint2 *>(a.out + ((size_t)bb * hq + h) * kD + 32 * c + 4 * r) =
-                make_uint2(pack_bf16x2(z[0] * inv, z[1] * inv), pack_bf16x2(z[2] * inv, z[3] * inv));
+        int before = d == 0 ? prev.x : prev.y;
+        float z[GROUP][4], m[GROUP], ls[GROUP];
+        if (grouped[d]) {
+            const int q = v / kMergeMost;
+            const int a0 = max(v0[d], q * kMergeMost), a1 = min(v1[d], q * kMergeMost + kMergeMost - 1);
+            if (before != a1 - a0) continue;
+            merge<GROUP>(a.part_acc, a.part_ml, (size_t)a0 + bb, a1 - a0 + 1, hq, g, lane, z, m, ls);
+            if (lane == 0) *counter[d] = 0;
+            write_partial<GROUP>(a.group_acc, a.group_ml, (size_t)q + bb, hq, g, lane, z, m, ls);
+            before = count_in(a.arrivals + (size_t)bb * kMaxHkv + g, nullptr, lane).x;
+            const int q0 = v0[d] / kMergeMost, q1 = v1[d] / kMergeMost;
+            if (before != q1 - q0) continue;
+            merge<GROUP>(a.group_acc, a.group_ml, (size_t)q0 + bb, q1 - q0 + 1, hq, g, lane, z, m, ls);
+        } else {
+            if (before != v1[d] - v0[d]) continue;
+            merge<GROUP>(a.part_acc, a.part_ml, (size_t)v0[d] + bb, v1[d] - v0[d] + 1, hq, g, lane, z, m, ls);
         }
+        write_out<GROUP>(a.out, hq, bb, g, lane, z, ls);
         if (lane == 0) a.arrivals[(size_t)bb * kMaxHkv + g] = 0;
     }
 }
@@ -746,7 +852,10 @@ cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void 
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     a.part_acc = reinterpret_cast<float *>(ws + w.acc);
     a.part_ml = reinterpret_cast<float *>(ws + w.ml);
+    a.group_acc = reinterpret_cast<float *>(ws + w.group_acc);
+    a.group_ml = reinterpret_cast<float *>(ws + w.group_ml);
     a.arrivals = reinterpret_cast<int *>(ws + w.arrivals);
+    a.group_arrivals = reinterpret_cast<int *>(ws + w.group_arrivals);
     if (app) {
         const qa_rope &rope = *app->rope;
         a.k_new = static_cast<const uint16_t *>(app->k_new);
