@@ -284,24 +284,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 __device__ __forceinline__ int exponent_of(float x) { return (__float_as_int(x) >> 23 & 255) - 127; }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-
 // Merges the partials at slots [s0, s0 + n) of both heads of KV head g: the
 // lane's dims, maximum and sum.  A round loads kMergeMost partials at once;
 // lane 16 i + u holds the maximum and sum of the round's partial u of head i.
@@ -414,8 +396,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     float2 *freq = reinterpret_cast<float2 *>(smem + L.off_freq);
     uint8_t *axis = smem + L.off_freq + kD / 2 * 8;
     if (APPEND && threadIdx.x < kD / 2) {
-        freq[threadIdx.x] = make_float2(a.freq_hi[threadIdx.x], a.freq_lo[threadIdx.x]);
-        axis[threadIdx.x] = a.pair_axis[threadIdx.x];
+        const float *f_hi = a.freq_hi, *f_lo = a.freq_lo;
+        const uint8_t *pair_axis = a.pair_axis;
+        asm("" : "+l"(f_hi), "+l"(f_lo), "+l"(pair_axis));  // as memory: the constant bank serves one address at a time
+        freq[threadIdx.x] = make_float2(f_hi[threadIdx.x], f_lo[threadIdx.x]);
+        axis[threadIdx.x] = pair_axis[threadIdx.x];
     }
     // prefix sums of the page counts, one request a thread
     for (int base = 0, carry = 0; base < a.batch; base += kWarps * 32) {

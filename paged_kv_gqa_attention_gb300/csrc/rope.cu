@@ -4,14 +4,20 @@
 //   y = x / sqrt(mean x^2 + eps) * gain;  a_i = positions[axis(i)][t] theta^(-2i/D)
 //   z_i = y_i cos a_i - y_{i+D/2} sin a_i,  z_{i+D/2} = y_i sin a_i + y_{i+D/2} cos a_i
 //
-// A CTA takes kRows rows.  Its threads first compute the rows' D/2 angles
-// once into shared memory (every head of a row turns by the same angles),
-// then D/8 lanes share a head: a lane holds dims [4l, 4l + 4) and their
-// partners D/2 further, two 8-byte loads and stores.
+// Every warp works by itself.  An item is one row and PASSES x 512 / D of its
+// heads: D/16 lanes share a head, a lane holds dims [8l, 8l + 8) and their
+// partners D/2 further.  A warp has kStages items in flight in its part of
+// shared memory (16-byte asynchronous copies, each lane its own bytes, so
+// nothing waits on other lanes), and computes each of a row's D/2 angles once
+// and exchanges them by shuffles.  Frequencies are read once a warp, and as
+// memory: the constant bank serves one address at a time, and read so for
+// every row it was what bounded.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "qa_internal.h"
@@ -22,6 +28,10 @@ namespace {
 __device__ unsigned int g_status;
 
 constexpr int kMaxHalf = 64;
+constexpr int kFewHeads = 16384;   // head vectors up to which an item is one pass
+constexpr int kThreads = 128;
+constexpr int kStages = 2;
+constexpr int kCtasPerSm = 10;
 constexpr int kMaxPos = 1 << 18;  // sincos_pos_freq's range
 
 struct RopeArgs {
@@ -37,74 +47,134 @@ struct RopeArgs {
     float freq_hi[kMaxHalf], freq_lo[kMaxHalf];
 };
 
-template <int D, int ROWS, int THREADS>
-__global__ void __launch_bounds__(THREADS) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
+template <int D, int PASSES, bool NORM>
+__global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int HALF = D / 2;
-    constexpr int LANES = D / 8;  // lanes of a head
-    __shared__ float2 turn[ROWS][HALF];  // cos, sin
-    __shared__ int row_ok[ROWS];
-    if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int r0 = blockIdx.x * ROWS;
-    const int n_rows = min(ROWS, a.rows - r0);
-    if (threadIdx.x < (unsigned)n_rows) {
-        int ok = 1;
-        for (int x = 0; x < a.n_axes; ++x) {
-            const int pos = a.positions[(size_t)x * a.rows + r0 + threadIdx.x];
-            ok &= pos >= 0 && pos < kMaxPos;
-        }
-        if (!ok) atomicOr(&g_status, QA_DEVICE_BAD_POSITION);
-        row_ok[threadIdx.x] = ok;
-    }
-    for (int u = threadIdx.x; u < n_rows * HALF; u += THREADS) {
-        const int row = u / HALF, i = u % HALF;
-        const int pos = a.positions[(size_t)a.pair_axis[i] * a.rows + r0 + row];
-        float s, c;
-        sincos_pos_freq(pos, a.freq_hi[i], a.freq_lo[i], &s, &c);
-        turn[row][i] = make_float2(c, s);
-    }
-    __syncthreads();
-    if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int LANES = D / 16;        // lanes of a head
+    constexpr int HEADS = 32 / LANES;    // of a pass
+    constexpr int OWN = HALF / 32;       // angles of a lane
+    constexpr int STAGE = PASSES * 1024;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
+    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * (kStages * STAGE) + 16 * lane;
+    const int h0 = blockIdx.y * (HEADS * PASSES) + sub;  // the lane's head of the first pass
+    const int stride = gridDim.x * (kThreads / 32);
+    int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
 
-    const int l = threadIdx.x % LANES;
-    for (int h = threadIdx.x / LANES; h < a.heads; h += THREADS / LANES) {
-        const bool is_q = h < a.hq;
-        const float *gain = is_q ? a.q_gain : a.k_gain;
-        float4 g0 = make_float4(1.f, 1.f, 1.f, 1.f), g1 = g0;
-        if (gain) {
-            g0 = *reinterpret_cast<const float4 *>(gain + 4 * l);
-            g1 = *reinterpret_cast<const float4 *>(gain + HALF + 4 * l);
-        }
-        for (int row = 0; row < n_rows; ++row) {
-            const long long t = r0 + row;
-            const int hh = is_q ? h : h - a.hq;
-            const uint16_t *src = (is_q ? a.q + t * a.ldq : a.k + t * a.ldk) + hh * D + 4 * l;
-            uint16_t *dst = (is_q ? a.q_out + t * a.ldq_out : a.k_out + t * a.ldk_out) + hh * D + 4 * l;
-            const uint2 w0 = *reinterpret_cast<const uint2 *>(src), w1 = *reinterpret_cast<const uint2 *>(src + HALF);
-            float x[4] = {bf16lo(w0.x), bf16hi(w0.x), bf16lo(w0.y), bf16hi(w0.y)};
-            float y[4] = {bf16lo(w1.x), bf16hi(w1.x), bf16lo(w1.y), bf16hi(w1.y)};
-            if (gain) {
-                float ss = 0.f;
+    float f_hi[OWN], f_lo[OWN];
+    int axis[OWN];
+    const float *hi = a.freq_hi, *lo = a.freq_lo;
+    const uint8_t *pair_axis = a.pair_axis;
+    asm("" : "+l"(hi), "+l"(lo), "+l"(pair_axis));  // generic addresses: the lanes' loads go together
 #pragma unroll
-                for (int c = 0; c < 4; ++c) ss += x[c] * x[c] + y[c] * y[c];
-                const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
+    for (int y = 0; y < OWN; ++y) {  // of the lane's 8 pairs 8 l + j, j = OWN sub + y
+        const int i = 8 * l + OWN * sub + y;
+        f_hi[y] = hi[i], f_lo[y] = lo[i], axis[y] = pair_axis[i];
+    }
+    // where the lane's head of pass p lies in a row: its first pass's place as a query or as a key, p HEADS D further
+    const int at_q = h0 * D + 8 * l, at_k = (h0 - a.hq) * D + 8 * l;
+    auto fetch = [&](long long row, int stage) {  // a row's copies, or nothing past the last: a group either way
+        if (row < a.rows) {
+            const uint16_t *q = a.q + row * a.ldq + at_q, *k = a.k + row * a.ldk + at_k;
 #pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-                const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-                x[0] *= r * g0.x, x[1] *= r * g0.y, x[2] *= r * g0.z, x[3] *= r * g0.w;
-                y[0] *= r * g1.x, y[1] *= r * g1.y, y[2] *= r * g1.z, y[3] *= r * g1.w;
+            for (int p = 0; p < PASSES; ++p) {
+                const int h = h0 + p * HEADS;
+                if (h < a.heads) {
+                    const uint16_t *src = (h < a.hq ? q : k) + p * (HEADS * D);
+                    copy16(ring + stage * STAGE + p * 1024, src);
+                    copy16(ring + stage * STAGE + p * 1024 + 512, src + HALF);
+                }
             }
-            if (!row_ok[row]) continue;
-            float z[4], u[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 cs = turn[row][4 * l + c];
-                z[c] = x[c] * cs.x - y[c] * cs.y;
-                u[c] = x[c] * cs.y + y[c] * cs.x;
-            }
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
-            *reinterpret_cast<uint2 *>(dst + HALF) = make_uint2(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
         }
+        copy_commit();
+    };
+    auto position = [&](long long row) -> int {  // lane x: the row's position on axis x
+        return row < a.rows && lane < a.n_axes ? a.positions[(size_t)lane * a.rows + row] : 0;
+    };
+    const auto wait = [] {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    };
+    if (!a.early) wait();
+    int pos_next = position(t);
+    if (a.early) wait();
+#pragma unroll
+    for (int n = 0; n < kStages; ++n) fetch(t + (long long)n * stride, n);
+    int stage = 0;
+    for (; t < a.rows; t += stride) {
+        const int pos = pos_next;
+        pos_next = position((long long)t + stride);
+        const bool bad = __any_sync(0xffffffffu, pos < 0 || pos >= kMaxPos);
+        if (bad && lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_POSITION);
+        float c_own[OWN], s_own[OWN];
+        float2 c[4], s[4];
+#pragma unroll
+        for (int y = 0; y < OWN; ++y)
+            sincos_pos_freq_fast(__shfl_sync(0xffffffffu, pos, axis[y]), f_hi[y], f_lo[y], &s_own[y], &c_own[y]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float cj = __shfl_sync(0xffffffffu, c_own[j % OWN], j / OWN * LANES + l);
+            const float sj = __shfl_sync(0xffffffffu, s_own[j % OWN], j / OWN * LANES + l);
+            if (j & 1) c[j / 2].y = cj, s[j / 2].y = sj; else c[j / 2].x = cj, s[j / 2].x = sj;
+        }
+        // z = xc x - ys y, u = xs x + yc y, times 1 / rms: the gains of query heads, then of key heads, are in the factors
+        float2 xc[4], xs[4], yc[4], ys[4];
+        auto factors = [&](bool is_q) {
+            const float *gain = (is_q ? a.q_gain : a.k_gain) + 8 * l;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 g0 = make_float2(1.f, 1.f), g1 = g0;
+                if (NORM) g0 = __ldg(reinterpret_cast<const float2 *>(gain) + i), g1 = __ldg(reinterpret_cast<const float2 *>(gain + HALF) + i);
+                xc[i] = fmul2(c[i], g0), xs[i] = fmul2(s[i], g0), yc[i] = fmul2(c[i], g1);
+                ys[i] = fmul2(s[i], make_float2(-g1.x, -g1.y));
+            }
+        };
+        factors(h0 < a.hq);
+        uint16_t *q_out = a.q_out + (long long)t * a.ldq_out + at_q, *k_out = a.k_out + (long long)t * a.ldk_out + at_k;
+        copy_wait<kStages - 1>();
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int h = h0 + p * HEADS;
+            if (NORM && p > 0) {
+                const bool turned = h >= a.hq && h - HEADS < a.hq;  // the lane's first key head
+                if (__any_sync(0xffffffffu, turned)) {
+                    if (turned) factors(false);
+                }
+            }
+            const uint4 w0 = lds128(ring + stage * STAGE + p * 1024), w1 = lds128(ring + stage * STAGE + p * 1024 + 512);
+            const uint32_t wx[4] = {w0.x, w0.y, w0.z, w0.w}, wy[4] = {w1.x, w1.y, w1.z, w1.w};
+            float2 x[4], y[4];
+            float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = make_float2(bf16lo(wx[i]), bf16hi(wx[i]));
+                y[i] = make_float2(bf16lo(wy[i]), bf16hi(wy[i]));
+                if (NORM) s2 = ffma2(x[i], x[i], ffma2(y[i], y[i], s2));
+            }
+            float r = 1.f;
+            if (NORM) {
+                float ss = s2.x + s2.y;
+#pragma unroll
+                for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                r = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
+            }
+            const float2 rr = make_float2(r, r);
+            uint32_t z[4], u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 lo = ffma2(x[i], xc[i], fmul2(y[i], ys[i])), hi = ffma2(x[i], xs[i], fmul2(y[i], yc[i]));
+                if (NORM) lo = fmul2(lo, rr), hi = fmul2(hi, rr);
+                z[i] = pack_bf16x2(lo.x, lo.y);
+                u[i] = pack_bf16x2(hi.x, hi.y);
+            }
+            if (h < a.heads && !bad) {
+                uint16_t *dst = (h < a.hq ? q_out : k_out) + p * (HEADS * D);
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(z[0], z[1], z[2], z[3]);
+                *reinterpret_cast<uint4 *>(dst + HALF) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+        }
+        fetch((long long)t + (long long)kStages * stride, stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 }
 
@@ -154,18 +224,30 @@ cudaError_t launch_rope_rows(const void *q, long long ldq, const void *k, long l
     if (rope.pair_axis) memcpy(a.pair_axis, rope.pair_axis, p.head_dim / 2);
     rope_frequencies(rope.theta, p.head_dim, a.freq_hi, a.freq_lo);
 
-    constexpr int kThreads = 384, kRowsPerCta = 4;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + kRowsPerCta - 1) / kRowsPerCta));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto kernel = p.head_dim == 128 ? rope_rows_kernel<128, kRowsPerCta, kThreads> : rope_rows_kernel<64, kRowsPerCta, kThreads>;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    const bool wide = p.head_dim == 128, norm = rope.q_gain != nullptr;
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
+        return cudaErrorInvalidDevice;
+    const auto pick = [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        const int heads_an_item = 512 / p.head_dim * N, chunks = (a.heads + heads_an_item - 1) / heads_an_item;
+        const int ctas = (rows + kThreads / 32 - 1) / (kThreads / 32), most = (sms * kCtasPerSm + chunks - 1) / chunks;
+        cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most), (unsigned)chunks);
+        cfg.dynamicSmemBytes = (kThreads / 32) * kStages * N * 1024;
+        return norm ? cudaLaunchKernelEx(&cfg, wide ? rope_rows_kernel<128, N, true> : rope_rows_kernel<64, N, true>, a)
+                    : cudaLaunchKernelEx(&cfg, wide ? rope_rows_kernel<128, N, false> : rope_rows_kernel<64, N, false>, a);
+    };
+    if ((long long)rows * a.heads <= kFewHeads) return pick(std::integral_constant<int, 1>());
+    return pick(std::integral_constant<int, 2>());
 }
 
 unsigned int status_read_clear_rope(cudaStream_t stream, cudaError_t *err) {
