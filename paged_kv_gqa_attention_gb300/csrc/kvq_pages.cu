@@ -6,8 +6,8 @@
 // tensor-core fragment in decode (kvq.cuh): of K, tokens r and r + 8, the 8
 // dims [8c, 8c + 8) of each group; of V, tokens 2c, 2c + 1 (+ 8), the 4 dims
 // [4r, 4r + 4) of each group.  So a group of K is spread over the 4 lanes of
-// equal r and one of V over the 8 of equal c, its range takes 2 or 3
-// shuffles, and every code a lane makes goes into its own words.
+// equal r and one of V over the 8 of equal c, and every code a lane makes
+// goes into its own words.
 //
 // Pages of a request are found without a prefix sum: request r's pages have
 // the ids S(r) + j with S(r) = cu[r] / 16 + 2 r.  S grows from r to r + 1 by
@@ -101,15 +101,51 @@ __device__ __forceinline__ void wait_dependency() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-__device__ __forceinline__ float nan_min(float a, float b) {
-    float d;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of bf16 pairs; NaN stays
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ float nan_max(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
+}
+// (maximum, minus minimum) of the two halves of maxima and of minima: a range that max2 alone reduces further.
+__device__ __forceinline__ uint32_t range_of(uint32_t mx, uint32_t mn) {
+    return max2(__byte_perm(mx, mn, 0x5410) ^ 0x80000000u, __byte_perm(mx, mn, 0x7632) ^ 0x80000000u);
+}
+__device__ __forceinline__ KvqGroup group_of(uint32_t range) {
+    return kvq_group(bf16lo(range >> 16 ^ 0x8000u), bf16lo(range));
+}
+
+// One step of a reduction over lanes that shares the results out: of 2 N
+// ranges, lanes with the bit `o` clear go on with the first N, the others
+// with the last N.
+template <int N>
+__device__ __forceinline__ void reduce_half(uint32_t *x, int lane, int o) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[i + N], o);
+        x[i] = max2(upper ? x[i + N] : x[i], got);
+    }
+}
+
+// Codes of 2 N values in the low 8 N bits: rint((x - m) r) by adding
+// 1.5 * 2^23 (kvq_code), whose bits a multiply-add chain shifts together.
+template <int N>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[N], float m, float r) {
+    uint32_t code = 0;
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i) {
+        // (a packed multiply and add would be joined, and the product has to be rounded by itself)
+        const float2 d = fsub2(make_float2(bf16lo(w[i]), bf16hi(w[i])), make_float2(m, m));
+        const float2 y = make_float2(__fadd_rn(__fmul_rn(d.x, r), 12582912.0f), __fadd_rn(__fmul_rn(d.y, r), 12582912.0f));
+        code = code * 16u + (__float_as_uint(y.y) - 0x4b400000u);
+        code = code * 16u + (__float_as_uint(y.x) - 0x4b400000u);
+    }
+    return isnan(r) ? 0u : code;
 }
 
 __global__ void __launch_bounds__(256) kvq_write_kernel(const __grid_constant__ PagesArgs a) {
@@ -121,79 +157,89 @@ __global__ void __launch_bounds__(256) kvq_write_kernel(const __grid_constant__ 
     if (a.early) wait_dependency();
     if (!work) return;
     const int r = lane >> 2, c = lane & 3;
+
+    // K: tokens r and r + 8, dims [32 g + 8 c, + 8).  V: tokens 8 u + 2 c + e, dims [32 g + 4 r, + 4).
+    uint4 k[2][4];
+    uint2 v[4][4];  // [2 u + e][g]
+    bool k_in[2], v_in[4];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int t = r + 8 * y;
+        k_in[y] = t >= j.t0 && t < j.t1;
+        const uint16_t *p = a.k_in + (j.row0 + t) * a.ldk + h * kKvqDim + 8 * c;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) k[y][g] = k_in[y] ? *reinterpret_cast<const uint4 *>(p + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const int t = 8 * (y >> 1) + 2 * c + (y & 1);
+        v_in[y] = t >= j.t0 && t < j.t1;
+        const uint16_t *p = a.v_in + (j.row0 + t) * a.ldv + h * kKvqDim + 4 * r;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) v[y][g] = v_in[y] ? *reinterpret_cast<const uint2 *>(p + 32 * g) : make_uint2(0u, 0u);
+    }
     uint8_t *kp = a.k_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
     uint8_t *vp = a.v_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
 
+    // Ranges: the reductions over a group's lanes end with each lane holding two groups of one token, whose parameters
+    // it computes, writes, and gives to the others.
+    uint32_t kr[8], vr[16];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {  // K: token r + 8 half
-        const int t = r + 8 * half;
-        const bool in = t >= j.t0 && t < j.t1;
-        uint32_t code[4], par[4];
+    for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (in) w = *reinterpret_cast<const uint4 *>(a.k_in + (j.row0 + t) * a.ldk + h * kKvqDim + 32 * g + 8 * c);
-            const float x[8] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y),
-                                bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)};
-            float lo = x[0], hi = x[0];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) lo = nan_min(lo, x[i]), hi = nan_max(hi, x[i]);
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                lo = nan_min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-                hi = nan_max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            }
-            const KvqGroup gr = kvq_group(lo, hi);
-            uint32_t word = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) word |= kvq_code(x[i], gr) << (4 * i);
-            code[g] = word;
-            par[g] = gr.sm;
+            const uint4 w = k[y][g];
+            kr[4 * y + g] = range_of(max2(max2(w.x, w.y), max2(w.z, w.w)), min2(min2(w.x, w.y), min2(w.z, w.w)));
         }
-        if (in) {
-            *reinterpret_cast<uint4 *>(kp + t * 64 + c * 16) = make_uint4(code[0], code[1], code[2], code[3]);
-            if (c == 0) *reinterpret_cast<uint4 *>(kp + kvq_param_offset(t, 0)) = make_uint4(par[0], par[1], par[2], par[3]);
-        }
+    reduce_half<4>(kr, lane, 1);  // token r + 8 (c & 1)
+    reduce_half<2>(kr, lane, 2);  // groups 2 (c >> 1), + 1
+    // order [e][u][g], so that each step halves it
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) vr[8 * (y & 1) + 4 * (y >> 1) + g] = range_of(max2(v[y][g].x, v[y][g].y), min2(v[y][g].x, v[y][g].y));
+    reduce_half<8>(vr, lane, 4);
+    reduce_half<4>(vr, lane, 8);
+    reduce_half<2>(vr, lane, 16);
+    const KvqGroup ka = group_of(kr[0]), kb = group_of(kr[1]), va = group_of(vr[0]), vb = group_of(vr[1]);
+    {
+        const int t = r + 8 * (c & 1);
+        if (t >= j.t0 && t < j.t1) *reinterpret_cast<uint2 *>(kp + kvq_param_offset(t, 2 * (c >> 1))) = make_uint2(ka.sm, kb.sm);
+        const int s = 8 * (r >> 1 & 1) + 2 * c + (r & 1);
+        if (s >= j.t0 && s < j.t1) *reinterpret_cast<uint2 *>(vp + kvq_param_offset(s, 2 * (r >> 2))) = make_uint2(va.sm, vb.sm);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {  // V: tokens 8 u + 2 c, + 1
-        uint32_t code[2][4];
-        bool in[2];
+    for (int y = 0; y < 2; ++y) {
+        uint32_t code[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int t = 8 * u + 2 * c + e;
-            in[e] = t >= j.t0 && t < j.t1;
-            uint32_t par[4];
+        for (int g = 0; g < 4; ++g) {
+            const int from = (lane & ~3) | y | (g >> 1) << 1;
+            const float m = __shfl_sync(0xffffffffu, g & 1 ? kb.m : ka.m, from), rr = __shfl_sync(0xffffffffu, g & 1 ? kb.r : ka.r, from);
+            const uint32_t w[4] = {k[y][g].x, k[y][g].y, k[y][g].z, k[y][g].w};
+            code[g] = codes_of<4>(w, m, rr);
+        }
+        if (k_in[y]) *reinterpret_cast<uint4 *>(kp + (r + 8 * y) * 64 + c * 16) = make_uint4(code[0], code[1], code[2], code[3]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        uint32_t code[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                uint2 w = make_uint2(0u, 0u);
-                if (in[e]) w = *reinterpret_cast<const uint2 *>(a.v_in + (j.row0 + t) * a.ldv + h * kKvqDim + 32 * g + 4 * r);
-                const float x[4] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
-                float lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
-                float hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    lo = nan_min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-                    hi = nan_max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                }
-                const KvqGroup gr = kvq_group(lo, hi);
-                uint32_t word = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) word |= kvq_code(x[i], gr) << (4 * i);
-                code[e][g] = word;
-                par[g] = gr.sm;
+                const int from = c | (e | u << 1 | (g >> 1) << 2) << 2;
+                const float m = __shfl_sync(0xffffffffu, g & 1 ? vb.m : va.m, from), rr = __shfl_sync(0xffffffffu, g & 1 ? vb.r : va.r, from);
+                const uint32_t w[2] = {v[2 * u + e][g].x, v[2 * u + e][g].y};
+                code[e][g] = codes_of<2>(w, m, rr);
             }
-            if (in[e] && r == 0)
-                *reinterpret_cast<uint4 *>(vp + kvq_param_offset(t, 0)) = make_uint4(par[0], par[1], par[2], par[3]);
-        }
         uint8_t *dst = vp + u * 512 + lane * 16;
-        if (in[0] && in[1]) {
+        if (v_in[2 * u] && v_in[2 * u + 1]) {
             *reinterpret_cast<uint4 *>(dst) = make_uint4(code[0][0] | code[1][0] << 16, code[0][1] | code[1][1] << 16,
                                                          code[0][2] | code[1][2] << 16, code[0][3] | code[1][3] << 16);
         } else {  // the neighbour's codes stay as they are
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (in[e])
+                if (v_in[2 * u + e])
 #pragma unroll
                     for (int g = 0; g < 4; ++g) *reinterpret_cast<uint16_t *>(dst + g * 4 + e * 2) = (uint16_t)code[e][g];
         }
