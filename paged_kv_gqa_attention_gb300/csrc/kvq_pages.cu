@@ -1,8 +1,8 @@
 // Writing packed K/V rows into 4-bit pages (qa_kvq_write) and reading them
 // back (qa_kvq_read).
 //
-// One warp takes one KV head of one page: its 16 tokens x 128 dims of K and
-// of V.  Lane 4 r + c owns exactly the bytes of the page that it owns as a
+// One warp takes one KV head of one page: its 16 tokens x 128 dims of K, of
+// V, or (reading) of both.  Lane 4 r + c owns exactly the bytes of the page that it owns as a
 // tensor-core fragment in decode (kvq.cuh): of K, tokens r and r + 8, the 8
 // dims [8c, 8c + 8) of each group; of V, tokens 2c, 2c + 1 (+ 8), the 4 dims
 // [4r, 4r + 4) of each group.  So a group of K is spread over the 4 lanes of
@@ -33,11 +33,12 @@ struct PagesArgs {
     int batch, total, hkv, max_pages, num_pages, early;
 };
 
-// What one warp works on: slots [t0, t1) of a page, whose slot t holds packed
+// What a CTA works on: slots [t0, t1) of a page, whose slot t holds packed
 // row `row0 + t` (row0 may be negative: only rows of [t0, t1) exist).
 struct Job {
-    int t0, t1, page;
+    int t0, t1;
     long long row0;
+    size_t entry;  // of the page table
 };
 
 // The job of page id `id`; false when there is none.  Warp-collective.
@@ -76,16 +77,31 @@ __device__ __forceinline__ bool find_job(const PagesArgs &a, int id, Job &j, boo
     const long long pg = (long long)past / kKvqTokens + k;
     const long long p0 = pg * kKvqTokens;
     if (p0 >= end) return false;
-    j.t0 = (int)max(0LL, past - p0);
+    j.t0 = (int)max(0LL, past - p0);  // t1 where there are no rows
     j.t1 = (int)min((long long)kKvqTokens, end - p0);
-    if (j.t1 <= j.t0) return false;
     j.row0 = c0 + p0 - past;
-    j.page = a.page_table[(size_t)r * a.max_pages + pg];
-    if (j.page < 0 || j.page >= a.num_pages) {
-        if (report) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
-        return false;
-    }
+    j.entry = (size_t)r * a.max_pages + pg;
     return true;
+}
+
+// Whether a job's page is one.
+__device__ __forceinline__ bool page_ok(const PagesArgs &a, int page) {
+    if (page >= 0 && page < a.num_pages) return true;
+    if (threadIdx.x == 0) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
+    return false;
+}
+
+// The CTA's job, found by its first warp.
+__device__ __forceinline__ bool cta_job(const PagesArgs &a, Job &j) {
+    __shared__ Job shared;
+    if (threadIdx.x < 32) {
+        Job own = {0, 0, 0, 0};
+        find_job(a, blockIdx.x, own, threadIdx.x == 0);
+        if (threadIdx.x == 0) shared = own;
+    }
+    __syncthreads();
+    j = shared;
+    return j.t1 > j.t0;
 }
 
 // cu_seqlens as a whole, checked once a call.
@@ -133,117 +149,144 @@ __device__ __forceinline__ void reduce_half(uint32_t *x, int lane, int o) {
 }
 
 // Codes of 2 N values in the low 8 N bits: rint((x - m) r) by adding
-// 1.5 * 2^23 (kvq_code), whose bits a multiply-add chain shifts together.
+// 1.5 * 2^23 (kvq_code), whose bits, 0x4b400000 + n, a multiply-add chain
+// shifts together; what the constants add up to is taken off in advance.
 template <int N>
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[N], float m, float r) {
+    constexpr uint32_t kOffset = 0x4b400000u * (N == 4 ? 0x11111111u : 0x1111u);
     uint32_t code = 0;
 #pragma unroll
     for (int i = N - 1; i >= 0; --i) {
-        // (a packed multiply and add would be joined, and the product has to be rounded by itself)
-        const float2 d = fsub2(make_float2(bf16lo(w[i]), bf16hi(w[i])), make_float2(m, m));
-        const float2 y = make_float2(__fadd_rn(__fmul_rn(d.x, r), 12582912.0f), __fadd_rn(__fmul_rn(d.y, r), 12582912.0f));
-        code = code * 16u + (__float_as_uint(y.y) - 0x4b400000u);
-        code = code * 16u + (__float_as_uint(y.x) - 0x4b400000u);
+        // the product is rounded by itself: the sums are not packed, or the two would be joined
+        const float2 d = fmul2(fsub2(make_float2(bf16lo(w[i]), bf16hi(w[i])), make_float2(m, m)), make_float2(r, r));
+        code = code * 16u + __float_as_uint(__fadd_rn(d.y, 12582912.0f));
+        code = code * 16u + __float_as_uint(__fadd_rn(d.x, 12582912.0f));
     }
-    return isnan(r) ? 0u : code;
+    return code - kOffset;
 }
 
-__global__ void __launch_bounds__(256) kvq_write_kernel(const __grid_constant__ PagesArgs a) {
-    if (!a.early) wait_dependency();
-    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Job j;
-    const bool work = find_job(a, blockIdx.x, j, threadIdx.x == 0);
-    check_segments(a);
-    if (a.early) wait_dependency();
-    if (!work) return;
+// The K rows of a job: tokens r and r + 8, dims [32 g + 8 c, + 8) of each
+// group.  Slots without a row read a neighbour's, and write nothing.  The
+// reduction over a group's lanes ends with each lane holding two groups of
+// one token, whose parameters it computes, writes, and leaves in `params`
+// (m and 1 / s of two groups, by token and group pair) for the others.
+__device__ __forceinline__ void write_k(const PagesArgs &a, const Job &j, int h, int lane, float4 *params) {
     const int r = lane >> 2, c = lane & 3;
-
-    // K: tokens r and r + 8, dims [32 g + 8 c, + 8).  V: tokens 8 u + 2 c + e, dims [32 g + 4 r, + 4).
+    const auto in = [&](int t) { return t >= j.t0 && t < j.t1; };
+    const uint16_t *row = a.k_in + j.row0 * a.ldk + h * kKvqDim + 8 * c;
+    const int id = a.page_table[j.entry];  // on its way together with the rows
     uint4 k[2][4];
-    uint2 v[4][4];  // [2 u + e][g]
-    bool k_in[2], v_in[4];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-        const int t = r + 8 * y;
-        k_in[y] = t >= j.t0 && t < j.t1;
-        const uint16_t *p = a.k_in + (j.row0 + t) * a.ldk + h * kKvqDim + 8 * c;
+        const uint16_t *p = row + (long long)min(max(r + 8 * y, j.t0), j.t1 - 1) * a.ldk;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) k[y][g] = k_in[y] ? *reinterpret_cast<const uint4 *>(p + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
+        for (int g = 0; g < 4; ++g) k[y][g] = *reinterpret_cast<const uint4 *>(p + 32 * g);
     }
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-        const int t = 8 * (y >> 1) + 2 * c + (y & 1);
-        v_in[y] = t >= j.t0 && t < j.t1;
-        const uint16_t *p = a.v_in + (j.row0 + t) * a.ldv + h * kKvqDim + 4 * r;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) v[y][g] = v_in[y] ? *reinterpret_cast<const uint2 *>(p + 32 * g) : make_uint2(0u, 0u);
-    }
-    uint8_t *kp = a.k_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
-    uint8_t *vp = a.v_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
-
-    // Ranges: the reductions over a group's lanes end with each lane holding two groups of one token, whose parameters
-    // it computes, writes, and gives to the others.
-    uint32_t kr[8], vr[16];
+    if (!page_ok(a, id)) return;
+    uint8_t *page = a.k_pages + ((size_t)id * a.hkv + h) * kKvqHeadBytes;
+    uint32_t range[8];
 #pragma unroll
     for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const uint4 w = k[y][g];
-            kr[4 * y + g] = range_of(max2(max2(w.x, w.y), max2(w.z, w.w)), min2(min2(w.x, w.y), min2(w.z, w.w)));
+            range[4 * y + g] = range_of(max2(max2(w.x, w.y), max2(w.z, w.w)), min2(min2(w.x, w.y), min2(w.z, w.w)));
         }
-    reduce_half<4>(kr, lane, 1);  // token r + 8 (c & 1)
-    reduce_half<2>(kr, lane, 2);  // groups 2 (c >> 1), + 1
-    // order [e][u][g], so that each step halves it
+    reduce_half<4>(range, lane, 1);  // token r + 8 (c & 1)
+    reduce_half<2>(range, lane, 2);  // groups 2 (c >> 1), + 1
+    const KvqGroup ga = group_of(range[0]), gb = group_of(range[1]);
+    const int own = r + 8 * (c & 1);
+    if (in(own)) *reinterpret_cast<uint2 *>(page + kvq_param_offset(own, 2 * (c >> 1))) = make_uint2(ga.sm, gb.sm);
+    params[2 * own + (c >> 1)] = make_float4(ga.m, ga.r, gb.m, gb.r);
+    const bool nan = __any_sync(0xffffffffu, isnan(ga.r) || isnan(gb.r));
+    __syncwarp();
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int t = r + 8 * y;
+        uint32_t code[4];
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            const float4 p = params[2 * t + g / 2];
+            const uint32_t w0[4] = {k[y][g].x, k[y][g].y, k[y][g].z, k[y][g].w};
+            const uint32_t w1[4] = {k[y][g + 1].x, k[y][g + 1].y, k[y][g + 1].z, k[y][g + 1].w};
+            code[g] = codes_of<4>(w0, p.x, p.y);
+            code[g + 1] = codes_of<4>(w1, p.z, p.w);
+            if (nan) code[g] = isnan(p.y) ? 0u : code[g], code[g + 1] = isnan(p.w) ? 0u : code[g + 1];
+        }
+        if (in(t)) *reinterpret_cast<uint4 *>(page + t * 64 + c * 16) = make_uint4(code[0], code[1], code[2], code[3]);
+    }
+}
+
+// The V rows of a job: tokens 8 u + 2 c + e, dims [32 g + 4 r, + 4).
+__device__ __forceinline__ void write_v(const PagesArgs &a, const Job &j, int h, int lane, float4 *params) {
+    const int r = lane >> 2, c = lane & 3;
+    const auto in = [&](int t) { return t >= j.t0 && t < j.t1; };
+    const uint16_t *row = a.v_in + j.row0 * a.ldv + h * kKvqDim + 4 * r;
+    const int id = a.page_table[j.entry];
+    uint2 v[4][4];  // [2 u + e][g]
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const uint16_t *p = row + (long long)min(max(8 * (y >> 1) + 2 * c + (y & 1), j.t0), j.t1 - 1) * a.ldv;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) v[y][g] = *reinterpret_cast<const uint2 *>(p + 32 * g);
+    }
+    if (!page_ok(a, id)) return;
+    uint8_t *page = a.v_pages + ((size_t)id * a.hkv + h) * kKvqHeadBytes;
+    uint32_t range[16];  // [e][u][g], so that each step halves it
 #pragma unroll
     for (int y = 0; y < 4; ++y)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) vr[8 * (y & 1) + 4 * (y >> 1) + g] = range_of(max2(v[y][g].x, v[y][g].y), min2(v[y][g].x, v[y][g].y));
-    reduce_half<8>(vr, lane, 4);
-    reduce_half<4>(vr, lane, 8);
-    reduce_half<2>(vr, lane, 16);
-    const KvqGroup ka = group_of(kr[0]), kb = group_of(kr[1]), va = group_of(vr[0]), vb = group_of(vr[1]);
-    {
-        const int t = r + 8 * (c & 1);
-        if (t >= j.t0 && t < j.t1) *reinterpret_cast<uint2 *>(kp + kvq_param_offset(t, 2 * (c >> 1))) = make_uint2(ka.sm, kb.sm);
-        const int s = 8 * (r >> 1 & 1) + 2 * c + (r & 1);
-        if (s >= j.t0 && s < j.t1) *reinterpret_cast<uint2 *>(vp + kvq_param_offset(s, 2 * (r >> 2))) = make_uint2(va.sm, vb.sm);
-    }
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        uint32_t code[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int from = (lane & ~3) | y | (g >> 1) << 1;
-            const float m = __shfl_sync(0xffffffffu, g & 1 ? kb.m : ka.m, from), rr = __shfl_sync(0xffffffffu, g & 1 ? kb.r : ka.r, from);
-            const uint32_t w[4] = {k[y][g].x, k[y][g].y, k[y][g].z, k[y][g].w};
-            code[g] = codes_of<4>(w, m, rr);
-        }
-        if (k_in[y]) *reinterpret_cast<uint4 *>(kp + (r + 8 * y) * 64 + c * 16) = make_uint4(code[0], code[1], code[2], code[3]);
-    }
+        for (int g = 0; g < 4; ++g) range[8 * (y & 1) + 4 * (y >> 1) + g] = range_of(max2(v[y][g].x, v[y][g].y), min2(v[y][g].x, v[y][g].y));
+    reduce_half<8>(range, lane, 4);
+    reduce_half<4>(range, lane, 8);
+    reduce_half<2>(range, lane, 16);
+    const KvqGroup ga = group_of(range[0]), gb = group_of(range[1]);
+    const int own = 8 * (r >> 1 & 1) + 2 * c + (r & 1);
+    if (in(own)) *reinterpret_cast<uint2 *>(page + kvq_param_offset(own, 2 * (r >> 2))) = make_uint2(ga.sm, gb.sm);
+    params[2 * own + (r >> 2)] = make_float4(ga.m, ga.r, gb.m, gb.r);
+    const bool nan = __any_sync(0xffffffffu, isnan(ga.r) || isnan(gb.r));
+    __syncwarp();
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         uint32_t code[2][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int from = c | (e | u << 1 | (g >> 1) << 2) << 2;
-                const float m = __shfl_sync(0xffffffffu, g & 1 ? vb.m : va.m, from), rr = __shfl_sync(0xffffffffu, g & 1 ? vb.r : va.r, from);
-                const uint32_t w[2] = {v[2 * u + e][g].x, v[2 * u + e][g].y};
-                code[e][g] = codes_of<2>(w, m, rr);
+            for (int g = 0; g < 4; g += 2) {
+                const float4 p = params[2 * (8 * u + 2 * c + e) + g / 2];
+                const uint32_t w0[2] = {v[2 * u + e][g].x, v[2 * u + e][g].y}, w1[2] = {v[2 * u + e][g + 1].x, v[2 * u + e][g + 1].y};
+                code[e][g] = codes_of<2>(w0, p.x, p.y);
+                code[e][g + 1] = codes_of<2>(w1, p.z, p.w);
+                if (nan) code[e][g] = isnan(p.y) ? 0u : code[e][g], code[e][g + 1] = isnan(p.w) ? 0u : code[e][g + 1];
             }
-        uint8_t *dst = vp + u * 512 + lane * 16;
-        if (v_in[2 * u] && v_in[2 * u + 1]) {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(code[0][0] | code[1][0] << 16, code[0][1] | code[1][1] << 16,
-                                                         code[0][2] | code[1][2] << 16, code[0][3] | code[1][3] << 16);
+        uint8_t *dst = page + u * 512 + lane * 16;
+        const int t = 8 * u + 2 * c;
+        if (in(t) && in(t + 1)) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(code[0][0], code[1][0], 0x5410), __byte_perm(code[0][1], code[1][1], 0x5410),
+                                                         __byte_perm(code[0][2], code[1][2], 0x5410), __byte_perm(code[0][3], code[1][3], 0x5410));
         } else {  // the neighbour's codes stay as they are
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (v_in[2 * u + e])
+                if (in(t + e))
 #pragma unroll
                     for (int g = 0; g < 4; ++g) *reinterpret_cast<uint16_t *>(dst + g * 4 + e * 2) = (uint16_t)code[e][g];
         }
     }
+}
+
+// blockIdx.y 0 writes K, 1 writes V: with half the rows a warp holds, twice
+// the warps fit, and their loads cover one another's arithmetic.
+__global__ void __launch_bounds__(256, 4) kvq_write_kernel(const __grid_constant__ PagesArgs a) {
+    __shared__ float4 params[8][32];
+    if (!a.early) wait_dependency();
+    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Job j;
+    const bool work = cta_job(a, j);
+    if (blockIdx.y == 0) check_segments(a);
+    if (a.early) wait_dependency();
+    if (!work) return;
+    if (blockIdx.y == 0) write_k(a, j, h, lane, params[h]);
+    else write_v(a, j, h, lane, params[h]);
 }
 
 // Two values (codes in nibble positions 0 and 4 of `pair`) of a group.
@@ -253,13 +296,15 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(const __grid_constant__ P
     if (!a.early) wait_dependency();
     const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Job j;
-    const bool work = find_job(a, blockIdx.x, j, threadIdx.x == 0);
+    const bool work = cta_job(a, j);
     check_segments(a);
     if (a.early) wait_dependency();
     if (!work) return;
+    const int id = a.page_table[j.entry];
+    if (!page_ok(a, id)) return;
     const int r = lane >> 2, c = lane & 3;
-    const uint8_t *kp = a.k_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
-    const uint8_t *vp = a.v_pages + ((size_t)j.page * a.hkv + h) * kKvqHeadBytes;
+    const uint8_t *kp = a.k_pages + ((size_t)id * a.hkv + h) * kKvqHeadBytes;
+    const uint8_t *vp = a.v_pages + ((size_t)id * a.hkv + h) * kKvqHeadBytes;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int t = r + 8 * half;
@@ -305,7 +350,7 @@ cudaError_t launch_pages(const PagesArgs &a, bool write, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.total / kKvqTokens + 2 * a.batch));
+    cfg.gridDim = dim3((unsigned)(a.total / kKvqTokens + 2 * a.batch), write ? 2u : 1u);
     cfg.blockDim = dim3((unsigned)(a.hkv * 32));
     cfg.stream = stream;
     cfg.attrs = attr;
