@@ -619,62 +619,26 @@ def qa_window_plan(token_counts, window_tokens: int = 0) -> np.ndarray:
     return cu[: n + 1]
 
 
-_KVQ_HEAD_BYTES = 1280  # one KV head of a 4-bit page (qa_kvq_page_bytes)
-
-# The calls below are made once a layer and token, and a small one's kernel is
-# done in a few microseconds: their host side avoids what costs as much
-# (torch.cuda.current_stream 2.9 us, a stream context 2.3 us, setting a
-# struct's fields one by one 2 us, measured on a Grace core) and checks each
-# tensor with five attribute reads (0.4 us).
+_BINDING = None
 
 
-def _ptr(t, name, dtype, ndim, device, allow_host=False):
-    """Device address of a contiguous tensor on the current device."""
-    try:
-        if t.dtype is dtype and t.dim() == ndim and t.get_device() == device and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch.Tensor") from None
-    _dev(t, name, dtype, ndim, allow_host)
-    if t.is_cuda:
-        raise ValueError(f"tensors must be on the current CUDA device ({device}), {name} is on {t.device}")
-    return t.data_ptr()  # page-locked host memory
+def _fast():
+    """The compiled binding (csrc/binding.cpp): it needs torch, so it is loaded
+    with the first call of the functions below."""
+    global _BINDING
+    if _BINDING is None:
+        _torch()
+        from . import _binding
+
+        _BINDING = _binding
+    return _BINDING
 
 
-def _rows(t, name, device):
-    """Device address and row stride of a bf16 [rows, heads, head_dim] tensor
-    whose rows are packed inside, but may lie apart (views into a fused
-    projection's rows)."""
-    try:
-        n, h, d = t.shape
-        s = t.stride()
-        if t.dtype is _torch().bfloat16 and t.get_device() == device and (
-                n == 0 or (s[2] == 1 and (h == 1 or s[1] == d))):
-            return t.data_ptr(), (s[0] if n > 1 else 0)
-    except (AttributeError, ValueError):
-        if not isinstance(t, _torch().Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor") from None
-    _ptr(t if t.is_contiguous() else t.contiguous(), name, _torch().bfloat16, 3, device)
-    raise ValueError(f"{name} must be contiguous within each row")
-
-
-def _raw_stream(stream, device):
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(device)
-    if stream.device_index != device:
-        raise ValueError(f"stream must be of the current CUDA device ({device}), got {stream.device}")
-    return stream.cuda_stream
-
-
-def _made(stream, *shape, dtype, device, zeros=False):
-    """A buffer made inside a call: allocated (and zeroed, and later reused)
-    in the order of the stream that the call runs on."""
-    torch = _torch()
-    make = torch.zeros if zeros else torch.empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
+def _done(fn, result):
+    """A compiled call's outputs; it gives the status where it was refused."""
+    if type(result) is int:
+        _check(fn, result)
+    return result
 
 
 def qa_rope_axes(sections, *, interleaved=False, head_dim=128):
@@ -688,32 +652,6 @@ def qa_rope_axes(sections, *, interleaved=False, head_dim=128):
     return out
 
 
-def _rope(positions, rows, q_gain, k_gain, pair_axis, head_dim, rms_eps, rope_theta, device):
-    """The qa_rope struct (it keeps pair_axis's bytes alive)."""
-    torch = _torch()
-    qg = kg = pos = None
-    axes = 1
-    if q_gain is not None:
-        qg = _ptr(q_gain, "q_gain", torch.float32, 1, device)
-        if q_gain.shape[0] != head_dim:
-            raise ValueError("gains must be [head_dim]")
-    if k_gain is not None:
-        kg = _ptr(k_gain, "k_gain", torch.float32, 1, device)
-        if k_gain.shape[0] != head_dim:
-            raise ValueError("gains must be [head_dim]")
-    if positions is not None:
-        ndim = positions.dim()
-        if ndim not in (1, 2) or positions.shape[-1] != rows:
-            raise ValueError(f"positions must be [rows] or [n_axes, rows] with {rows} rows")
-        axes = positions.shape[0] if ndim == 2 else 1
-        pos = _ptr(positions, "positions", torch.int32, ndim, device)
-    if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
-        if len(pair_axis) != head_dim // 2:
-            raise ValueError("pair_axis must have head_dim / 2 entries")
-    return qa_rope(qg, kg, rms_eps, rope_theta, axes, pos, pair_axis)
-
-
 def qa_rope_rows(q, k, positions, q_out=None, k_out=None, *, q_gain=None, k_gain=None, rms_eps=1e-6, rope_theta=1e6,
                  pair_axis=None, stream=None, debug_checks=False, stable_metadata=False):
     """Per-head RMSNorm (gains float32 [D], both or neither) and NEOX rotation
@@ -722,39 +660,8 @@ def qa_rope_rows(q, k, positions, q_out=None, k_out=None, *, q_gain=None, k_gain
     (qa_rope_axes; default axis 0).  q, k and the outputs may be views whose
     rows lie apart; q_out=q and k_out=k work in place.  Returns (q_out,
     k_out)."""
-    torch = _torch()
-    device = torch.cuda.current_device()
-    T, Hq, D = q.shape
-    if positions is None:
-        raise ValueError("positions are required")
-    qp, ldq = _rows(q, "q", device)
-    if q_out is None:
-        q_out = _made(stream, T, Hq, D, dtype=torch.bfloat16, device=q.device)
-        qop, ldqo = q_out.data_ptr(), 0
-    else:
-        qop, ldqo = _rows(q_out, "q_out", device)
-        if q_out.shape != q.shape:
-            raise ValueError("outputs must have their inputs' shapes")
-    Hkv, kp, ldk, kop, ldko = 1, None, 0, None, 0
-    if k is not None:
-        Tk, Hkv, Dk = k.shape
-        if Tk != T or Dk != D:
-            raise ValueError("inconsistent rope shapes")
-        kp, ldk = _rows(k, "k", device)
-        if k_out is None:
-            k_out = _made(stream, T, Hkv, D, dtype=torch.bfloat16, device=k.device)
-            kop = k_out.data_ptr()
-        else:
-            kop, ldko = _rows(k_out, "k_out", device)
-            if k_out.shape != k.shape:
-                raise ValueError("outputs must have their inputs' shapes")
-    r = _rope(positions, T, q_gain, k_gain, pair_axis, D, rms_eps, rope_theta, device)
-    p = qa_attn_params(QA_ABI_VERSION, Hq, Hkv, D, 16, 0, 0, 0.0, _raw_stream(stream, device), None, 0,
-                       1 if debug_checks else 0, stable_metadata)
-    st = _lib.qa_rope_rows(qp, ldq, kp, ldk, T, qop, ldqo, kop, ldko, ctypes.byref(r), ctypes.byref(p))
-    if st:
-        _check("qa_rope_rows", st)
-    return q_out, k_out
+    return _done("qa_rope_rows", _fast().rope_rows(q, k, positions, q_out, k_out, q_gain, k_gain, rms_eps, rope_theta,
+                                                   pair_axis, stream, debug_checks, stable_metadata))
 
 
 def qa_kvq_page_bytes(n_kv_heads=8) -> int:
@@ -767,46 +674,14 @@ def qa_kvq_page_bytes(n_kv_heads=8) -> int:
     return int(n)
 
 
-def _kvq_pools(k_pages, v_pages, device):
-    """Addresses of the pools, their page count and KV heads."""
-    u8 = _torch().uint8
-    P, width = k_pages.shape if k_pages.dim() == 2 else (0, 0)
-    if width == 0 or width % _KVQ_HEAD_BYTES or k_pages.shape != v_pages.shape:
-        raise ValueError("4-bit pools must be uint8 [num_pages, qa_kvq_page_bytes(n_kv_heads)], of one shape")
-    return _ptr(k_pages, "k_pages", u8, 2, device), _ptr(v_pages, "v_pages", u8, 2, device), P, width // _KVQ_HEAD_BYTES
-
-
-def _kvq_rows_args(cu_seqlens, n_past, page_table, device):
-    """Addresses of the row metadata, the batch and the table's width."""
-    i32 = _torch().int32
-    cu = _ptr(cu_seqlens, "cu_seqlens", i32, 1, device)
-    table = _ptr(page_table, "page_table", i32, 2, device)
-    past = None if n_past is None else _ptr(n_past, "n_past", i32, 1, device)
-    B, width = page_table.shape
-    if cu_seqlens.shape[0] != B + 1 or (past is not None and n_past.shape[0] != B):
-        raise ValueError("page_table must be [batch, max_pages], cu_seqlens [batch + 1] and n_past [batch]")
-    return cu, past, table, B, width
-
-
 def qa_kvq_write(k, v, cu_seqlens, page_table, k_pages, v_pages, *, n_past=None, stream=None, debug_checks=False,
                  stable_metadata=False):
     """Quantises packed K/V rows into 4-bit pages.  k/v bf16 [T,Hkv,128] (rows
     may lie apart); cu_seqlens int32 [B+1]; page_table int32 [B,max_pages];
     pools uint8 [P, qa_kvq_page_bytes(Hkv)], written in place; n_past int32
     [B]: request r's row i is position n_past[r] + i (default 0)."""
-    device = _torch().cuda.current_device()
-    T, Hkv, D = k.shape
-    kpp, vpp, P, H = _kvq_pools(k_pages, v_pages, device)
-    if v.shape != k.shape or H != Hkv:
-        raise ValueError("inconsistent 4-bit write shapes")
-    kp, ldk = _rows(k, "k", device)
-    vp, ldv = _rows(v, "v", device)
-    cu, past, table, B, width = _kvq_rows_args(cu_seqlens, n_past, page_table, device)
-    p = qa_attn_params(QA_ABI_VERSION, Hkv, Hkv, D, 16, P, width, 0.0, _raw_stream(stream, device), None, 0,
-                       1 if debug_checks else 0, stable_metadata)
-    st = _lib.qa_kvq_write(kp, ldk, vp, ldv, cu, past, B, T, table, kpp, vpp, ctypes.byref(p))
-    if st:
-        _check("qa_kvq_write", st)
+    _done("qa_kvq_write", _fast().kvq_write(k, v, cu_seqlens, page_table, k_pages, v_pages, n_past, stream, debug_checks,
+                                            stable_metadata))
 
 
 def qa_kvq_read(k_pages, v_pages, page_table, cu_seqlens, total_tokens, k_out=None, v_out=None, *, n_past=None,
@@ -814,24 +689,8 @@ def qa_kvq_read(k_pages, v_pages, page_table, cu_seqlens, total_tokens, k_out=No
     """Reads cached rows back as bf16 [total_tokens,Hkv,128]: row
     cu_seqlens[r] + i is position n_past[r] + i of request r (arguments as
     for qa_kvq_write).  Returns (k_out, v_out)."""
-    torch = _torch()
-    device = torch.cuda.current_device()
-    T = int(total_tokens)
-    kpp, vpp, P, Hkv = _kvq_pools(k_pages, v_pages, device)
-    cu, past, table, B, width = _kvq_rows_args(cu_seqlens, n_past, page_table, device)
-    if k_out is None:
-        k_out = _made(stream, T, Hkv, 128, dtype=torch.bfloat16, device=k_pages.device)
-    if v_out is None:
-        v_out = _made(stream, T, Hkv, 128, dtype=torch.bfloat16, device=k_pages.device)
-    kp, vp = _ptr(k_out, "k_out", torch.bfloat16, 3, device), _ptr(v_out, "v_out", torch.bfloat16, 3, device)
-    if k_out.shape != (T, Hkv, 128) or v_out.shape != (T, Hkv, 128):
-        raise ValueError("k_out and v_out must be [total_tokens, n_kv_heads, 128]")
-    p = qa_attn_params(QA_ABI_VERSION, Hkv, Hkv, 128, 16, P, width, 0.0, _raw_stream(stream, device), None, 0,
-                       1 if debug_checks else 0, stable_metadata)
-    st = _lib.qa_kvq_read(kpp, vpp, table, cu, past, B, T, kp, vp, ctypes.byref(p))
-    if st:
-        _check("qa_kvq_read", st)
-    return k_out, v_out
+    return _done("qa_kvq_read", _fast().kvq_read(k_pages, v_pages, page_table, cu_seqlens, total_tokens, k_out, v_out,
+                                                 n_past, stream, debug_checks, stable_metadata))
 
 
 def qa_kvq_decode_workspace_size(batch: int, max_seq_len: int, *, n_q_heads=16, n_kv_heads=8, head_dim=128,
@@ -846,32 +705,6 @@ def qa_kvq_decode_workspace_size(batch: int, max_seq_len: int, *, n_q_heads=16, 
     return int(n)
 
 
-def _kvq_decode_args(shape, k_pages, v_pages, page_table, seq_lens, out, workspace, scale, stream, debug_checks,
-                     stable_metadata, device):
-    """What the 4-bit decode calls share: output, addresses and params."""
-    torch = _torch()
-    B, Hq, D = shape
-    kpp, vpp, P, Hkv = _kvq_pools(k_pages, v_pages, device)
-    table = _ptr(page_table, "page_table", torch.int32, 2, device, True)
-    lens = _ptr(seq_lens, "seq_lens", torch.int32, 1, device, True)
-    if page_table.shape[0] != B or seq_lens.shape[0] != B:
-        raise ValueError("inconsistent decode shapes")
-    width = page_table.shape[1]
-    if out is None:
-        out = _made(stream, B, Hq, D, dtype=torch.bfloat16, device=k_pages.device)
-    op = _ptr(out, "out", torch.bfloat16, 3, device, True)
-    if out.shape != shape:
-        raise ValueError("out must have q's shape")
-    if workspace is None:
-        nbytes = qa_kvq_decode_workspace_size(B, 0, n_q_heads=Hq, n_kv_heads=Hkv, head_dim=D, num_pages=P,
-                                              max_pages_per_seq=width)
-        workspace = _made(stream, nbytes, dtype=torch.uint8, device=k_pages.device, zeros=True)
-    ws = _ptr(workspace, "workspace", workspace.dtype, workspace.dim(), device)
-    p = qa_attn_params(QA_ABI_VERSION, Hq, Hkv, D, 16, P, width, scale, _raw_stream(stream, device), ws, workspace.nbytes,
-                       1 if debug_checks else 0, stable_metadata)
-    return out, op, kpp, vpp, Hkv, table, lens, p, workspace
-
-
 def qa_kvq_decode_attn(q, k_pages, v_pages, page_table, seq_lens, out=None, *, workspace=None, scale=0.0, stream=None,
                        debug_checks=False, stable_metadata=False):
     """Paged GQA decode over 4-bit pools (uint8 [P, qa_kvq_page_bytes(Hkv)]).
@@ -880,16 +713,8 @@ def qa_kvq_decode_attn(q, k_pages, v_pages, page_table, seq_lens, out=None, *, w
     workspace: zero-filled uint8, qa_kvq_decode_workspace_size(B, ...) bytes
     (allocated here if omitted), reusable across calls on one stream.
     stable_metadata as for qa_decode_attn.  Returns out bf16 [B,Hq,128]."""
-    torch = _torch()
-    device = torch.cuda.current_device()
-    qp = _ptr(q, "q", torch.bfloat16, 3, device, True)
-    out, op, kpp, vpp, _, table, lens, p, _ws = _kvq_decode_args(
-        q.shape, k_pages, v_pages, page_table, seq_lens, out, workspace, scale, stream, debug_checks, stable_metadata,
-        device)
-    st = _lib.qa_kvq_decode_attn(qp, kpp, vpp, table, lens, q.shape[0], op, ctypes.byref(p))
-    if st:
-        _check("qa_kvq_decode_attn", st)
-    return out
+    return _done("qa_kvq_decode_attn", _fast().kvq_decode_attn(
+        q, k_pages, v_pages, page_table, seq_lens, out, workspace, scale, stream, debug_checks, stable_metadata))
 
 
 def qa_kvq_decode_step(q, k, v, q_gain, k_gain, page_table, seq_lens, k_pages, v_pages, out=None, *, positions=None,
@@ -902,23 +727,9 @@ def qa_kvq_decode_step(q, k, v, q_gain, k_gain, page_table, seq_lens, k_pages, v
     gains float32 [128]; positions int32 [B] or [n_axes,B] (default
     seq_lens - 1) with pair_axis as for qa_rope_rows; the rest as for
     qa_kvq_decode_attn.  Returns out bf16 [B,Hq,128]."""
-    device = _torch().cuda.current_device()
-    B, Hq, D = q.shape
-    qp, ldq = _rows(q, "q", device)
-    kp, ldk = _rows(k, "k", device)
-    vp, ldv = _rows(v, "v", device)
-    out, op, kpp, vpp, Hkv, table, lens, p, _ws = _kvq_decode_args(
-        q.shape, k_pages, v_pages, page_table, seq_lens, out, workspace, scale, stream, debug_checks, stable_metadata,
-        device)
-    if k.shape != (B, Hkv, D) or v.shape != (B, Hkv, D):
-        raise ValueError("inconsistent decode-step shapes")
-    if ldk != ldv:
-        raise ValueError("k and v must have the same row stride")
-    r = _rope(positions, B, q_gain, k_gain, pair_axis, D, rms_eps, rope_theta, device)
-    st = _lib.qa_kvq_decode_step(qp, ldq, kp, vp, ldk, ctypes.byref(r), kpp, vpp, table, lens, B, op, ctypes.byref(p))
-    if st:
-        _check("qa_kvq_decode_step", st)
-    return out
+    return _done("qa_kvq_decode_step", _fast().kvq_decode_step(
+        q, k_pages, v_pages, page_table, seq_lens, out, workspace, scale, stream, debug_checks, stable_metadata, k, v,
+        q_gain, k_gain, positions, pair_axis, rms_eps, rope_theta))
 
 
 def qa_check_bounded_wait(limit_us=20000, stream=None) -> None:

@@ -1,12 +1,15 @@
 """Builds libqa.so in-tree with nvcc for sm_103a (no cmake, no torch
 extension machinery): every .cu under csrc/ is compiled in parallel, then
-linked into one shared library that exports only the qa_* symbols."""
+linked into one shared library that exports only the qa_* symbols.  Beside
+it the Python binding of the calls whose host time counts (csrc/binding.cpp,
+against torch's headers) becomes the module _binding."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqa.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler",
@@ -40,7 +44,8 @@ def _deps_mtime() -> float:
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     """Compile and link libqa.so; returns its path.  Skips work when the
     library is newer than every source and header."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime() and not extra_flags:
+    newest = _deps_mtime()
+    if not force and not extra_flags and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     exe = nvcc()
@@ -58,14 +63,47 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
 
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "--exclude-libs,ALL"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
+
+
+def _torch_dir() -> str:
+    import importlib.util
+
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _run(cmd: list[str], what: str) -> None:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def _compile_binding() -> str:
+    torch_dir, obj = _torch_dir(), os.path.join(BUILD, "binding.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+          "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
+          "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+          "-isystem", os.path.join(cuda, "include"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj],
+         "g++ on binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    torch_lib, tmp = os.path.join(_torch_dir(), "lib"), BINDING + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lqa", "-Wl,-rpath,$ORIGIN", "-L", torch_lib, "-ltorch_python",
+          "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "link of _binding.so")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

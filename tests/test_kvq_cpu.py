@@ -156,25 +156,30 @@ def test_sizes():
         qa.qa_kvq_decode_workspace_size(1, 17)  # past max_pages_per_seq * 16
 
 
-def test_python_checks(monkeypatch):
+def test_python_checks():
     torch = pytest.importorskip("torch")
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     rows = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
     pool = torch.zeros(3, 10240, dtype=torch.uint8)
     cu, table = torch.zeros(2, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32)
-    for bad, error, word in ((rows, ValueError, "CUDA"), (rows.float(), (TypeError, ValueError), ""), (rows[0], ValueError, ""),
-                             (rows.transpose(1, 2), ValueError, ""), (rows.numpy, TypeError, "torch.Tensor")):
-        with pytest.raises(error, match=word):
-            qa._rows(bad, "k", 0)
-    for bad, error, word in ((pool, ValueError, "CUDA"), (None, TypeError, "torch.Tensor")):
-        with pytest.raises(error, match=word):
-            qa._ptr(bad, "k_pages", torch.uint8, 2, 0)
+    lens = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="k_pages must be a CUDA tensor"):
+        qa.qa_kvq_write(rows, rows, cu, table, pool, pool)
     with pytest.raises(ValueError, match="4-bit pools"):
         qa.qa_kvq_write(rows, rows, cu, table, pool[:, :100], pool[:, :100])
+    with pytest.raises(ValueError, match="4-bit pools"):
+        qa.qa_kvq_read(pool, pool[:2], table, cu, 4)
+    with pytest.raises(TypeError, match="v must be a torch.Tensor"):
+        qa.qa_kvq_write(rows, None, cu, table, pool, pool)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        qa.qa_rope_rows(rows, rows, lens)
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        qa.qa_rope_rows(np.zeros((4, 8, 128)), rows, lens)
     with pytest.raises(ValueError, match="CUDA"):
-        qa.qa_kvq_read(pool, pool, table, cu, 4)
-    with pytest.raises(ValueError, match="required"):
-        qa.qa_rope_rows(rows, rows, None)
+        qa.qa_kvq_decode_attn(rows, pool, pool, table, lens)
+    with pytest.raises(ValueError, match="3 dims"):
+        qa.qa_kvq_decode_attn(rows[0], pool, pool, table, lens)
+    with pytest.raises(ValueError, match="CUDA"):
+        qa.qa_kvq_decode_step(rows, rows, rows, lens, lens, table, lens, pool, pool)
 
 
 def test_code_places_cover_every_nibble_once():

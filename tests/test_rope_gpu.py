@@ -93,6 +93,34 @@ def test_no_rows():
     assert qo.shape == (0, 16, 128)
 
 
+def test_refused_tensors():
+    q, k, pos, gains, axis = inputs(6, 8, 16, 8, 128, 2, True)
+    dq, dk, dpos, g = to_dev(q), to_dev(k), to_dev(pos), [to_dev(v) for v in gains]
+    for bad, error, word in (
+            (dict(q=dq.float()), TypeError, "bfloat16"), (dict(q=dq[0]), ValueError, "dims"),
+            (dict(q=dq.transpose(1, 2)), ValueError, "contiguous"), (dict(q=dq[:1].expand(8, 16, 128)), ValueError, "overlap"),
+            (dict(q=dq.cpu()), ValueError, "CUDA"), (dict(k=dk[:7]), ValueError, "shapes"), (dict(k=dk[:, :, :64].contiguous()), ValueError, "shapes"),
+            (dict(positions=dpos[:, :5]), ValueError, "positions"), (dict(positions=dpos.long()), TypeError, "int32"),
+            (dict(positions=dpos.T), ValueError, "positions"), (dict(positions=None), ValueError, "required"),
+            (dict(q_out=torch.empty_like(dq[:7])), ValueError, "shapes"), (dict(q_gain=g[0][:64]), ValueError, "head_dim"),
+            (dict(q_gain=None), qa.QAError, "both"), (dict(pair_axis=[0] * 63), ValueError, "pair_axis"),
+            (dict(pair_axis=[-1] * 64), ValueError, "pair_axis"), (dict(pair_axis=3), TypeError, "pair_axis"),
+            (dict(pair_axis=[2] * 64), qa.QAError, "pair_axis"), (dict(stream=5), TypeError, "stream"),
+            (dict(rope_theta="x"), TypeError, "rope_theta"), (dict(rms_eps=0.0), qa.QAError, "rms_eps"),
+            (dict(stable_metadata=3), qa.QAError, "stable_metadata")):
+        args = dict(dict(q=dq, k=dk, positions=dpos, q_gain=g[0], k_gain=g[1], pair_axis=axis), **bad)
+        with pytest.raises(error, match=word):
+            qa.qa_rope_rows(**args)
+
+
+def test_kinds_of_pair_axis():
+    q, k, pos, gains, axis = inputs(7, 8, 16, 8, 128, 3, True)
+    dq, dpos = to_dev(q), to_dev(pos)
+    outs = [qa.qa_rope_rows(dq, None, dpos, pair_axis=x)[0] for x in (axis, axis.tolist(), bytes(axis), axis.astype(np.int64), tuple(axis))]
+    for o in outs:
+        check(o, q, pos, None, axis, "q")
+
+
 def test_graph_and_other_stream():
     q, k, pos, gains, axis = inputs(5, 65, 16, 8, 128, 3, True)
     dq, dk, dpos, g = to_dev(q), to_dev(k), to_dev(pos), [to_dev(v) for v in gains]
