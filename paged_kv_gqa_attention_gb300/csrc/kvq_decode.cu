@@ -18,10 +18,10 @@
 //
 // A request that lies in one worker's range is finished there.  Otherwise
 // each worker writes an fp32 partial (maximum, sum, outputs) to slot v + b
-// (worker v, request b: unique, since both ranges are ordered), and after its
-// last page counts itself in the arrival counter of (request, KV head); the
-// warp that arrives last merges the partials and resets the counter, so
-// nothing waits on another CTA.  Many partials are merged in two levels.
+// (worker v, request b: unique, since both ranges are ordered) and counts
+// itself in the arrival counter of (request, KV head); the warp that arrives
+// last merges the partials and resets the counter, so nothing waits on
+// another CTA.  Many partials are merged in two levels.
 //
 // Arithmetic of one page and KV head (16 tokens, mma.m16n8k16 on fp16, fp32
 // sums).  A masked nibble of both halves of a code word is a pair of fp16
@@ -362,20 +362,19 @@ __device__ __forceinline__ void write_out(uint16_t *out, int hq, int b, int g, i
     }
 }
 
-// Counts this warp in on up to two counters, after all its writes; lane 0's
-// fences order the partials before the counts and the reads after them.
-// Returns (to every lane) how many were there before.
-__device__ __forceinline__ int2 count_in(int *c0, int *c1, int lane) {
+// Counts this warp in after all its writes; lane 0's fences order the
+// partials before the count and the reads after it.  Returns (to every lane)
+// how many were there before.
+__device__ __forceinline__ int count_in(int *counter, int lane) {
     __syncwarp();
-    int2 prev = make_int2(0, 0);
+    int before = 0;
     if (lane == 0) {
         asm volatile("fence.acq_rel.gpu;" ::: "memory");
-        if (c0) asm volatile("atom.add.relaxed.gpu.s32 %0, [%1], 1;" : "=r"(prev.x) : "l"(c0) : "memory");
-        if (c1) asm volatile("atom.add.relaxed.gpu.s32 %0, [%1], 1;" : "=r"(prev.y) : "l"(c1) : "memory");
+        asm volatile("atom.add.relaxed.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
         asm volatile("fence.acq_rel.gpu;" ::: "memory");
     }
     __syncwarp();
-    return make_int2(__shfl_sync(0xffffffffu, prev.x, 0), __shfl_sync(0xffffffffu, prev.y, 0));
+    return __shfl_sync(0xffffffffu, before, 0);
 }
 
 template <int GROUP, bool APPEND>
@@ -499,7 +498,32 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     };
     int b = request_of(prefix, a.batch, lo);
     load_ahead(b);
-    int split_b[2] = {-1, -1};  // requests whose partials this worker wrote: its first and last at most
+    // A split request's partial: written, counted in, and merged with the others where this warp is the last.  A request
+    // over more workers than two rounds of loads take is merged by groups of neighbouring workers first, each by the
+    // last of its group.  The first of a worker's two split requests is settled before its other pages: left to the
+    // end, one warp merged both, which the whole grid waited for.
+    auto settle = [&](int b, const float (&acc)[GROUP][4], const float (&ref)[GROUP], const float (&sum)[GROUP]) {
+        write_partial<GROUP>(a.part_acc, a.part_ml, (size_t)v + b, hq, g, lane, acc, ref, sum);
+        const int v0 = split.of_page(prefix[b]), v1 = split.of_page(prefix[b + 1] - 1);
+        int *counter = a.arrivals + (size_t)b * kMaxHkv + g;
+        float z[GROUP][4], m[GROUP], l[GROUP];
+        if (v1 - v0 >= 2 * kMergeMost) {
+            const int q = v / kMergeMost, q0 = v0 / kMergeMost, q1 = v1 / kMergeMost;
+            const int a0 = max(v0, q * kMergeMost), a1 = min(v1, q * kMergeMost + kMergeMost - 1);
+            int *group = a.group_arrivals + (size_t)(q + b) * kMaxHkv + g;
+            if (count_in(group, lane) != a1 - a0) return;
+            merge<GROUP>(a.part_acc, a.part_ml, (size_t)a0 + b, a1 - a0 + 1, hq, g, lane, z, m, l);
+            if (lane == 0) *group = 0;
+            write_partial<GROUP>(a.group_acc, a.group_ml, (size_t)q + b, hq, g, lane, z, m, l);
+            if (count_in(counter, lane) != q1 - q0) return;
+            merge<GROUP>(a.group_acc, a.group_ml, (size_t)q0 + b, q1 - q0 + 1, hq, g, lane, z, m, l);
+        } else {
+            if (count_in(counter, lane) != v1 - v0) return;
+            merge<GROUP>(a.part_acc, a.part_ml, (size_t)v0 + b, v1 - v0 + 1, hq, g, lane, z, m, l);
+        }
+        write_out<GROUP>(a.out, hq, b, g, lane, z, l);
+        if (lane == 0) *counter = 0;
+    };
     uint32_t at = ring_base;    // stage of the next page
 
     for (int x = lo; x < hi;) {
@@ -759,52 +783,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         if (j0 == 0 && j1 == p1 - p0) {
             write_out<GROUP>(a.out, hq, b, g, lane, acc, l_sum);
         } else {
-            write_partial<GROUP>(a.part_acc, a.part_ml, (size_t)v + b, hq, g, lane, acc, ref_of, l_sum);
-            split_b[x == lo ? 0 : 1] = b;
+            settle(b, acc, ref_of, l_sum);
         }
         x = p0 + j1;
         b = b_next;
-    }
-
-    // Split requests: count in, and merge where this warp is the last.  A request over more workers than two rounds of
-    // loads take is merged by groups of neighbouring workers first, each by the last of its group.
-    if (split_b[0] < 0 && split_b[1] < 0) return;
-    int v0[2], v1[2];
-    int *counter[2];
-    bool grouped[2];
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-        const int bb = max(split_b[d], 0);
-        v0[d] = split.of_page(prefix[bb]), v1[d] = split.of_page(prefix[bb + 1] - 1);
-        grouped[d] = v1[d] - v0[d] >= 2 * kMergeMost;
-        counter[d] = split_b[d] < 0 ? nullptr
-                     : grouped[d]   ? a.group_arrivals + (size_t)(v / kMergeMost + bb) * kMaxHkv + g
-                                    : a.arrivals + (size_t)bb * kMaxHkv + g;
-    }
-    const int2 prev = count_in(counter[0], counter[1], lane);
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-        const int bb = split_b[d];
-        if (bb < 0) continue;
-        int before = d == 0 ? prev.x : prev.y;
-        float z[GROUP][4], m[GROUP], ls[GROUP];
-        if (grouped[d]) {
-            const int q = v / kMergeMost;
-            const int a0 = max(v0[d], q * kMergeMost), a1 = min(v1[d], q * kMergeMost + kMergeMost - 1);
-            if (before != a1 - a0) continue;
-            merge<GROUP>(a.part_acc, a.part_ml, (size_t)a0 + bb, a1 - a0 + 1, hq, g, lane, z, m, ls);
-            if (lane == 0) *counter[d] = 0;
-            write_partial<GROUP>(a.group_acc, a.group_ml, (size_t)q + bb, hq, g, lane, z, m, ls);
-            before = count_in(a.arrivals + (size_t)bb * kMaxHkv + g, nullptr, lane).x;
-            const int q0 = v0[d] / kMergeMost, q1 = v1[d] / kMergeMost;
-            if (before != q1 - q0) continue;
-            merge<GROUP>(a.group_acc, a.group_ml, (size_t)q0 + bb, q1 - q0 + 1, hq, g, lane, z, m, ls);
-        } else {
-            if (before != v1[d] - v0[d]) continue;
-            merge<GROUP>(a.part_acc, a.part_ml, (size_t)v0[d] + bb, v1[d] - v0[d] + 1, hq, g, lane, z, m, ls);
-        }
-        write_out<GROUP>(a.out, hq, bb, g, lane, z, ls);
-        if (lane == 0) a.arrivals[(size_t)bb * kMaxHkv + g] = 0;
     }
 }
 
