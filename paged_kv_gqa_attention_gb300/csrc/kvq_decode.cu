@@ -129,7 +129,7 @@ constexpr int kMaxStages = 5;         // pages in a warp's ring
 // A stage: K codes, V codes, K parameters, V parameters, so that lane l copies
 // 16 bytes at 16 l of each 512.
 constexpr int kStageBytes = 2 * kKvqHeadBytes;
-constexpr int kMinPages = 2;          // of a worker
+constexpr int kMinPages = 3;          // of a worker
 constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group
 constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 384 SMs
 constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;
@@ -362,19 +362,19 @@ __device__ __forceinline__ void write_out(uint16_t *out, int hq, int b, int g, i
     }
 }
 
-// Counts this warp in after all its writes; lane 0's fences order the
-// partials before the count and the reads after it.  Returns (to every lane)
-// how many were there before.
-__device__ __forceinline__ int count_in(int *counter, int lane) {
+// Counts this warp in after all its writes, and tells (every lane) whether it
+// was the last of `others` + 1.  Lane 0's fences order the partials before
+// the count and, in the last one, the reads after it.
+__device__ __forceinline__ bool last_in(int *counter, int others, int lane) {
     __syncwarp();
     int before = 0;
     if (lane == 0) {
         asm volatile("fence.acq_rel.gpu;" ::: "memory");
         asm volatile("atom.add.relaxed.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
-        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+        if (before == others) asm volatile("fence.acq_rel.gpu;" ::: "memory");
     }
     __syncwarp();
-    return __shfl_sync(0xffffffffu, before, 0);
+    return __shfl_sync(0xffffffffu, before, 0) == others;
 }
 
 template <int GROUP, bool APPEND>
@@ -511,14 +511,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             const int q = v / kMergeMost, q0 = v0 / kMergeMost, q1 = v1 / kMergeMost;
             const int a0 = max(v0, q * kMergeMost), a1 = min(v1, q * kMergeMost + kMergeMost - 1);
             int *group = a.group_arrivals + (size_t)(q + b) * kMaxHkv + g;
-            if (count_in(group, lane) != a1 - a0) return;
+            if (!last_in(group, a1 - a0, lane)) return;
             merge<GROUP>(a.part_acc, a.part_ml, (size_t)a0 + b, a1 - a0 + 1, hq, g, lane, z, m, l);
             if (lane == 0) *group = 0;
             write_partial<GROUP>(a.group_acc, a.group_ml, (size_t)q + b, hq, g, lane, z, m, l);
-            if (count_in(counter, lane) != q1 - q0) return;
+            if (!last_in(counter, q1 - q0, lane)) return;
             merge<GROUP>(a.group_acc, a.group_ml, (size_t)q0 + b, q1 - q0 + 1, hq, g, lane, z, m, l);
         } else {
-            if (count_in(counter, lane) != v1 - v0) return;
+            if (!last_in(counter, v1 - v0, lane)) return;
             merge<GROUP>(a.part_acc, a.part_ml, (size_t)v0 + b, v1 - v0 + 1, hq, g, lane, z, m, l);
         }
         write_out<GROUP>(a.out, hq, b, g, lane, z, l);

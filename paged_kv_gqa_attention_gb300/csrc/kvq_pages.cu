@@ -44,9 +44,10 @@ struct Job {
 // The job of page id `id`; false when there is none.  Warp-collective.
 __device__ __forceinline__ bool find_job(const PagesArgs &a, int id, Job &j, bool report) {
     const int lane = threadIdx.x & 31;
-    // the last request with S(r) <= id: 32 candidates a round
+    // the last request with S(r) <= id: of the last 32 candidates each lane reads all there is to know of one, so that
+    // a small batch costs one round trip to memory (larger ones one more for each factor of 32)
     int lo = 0, n = a.batch;  // the answer is in [lo, lo + n), or there is none
-    while (n > 1) {
+    while (n > 32) {
         const int step = (n + 31) / 32;
         const int r = lo + lane * step;
         const bool le = lane * step < n && a.cu[r] / 16 + 2 * r <= id;
@@ -55,13 +56,17 @@ __device__ __forceinline__ bool find_job(const PagesArgs &a, int id, Job &j, boo
         n = min(step, n - last * step);
         lo += last * step;
     }
-    const int r = lo;
-    const int c0 = a.cu[r], c1 = a.cu[r + 1];
+    const int mine = min(lo + lane, lo + n - 1);
+    const int c0_own = a.cu[mine], c1_own = a.cu[mine + 1], past_own = a.n_past ? a.n_past[mine] : 0;
+    const unsigned votes = __ballot_sync(0xffffffffu, lane < n && c0_own / 16 + 2 * mine <= id);
+    const int from = votes ? 31 - __clz(votes) : 0;
+    const int r = lo + from;
+    const int c0 = __shfl_sync(0xffffffffu, c0_own, from), c1 = __shfl_sync(0xffffffffu, c1_own, from);
+    const int past = __shfl_sync(0xffffffffu, past_own, from);
     if (c0 < 0 || c1 > a.total || c1 < c0) {
         if (report) atomicOr(&g_status, QA_DEVICE_BAD_SEGMENTS);
         return false;
     }
-    const int past = a.n_past ? a.n_past[r] : 0;
     const long long cap = (long long)a.max_pages * kKvqTokens;
     if (past < 0 || past > cap) {
         if (report) atomicOr(&g_status, QA_DEVICE_BAD_LENGTH);
