@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         }
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) qw[i] = q_next[i];
-        uint32_t new_k = 0, new_v = 0, new_ksm = 0, new_vsm = 0;
+        uint32_t new_codes = 0, new_sm = 0;  // the new row: codes of K (low half) and V, parameters of K (even lanes) and V
         if (APPEND) {
             // angles of pairs 4 (l mod 16) + u: each of two lanes takes half of them
             float cs[4], sn[4];
@@ -561,8 +561,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
 #pragma unroll
             for (int i = 0; i < GROUP; ++i) qw[i] = norm_rope(qw[i], gq, a.eps, cs, sn, lane);
             if (has_new) {
-                new_k = quantise_row(norm_rope(kw, gk, a.eps, cs, sn, lane), lane, new_ksm);
-                new_v = quantise_row(vw, lane, new_vsm);
+                uint32_t k_sm, v_sm;
+                new_codes = quantise_row(norm_rope(kw, gk, a.eps, cs, sn, lane), lane, k_sm);
+                new_codes |= quantise_row(vw, lane, v_sm) << 16;
+                new_sm = lane & 1 ? v_sm : k_sm;
             }
         }
         int b_next = b + 1;
@@ -633,16 +635,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                 const int t = nt[NP - 1] - 1, page = a.page_table[(size_t)b * a.max_pages + j1 - 1];
                 uint8_t *stage = ring + (ks[NP - 1] - ring_base);
                 const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-                *reinterpret_cast<uint16_t *>(stage + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
-                *reinterpret_cast<uint16_t *>(stage + kAtV + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
-                *reinterpret_cast<uint16_t *>(a.k_pages + off + kvq_k_quad_offset(t, lane)) = (uint16_t)new_k;
-                *reinterpret_cast<uint16_t *>(a.v_pages + off + kvq_v_quad_offset(t, lane)) = (uint16_t)new_v;
-                if ((lane & 7) == 0) {
+                *reinterpret_cast<uint16_t *>(stage + kvq_k_quad_offset(t, lane)) = (uint16_t)new_codes;
+                *reinterpret_cast<uint16_t *>(stage + kAtV + kvq_v_quad_offset(t, lane)) = (uint16_t)(new_codes >> 16);
+                *reinterpret_cast<uint16_t *>(a.k_pages + off + kvq_k_quad_offset(t, lane)) = (uint16_t)new_codes;
+                *reinterpret_cast<uint16_t *>(a.v_pages + off + kvq_v_quad_offset(t, lane)) = (uint16_t)(new_codes >> 16);
+                if ((lane & 6) == 0) {  // two lanes of each group
                     const int p = kvq_param_offset(t, lane >> 3);
-                    *reinterpret_cast<uint32_t *>(stage + kAtKp - kKvqCodeBytes + p) = new_ksm;
-                    *reinterpret_cast<uint32_t *>(stage + kAtVp - kKvqCodeBytes + p) = new_vsm;
-                    *reinterpret_cast<uint32_t *>(a.k_pages + off + p) = new_ksm;
-                    *reinterpret_cast<uint32_t *>(a.v_pages + off + p) = new_vsm;
+                    *reinterpret_cast<uint32_t *>(stage + (lane & 1 ? kAtVp : kAtKp) - kKvqCodeBytes + p) = new_sm;
+                    *reinterpret_cast<uint32_t *>((lane & 1 ? a.v_pages : a.k_pages) + off + p) = new_sm;
                 }
                 __syncwarp();
             }
