@@ -259,6 +259,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same from zero.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 8 x 8 transpose of 16-bit values over the warp: lane 4 i + j gives and gets
 // row i, columns 2j and 2j + 1.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -430,49 +438,63 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     const int v = split.worker(blockIdx.x, gridDim.x, e, S);
     const bool working = e < S && v < split.nv;
     const int lo = working ? split.lo(v) : 0, hi = working ? split.lo(v + 1) : 0;
-    // page ids, 32 at a time, one a lane: bad ones are -1
+    // page ids, 32 at a time, one a lane: bad ones are -1.  Windows overlap by two, so that a pair of pages lies in one.
+    bool any_bad = false;
     auto find = [&](int x) -> int {
-        if (x >= hi) return -1;
-        const int b = request_of(prefix, a.batch, x);
-        const int page = a.page_table[(size_t)b * a.max_pages + (x - prefix[b])];
-        return page < 0 || page >= a.num_pages ? -1 : page;
+        int page = -1;
+        bool bad = false;
+        if (x < hi) {
+            const int b = request_of(prefix, a.batch, x);
+            page = a.page_table[(size_t)b * a.max_pages + (x - prefix[b])];
+            if (page < 0 || page >= a.num_pages) {
+                atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
+                page = -1;
+                bad = true;
+            }
+        }
+        any_bad |= __any_sync(0xffffffffu, bad);
+        return page;
     };
     int ids = find(lo + lane), ids_next = -1;
-    int issued = 0;                  // pages copied so far
-    uint32_t fill = ring_base;       // the stage that the next one goes to
-    uint32_t bad = 0;                // bit i: the page copied i pages before the last one is bad
+    int to_issue = hi - lo, in_window = 0;  // pages to copy yet, and the next one's place among the ids
     const uint64_t policy = policy_evict_first();
     const size_t head_at = (size_t)g * kKvqHeadBytes + 16 * lane;
     const uint8_t *k_src = a.k_pages + head_at, *v_src = a.v_pages + head_at;
     const uint8_t *p_src = (lane < 16 ? a.k_pages : a.v_pages - 256) + kKvqCodeBytes + head_at;
     const uint32_t page_stride = (uint32_t)a.hkv * kKvqHeadBytes;
-    auto issue = [&]() {  // the next page, or nothing after the last: a group either way
-        if (issued < hi - lo) {
-            const int page = __shfl_sync(0xffffffffu, ids, issued & 31);
-            bad = bad << 1 | (page < 0);
-            if (page >= 0) {
-                const size_t off = (size_t)(uint32_t)page * page_stride;
-                const uint32_t dst = fill + 16 * lane;
-                copy16(dst, k_src + off, policy);
-                copy16(dst + 512, k_src + off + 512, policy);
-                copy16(dst + kAtV, v_src + off, policy);
-                copy16(dst + kAtV + 512, v_src + off + 512, policy);
-                copy16(dst + kAtKp, p_src + off, policy);
-            } else if (lane == 0) {
-                atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
+    auto issue = [&](auto np, const uint32_t *stage) {  // the next NP pages, or nothing after the last: groups either way
+        constexpr int NP = decltype(np)::value;
+#pragma unroll
+        for (int y = 0; y < NP; ++y) {
+            if (y < to_issue) {
+                const int page = __shfl_sync(0xffffffffu, ids, in_window + y);
+                if (page >= 0) {
+                    const size_t off = (size_t)(uint32_t)page * page_stride;
+                    const uint32_t dst = stage[y] + 16 * lane;
+                    copy16(dst, k_src + off, policy);
+                    copy16(dst + 512, k_src + off + 512, policy);
+                    copy16(dst + kAtV, v_src + off, policy);
+                    copy16(dst + kAtV + 512, v_src + off + 512, policy);
+                    copy16(dst + kAtKp, p_src + off, policy);
+                }
             }
-            ++issued;
-            if ((issued & 31) == 16) ids_next = find(lo + issued + 16 + lane);
-            if ((issued & 31) == 0) ids = ids_next;
-            fill = fill + kStageBytes == ring_end ? ring_base : fill + kStageBytes;
+            copy_commit();
         }
-        copy_commit();
+        to_issue -= NP, in_window += NP;
+        if (in_window >= 30) {
+            ids = ids_next, in_window -= 30;
+        } else if (in_window >= 16 && in_window < 16 + NP) {
+            ids_next = find(hi - to_issue - in_window + 30 + lane);
+        }
     };
 
     // With the pools vouched for (early_pools) the rings fill before the wait.
     if (a.early && !a.early_pools) grid_wait();
 #pragma unroll 1
-    for (int s = 0; s < n_stages; ++s) issue();
+    for (int s = 0; s < n_stages; ++s) {
+        const uint32_t stage[1] = {ring_base + s * kStageBytes};
+        issue(std::integral_constant<int, 1>(), stage);
+    }
     if (a.early && a.early_pools) grid_wait();
 
     if (blockIdx.x == 0) {  // zero rows of requests with nothing to attend over
@@ -622,29 +644,29 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             if (n_stages == kMaxStages) copy_wait<kMaxStages - NP>(); else copy_wait<kMaxStages - 1 - NP>();
             __syncwarp();
             uint32_t ks[NP], vp0[NP], vp1[NP];
-            int nt[NP];
 #pragma unroll
             for (int y = 0; y < NP; ++y) {
                 ks[y] = at;
                 at = at + kStageBytes == ring_end ? ring_base : at + kStageBytes;
-                nt[y] = min(kPS, seq_len - (j + y) * kPS);
-                if (bad && (bad >> (issued - 1 - (x - lo + j + y - j0)) & 1)) nt[y] = 0;  // nothing of a bad page
             }
-            if (has_new && j + NP == j1 && nt[NP - 1] > 0) {
+            const int left = seq_len - j * kPS;  // tokens from the first of these pages on
+            if (has_new && j + NP == j1) {
                 // the new token's row, in the stage and in the pools
-                const int t = nt[NP - 1] - 1, page = a.page_table[(size_t)b * a.max_pages + j1 - 1];
-                uint8_t *stage = ring + (ks[NP - 1] - ring_base);
-                const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
-                *reinterpret_cast<uint16_t *>(stage + kvq_k_quad_offset(t, lane)) = (uint16_t)new_codes;
-                *reinterpret_cast<uint16_t *>(stage + kAtV + kvq_v_quad_offset(t, lane)) = (uint16_t)(new_codes >> 16);
-                *reinterpret_cast<uint16_t *>(a.k_pages + off + kvq_k_quad_offset(t, lane)) = (uint16_t)new_codes;
-                *reinterpret_cast<uint16_t *>(a.v_pages + off + kvq_v_quad_offset(t, lane)) = (uint16_t)(new_codes >> 16);
-                if ((lane & 6) == 0) {  // two lanes of each group
-                    const int p = kvq_param_offset(t, lane >> 3);
-                    *reinterpret_cast<uint32_t *>(stage + (lane & 1 ? kAtVp : kAtKp) - kKvqCodeBytes + p) = new_sm;
-                    *reinterpret_cast<uint32_t *>((lane & 1 ? a.v_pages : a.k_pages) + off + p) = new_sm;
+                const int t = left - 1 - (NP - 1) * kPS, page = a.page_table[(size_t)b * a.max_pages + j1 - 1];
+                if (page >= 0 && page < a.num_pages) {
+                    uint8_t *stage = ring + (ks[NP - 1] - ring_base);
+                    const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
+                    *reinterpret_cast<uint16_t *>(stage + kvq_k_quad_offset(t, lane)) = (uint16_t)new_codes;
+                    *reinterpret_cast<uint16_t *>(stage + kAtV + kvq_v_quad_offset(t, lane)) = (uint16_t)(new_codes >> 16);
+                    *reinterpret_cast<uint16_t *>(a.k_pages + off + kvq_k_quad_offset(t, lane)) = (uint16_t)new_codes;
+                    *reinterpret_cast<uint16_t *>(a.v_pages + off + kvq_v_quad_offset(t, lane)) = (uint16_t)(new_codes >> 16);
+                    if ((lane & 6) == 0) {  // two lanes of each group
+                        const int p = kvq_param_offset(t, lane >> 3);
+                        *reinterpret_cast<uint32_t *>(stage + (lane & 1 ? kAtVp : kAtKp) - kKvqCodeBytes + p) = new_sm;
+                        *reinterpret_cast<uint32_t *>((lane & 1 ? a.v_pages : a.k_pages) + off + p) = new_sm;
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             // scores: A rows are tokens r and r + 8
             float d[NP][4];
@@ -656,11 +678,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                 kp0[y] = lds32(ks[y] + kAtKp + 4 * lane), kp1[y] = lds32(ks[y] + kAtKp + 128 + 4 * lane);
                 vp0[y] = lds32(ks[y] + kAtVp + 4 * lane), vp1[y] = lds32(ks[y] + kAtVp + 128 + 4 * lane);
                 const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-                d[y][0] = d[y][1] = d[y][2] = d[y][3] = 0.f;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    mma16816(d[y], code_pair<0>(w0[u]), code_pair<0>(w1[u]), code_pair<1>(w0[u]), code_pair<1>(w1[u]), bq[4 * u],
-                             bq[4 * u + 1]);
+                    if (u == 0)
+                        mma16816_first(d[y], code_pair<0>(w0[u]), code_pair<0>(w1[u]), code_pair<1>(w0[u]), code_pair<1>(w1[u]), bq[0], bq[1]);
+                    else
+                        mma16816(d[y], code_pair<0>(w0[u]), code_pair<0>(w1[u]), code_pair<1>(w0[u]), code_pair<1>(w1[u]), bq[4 * u],
+                                 bq[4 * u + 1]);
                     mma16816(d[y], code_pair<2>(w0[u]), code_pair<2>(w1[u]), code_pair<3>(w0[u]), code_pair<3>(w1[u]),
                              bq[4 * u + 2], bq[4 * u + 3]);
                 }
@@ -682,15 +706,25 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                         if (GROUP == 2) w.y = __shfl_xor_sync(0xffffffffu, sc[y][h].y, z);
                         sc[y][h] = fadd2(sc[y][h], w);
                     }
+            bool none = false;
+            if (left < NP * kPS || any_bad) {  // slots past the length, and bad pages, may hold anything
+                int tokens = 0;
+#pragma unroll
+                for (int y = 0; y < NP; ++y) {
+                    int nt = min(kPS, left - y * kPS);
+                    if (any_bad) {
+                        const int page = a.page_table[(size_t)b * a.max_pages + j + y];
+                        if (page < 0 || page >= a.num_pages) nt = 0;
+                    }
+                    if (r >= nt) sc[y][0] = make_float2(-INFINITY, -INFINITY), vp0[y] = 0u;
+                    if (r + 8 >= nt) sc[y][1] = make_float2(-INFINITY, -INFINITY), vp1[y] = 0u;
+                    tokens += nt;
+                }
+                none = tokens == 0;  // there may be no reference yet
+            }
             float t_max = 0.f;
 #pragma unroll
-            for (int y = 0; y < NP; ++y) {
-                if (nt[y] < kPS) {  // slots past the length may hold anything
-                    if (r >= nt[y]) sc[y][0] = make_float2(-INFINITY, -INFINITY), vp0[y] = 0u;
-                    if (r + 8 >= nt[y]) sc[y][1] = make_float2(-INFINITY, -INFINITY), vp1[y] = 0u;
-                }
-                t_max = fmax3(t_max, fabsf(bf16lo(vp0[y])), fabsf(bf16lo(vp1[y])));
-            }
+            for (int y = 0; y < NP; ++y) t_max = fmax3(t_max, fabsf(bf16lo(vp0[y])), fabsf(bf16lo(vp1[y])));
             float2 e[NP][2];  // log2 p
             float e_max = -INFINITY;
 #pragma unroll
@@ -733,7 +767,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             }
 #pragma unroll
             for (int y = 0; y < NP; ++y) {
-                if ((nt[0] | nt[NP - 1]) == 0) continue;  // bad pages alone: there may be no reference yet
+                if (none) continue;
                 // p s of (token, group c) for both heads, rounded to fp16, transposed into B
                 const float u0 = bf16lo(vp0[y]) * s_up, u1 = bf16lo(vp1[y]) * s_up, c0 = bf16hi(vp0[y]), c1 = bf16hi(vp1[y]);
                 float2 pa = make_float2(exp2_approx(e[y][0].x), 0.f), pb = make_float2(exp2_approx(e[y][1].x), 0.f);
@@ -753,8 +787,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                 }
             }
             __syncwarp();
-#pragma unroll
-            for (int y = 0; y < NP; ++y) issue();
+            issue(np, ks);  // into the stages that these pages leave
         };
         int j = j0;
         for (; j + 2 <= j1; j += 2) pages(std::integral_constant<int, 2>(), j);
