@@ -154,7 +154,7 @@ QA_API qa_status qa_rope_rows(const void *q, long long ldq, const void *k, long 
         return reject(QA_STATUS_INVALID_PARAMS, "%s: head_dim %d unsupported (64 or 128)", fn, p->head_dim);
     if (p->n_q_heads < 1 || p->n_q_heads > 1024 || (k && (p->n_kv_heads < 1 || p->n_kv_heads > 1024)))
         return reject(QA_STATUS_INVALID_PARAMS, "%s: head counts (%d, %d) outside [1, 1024]", fn, p->n_q_heads, p->n_kv_heads);
-    if (rows < 0) return reject(QA_STATUS_INVALID_PARAMS, "%s: rows %d < 0", fn, rows);
+    if (rows < 0 || rows > 1 << 30) return reject(QA_STATUS_INVALID_PARAMS, "%s: rows %d outside [0, 2^30]", fn, rows);
     if (rows == 0) return QA_STATUS_OK;  // empty tensors have no address
     if (!q || !q_out || (k && !k_out)) return invalid(fn, "NULL tensor pointer");
     if ((st = check_rope(fn, rope, p->head_dim, false, true)) != QA_STATUS_OK) return st;

@@ -36,10 +36,10 @@
 // applied in fp32.  B of the outputs holds p_jh s_jg, rounded to fp16 (2^-12
 // of itself), and the columns of a dim's own group are kept; sum p m is kept
 // in fp32 beside it.  fp16's range: p is taken against a reference maximum
-// that is moved when a score passes it by 2^4, s against a power of two that
-// is moved when an s passes 16 times its target, so p s stays below 2^14 and
-// is a normal number down to 2^-20 of the largest; most pages move neither,
-// which leaves the reductions over tokens out.
+// that is moved when a score passes it by 2^4, s against a power of two for
+// each group that is moved when an s passes 16 times its target, so p s stays
+// below 2^14 and is a normal number down to 2^-20 of the group's largest;
+// most pages move neither, which leaves the reductions over tokens out.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -134,7 +134,7 @@ constexpr int kMergeMost = 8;         // partials merged in one round of loads, 
 constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 384 SMs
 constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;
 constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
-constexpr float kScaleMost = 1024.f;  // s times its factor: set to [32, 64), moved past this
+constexpr float kScaleMost = 1024.f;  // s times its group's factor: set to [32, 64), moved past this
 
 // Workers of a CTA.
 __host__ __device__ constexpr int workers_of(int hkv) { return kWarps / hkv; }
@@ -598,28 +598,23 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         // own group, as the pairs (j, j + 4) that the code words hold, a 16th of the pairs whose codes come 16-fold
         uint32_t bq[16];
         float2 qsum = make_float2(0.f, 0.f);  // softmax scale times the sum of the heads' q over group c
-        float qback;                          // softmax scale times 2^24 / q's scale
+        float2 qback = qsum;                  // softmax scale times 2^24 / q's scale
         {
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < GROUP; ++i)
-                m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16lo(qw[i].x)), fabsf(bf16hi(qw[i].x))),
-                                   fmaxf(fabsf(bf16lo(qw[i].y)), fabsf(bf16hi(qw[i].y)))));
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const int k = max(min(14 - exponent_of(m), 126), -100);  // 126: q is zero or nearly; -100: it is past 2^114
-            const float up = pow2i(k);
-            qback = pow2i(24 - k) * a.scale_log2;
             float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const int src = 8 * (r >> 1) + 2 * c;
 #pragma unroll
             for (int i = 0; i < GROUP; ++i) {
                 const float x[4] = {bf16lo(qw[i].x), bf16hi(qw[i].x), bf16lo(qw[i].y), bf16hi(qw[i].y)};
+                float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
                 float s = (x[0] + x[1]) + (x[2] + x[3]);
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const int k = max(min(14 - exponent_of(m), 126), -100);  // 126: q is zero or nearly; -100: it is past 2^114
+                const float up = pow2i(k), back = pow2i(24 - k) * a.scale_log2;
                 s = __shfl_sync(0xffffffffu, s, 8 * c) * a.scale_log2;
-                if (i == 0) qsum.x = s; else qsum.y = s;
+                if (i == 0) qsum.x = s, qback.x = back; else qsum.y = s, qback.y = back;
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     const float y0 = __shfl_sync(0xffffffffu, x[d] * up, src), y1 = __shfl_sync(0xffffffffu, x[d] * up, src + 1);
@@ -692,9 +687,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             // s and m of (token, group c), then the sum over groups (the 4 lanes of a token)
 #pragma unroll
             for (int y = 0; y < NP; ++y) {
-                const float s0 = bf16lo(kp0[y]) * qback, m0 = bf16hi(kp0[y]), s1 = bf16lo(kp1[y]) * qback, m1 = bf16hi(kp1[y]);
-                sc[y][0] = ffma2(make_float2(d[y][0], d[y][1]), make_float2(s0, s0), fmul2(make_float2(m0, m0), qsum));
-                sc[y][1] = ffma2(make_float2(d[y][2], d[y][3]), make_float2(s1, s1), fmul2(make_float2(m1, m1), qsum));
+                const float s0 = bf16lo(kp0[y]), m0 = bf16hi(kp0[y]), s1 = bf16lo(kp1[y]), m1 = bf16hi(kp1[y]);
+                sc[y][0] = ffma2(fmul2(make_float2(d[y][0], d[y][1]), qback), make_float2(s0, s0), fmul2(make_float2(m0, m0), qsum));
+                sc[y][1] = ffma2(fmul2(make_float2(d[y][2], d[y][3]), qback), make_float2(s1, s1), fmul2(make_float2(m1, m1), qsum));
             }
 #pragma unroll
             for (int z = 1; z < 4; z <<= 1)
@@ -736,7 +731,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                 }
             if (__any_sync(0xffffffffu, e_max > kRefSlack || t_max > s_most)) {  // move the references to the maxima so far
 #pragma unroll
-                for (int z = 1; z < 32; z <<= 1) t_max = fmaxf(t_max, __shfl_xor_sync(0xffffffffu, t_max, z));
+                for (int z = 4; z < 32; z <<= 1) t_max = fmaxf(t_max, __shfl_xor_sync(0xffffffffu, t_max, z));
                 float alpha[2] = {1.f, 1.f};
                 if (t_max > s_most) {
                     const float up = pow2i(min(5 - exponent_of(t_max), 126));

@@ -108,6 +108,81 @@ def test_nan_in_a_cached_group_stays_in_its_head():
     check(attn(w), w, "mended")
 
 
+def test_heads_and_groups_of_very_different_size():
+    # query heads 2^40 apart in size over one KV head, and an infinite one: each by itself
+    w = setup(36, (300, 41))
+    q = wl.bf16_to_f64(w["q"]).astype(np.float32)
+    q[:, 1::4] *= np.float32(2.0 ** -40)
+    q[:, 2::4] *= np.float32(2.0 ** 30)
+    w["q"] = wl.bf16_bits(q).reshape(q.shape)
+    g = f64(attn(w))
+    small = dict(w, q=w["q"][:, 0::2]), dict(w, q=w["q"][:, 1::2])
+    for i, part in enumerate(small):
+        ref, bound = _kvq.decode(wl.bf16_to_f64(part["q"]), w["k_pages"], w["v_pages"], w["table"], w["lens"])
+        keep = [h for h in range(8) if (2 * h + i) % 4 != 2]  # scores of 2^30: one token takes all, in any arithmetic
+        assert (np.abs(g[:, i::2] - ref)[:, keep] <= bound[:, keep]).all()
+    assert np.isfinite(g).all()
+    w = setup(37, (300, 41))
+    ref, bound = _kvq.decode(wl.bf16_to_f64(w["q"]), w["k_pages"], w["v_pages"], w["table"], w["lens"])
+    w["q"][0, 5, 77] = 0x7F80
+    g = f64(attn(w))
+    assert not np.isfinite(g[0, 5]).any()
+    g[0, 5], ref[0, 5] = 0, 0
+    assert (np.abs(g - ref) <= bound).all()
+    # value groups 2^90 apart in one head: each to its own accuracy
+    w = setup(38, (700, 30))
+    heads = w["v_pages"].reshape(-1, 8, 1280)
+    params = heads[:, :, 1024:].copy().view(np.uint16).reshape(-1, 8, 16, 4, 2)
+    scale = np.array([2.0 ** -60, 1.0, 2.0 ** 30, 2.0 ** -20], np.float32)[None, None, None, :, None]
+    heads[:, :, 1024:] = wl.bf16_bits((_kvq.f32(params) * scale).astype(np.float32)).reshape(params.shape).view(np.uint8).reshape(-1, 8, 256)
+    _kvq.poison_after(w["v_pages"], w["table"], w["lens"])
+    g = f64(attn(w))
+    ref, bound = _kvq.decode(wl.bf16_to_f64(w["q"]), w["k_pages"], w["v_pages"], w["table"], w["lens"])
+    assert (np.abs(g - ref) <= bound).all()
+    for grp in range(4):
+        sl = np.s_[:, :, 32 * grp:32 * grp + 32]
+        assert np.linalg.norm((g - ref)[sl]) <= 5e-3 * np.linalg.norm(ref[sl])
+
+
+def test_constant_groups():
+    # s = 0 in every value group: the output is the minimum's average; in every key group: all scores of a token equal m sum q
+    w = setup(39, (200, 3))
+    for n in ("k_pages", "v_pages"):
+        heads = w[n].reshape(-1, 8, 1280)
+        params = heads[:, :, 1024:].copy().view(np.uint16).reshape(-1, 8, 16, 4, 2)
+        params[..., 0] = 0
+        heads[:, :, 1024:] = params.view(np.uint8).reshape(-1, 8, 256)
+        _kvq.poison_after(w[n], w["table"], w["lens"])
+    check(attn(w), w, "constant groups")
+
+
+@pytest.mark.parametrize("batch", [2049, 4096])
+def test_largest_batches(batch):
+    rng = np.random.default_rng(batch)
+    w = setup(batch, rng.integers(0, 70, size=batch), 4, 2)
+    check(attn(w, debug_checks=True), w, f"batch {batch}")
+    s = step_setup(batch, rng.integers(1, 40, size=batch), 2, 1)
+    out, d = run_step(s, debug_checks=True)
+    got = {n: d[n].cpu().numpy() for n in ("k_pages", "v_pages")}
+    q, _ = _kvq.rope(wl.bf16_to_f64(s["q"]), (s["lens"] - 1)[None], s["q_gain"], None)
+    check(out, dict(s, **got), f"step of batch {batch}", q=wl.bf16_to_f64(wl.bf16_bits(q.astype(np.float32)).reshape(q.shape)))
+
+
+def test_more_pages_than_32_bit_products_serve():
+    # 4096 requests of 129 pages, 528384 in all, over three requests' worth of real pages
+    w = setup(40, (2064, 2050, 2049), 2, 1)
+    ref, bound = _kvq.decode(wl.bf16_to_f64(w["q"]), w["k_pages"], w["v_pages"], w["table"], w["lens"])
+    pick = np.arange(4096) % 3
+    big = dict(w, q=w["q"][pick], table=w["table"][pick], lens=w["lens"][pick])
+    g = f64(attn(big, debug_checks=True))
+    assert (np.abs(g - ref[pick]) <= bound[pick]).all()
+
+
+def test_no_tokens_at_all():
+    w = setup(41, (0, 0, 0))
+    assert not bits(attn(w, out=torch.full((3, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda"), debug_checks=True)).any()
+
+
 def test_bad_pages_and_lengths():
     w = setup(12, (100, 40, 50, 20), width=8)
     w["table"][0, 2] = -5
