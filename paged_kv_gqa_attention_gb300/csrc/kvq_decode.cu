@@ -85,7 +85,7 @@ struct KvqArgs {
 __device__ __forceinline__ uint2 norm_rope(uint2 w, float4 g, float eps, const float (&cs)[4], const float (&sn)[4], int lane) {
     const float x[4] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
     const float ss = warp_sum(x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3]);
-    const float r = 1.0f / sqrtf(ss * (1.0f / kD) + eps);
+    const float r = rsqrtf(fmaf(ss, 1.0f / kD, eps));
     const float y[4] = {x[0] * r * g.x, x[1] * r * g.y, x[2] * r * g.z, x[3] * r * g.w};
     float z[4];
 #pragma unroll
@@ -140,7 +140,7 @@ constexpr float kScaleMost = 1024.f;  // s times its group's factor: set to [32,
 __host__ __device__ constexpr int workers_of(int hkv) { return kWarps / hkv; }
 
 struct SmemLayout {
-    uint32_t stages, off_scan, off_freq, off_prefix, total;
+    uint32_t stages, off_scan, off_new, off_freq, off_prefix, total;
 };
 
 // Two CTAs share an SM's 227 KB; the prefix sums of a large batch cost one
@@ -151,6 +151,8 @@ __host__ __device__ inline SmemLayout smem_layout(int batch) {
     uint32_t o = s.stages * kStageBytes * kWarps;
     s.off_scan = o;  // warp sums of the prefix scan
     o += kWarps * 4;
+    s.off_new = o;  // the step's new row of each warp: codes and parameters
+    o += kWarps * 32 * 8;
     s.off_freq = o;  // rotation frequencies (hi, lo) and axes of the 64 pairs
     o += kD / 2 * 8 + kD / 2;
     s.off_prefix = o;
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     if (!a.early) grid_wait();
     if (threadIdx.x == 0) prefix[0] = 0;
     float2 *freq = reinterpret_cast<float2 *>(smem + L.off_freq);
+    uint2 *new_row = reinterpret_cast<uint2 *>(smem + L.off_new) + 32 * warp;
     uint8_t *axis = smem + L.off_freq + kD / 2 * 8;
     if (APPEND && threadIdx.x < kD / 2) {
         const float *f_hi = a.freq_hi, *f_lo = a.freq_lo;
@@ -488,6 +491,24 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         }
     };
 
+    // The first request's length, and (step) the angles that its position gives: metadata, read before the wait too.
+    int b = lo < hi ? request_of(prefix, a.batch, lo) : 0;
+    int seq_len = lo < hi ? a.seq_lens[b] : 0;
+    float cs[4], sn[4];
+    auto angles = [&]() {  // of pairs 4 (l mod 16) + u: each of two lanes takes half of them
+        int pos_own = seq_len - 1;
+        if (a.positions) pos_own = lane < a.n_axes ? a.positions[(size_t)lane * a.batch + b] : 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = 4 * (lane & 15) + (lane >> 4) * 2 + u;
+            const int pos = a.positions ? __shfl_sync(0xffffffffu, pos_own, axis[i]) : pos_own;
+            float s1, c1;
+            sincos_pos_freq_fast(pos, freq[i].x, freq[i].y, &s1, &c1);
+            const float s2 = __shfl_xor_sync(0xffffffffu, s1, 16), c2 = __shfl_xor_sync(0xffffffffu, c1, 16);
+            sn[u] = lane < 16 ? s1 : s2, sn[2 + u] = lane < 16 ? s2 : s1;
+            cs[u] = lane < 16 ? c1 : c2, cs[2 + u] = lane < 16 ? c2 : c1;
+        }
+    };
     // With the pools vouched for (early_pools) the rings fill before the wait.
     if (a.early && !a.early_pools) grid_wait();
 #pragma unroll 1
@@ -495,6 +516,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         const uint32_t stage[1] = {ring_base + s * kStageBytes};
         issue(std::integral_constant<int, 1>(), stage);
     }
+    if (APPEND && lo < hi) angles();
     if (a.early && a.early_pools) grid_wait();
 
     if (blockIdx.x == 0) {  // zero rows of requests with nothing to attend over
@@ -508,18 +530,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     if (lo >= hi) return;
     const int r = lane >> 2, c = lane & 3;
 
-    // what a segment reads of its request, loaded a segment ahead: q, the length and the positions (lane x: axis x)
-    uint2 q_next[GROUP];
-    int len_next, pos_next = 0;
-    auto load_ahead = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < GROUP; ++i)
-            q_next[i] = *reinterpret_cast<const uint2 *>(a.q + b * a.ldq + (g * GROUP + i) * kD + 4 * lane);
-        len_next = a.seq_lens[b];
-        if (APPEND && a.positions && lane < a.n_axes) pos_next = a.positions[(size_t)lane * a.batch + b];
-    };
-    int b = request_of(prefix, a.batch, lo);
-    load_ahead(b);
     // A split request's partial: written, counted in, and merged with the others where this warp is the last.  A request
     // over more workers than two rounds of loads take is merged by groups of neighbouring workers first, each by the
     // last of its group.  The first of a worker's two split requests is settled before its other pages: left to the
@@ -551,48 +561,37 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     for (int x = lo; x < hi;) {
         const int p0 = prefix[b], p1 = prefix[b + 1];
         const int j0 = x - p0, j1 = min(hi, p1) - p0;
-        const int seq_len = len_next;
-        const bool has_new = APPEND && j1 == p1 - p0;
         uint2 qw[GROUP], kw = make_uint2(0u, 0u), vw = kw;
-        float4 gq, gk;
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i)
+            qw[i] = *reinterpret_cast<const uint2 *>(a.q + b * a.ldq + (g * GROUP + i) * kD + 4 * lane);
+        const bool has_new = APPEND && j1 == p1 - p0;
         if (APPEND) {
-            gq = *reinterpret_cast<const float4 *>(a.q_gain + 4 * lane);
+            const float4 gq = *reinterpret_cast<const float4 *>(a.q_gain + 4 * lane);
+            float4 gk;
             if (has_new) {
                 const size_t o = b * a.ldkv + g * kD + 4 * lane;
                 kw = *reinterpret_cast<const uint2 *>(a.k_new + o);
                 vw = *reinterpret_cast<const uint2 *>(a.v_new + o);
                 gk = *reinterpret_cast<const float4 *>(a.k_gain + 4 * lane);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < GROUP; ++i) qw[i] = q_next[i];
-        uint32_t new_codes = 0, new_sm = 0;  // the new row: codes of K (low half) and V, parameters of K (even lanes) and V
-        if (APPEND) {
-            // angles of pairs 4 (l mod 16) + u: each of two lanes takes half of them
-            float cs[4], sn[4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int i = 4 * (lane & 15) + (lane >> 4) * 2 + u;
-                const int pos = a.positions ? __shfl_sync(0xffffffffu, pos_next, axis[i]) : seq_len - 1;
-                float s1, c1;
-                sincos_pos_freq_fast(pos, freq[i].x, freq[i].y, &s1, &c1);
-                const float s2 = __shfl_xor_sync(0xffffffffu, s1, 16), c2 = __shfl_xor_sync(0xffffffffu, c1, 16);
-                sn[u] = lane < 16 ? s1 : s2, sn[2 + u] = lane < 16 ? s2 : s1;
-                cs[u] = lane < 16 ? c1 : c2, cs[2 + u] = lane < 16 ? c2 : c1;
-            }
+            if (x != lo) angles();
 #pragma unroll
             for (int i = 0; i < GROUP; ++i) qw[i] = norm_rope(qw[i], gq, a.eps, cs, sn, lane);
             if (has_new) {
                 uint32_t k_sm, v_sm;
-                new_codes = quantise_row(norm_rope(kw, gk, a.eps, cs, sn, lane), lane, k_sm);
-                new_codes |= quantise_row(vw, lane, v_sm) << 16;
-                new_sm = lane & 1 ? v_sm : k_sm;
+                const uint32_t k_codes = quantise_row(norm_rope(kw, gk, a.eps, cs, sn, lane), lane, k_sm);
+                const uint32_t v_codes = quantise_row(vw, lane, v_sm);
+                new_row[lane] = make_uint2(k_codes | v_codes << 16, lane & 1 ? v_sm : k_sm);  // parameters of K on even lanes
             }
         }
-        int b_next = b + 1;
+        // the next request: its q on its way to L2 (in registers a segment ahead it cost spills), its length read
+        int b_next = b + 1, len_next = 0;
         if (p1 < hi) {
             while (prefix[b_next + 1] == prefix[b_next]) ++b_next;
-            load_ahead(b_next);
+            len_next = a.seq_lens[b_next];
+            const uint8_t *q_row = reinterpret_cast<const uint8_t *>(a.q + b_next * a.ldq + g * GROUP * kD);
+            if (lane < GROUP * 2) prefetch_l2(q_row + 128 * lane);
         }
         // B of the scores: lane (n, c), n = (group n / 2, head n % 2), holds head n % 2's dims [32 g + 8 c, + 8) of its
         // own group, as the pairs (j, j + 4) that the code words hold, a 16th of the pairs whose codes come 16-fold
@@ -648,6 +647,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             if (has_new && j + NP == j1) {
                 // the new token's row, in the stage and in the pools
                 const int t = left - 1 - (NP - 1) * kPS, page = a.page_table[(size_t)b * a.max_pages + j1 - 1];
+                const uint32_t new_codes = new_row[lane].x, new_sm = new_row[lane].y;
                 if (page >= 0 && page < a.num_pages) {
                     uint8_t *stage = ring + (ks[NP - 1] - ring_base);
                     const size_t off = ((size_t)page * a.hkv + g) * kKvqHeadBytes;
@@ -815,6 +815,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         }
         x = p0 + j1;
         b = b_next;
+        seq_len = len_next;
     }
 }
 
