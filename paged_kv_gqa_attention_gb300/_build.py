@@ -102,7 +102,7 @@ def _compile_binding() -> str:
 def _link_binding(obj: str) -> None:
     torch_lib, tmp = os.path.join(_torch_dir(), "lib"), BINDING + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lqa", "-Wl,-rpath,$ORIGIN", "-L", torch_lib, "-ltorch_python",
-          "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "link of _binding.so")
+          "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], "link of _binding.so")
     os.replace(tmp, BINDING)
 
 
