@@ -129,6 +129,8 @@ constexpr int kMaxStages = 5;         // pages in a warp's ring
 // A stage: K codes, V codes, K parameters, V parameters, so that lane l copies
 // 16 bytes at 16 l of each 512.
 constexpr int kStageBytes = 2 * kKvqHeadBytes;
+constexpr int kAlignedBatch = 256;   // requests up to which a split may follow their boundaries
+constexpr int kAlignedPages = 16;    // of a worker on average, up to which it may
 constexpr int kMinPages = 3;          // of a worker
 constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group
 constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 384 SMs
@@ -140,7 +142,7 @@ constexpr float kScaleMost = 1024.f;  // s times its group's factor: set to [32,
 __host__ __device__ constexpr int workers_of(int hkv) { return kWarps / hkv; }
 
 struct SmemLayout {
-    uint32_t stages, off_scan, off_new, off_freq, off_prefix, total;
+    uint32_t stages, off_scan, off_new, off_freq, off_pieces, off_prefix, total;
 };
 
 // Two CTAs share an SM's 227 KB; the prefix sums of a large batch cost one
@@ -155,6 +157,8 @@ __host__ __device__ inline SmemLayout smem_layout(int batch) {
     o += kWarps * 32 * 8;
     s.off_freq = o;  // rotation frequencies (hi, lo) and axes of the 64 pairs
     o += kD / 2 * 8 + kD / 2;
+    s.off_pieces = o;  // workers of the requests before each, where a split follows them
+    o += (kAlignedBatch + 1) * 4;
     s.off_prefix = o;
     o += (batch + 1) * 4;
     s.total = (o + 15) & ~15u;
@@ -183,27 +187,25 @@ __host__ __device__ inline WorkspaceLayout workspace_layout(int batch, int hq, i
     return w;
 }
 
-// How the flat page list is cut: worker v has pages [total v / nv, total
-// (v + 1) / nv), none empty.  With kMinPages or more for every worker a CTA
-// has neighbouring ones, so CTAs differ by one page at most.  With fewer
-// there are as many workers as have kMinPages, spread over the CTAs (the
-// first ones of a grid lie on different SMs): a worker more would save less
-// than its partial costs to merge.
+// How the flat page list is cut into one range a worker, none empty.
+//
+// Evenly: worker v has pages [total v / nv, total (v + 1) / nv), and a CTA
+// has neighbouring workers, so CTAs differ by one page at most.  With fewer
+// than kMinPages for every worker there are as many workers as have that
+// many, on half the CTAs (the first ones of a grid lie on different SMs): a
+// worker more would save less than its partial costs to merge.
+//
+// By requests (pieces): where there are few pages a worker, each request gets
+// workers of its own, one for up to `most` pages, if that takes no more than
+// there are: a worker with the end of one request and the start of another
+// pays twice for beginning and for settling, about 2 us (4 requests of 500
+// tokens 9.2 -> 7.0 us), which a few pages' imbalance costs less than.
 struct Split {
     int total, nv;
-    bool spread;
-    __device__ __forceinline__ Split(int total_, int ctas, int s) {
-        total = total_;
-        spread = total_ < ctas * s * kMinPages;
-        nv = ctas * s;
-        if (spread) {
-            nv = max(1, total_ / kMinPages);
-            if (nv > ctas / kCtasPerSm * s) nv = ctas / kCtasPerSm * s;  // not two on some SMs and one on others
-            if (nv > total_) nv = total_;
-        }
-    }
+    bool half;          // on the first half of the CTAs
+    const int *pieces;  // prefix sums of the requests' workers, or nullptr: evenly
     __device__ __forceinline__ int worker(int cta, int ctas, int e, int s) const {
-        return !spread ? cta * s + e : e * (ctas / kCtasPerSm) + (cta < ctas / kCtasPerSm ? cta : ctas * s);
+        return !half ? cta * s + e : e * (ctas / kCtasPerSm) + (cta < ctas / kCtasPerSm ? cta : ctas * s);
     }
     // 64-bit divisions cost ten times 32-bit ones, which serve up to 2^19 pages (nv is below 2^13)
     __device__ __forceinline__ int lo(int v) const {
@@ -412,10 +414,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         freq[threadIdx.x] = make_float2(f_hi[threadIdx.x], f_lo[threadIdx.x]);
         axis[threadIdx.x] = pair_axis[threadIdx.x];
     }
-    // prefix sums of the page counts, one request a thread
-    for (int base = 0, carry = 0; base < a.batch; base += kWarps * 32) {
-        const int b = base + threadIdx.x;
-        int v = b < a.batch ? pages_of<APPEND>(a, b, blockIdx.x == 0) : 0;
+    // sums over the CTA's threads before this one, and of all; every thread calls it
+    auto scan_block = [&](int own, int &sum) -> int {
+        int v = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -423,24 +424,70 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         }
         if (lane == 31) scan[warp] = v;
         __syncthreads();
-        int before = carry;
+        int before = v - own;
+        sum = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const int x = scan[w];
             before += w < warp ? x : 0;
-            carry += x;
+            sum += x;
         }
-        if (b < a.batch) prefix[b + 1] = before + v;
+        __syncthreads();
+        return before;
+    };
+    // prefix sums of the page counts, one request a thread
+    int total = 0, own_pages = 0;
+    for (int base = 0; base < a.batch; base += kWarps * 32) {
+        const int b = base + threadIdx.x;
+        own_pages = b < a.batch ? pages_of<APPEND>(a, b, blockIdx.x == 0) : 0;
+        int sum;
+        const int before = total + scan_block(own_pages, sum);
+        if (b < a.batch) prefix[b + 1] = before + own_pages;
+        total += sum;
+    }
+    Split split;
+    {
+        const int most_workers = gridDim.x * S;
+        split.total = total;
+        split.half = total < most_workers * kMinPages;
+        split.nv = split.half ? most_workers / kCtasPerSm : most_workers;
+        split.pieces = nullptr;
+        if (a.batch <= kAlignedBatch && total > 0 && total < most_workers * kAlignedPages) {
+            // the smallest of four sizes that serves, from the even one to a quarter above; two sums a word
+            int most = max(kMinPages, (total + split.nv - 1) / split.nv), chosen = 0, sum;
+            for (int k = 0; k < 4 && !chosen; k += 2) {
+                const int m0 = most + (most * k + 11) / 12, m1 = most + (most * (k + 1) + 11) / 12;
+                scan_block((own_pages + m0 - 1) / m0 | (own_pages + m1 - 1) / m1 << 16, sum);
+                chosen = (sum & 0xffff) <= split.nv ? m0 : sum >> 16 <= split.nv ? m1 : 0;
+            }
+            if (chosen) {
+                int *pieces = reinterpret_cast<int *>(smem + L.off_pieces);
+                const int own = (own_pages + chosen - 1) / chosen, before = scan_block(own, split.nv);
+                if (threadIdx.x == 0) pieces[0] = 0;
+                if ((int)threadIdx.x < a.batch) pieces[threadIdx.x + 1] = before + own;
+                split.pieces = pieces;
+            }
+        }
+        if (!split.pieces && split.half) split.nv = min(split.nv, max(1, total / kMinPages));
+        if (split.nv > total) split.nv = total;
         __syncthreads();
     }
-    const int total = prefix[a.batch];
-    const Split split(total, gridDim.x, S);
 
     // this warp: KV head g of worker v, pages [lo, hi) of the flat list
     const int g = warp % a.hkv, e = warp / a.hkv;
     const int v = split.worker(blockIdx.x, gridDim.x, e, S);
     const bool working = e < S && v < split.nv;
-    const int lo = working ? split.lo(v) : 0, hi = working ? split.lo(v + 1) : 0;
+    int lo = 0, hi = 0, b = 0;  // b: the request of page lo
+    if (working) {
+        if (split.pieces) {
+            b = request_of(split.pieces, a.batch, v);
+            const int i = v - split.pieces[b], n = split.pieces[b + 1] - split.pieces[b], p0 = prefix[b], pages = prefix[b + 1] - p0;
+            lo = p0 + (int)((uint32_t)pages * i / n), hi = p0 + (int)((uint32_t)pages * (i + 1) / n);
+        } else {
+            lo = split.lo(v), hi = split.lo(v + 1);
+            b = request_of(prefix, a.batch, lo);
+        }
+    }
     // page ids, 32 at a time, one a lane: bad ones are -1.  Windows overlap by two, so that a pair of pages lies in one.
     bool any_bad = false;
     auto find = [&](int x) -> int {
@@ -492,7 +539,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     };
 
     // The first request's length, and (step) the angles that its position gives: metadata, read before the wait too.
-    int b = lo < hi ? request_of(prefix, a.batch, lo) : 0;
     int seq_len = lo < hi ? a.seq_lens[b] : 0;
     float cs[4], sn[4];
     auto angles = [&]() {  // of pairs 4 (l mod 16) + u: each of two lanes takes half of them
@@ -536,7 +582,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
     // end, one warp merged both, which the whole grid waited for.
     auto settle = [&](int b, const float (&acc)[GROUP][4], const float (&ref)[GROUP], const float (&sum)[GROUP]) {
         write_partial<GROUP>(a.part_acc, a.part_ml, (size_t)v + b, hq, g, lane, acc, ref, sum);
-        const int v0 = split.of_page(prefix[b]), v1 = split.of_page(prefix[b + 1] - 1);
+        const int v0 = split.pieces ? split.pieces[b] : split.of_page(prefix[b]);
+        const int v1 = split.pieces ? split.pieces[b + 1] - 1 : split.of_page(prefix[b + 1] - 1);
         int *counter = a.arrivals + (size_t)b * kMaxHkv + g;
         float z[GROUP][4], m[GROUP], l[GROUP];
         if (v1 - v0 >= 2 * kMergeMost) {
