@@ -504,8 +504,9 @@ int qa_rope_axes(const int *sections, int n_axes, int interleaved, int head_dim,
  *   a_i = positions[pair_axis[i]][t] * theta^(-2 i / D),     i in [0, D/2)
  *   z[i] = y[i] cos a_i - y[i + D/2] sin a_i,  z[i + D/2] = y[i] sin a_i + y[i + D/2] cos a_i
  *
- * for every head of row t of q and of k, in fp32 with angles as in
- * qa_decode_append, rounded to bf16 once.
+ * for every head of row t of q and of k, in fp32, rounded to bf16 once.  Each
+ * angle is reduced to a fraction of a turn exactly before the hardware sine
+ * and cosine (within 2^-20.5).
  *
  *   q, q_out   bf16, row t's [n_q_heads][head_dim] at t * ldq, t * ldq_out
  *   k, k_out   bf16, row t's [n_kv_heads][head_dim] at t * ldk, t * ldk_out;

@@ -83,7 +83,7 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // C1 + C2 + C3 with C1 = 6.28125 (8 significant bits), so n * C1 is exact for
 // n < 2^16 and the first subtraction is exact.  The reduced angle is within a
 // few fp32 ulps of the true one, then an fp32 sincos.
-__device__ __forceinline__ float reduced_angle(int pos, float f_hi, float f_lo) {
+__device__ __forceinline__ void sincos_pos_freq(int pos, float f_hi, float f_lo, float *s, float *c) {
     constexpr double kTwoPiD = 6.283185307179586476925286766559;
     constexpr float kC1 = 6.28125f;
     constexpr float kC2 = (float)(kTwoPiD - 6.28125);
@@ -96,20 +96,7 @@ __device__ __forceinline__ float reduced_angle(int pos, float f_hi, float f_lo) 
     float r = fmaf(-n, kC1, a_hi);
     r = fmaf(-n, kC2, r);
     r = fmaf(-n, kC3, r);
-    return r + a_lo;
-}
-
-__device__ __forceinline__ void sincos_pos_freq(int pos, float f_hi, float f_lo, float *s, float *c) {
-    sincosf(reduced_angle(pos, f_hi, f_lo), s, c);
-}
-
-// The same angle with the hardware sine and cosine (sin.approx, cos.approx:
-// within 2^-20.5 absolute, the reduced angle being within [-pi, pi]), for
-// results that are rounded to bf16, whose half step is 2^-9 or more.
-__device__ __forceinline__ void sincos_pos_freq_fast(int pos, float f_hi, float f_lo, float *s, float *c) {
-    const float r = reduced_angle(pos, f_hi, f_lo);
-    *s = __sinf(r);
-    *c = __cosf(r);
+    sincosf(r + a_lo, s, c);
 }
 
 __device__ __forceinline__ void prefetch_l2(const void *p) {
@@ -200,30 +187,6 @@ __device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void *src, uin
         "%4;" ::"r"(dst),
         "l"(src), "r"(bytes), "r"(bar), "l"(policy)
         : "memory");
-}
-
-// ----------------------------------------------- 16-byte asynchronous copies
-// Each thread copies 16 bytes, past L1; the groups it commits complete in
-// order, for itself (for other lanes after a __syncwarp).
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
 }
 
 // Named barrier over `count` threads (a multiple of 32); id 0 is __syncthreads.

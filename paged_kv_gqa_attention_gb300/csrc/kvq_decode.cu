@@ -46,8 +46,10 @@
 #include <string.h>
 #include <type_traits>
 
+#include "async.cuh"
 #include "kvq.cuh"
 #include "qa_internal.h"
+#include "rotary.cuh"
 
 namespace qa {
 namespace {
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             const int i = 4 * (lane & 15) + (lane >> 4) * 2 + u;
             const int pos = a.positions ? __shfl_sync(0xffffffffu, pos_own, axis[i]) : pos_own;
             float s1, c1;
-            sincos_pos_freq_fast(pos, freq[i].x, freq[i].y, &s1, &c1);
+            sincos_turns(pos, freq[i].x, freq[i].y, &s1, &c1);
             const float s2 = __shfl_xor_sync(0xffffffffu, s1, 16), c2 = __shfl_xor_sync(0xffffffffu, c1, 16);
             sn[u] = lane < 16 ? s1 : s2, sn[2 + u] = lane < 16 ? s2 : s1;
             cs[u] = lane < 16 ? c1 : c2, cs[2 + u] = lane < 16 ? c2 : c1;

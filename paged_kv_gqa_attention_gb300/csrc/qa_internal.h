@@ -83,7 +83,7 @@ cudaError_t launch_encoder_layer(const void *x, const int32_t *cu_windows, int n
 cudaError_t launch_rope_rows(const void *q, long long ldq, const void *k, long long ldk, int rows, void *q_out,
                              long long ldq_out, void *k_out, long long ldk_out, const qa_rope &rope,
                              const qa_attn_params &p, cudaStream_t stream);
-// theta^(-2i/D) of the D/2 pairs, computed in fp64, as fp32 hi + lo parts
+// theta^(-2i/D) / 2 pi of the D/2 pairs (turns a position), computed in fp64, as fp32 hi + lo parts
 void rope_frequencies(float theta, int head_dim, float *hi, float *lo);
 unsigned int status_read_clear_rope(cudaStream_t stream, cudaError_t *err);
 

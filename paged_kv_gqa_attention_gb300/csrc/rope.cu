@@ -19,8 +19,10 @@
 
 #include <type_traits>
 
+#include "async.cuh"
 #include "common.cuh"
 #include "qa_internal.h"
+#include "rotary.cuh"
 
 namespace qa {
 namespace {
@@ -32,7 +34,7 @@ constexpr int kFewHeads = 16384;   // head vectors up to which an item is one pa
 constexpr int kThreads = 128;
 constexpr int kStages = 2;
 constexpr int kCtasPerSm = 10;
-constexpr int kMaxPos = 1 << 18;  // sincos_pos_freq's range
+constexpr int kMaxPos = 1 << 18;  // sincos_turns's range
 
 struct RopeArgs {
     const uint16_t *q, *k;
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_consta
         float2 c[4], s[4];
 #pragma unroll
         for (int y = 0; y < OWN; ++y)
-            sincos_pos_freq_fast(__shfl_sync(0xffffffffu, pos, axis[y]), f_hi[y], f_lo[y], &s_own[y], &c_own[y]);
+            sincos_turns(__shfl_sync(0xffffffffu, pos, axis[y]), f_hi[y], f_lo[y], &s_own[y], &c_own[y]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float cj = __shfl_sync(0xffffffffu, c_own[j % OWN], j / OWN * LANES + l);
@@ -188,7 +190,7 @@ void rope_frequencies(float theta, int head_dim, float *hi, float *lo) {
     const int half = head_dim / 2;
     if (theta != t_theta || head_dim != t_dim) {
         for (int i = 0; i < half; ++i) {
-            const double f = pow((double)theta, -2.0 * i / head_dim);
+            const double f = pow((double)theta, -2.0 * i / head_dim) / 6.283185307179586476925286766559;
             t_hi[i] = (float)f;
             t_lo[i] = (float)(f - (double)t_hi[i]);
         }
