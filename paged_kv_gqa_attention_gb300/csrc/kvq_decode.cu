@@ -5,16 +5,25 @@
 //   score_j = scale sum_g (m_jg sum_{d in g} q_d + s_jg sum_{d in g} q_d n_jd)
 //   out = sum_j p_j (m_j + s_j n_j) / sum_j p_j,  p = exp(score - max)
 //
+// What bounds it: for long contexts HBM, 160 bytes a token and KV head (80 of K,
+// 80 of V); below that the latency of a page's chain at 16 warps an SM
+// (about 245 instructions a page and head, issue slots 50 % full, ALU 48 %,
+// tensor pipe 26 %).  64 requests of 2000..16000 tokens (651 MB) take 100..105
+// us, 6.2..6.5 TB/s, 91..96 % of the copy rate; 32 of 200..2000 (48 MB) 14.4
+// us, of which 7 are the bytes: the rest is the launch, the first pages' round
+// trip and the merging of split requests.  A step of 128 requests of 100..4000
+// tokens takes 61 us, 5 more than its attention.
+//
 // Work split.  The pages of all requests form one flat list (request-major),
-// cut into equal contiguous ranges, one a worker.  A worker is one warp for
+// cut into contiguous ranges (Split), one a worker.  A worker is one warp for
 // each KV head, and a CTA of 8 warps holds 8 / Hkv workers, two CTAs an SM.
 // Every warp streams the part of its own head (1280 contiguous bytes of a K
 // page and of a V page) through its own ring of shared memory with 16-byte
 // asynchronous copies, five a lane and page, so the warps of a CTA never
 // meet after the prologue: there is no producer warp to feed, no barrier to
-// poll and none to release a stage (a producer warp with bulk copies into a
-// ring shared by the heads, and bulk copies issued by each warp, took more
-// instructions a page).
+// poll and none to release a stage (651 MB: a producer warp with bulk copies
+// into a ring shared by the heads 110 us, bulk copies by each warp 115 us,
+// these, with arithmetic in pairs, 103 us: successive steps, not one change).
 //
 // A request that lies in one worker's range is finished there.  Otherwise
 // each worker writes an fp32 partial (maximum, sum, outputs) to slot v + b
@@ -33,13 +42,16 @@
 // 2^-22 of the largest.  The 8 columns are (group g, query head h): B of the
 // scores holds head h's dims of group g and zeros elsewhere, so one product
 // gives sum_{d in g} q_d n_jd for each group apart, to which its s and m are
-// applied in fp32.  B of the outputs holds p_jh s_jg, rounded to fp16 (2^-12
+// applied in fp32.  B of the outputs holds p_jh s_jg, rounded to fp16 (2^-11
 // of itself), and the columns of a dim's own group are kept; sum p m is kept
 // in fp32 beside it.  fp16's range: p is taken against a reference maximum
 // that is moved when a score passes it by 2^4, s against a power of two for
 // each group that is moved when an s passes 16 times its target, so p s stays
 // below 2^14 and is a normal number down to 2^-20 of the group's largest;
 // most pages move neither, which leaves the reductions over tokens out.
+//
+// Two pages go through together: their chains of products, shuffles and
+// exponentials cover one another, on 4 warps a scheduler.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -131,10 +143,10 @@ constexpr int kMaxStages = 5;         // pages in a warp's ring
 // A stage: K codes, V codes, K parameters, V parameters, so that lane l copies
 // 16 bytes at 16 l of each 512.
 constexpr int kStageBytes = 2 * kKvqHeadBytes;
-constexpr int kAlignedBatch = 256;   // requests up to which a split may follow their boundaries
-constexpr int kAlignedPages = 16;    // of a worker on average, up to which it may
-constexpr int kMinPages = 3;          // of a worker
-constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group
+constexpr int kAlignedBatch = 256;    // requests up to which a split may follow their boundaries
+constexpr int kAlignedPages = 16;     // of a worker on average, up to which it may
+constexpr int kMinPages = 3;          // of a worker (one request of 257 tokens: 1 page 7.3 us, 2 6.4, 3 6.2, 4 6.8)
+constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group (10 and 12 spill)
 constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 384 SMs
 constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;
 constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
@@ -200,8 +212,9 @@ __host__ __device__ inline WorkspaceLayout workspace_layout(int batch, int hq, i
 // By requests (pieces): where there are few pages a worker, each request gets
 // workers of its own, one for up to `most` pages, if that takes no more than
 // there are: a worker with the end of one request and the start of another
-// pays twice for beginning and for settling, about 2 us (4 requests of 500
-// tokens 9.2 -> 7.0 us), which a few pages' imbalance costs less than.
+// pays twice for beginning and for settling, about 2 us (32 requests of
+// 200..2000 tokens 16.9 -> 14.4 us, 4 of 500 9.4 -> 7.3 us), which a few
+// pages' imbalance costs less than.
 struct Split {
     int total, nv;
     bool half;          // on the first half of the CTAs

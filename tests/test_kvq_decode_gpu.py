@@ -419,6 +419,24 @@ def test_step_equals_the_three_calls():
     assert int((d["k_pages"] != e["k_pages"]).sum()) <= 64 and torch.equal(d["v_pages"], e["v_pages"])
 
 
+def test_step_of_non_finite_rows():
+    w = step_setup(67, (40, 33, 20))
+    w["v"][0, 2, 70] = 0x7FC0  # NaN in a value group: that group of the head's outputs
+    w["v"][1, 5, 3] = 0xFF80  # -inf
+    # inf in a key: its mean square is inf, so the norm leaves x / inf = 0 of the finite dims and inf / inf = NaN of dim
+    # 9, which the rotation spreads to its partner 9 + 64; the groups of the two, 0 and 2, are NaN, and so every score
+    w["k"][2, 4, 9] = 0x7F80
+    out, d = run_step(w)
+    nan = np.isnan(f64(out))
+    want = np.zeros_like(nan)
+    want[0, 4:6, 64:96] = want[1, 10:12, 0:32] = want[2, 8:10] = True
+    np.testing.assert_array_equal(nan, want)
+    k, v = new_rows(None, w, d)
+    assert bool(torch.isnan(v[0, 2, 64:96]).all()) and int(torch.isnan(v).sum()) == 64
+    assert bool(torch.isnan(k[2, 4].view(4, 32)[[0, 2]]).all()) and int(torch.isnan(k).sum()) == 64
+    assert bool((k[2, 4].view(4, 32)[[1, 3]] == 0).all())
+
+
 def test_step_refusals_on_the_device():
     w = step_setup(64, (20, 30, 40, 50), axes=3, width=5)
     before = {n: w[n].copy() for n in ("k_pages", "v_pages")}
