@@ -96,7 +96,7 @@ bool shape_is(const at::Tensor &t, int64_t a, int64_t b, int64_t c) {
 }
 
 int as_int(int64_t x, const char *name) {
-    if (x < 0 || x > 0x7fffffff) refuse(PyExc_ValueError, "%s is too large", name);
+    if (x < 0 || x > 0x7fffffff) refuse(PyExc_ValueError, "%s %lld is outside [0, 2^31)", name, (long long)x);
     return (int)x;
 }
 
@@ -105,6 +105,15 @@ long as_long(PyObject *o, const char *name) {
     if (x == -1 && PyErr_Occurred()) {
         PyErr_Clear();
         refuse(PyExc_TypeError, "%s must be an integer", name);
+    }
+    return x;
+}
+
+bool as_bool(PyObject *o, const char *name) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) {
+        PyErr_Clear();
+        refuse(PyExc_TypeError, "%s must be true or false", name);
     }
     return x;
 }
@@ -165,8 +174,8 @@ qa_attn_params params_of(int64_t hq, int64_t hkv, int64_t d, int64_t pages, int6
     p.max_pages_per_seq = as_int(width, "max_pages");
     p.scale = (float)scale;
     p.stream = stream;
-    p.debug_checks = PyObject_IsTrue(debug) ? 1 : 0;
-    p.stable_metadata = (int)as_long(stable, "stable_metadata");
+    p.debug_checks = as_bool(debug, "debug_checks") ? 1 : 0;
+    p.stable_metadata = as_int(as_long(stable, "stable_metadata"), "stable_metadata");
     return p;
 }
 
@@ -231,11 +240,13 @@ void rope_of(Rope &out, PyObject *positions, int64_t n_rows, PyObject *q_gain, P
     r.pair_axis = out.axes;
 }
 
-// A qa_* call; one that waits for the GPU lets other Python threads run.
+// A qa_* call, with other Python threads running meanwhile: a launch waits
+// where the stream's queue is full, and a checked call for the GPU.  Nothing
+// in it may throw, so arguments are checked before.
 template <typename F>
-qa_status call(const qa_attn_params &p, F f) {
-    if (!p.debug_checks) return f();
+qa_status call(F f) {
     qa_status st;
+    static_assert(noexcept(f()), "an exception would leave the interpreter's lock released");
     Py_BEGIN_ALLOW_THREADS st = f();
     Py_END_ALLOW_THREADS return st;
 }
@@ -287,8 +298,9 @@ PyObject *rope_rows(PyObject *const *a) {
     Rope r;
     rope_of(r, a[2], T, a[5], a[6], a[9], D, a[7], a[8], device);
     const qa_attn_params p = params_of(Hq, Hkv, D, 0, 0, 0.0, s.raw, a[11], a[12]);
-    const qa_status st = call(p, [&] {
-        return qa_rope_rows(rq.p, rq.ld, rk.p, rk.ld, as_int(T, "rows"), ro.p, ro.ld, rko.p, rko.ld, &r.r, &p);
+    const int n = as_int(T, "rows");
+    const qa_status st = call([&]() noexcept {
+        return qa_rope_rows(rq.p, rq.ld, rk.p, rk.ld, n, ro.p, ro.ld, rko.p, rko.ld, &r.r, &p);
     });
     if (st != QA_STATUS_OK) return PyLong_FromLong(st);
     return pair_of(object_of(a[3], std::move(q_made)),
@@ -339,9 +351,9 @@ PyObject *kvq_write(PyObject *const *a) {
     const RowArgs r = row_args(a[2], a[6], a[3], device);
     const Stream s = stream_of(a[7], device);
     const qa_attn_params p = params_of(pools.hkv, pools.hkv, k.size(2), pools.pages, r.width, 0.0, s.raw, a[8], a[9]);
-    const int T = as_int(k.size(0), "total_tokens");
-    const qa_status st = call(p, [&] {
-        return qa_kvq_write(rk.p, rk.ld, rv.p, rv.ld, r.cu, r.past, as_int(r.batch, "batch"), T, r.table, pools.k, pools.v, &p);
+    const int T = as_int(k.size(0), "total_tokens"), batch = as_int(r.batch, "batch");
+    const qa_status st = call([&]() noexcept {
+        return qa_kvq_write(rk.p, rk.ld, rv.p, rv.ld, r.cu, r.past, batch, T, r.table, pools.k, pools.v, &p);
     });
     if (st != QA_STATUS_OK) return PyLong_FromLong(st);
     Py_RETURN_NONE;
@@ -368,8 +380,9 @@ PyObject *kvq_read(PyObject *const *a) {
         }
     }
     const qa_attn_params p = params_of(pools.hkv, pools.hkv, 128, pools.pages, r.width, 0.0, s.raw, a[9], a[10]);
-    const qa_status st = call(p, [&] {
-        return qa_kvq_read(pools.k, pools.v, r.table, r.cu, r.past, as_int(r.batch, "batch"), T, out[0], out[1], &p);
+    const int batch = as_int(r.batch, "batch");
+    const qa_status st = call([&]() noexcept {
+        return qa_kvq_read(pools.k, pools.v, r.table, r.cu, r.past, batch, T, out[0], out[1], &p);
     });
     if (st != QA_STATUS_OK) return PyLong_FromLong(st);
     return pair_of(object_of(a[5], std::move(buf[0])), object_of(a[6], std::move(buf[1])));
@@ -416,7 +429,7 @@ PyObject *decode(PyObject *const *a, bool step) {
     qa_status st;
     if (!step) {
         const void *qp = address(q, "q", at::kBFloat16, 3, device, true);
-        st = call(p, [&] { return qa_kvq_decode_attn(qp, pools.k, pools.v, tp, lp, batch, out, &p); });
+        st = call([&]() noexcept { return qa_kvq_decode_attn(qp, pools.k, pools.v, tp, lp, batch, out, &p); });
     } else {
         const at::Tensor &k = tensor(a[11], "k"), &v = tensor(a[12], "v");
         const Rows rq = rows(q, "q", device), rk = rows(k, "k", device), rv = rows(v, "v", device);
@@ -425,7 +438,7 @@ PyObject *decode(PyObject *const *a, bool step) {
         if ((rk.ld ? rk.ld : width) != (rv.ld ? rv.ld : width)) refuse(PyExc_ValueError, "k and v must have the same row stride");
         Rope r;
         rope_of(r, a[15], B, a[13], a[14], a[16], D, a[17], a[18], device);
-        st = call(p, [&] { return qa_kvq_decode_step(rq.p, rq.ld, rk.p, rv.p, rk.ld, &r.r, pools.k, pools.v, tp, lp, batch, out, &p); });
+        st = call([&]() noexcept { return qa_kvq_decode_step(rq.p, rq.ld, rk.p, rv.p, rk.ld, &r.r, pools.k, pools.v, tp, lp, batch, out, &p); });
     }
     if (st != QA_STATUS_OK) return PyLong_FromLong(st);
     return object_of(a[5], std::move(out_made));

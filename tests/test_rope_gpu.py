@@ -113,6 +113,20 @@ def test_refused_tensors():
             qa.qa_rope_rows(**args)
 
 
+def test_refused_when_checked():
+    """A refusal of a checked call, too, is an exception."""
+    rows = 2**31  # of no heads: only the positions take memory
+    empty, pos = torch.empty(rows, 0, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(rows, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="rows"):
+        qa.qa_rope_rows(empty, None, pos, debug_checks=True)
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 16, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(TypeError, match="debug_checks"):
+        qa.qa_rope_rows(q, None, pos, debug_checks=np.zeros(2))
+    with pytest.raises(ValueError, match="stable_metadata"):
+        qa.qa_rope_rows(q, None, pos, stable_metadata=2**32)
+
+
 def test_kinds_of_pair_axis():
     q, k, pos, gains, axis = inputs(7, 8, 16, 8, 128, 3, True)
     dq, dpos = to_dev(q), to_dev(pos)
