@@ -482,7 +482,7 @@ typedef struct qa_rope {
     const float *q_gain;       /* device [head_dim]: per-head RMSNorm gains, both   */
     const float *k_gain;       /* or neither; NULL: no norm                         */
     float rms_eps;             /* > 0 (unused without gains)                        */
-    float theta;               /* > 0: frequency base                               */
+    float theta;               /* >= 1: frequency base                              */
     int n_axes;                /* position axes, 1..4                               */
     const int32_t *positions;  /* device [n_axes][rows]                             */
     const uint8_t *pair_axis;  /* HOST [head_dim/2]: the axis of each rotation pair */
@@ -565,7 +565,8 @@ size_t qa_kvq_page_bytes(const qa_attn_params *params);
  * row are skipped (QA_DEVICE_BAD_LENGTH), as are pages outside
  * [0, num_pages) (QA_DEVICE_BAD_PAGE) and requests whose cu_seqlens are
  * malformed (QA_DEVICE_BAD_SEGMENTS).  Requests may not share a page that
- * both write.  Supported: head_dim 128, page_size 16, n_kv_heads in [1, 8]
+ * both write, nor a request write one that stands twice in its row of the
+ * table.  Supported: head_dim 128, page_size 16, n_kv_heads in [1, 8]
  * (n_q_heads is checked as in the other calls, but not used).
  * stable_metadata >= 1 covers cu_seqlens, n_past and page_table. */
 qa_status qa_kvq_write(const void *k, long long ldk, const void *v, long long ldv, const int32_t *cu_seqlens,
@@ -591,7 +592,9 @@ qa_status qa_kvq_read(const void *k_pages, const void *v_pages, const int32_t *p
  *   out[b][h] = softmax_j(q[b][h] . K_b[j] * scale) V_b[j]
  *
  * with K and V rows m + s n as stored, never rounded to bf16.  Slots past
- * seq_lens[b] may hold any bytes. */
+ * seq_lens[b] may hold any bytes.  batch * max_pages_per_seq is at most 2^30;
+ * queries (in the step: normed and rotated ones) of 2^115 and more in size
+ * give NaN or infinities. */
 size_t qa_kvq_decode_workspace_size(int batch, int max_seq_len, const qa_attn_params *params);
 qa_status qa_kvq_decode_attn(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
                              const int32_t *seq_lens, int batch, void *out, const qa_attn_params *params);
@@ -609,7 +612,9 @@ qa_status qa_kvq_decode_attn(const void *q, const void *k_pages, const void *v_p
  *   other arguments as in qa_kvq_decode_attn; seq_lens[b] >= 1
  *
  * Device checks: those of the three calls.  A request with a bad length or a
- * bad position has no new token written; its out row is zero.  A bad page
+ * bad position has no new token written; its out row is zero.  The page that
+ * a new token goes to may not be another request's, nor stand twice in the
+ * request's own row of the table.  A bad page
  * among a request's pages is left out of its attention, as in
  * qa_decode_attn.  stable_metadata >= 1 covers positions and gains too. */
 qa_status qa_kvq_decode_step(const void *q, long long ldq, const void *k, const void *v, long long ldkv,

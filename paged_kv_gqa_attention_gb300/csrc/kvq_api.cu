@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kHeadBytes = 1280;
 constexpr int kMaxAxes = 4;
+constexpr long long kMaxPages = 1LL << 30;
 
 qa_status reject(qa_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 qa_status reject(qa_status st, const char *fmt, ...) {
@@ -47,7 +48,8 @@ qa_status check_stride(const char *fn, const char *name, long long ld, long long
 
 qa_status check_rope(const char *fn, const qa_rope *r, int head_dim, bool gains, bool positions) {
     if (!r) return invalid(fn, "rope is NULL");
-    if (!(r->theta > 0.f) || !isfinite(r->theta)) return invalid(fn, "rope theta must be finite and > 0");
+    // below 1 a pair would turn by more than a radian a position, which sincos_turns's reduction is not exact for
+    if (!(r->theta >= 1.f) || !isfinite(r->theta)) return invalid(fn, "rope theta must be finite and >= 1");
     if (!r->q_gain != !r->k_gain) return invalid(fn, "q_gain and k_gain must both be given or both be NULL");
     if (gains && !r->q_gain) return invalid(fn, "NULL gain");
     if (r->q_gain && (!(r->rms_eps > 0.f) || !isfinite(r->rms_eps))) return invalid(fn, "rms_eps must be finite and > 0");
@@ -87,6 +89,9 @@ qa_status decode_entry(const char *fn, const void *q, long long ldq, const void 
                        const qa::KvqAppend *app) {
     const qa_status ok = qa::check_decode_call(fn, q, k_pages, v_pages, page_table, seq_lens, batch, out, p);
     if (ok != QA_STATUS_OK) return ok;
+    if ((long long)batch * p->max_pages_per_seq > kMaxPages)  // a call's pages are numbered in 32 bits
+        return reject(QA_STATUS_INVALID_PARAMS, "%s: batch * max_pages_per_seq %lld above %lld", fn,
+                      (long long)batch * p->max_pages_per_seq, kMaxPages);
     const int ctas = qa::current_decode_ctas();
     if (ctas <= 0) return reject(QA_STATUS_LAUNCH_FAILED, "%s: no CUDA device", fn);
     const size_t need = qa::kvq_decode_workspace_bytes(batch, p->n_q_heads, p->n_kv_heads, ctas);

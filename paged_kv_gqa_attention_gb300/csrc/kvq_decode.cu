@@ -147,7 +147,7 @@ constexpr int kAlignedBatch = 256;    // requests up to which a split may follow
 constexpr int kAlignedPages = 16;     // of a worker on average, up to which it may
 constexpr int kMinPages = 3;          // of a worker (one request of 257 tokens: 1 page 7.3 us, 2 6.4, 3 6.2, 4 6.8)
 constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group (10 and 12 spill)
-constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 384 SMs
+constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 256 SMs
 constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;
 constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
 constexpr float kScaleMost = 1024.f;  // s times its group's factor: set to [32, 64), moved past this

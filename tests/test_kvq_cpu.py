@@ -100,6 +100,25 @@ def test_rope_rows_refuses():
     assert call(rows=0) == 0  # nothing to do, nothing launched
 
 
+def test_frequency_bases_below_one_are_refused():
+    """Pairs would turn by more than a radian a position, past what the reduction of angles is exact for."""
+    for theta in (0.99, 1e-30, -1.0, float("inf")):
+        refused(qa._lib.qa_rope_rows(FAKE, 0, FAKE, 0, 3, FAKE, 0, FAKE, 0, rope(theta=theta), params()), "theta")
+        refused(qa._lib.qa_kvq_decode_step(FAKE, 0, FAKE, FAKE, 0, rope(theta=theta), FAKE, FAKE, FAKE, FAKE, 1, FAKE, params()),
+                "theta")
+
+
+def test_more_pages_than_the_decode_numbers():
+    for batch, wide in ((9, 2**27 - 1), (4096, 2**18 + 1)):
+        p = params(max_pages_per_seq=wide)
+        refused(qa._lib.qa_kvq_decode_attn(FAKE, FAKE, FAKE, FAKE, FAKE, batch, FAKE, p), "max_pages_per_seq")
+        refused(qa._lib.qa_kvq_decode_step(FAKE, 0, FAKE, FAKE, 0, rope(), FAKE, FAKE, FAKE, FAKE, batch, FAKE, p),
+                "max_pages_per_seq")
+    p = params(max_pages_per_seq=2**18)
+    assert qa._lib.qa_kvq_decode_attn(FAKE, FAKE, FAKE, FAKE, FAKE, 4096, FAKE, p) in (-1, -3)
+    assert "max_pages_per_seq" not in qa.qa_last_error()  # no workspace, or no device
+
+
 def test_pages_refuse():
     def write(k=FAKE, ldk=0, v=FAKE, ldv=0, cu=FAKE, past=FAKE, batch=2, total=5, table=FAKE, kp=FAKE, vp=FAKE, p=None):
         return qa._lib.qa_kvq_write(k, ldk, v, ldv, cu, past, batch, total, table, kp, vp, p or params())

@@ -113,6 +113,16 @@ def test_refused_tensors():
             qa.qa_rope_rows(**args)
 
 
+def test_smallest_frequency_base():
+    """theta 1: every pair turns by a radian a position, 41721 turns at the last one."""
+    q, k, pos, gains, axis = inputs(8, 9, 16, 8, 128, 1, False)
+    pos = np.array([[0, 1, 2, 3, 1000, 65537, 131072, 262142, 262143]], np.int32)
+    got, _ = qa.qa_rope_rows(to_dev(q), None, to_dev(pos), rope_theta=1.0)
+    want, size = _kvq.rope(wl.bf16_to_f64(q), pos, None, axis, theta=1.0)
+    torch.cuda.synchronize()
+    assert_rounded_match(bits(got), want, size, "theta 1")
+
+
 def test_refused_when_checked():
     """A refusal of a checked call, too, is an exception."""
     rows = 2**31  # of no heads: only the positions take memory
