@@ -13,7 +13,10 @@
 // rows of 8 heads (188 MB) are written in 38.4 us, 4.9 TB/s, 72 % of the copy
 // rate: 640 instructions a warp of K or V (issue slots 58 % full, ALU 48 %)
 // and the chain from cu_seqlens to the rows keep it below.  56691 rows (305
-// MB) are read back in 48.7 us, 6.26 TB/s, 92 %.
+// MB) are read back in 48.7 us, 6.26 TB/s, 92 %.  Warps that walk over pages
+// with the next rows on their way into shared memory were slower (written and
+// read back 77..81 us against 72.7): fewer fit, and it is warps that cover the
+// chains of the quantiser.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
