@@ -56,6 +56,7 @@
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
+#include <algorithm>
 #include <type_traits>
 
 #include "async.cuh"
@@ -152,6 +153,8 @@ constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + k
 constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
 constexpr float kScaleMost = 1024.f;  // s times its group's factor: set to [32, 64), moved past this
 
+constexpr int kFullRings = 2048;      // requests up to which rings have all their stages
+
 // Workers of a CTA.
 __host__ __device__ constexpr int workers_of(int hkv) { return kWarps / hkv; }
 
@@ -161,9 +164,9 @@ struct SmemLayout {
 
 // Two CTAs share an SM's 227 KB; the prefix sums of a large batch cost one
 // stage of every ring.
-__host__ __device__ inline SmemLayout smem_layout(int batch) {
-    SmemLayout s;
-    s.stages = batch <= 2048 ? kMaxStages : kMaxStages - 1;
+__host__ __device__ constexpr SmemLayout smem_layout(int batch) {
+    SmemLayout s = {};
+    s.stages = batch <= kFullRings ? kMaxStages : kMaxStages - 1;
     uint32_t o = s.stages * kStageBytes * kWarps;
     s.off_scan = o;  // warp sums of the prefix scan
     o += kWarps * 4;
@@ -178,6 +181,8 @@ __host__ __device__ inline SmemLayout smem_layout(int batch) {
     s.total = (o + 15) & ~15u;
     return s;
 }
+
+constexpr uint32_t kMostSmem = std::max(smem_layout(kFullRings).total, smem_layout(kDecodeMaxBatch).total);
 
 // Workspace: arrival counters in regions of fixed size, zero between calls
 // (one a request, one a request's group of workers), then the partials of
@@ -939,7 +944,8 @@ cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void 
     cfg.numAttrs = 1;
     auto kernel = app ? (group == 2 ? kvq_decode_kernel<2, true> : kvq_decode_kernel<1, true>)
                       : (group == 2 ? kvq_decode_kernel<2, false> : kvq_decode_kernel<1, false>);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    // the most of any batch, not this call's: another thread's call of another batch may set it before the launch
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }

@@ -1,6 +1,8 @@
 """GPU parity of qa_kvq_decode_attn and qa_kvq_decode_step against attention
 over the 4-bit cache in 64 bits (_kvq.decode, with its error bound), and a
 serving run through all the operators of the 4-bit cache."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -276,6 +278,35 @@ def test_two_streams_and_graphs():
     for w, o in zip(data, outs):
         check(o, w, "replayed on its own stream")
     del ref
+
+
+def test_host_threads_with_batches_of_their_own():
+    """Calls of two host threads interleave; their kernels need different amounts of shared memory."""
+    data = [setup(35, (40,)), setup(36, (3,) * 2000)]
+    want = [attn(w) for w in data]
+    torch.cuda.synchronize()
+    failed = []
+
+    def serve(w, ref):
+        try:
+            s = torch.cuda.Stream()
+            d = {n: to_dev(w[n]) for n in ("q", "k_pages", "v_pages", "table", "lens")}
+            ws = torch.zeros(qa.qa_kvq_decode_workspace_size(len(w["lens"]), 0), dtype=torch.uint8, device="cuda")
+            out = torch.empty_like(d["q"])
+            torch.cuda.synchronize()
+            for _ in range(400):
+                qa.qa_kvq_decode_attn(d["q"], d["k_pages"], d["v_pages"], d["table"], d["lens"], out, workspace=ws, stream=s)
+            s.synchronize()
+            assert torch.equal(out, ref)
+        except Exception as e:  # noqa: BLE001 - whatever it is, the test shows it
+            failed.append(e)
+
+    threads = [threading.Thread(target=serve, args=x) for x in zip(data, want)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not failed, failed
 
 
 def test_workspace_made_inside_a_call_on_another_stream():
