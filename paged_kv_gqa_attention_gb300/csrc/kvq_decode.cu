@@ -45,10 +45,13 @@
 // applied in fp32.  B of the outputs holds p_jh s_jg, rounded to fp16 (2^-11
 // of itself), and the columns of a dim's own group are kept; sum p m is kept
 // in fp32 beside it.  fp16's range: p is taken against a reference maximum
-// that is moved when a score passes it by 2^4, s against a power of two for
-// each group that is moved when an s passes 16 times its target, so p s stays
-// below 2^14 and is a normal number down to 2^-20 of the group's largest;
-// most pages move neither, which leaves the reductions over tokens out.
+// that is moved when a p passes 2^4, and p s of a group and head is
+// brought to 2^11 by a factor that is moved when a product passes 65000, or
+// with the reference, so it is a normal number down to 2^-25 of the largest
+// p s, and rounded to 2^-36 of that below.  The factor follows the products,
+// not s alone: a token of little weight may have values of any size, and one
+// of all the weight values of none.  Most pages move neither, which leaves
+// the reductions over tokens out.
 //
 // Two pages go through together: their chains of products, shuffles and
 // exponentials cover one another, on 4 warps a scheduler.
@@ -150,8 +153,9 @@ constexpr int kMinPages = 3;          // of a worker (one request of 257 tokens:
 constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group (10 and 12 spill)
 constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 256 SMs
 constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;
-constexpr float kRefSlack = 4.f;      // log2 units a score may pass the reference by
-constexpr float kScaleMost = 1024.f;  // s times its group's factor: set to [32, 64), moved past this
+constexpr float kRefSlack = 16.f;     // p above which the reference is moved
+constexpr float kProductAim = 2048.f;   // p s times its factor: the largest when the factor was set,
+constexpr float kProductMost = 65000.f; // and what moves it (fp16 ends at 65504)
 
 constexpr int kFullRings = 2048;      // requests up to which rings have all their stages
 
@@ -697,7 +701,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float2 ref = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f), corr = make_float2(0.f, 0.f);
-        float s_up = 0.f, s_most = -1.f;  // factor of s, and the largest s it serves: the first page sets them
+        float2 up = make_float2(INFINITY, GROUP == 2 ? INFINITY : 0.f);  // factor of p s: the first page sets it
 
         // NP neighbouring pages at once: their chains of products, shuffles and exponentials are independent
         auto pages = [&](auto np, int j) {
@@ -784,68 +788,94 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
                 }
                 none = tokens == 0;  // there may be no reference yet
             }
-            float t_max = 0.f;
+            // p of the tokens, and p s of (token, group c) times its factor, for both heads; sums of p and p m
+            float2 p[NP][2], ps[NP][2], l_next, corr_next;
+            auto weigh = [&]() {
+                l_next = l, corr_next = corr;
 #pragma unroll
-            for (int y = 0; y < NP; ++y) t_max = fmax3(t_max, fabsf(bf16lo(vp0[y])), fabsf(bf16lo(vp1[y])));
-            float2 e[NP][2];  // log2 p
-            float e_max = -INFINITY;
+                for (int y = 0; y < NP; ++y)
 #pragma unroll
-            for (int y = 0; y < NP; ++y)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    e[y][h] = fsub2(sc[y][h], ref);
-                    e_max = GROUP == 2 ? fmax3(e_max, e[y][h].x, e[y][h].y) : fmaxf(e_max, e[y][h].x);
-                }
-            if (__any_sync(0xffffffffu, e_max > kRefSlack || t_max > s_most)) {  // move the references to the maxima so far
-#pragma unroll
-                for (int z = 4; z < 32; z <<= 1) t_max = fmaxf(t_max, __shfl_xor_sync(0xffffffffu, t_max, z));
-                float alpha[2] = {1.f, 1.f};
-                if (t_max > s_most) {
-                    const float up = pow2i(min(5 - exponent_of(t_max), 126));
-                    if (s_up > 0.f) alpha[0] = alpha[1] = up / s_up;
-                    s_up = up;
-                    s_most = kScaleMost / up;
-                }
-#pragma unroll
-                for (int i = 0; i < GROUP; ++i) {
-                    float m = -INFINITY;
-#pragma unroll
-                    for (int y = 0; y < NP; ++y) m = i == 0 ? fmax3(m, sc[y][0].x, sc[y][1].x) : fmax3(m, sc[y][0].y, sc[y][1].y);
-#pragma unroll
-                    for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-                    float &rf = i == 0 ? ref.x : ref.y, &li = i == 0 ? l.x : l.y, &ci = i == 0 ? corr.x : corr.y;
-                    if (m > rf) {
-                        const float f = exp2_approx(rf - m);
-                        rf = m;
-                        alpha[i] *= f;
-                        li *= f;
-                        ci *= f;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sm = h ? vp1[y] : vp0[y];
+                        const float s = bf16lo(sm), m = bf16hi(sm);
+                        const float2 e = fsub2(sc[y][h], ref);
+                        p[y][h] = make_float2(exp2_approx(e.x), GROUP == 2 ? exp2_approx(e.y) : 0.f);
+                        l_next = fadd2(l_next, p[y][h]);
+                        corr_next = ffma2(p[y][h], make_float2(m, m), corr_next);
+                        ps[y][h] = fmul2(fmul2(p[y][h], make_float2(s, s)), up);
                     }
+            };
+            if (!none) {
+                bool move = j == j0;  // the first pages set the references
+                if (!move) {
+                    weigh();
+                    float p_max = 0.f, ps_max = 0.f;
+#pragma unroll
+                    for (int y = 0; y < NP; ++y)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            p_max = GROUP == 2 ? fmax3(p_max, p[y][h].x, p[y][h].y) : fmaxf(p_max, p[y][h].x);
+                            ps_max = GROUP == 2 ? fmax3(ps_max, fabsf(ps[y][h].x), fabsf(ps[y][h].y)) : fmaxf(ps_max, fabsf(ps[y][h].x));
+                        }
+                    move = __any_sync(0xffffffffu, p_max > kRefSlack || ps_max > kProductMost);
                 }
+                if (move) {  // the references, to the maxima so far
+                    float m[GROUP], w[GROUP];  // largest score, and score with log2 s on it (p s in units of any reference)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i][0] *= alpha[0], o[i][1] *= alpha[1], o[i][2] *= alpha[0], o[i][3] *= alpha[1];
+                    for (int i = 0; i < GROUP; ++i) m[i] = w[i] = -INFINITY;
 #pragma unroll
-                for (int y = 0; y < NP; ++y) e[y][0] = fsub2(sc[y][0], ref), e[y][1] = fsub2(sc[y][1], ref);
-            }
+                    for (int y = 0; y < NP; ++y) {
+                        const float s0 = __log2f(fabsf(bf16lo(vp0[y]))), s1 = __log2f(fabsf(bf16lo(vp1[y])));
 #pragma unroll
-            for (int y = 0; y < NP; ++y) {
-                if (none) continue;
-                // p s of (token, group c) for both heads, rounded to fp16, transposed into B
-                const float u0 = bf16lo(vp0[y]) * s_up, u1 = bf16lo(vp1[y]) * s_up, c0 = bf16hi(vp0[y]), c1 = bf16hi(vp1[y]);
-                float2 pa = make_float2(exp2_approx(e[y][0].x), 0.f), pb = make_float2(exp2_approx(e[y][1].x), 0.f);
-                if (GROUP == 2) pa.y = exp2_approx(e[y][0].y), pb.y = exp2_approx(e[y][1].y);
-                l = fadd2(l, fadd2(pa, pb));
-                corr = ffma2(pa, make_float2(c0, c0), ffma2(pb, make_float2(c1, c1), corr));
-                pa = fmul2(pa, make_float2(u0, u0));
-                pb = fmul2(pb, make_float2(u1, u1));
-                const uint32_t b0 = transpose8x8(pack_f16x2(pa.x, pa.y)), b1 = transpose8x8(pack_f16x2(pb.x, pb.y));
-                const uint4 v0 = lds128(ks[y] + kAtV + 16 * lane), v1 = lds128(ks[y] + kAtV + 512 + 16 * lane);
-                const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
+                        for (int i = 0; i < GROUP; ++i) {
+                            const float a0 = i == 0 ? sc[y][0].x : sc[y][0].y, a1 = i == 0 ? sc[y][1].x : sc[y][1].y;
+                            m[i] = fmax3(m[i], a0, a1);
+                            w[i] = fmax3(w[i], a0 + s0, a1 + s1);
+                        }
+                    }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    mma16816(o[2 * u], code_pair<0>(x0[u]), code_pair<1>(x0[u]), code_pair<0>(x1[u]), code_pair<1>(x1[u]), b0, b1);
-                    mma16816(o[2 * u + 1], code_pair<2>(x0[u]), code_pair<3>(x0[u]), code_pair<2>(x1[u]), code_pair<3>(x1[u]), b0,
-                             b1);
+                    for (int z = 4; z < 32; z <<= 1)
+#pragma unroll
+                        for (int i = 0; i < GROUP; ++i) {
+                            m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], z));
+                            w[i] = fmaxf(w[i], __shfl_xor_sync(0xffffffffu, w[i], z));
+                        }
+                    float alpha[2] = {1.f, 1.f};
+#pragma unroll
+                    for (int i = 0; i < GROUP; ++i) {
+                        float &rf = i == 0 ? ref.x : ref.y, &li = i == 0 ? l.x : l.y, &ci = i == 0 ? corr.x : corr.y;
+                        float &ui = i == 0 ? up.x : up.y;
+                        float f = 1.f;
+                        if (m[i] > rf) {
+                            f = exp2_approx(rf - m[i]);
+                            rf = m[i];
+                            li *= f;
+                            ci *= f;
+                        }
+                        // the largest p s of these tokens, or what the factor stood for, in units of the new reference;
+                        // within bounds where the factor and its inverse are normal numbers
+                        const float before = __fdividef(f, ui);  // 0 the first time
+                        const float t = fmaxf(exp2_approx(w[i] - rf), kProductAim * before);
+                        ui = __fdividef(kProductAim, fminf(fmaxf(t, kProductAim / 0x1p126f), 0x1p126f));
+                        alpha[i] = ui * before;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i][0] *= alpha[0], o[i][1] *= alpha[1], o[i][2] *= alpha[0], o[i][3] *= alpha[1];
+                    weigh();
+                }
+                l = l_next, corr = corr_next;
+#pragma unroll
+                for (int y = 0; y < NP; ++y) {
+                    // p s rounded to fp16, transposed into B
+                    const uint32_t b0 = transpose8x8(pack_f16x2(ps[y][0].x, ps[y][0].y)), b1 = transpose8x8(pack_f16x2(ps[y][1].x, ps[y][1].y));
+                    const uint4 v0 = lds128(ks[y] + kAtV + 16 * lane), v1 = lds128(ks[y] + kAtV + 512 + 16 * lane);
+                    const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        mma16816(o[2 * u], code_pair<0>(x0[u]), code_pair<1>(x0[u]), code_pair<0>(x1[u]), code_pair<1>(x1[u]), b0, b1);
+                        mma16816(o[2 * u + 1], code_pair<2>(x0[u]), code_pair<3>(x0[u]), code_pair<2>(x1[u]), code_pair<3>(x1[u]), b0,
+                                 b1);
+                    }
                 }
             }
             __syncwarp();
@@ -857,7 +887,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
 
         // sums over the tokens (lanes of equal c); the lane keeps dims [32 c + 4 r, + 4) of both heads
         float acc[GROUP][4], l_sum[GROUP], ref_of[GROUP];
-        const float s_back = s_up > 0.f ? 1.f / s_up : 0.f;
+        const float2 back = make_float2(1.f / up.x, 1.f / up.y);  // 0 where nothing was attended
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
             float ls = i == 0 ? l.x : l.y, cr = i == 0 ? corr.x : corr.y;
@@ -872,7 +902,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
             for (int d = 0; d < 4; ++d) {
                 const int k = (d & 1) * 2 + i, t = d >> 1;
                 const float lo2 = c & 1 ? o[2 + t][k] : o[t][k], hi2 = c & 1 ? o[6 + t][k] : o[4 + t][k];
-                acc[i][d] = fmaf((c & 2 ? hi2 : lo2) * (d & 1 ? 1048576.f : 16777216.f), s_back, cr);
+                acc[i][d] = fmaf((c & 2 ? hi2 : lo2) * (d & 1 ? 1048576.f : 16777216.f), i == 0 ? back.x : back.y, cr);
             }
         }
         if (j0 == 0 && j1 == p1 - p0) {

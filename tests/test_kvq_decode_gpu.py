@@ -146,6 +146,57 @@ def test_heads_and_groups_of_very_different_size():
         assert np.linalg.norm((g - ref)[sl]) <= 5e-3 * np.linalg.norm(ref[sl])
 
 
+def params_view(pool, hkv=8):
+    """The parameters of a pool as a writable bit view [pages, heads, 16 tokens, 4 groups, 2]."""
+    return pool.reshape(pool.shape[0], hkv, 1280)[:, :, 1024:].view(np.uint16).reshape(pool.shape[0], hkv, 16, 4, 2)
+
+
+def place_score(w, b, pos, nats):
+    """Gives request b's token `pos` constant key groups whose score is the largest of its head's others plus `nats`,
+    for both query heads of every KV head (q . K = sum_g m_g sum_{d in g} q_d: two equations for four minima)."""
+    n = int(w["lens"][b])
+    ks, km, kn = _kvq.rows(w["k_pages"], w["table"][b], 0, n, True)
+    q = wl.bf16_to_f64(w["q"])[b].reshape(8, 2, 128)
+    sc = np.einsum("hgd,htd->hgt", q, km + ks * kn)
+    sc[..., pos] = -np.inf
+    want = sc.max(-1) + nats * 128 ** 0.5
+    sums = q.reshape(8, 2, 4, 32).sum(-1)
+    sm = np.zeros((8, 4, 2), np.float32)
+    for h in range(8):
+        sm[h, :, 1] = np.linalg.lstsq(sums[h], want[h], rcond=None)[0]
+    params_view(w["k_pages"])[w["table"][b][pos // 16], :, pos % 16] = wl.bf16_bits(sm).reshape(sm.shape)
+
+
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("log2_ratio", [17, 24, 60])
+def test_a_huge_value_of_no_weight(where, log2_ratio):
+    """A token whose values are 2^17 and more times the others' and whose probability is e^-60 of the largest: the
+    others' part of the output stays exact to the bound, in its own group and the rest."""
+    w = setup(42, (700, 41, 5000))
+    for b, n in enumerate(w["lens"]):
+        pos = {"first": 0, "middle": int(n) // 2, "last": int(n) - 1}[where]
+        place_score(w, b, pos, -60.0)
+        group = params_view(w["v_pages"])[w["table"][b][pos // 16], :, pos % 16, 1]
+        group[...] = wl.bf16_bits(_kvq.f32(group) * np.float32(2.0 ** log2_ratio)).reshape(group.shape)
+    check(attn(w), w, f"{where}, 2^{log2_ratio}")
+
+
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+def test_a_sink_without_a_value(where):
+    """A token that takes nearly all of the softmax and whose value groups are 0 + 2^-30 n: the output is what the
+    others' probabilities of e^-19 give, all alike, so that their roundings would not average out."""
+    w = setup(43, (700, 41, 3000))
+    for n in ("k_pages", "v_pages"):
+        params_view(w[n])[...] = wl.bf16_bits(np.array([0.0, 0.0] if n == "k_pages" else [0.171875, -1.25], np.float32))
+    for b, n in enumerate(w["lens"]):
+        pos = {"first": 0, "middle": int(n) // 2, "last": int(n) - 1}[where]
+        place_score(w, b, pos, 19.0)
+        params_view(w["v_pages"])[w["table"][b][pos // 16], :, pos % 16] = wl.bf16_bits(np.array([2.0 ** -30, 0.0], np.float32))
+    for n in ("k_pages", "v_pages"):
+        _kvq.poison_after(w[n], w["table"], w["lens"])
+    check(attn(w), w, where)
+
+
 def test_constant_groups():
     # s = 0 in every value group: the output is the minimum's average; in every key group: all scores of a token equal m sum q
     w = setup(39, (200, 3))
