@@ -587,7 +587,8 @@ qa_status qa_kvq_read(const void *k_pages, const void *v_pages, const int32_t *p
 
 /* qa_decode_workspace_size and qa_decode_attn over 4-bit pools: the same
  * arguments, workspace rules (its own size; zero-filled before the first
- * use, ordered calls), stable_metadata levels, device checks and result,
+ * use, ordered calls; one workspace of the larger size may serve both forms
+ * in turn), stable_metadata levels, device checks and result,
  *
  *   out[b][h] = softmax_j(q[b][h] . K_b[j] * scale) V_b[j]
  *

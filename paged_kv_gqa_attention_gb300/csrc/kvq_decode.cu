@@ -56,6 +56,7 @@
 // Two pages go through together: their chains of products, shuffles and
 // exponentials cover one another, on 4 warps a scheduler.
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -84,8 +85,9 @@ struct KvqArgs {
     long long ldq, ldkv;
     float *part_acc, *group_acc;    // [slots][Hq][D]
     float *part_ml, *group_ml;      // [slots][Hq][2]
-    int *arrivals, *group_arrivals; // [request or slot][kMaxHkv], zero between calls
+    int *arrivals;                  // kCounters words, zero between calls
     int batch, hkv, max_pages, num_pages;
+    int group_from;  // workers_to_group
     float scale_log2;
     int early, early_pools;  // stable_metadata >= 1, >= 2
     // step only
@@ -151,7 +153,6 @@ constexpr int kAlignedBatch = 256;    // requests up to which a split may follow
 constexpr int kAlignedPages = 16;     // of a worker on average, up to which it may
 constexpr int kMinPages = 3;          // of a worker (one request of 257 tokens: 1 page 7.3 us, 2 6.4, 3 6.2, 4 6.8)
 constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group (10 and 12 spill)
-constexpr int kMaxGroups = 512;       // of workers: 2 CTAs x 8 workers on up to 256 SMs
 constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;
 constexpr float kRefSlack = 16.f;     // p above which the reference is moved
 constexpr float kProductAim = 2048.f;   // p s times its factor: the largest when the factor was set,
@@ -188,11 +189,15 @@ __host__ __device__ constexpr SmemLayout smem_layout(int batch) {
 
 constexpr uint32_t kMostSmem = std::max(smem_layout(kFullRings).total, smem_layout(kDecodeMaxBatch).total);
 
-// Workspace: arrival counters in regions of fixed size, zero between calls
-// (one a request, one a request's group of workers), then the partials of
-// workers and of groups.
+// Workspace: arrival counters in a region of fixed size, zero between calls,
+// then the partials of workers and of groups.  The region is the one that the
+// bf16 decode has its counters in, so that calls of both may share a
+// workspace: neither's partials lie on the other's counters.  A request's
+// counters (one a KV head) are counted from the region's start, those of
+// groups of workers from its end.
+constexpr int kCounters = kDecodeMaxBatch * kMaxHkv;
 struct WorkspaceLayout {
-    size_t arrivals, group_arrivals, acc, ml, group_acc, group_ml, total;
+    size_t arrivals, acc, ml, group_acc, group_ml, total;
 };
 
 __host__ __device__ inline WorkspaceLayout workspace_layout(int batch, int hq, int workers) {
@@ -201,13 +206,24 @@ __host__ __device__ inline WorkspaceLayout workspace_layout(int batch, int hq, i
     const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     WorkspaceLayout w;
     w.arrivals = 0;
-    w.group_arrivals = up((size_t)kDecodeMaxBatch * kMaxHkv * sizeof(int));
-    w.acc = w.group_arrivals + up((size_t)(kDecodeMaxBatch + kMaxGroups) * kMaxHkv * sizeof(int));
+    w.acc = up((size_t)kCounters * sizeof(int));
     w.ml = w.acc + up(slots * hq * kD * sizeof(float));
     w.group_acc = w.ml + up(slots * hq * 2 * sizeof(float));
     w.group_ml = w.group_acc + up(group_slots * hq * kD * sizeof(float));
     w.total = w.group_ml + up(group_slots * hq * 2 * sizeof(float));
     return w;
+}
+
+// Place, from the region's end, of the counter of group q of a request that is
+// merged by groups, q0 its first one, for KV head g.  Such a request has more
+// than 16 workers, so at most one begins in a group, and at most one comes
+// from the group before.
+__device__ __forceinline__ int group_counter(int q, int q0, int g, int hkv) { return (2 * q + (q == q0)) * hkv + g + 1; }
+// Workers from which a request is merged by groups: where their counters have
+// room behind those of the requests, which with 8 KV heads and 304 workers is
+// up to 4018 requests, with fewer heads always.
+inline int workers_to_group(int batch, int workers, int hkv) {
+    return (batch + 2 * (workers / kMergeMost + 1)) * hkv <= kCounters ? 2 * kMergeMost + 1 : INT_MAX;
 }
 
 // How the flat page list is cut into one range a worker, none empty.
@@ -608,12 +624,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kvq_decode_kernel(con
         write_partial<GROUP>(a.part_acc, a.part_ml, (size_t)v + b, hq, g, lane, acc, ref, sum);
         const int v0 = split.pieces ? split.pieces[b] : split.of_page(prefix[b]);
         const int v1 = split.pieces ? split.pieces[b + 1] - 1 : split.of_page(prefix[b + 1] - 1);
-        int *counter = a.arrivals + (size_t)b * kMaxHkv + g;
+        int *counter = a.arrivals + b * a.hkv + g;
         float z[GROUP][4], m[GROUP], l[GROUP];
-        if (v1 - v0 >= 2 * kMergeMost) {
+        if (v1 - v0 + 1 >= a.group_from) {
             const int q = v / kMergeMost, q0 = v0 / kMergeMost, q1 = v1 / kMergeMost;
             const int a0 = max(v0, q * kMergeMost), a1 = min(v1, q * kMergeMost + kMergeMost - 1);
-            int *group = a.group_arrivals + (size_t)(q + b) * kMaxHkv + g;
+            int *group = a.arrivals + kCounters - group_counter(q, q0, g, a.hkv);
             if (!last_in(group, a1 - a0, lane)) return;
             merge<GROUP>(a.part_acc, a.part_ml, (size_t)a0 + b, a1 - a0 + 1, hq, g, lane, z, m, l);
             if (lane == 0) *group = 0;
@@ -941,14 +957,15 @@ cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void 
     a.scale_log2 = scale * kLog2e;
     a.early = (p.abi_version >= 2 && p.stable_metadata >= 1) ? 1 : 0;
     a.early_pools = (p.abi_version >= 2 && p.stable_metadata >= 2) ? 1 : 0;
-    const WorkspaceLayout w = workspace_layout(batch, p.n_q_heads, ctas * kCtasPerSm * workers_of(p.n_kv_heads));
+    const int workers = ctas * kCtasPerSm * workers_of(p.n_kv_heads);
+    a.group_from = workers_to_group(batch, workers, p.n_kv_heads);
+    const WorkspaceLayout w = workspace_layout(batch, p.n_q_heads, workers);
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     a.part_acc = reinterpret_cast<float *>(ws + w.acc);
     a.part_ml = reinterpret_cast<float *>(ws + w.ml);
     a.group_acc = reinterpret_cast<float *>(ws + w.group_acc);
     a.group_ml = reinterpret_cast<float *>(ws + w.group_ml);
     a.arrivals = reinterpret_cast<int *>(ws + w.arrivals);
-    a.group_arrivals = reinterpret_cast<int *>(ws + w.group_arrivals);
     if (app) {
         const qa_rope &rope = *app->rope;
         a.k_new = static_cast<const uint16_t *>(app->k_new);

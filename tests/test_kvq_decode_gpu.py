@@ -287,6 +287,39 @@ def test_workspace_is_reusable_and_calls_repeat():
         attn(w, workspace=ws[:128])
 
 
+def test_workspace_shared_with_the_bf16_decode():
+    """Layers of both caches take turns on one workspace; requests are split over more than 16 workers, whose groups
+    have counters of their own."""
+    lens = (6000, 3, 9000, 700)
+    w, x = setup(44, lens), wl.decode_workload(45, lens, num_pages=1100, max_pages=600)
+    ref = oracle.decode(x["q"], x["k_pages"], x["v_pages"], x["page_table"], x["seq_lens"])
+    size = max(qa.qa_kvq_decode_workspace_size(4, 0), qa.qa_decode_workspace_size(4, 9000, num_pages=1100, max_pages_per_seq=600))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    dx = {n: to_dev(x[n]) for n in ("q", "k_pages", "v_pages", "page_table", "seq_lens")}
+    for i in range(4):
+        out = torch.full((4, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        qa.qa_decode_attn(dx["q"], dx["k_pages"], dx["v_pages"], dx["page_table"], dx["seq_lens"], out, workspace=ws)
+        assert_close(f64(out), ref, f"bf16 layer {i}")
+        out = torch.full((4, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        check(attn(w, workspace=ws, out=out, debug_checks=True), w, f"4-bit layer {i}")
+        assert not ws[:4096 * 8 * 4].any()
+
+
+@pytest.mark.parametrize("batch, hq, hkv", [(4018, 8, 8), (4019, 8, 8), (4096, 16, 8), (4096, 7, 7), (4096, 2, 1)])
+def test_long_requests_in_the_largest_batches(batch, hq, hkv):
+    """Requests over more than 16 workers among so many that the groups' counters have little room, or none."""
+    w = setup(46, (20000, 20, 13000), hq, hkv)
+    ref, bound = _kvq.decode(wl.bf16_to_f64(w["q"]), w["k_pages"], w["v_pages"], w["table"], w["lens"])
+    pick = np.ones(batch, int)
+    pick[[100, batch - 1]] = 0, 2
+    pick[101] = 2
+    ws = torch.zeros(qa.qa_kvq_decode_workspace_size(batch, 0, n_q_heads=hq, n_kv_heads=hkv), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        g = f64(attn(dict(w, q=w["q"][pick], table=w["table"][pick], lens=w["lens"][pick]), workspace=ws, debug_checks=True))
+        assert (np.abs(g - ref[pick]) <= bound[pick]).all()
+        assert not ws[:4096 * 8 * 4].any()
+
+
 @pytest.mark.parametrize("level", [0, 1, 2])
 def test_stable_metadata_levels(level):
     w = setup(24, (700, 1, 90, 3000))
