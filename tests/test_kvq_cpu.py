@@ -48,6 +48,26 @@ def test_rope_struct_has_the_c_layout(tmp_path):
     assert got == [ctypes.sizeof(qa.qa_rope)] + [getattr(qa.qa_rope, n).offset for n in names]
 
 
+def test_angles_are_reduced_to_half_a_turn(tmp_path):
+    """Every position at the largest frequency, a radian a position, and at a few smaller ones: the fraction of a turn is
+    in [-1/2, 1/2], where the hardware sine and cosine have their bound, and within 2^-24 of the true one (2^-25 for the
+    rounding of a sum below 1, the other terms are below 2^-30)."""
+    src, exe = tmp_path / "turns.cpp", tmp_path / "turns"
+    src.write_text('#include "rotary.cuh"\n#include <stdio.h>\n#include <stdlib.h>\nint main(int, char **v) {\n'
+                   "    const double t = atof(v[1]);\n    const float hi = (float)t, lo = (float)(t - (double)hi);\n"
+                   "    for (int p = 0; p < 1 << 18; ++p) {\n        const float f = qa::turn_fraction(p, hi, lo);\n"
+                   "        fwrite(&f, sizeof f, 1, stdout);\n    }\n    return 0;\n}\n")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-ffp-contract=off", "-I", os.path.join(ROOT, "paged_kv_gqa_attention_gb300", "csrc"), str(src), "-o",
+                    str(exe)], check=True)
+    pos = np.arange(1 << 18, dtype=np.float64)
+    for radians in (1.0, 1e4 ** (-2 / 128), 1e6 ** (-1 / 2), 0.5):
+        t = radians / (2 * np.pi)
+        got = np.frombuffer(subprocess.run([str(exe), repr(t)], stdout=subprocess.PIPE, check=True).stdout, np.float32)
+        off = got - pos * t  # pos t to 2^-37: a whole number of turns from the fraction
+        assert np.abs(off - np.rint(off)).max() <= 2.0 ** -24
+        assert np.abs(got).max() <= 0.5
+
+
 def params(**kw):
     p = qa.qa_attn_default_params()
     p.num_pages, p.max_pages_per_seq = 4, 4
