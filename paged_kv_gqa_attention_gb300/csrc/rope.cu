@@ -42,7 +42,11 @@ constexpr int kMaxHalf = 64;
 constexpr int kFewHeads = 4096;
 constexpr int kThreads = 128;
 constexpr int kStages = 2;
-constexpr int kCtasPerSm = 10;    // what registers and rings allow at two passes
+// CTAs a grid has for each SM at most.  Five are resident at two passes with a
+// norm (96 registers), so such a grid comes in two waves; rows of 24 heads of
+// 128, 5 / 8 / 10 / 15 / 20: 3000 rows 5.8 / 6.5 / 6.3 / 6.2 / 6.2 us, 8000 rows
+// 16.9 / 16.3 / 15.2 / 15.7 / 16.4, 16111 rows 36.0 / 32.5 / 32.3 / 31.7 / 31.5.
+constexpr int kCtasPerSm = 10;
 constexpr int kMaxPos = 1 << 18;  // sincos_turns's range
 
 struct RopeArgs {
