@@ -42,12 +42,24 @@ def _deps_mtime() -> float:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Compile and link libqa.so; returns its path.  Skips work when the
-    library is newer than every source and header."""
+    """Compile and link libqa.so, then the Python binding; returns the
+    library's path.  Skips what is newer than every source and header.  The
+    library needs nvcc alone: without torch, g++ or Python's headers it is
+    there all the same, and the error is the binding's."""
     newest = _deps_mtime()
-    if not force and not extra_flags and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
-        return LIB
+    lib_done, binding_done = (not force and not extra_flags and os.path.exists(f) and os.path.getmtime(f) >= newest
+                              for f in (LIB, BINDING))
     os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside nvcc's
+        binding = None if lib_done and binding_done else ex.submit(_compile_binding)
+        if not lib_done:
+            _build_library(verbose, extra_flags)
+        if binding is not None:
+            _link_binding(binding.result())
+    return LIB
+
+
+def _build_library(verbose: bool, extra_flags: list[str] | None) -> None:
     exe = nvcc()
     flags = NVCC_FLAGS + (extra_flags or [])
 
@@ -63,23 +75,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
 
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "--exclude-libs,ALL"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
-    return LIB
 
 
 def _torch_dir() -> str:
     import importlib.util
 
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("the Python binding needs torch's headers and libraries, and torch is not installed")
+    return os.path.dirname(spec.origin)
 
 
 def _run(cmd: list[str], what: str) -> None:

@@ -268,3 +268,21 @@ def test_bounded_wait_check_rejects_bad_limits_without_device(libqa):
     for limit in (0, 1000001):
         assert qa._lib.qa_check_bounded_wait(limit, None) == -1
         assert "limit_us" in qa.qa_last_error()
+
+
+def test_the_library_is_linked_where_the_binding_cannot_be_built(tmp_path, monkeypatch):
+    """C callers need nvcc alone: a failure of the binding (no torch, no g++) comes after the library is there."""
+    import __graft_entry__
+
+    _build = __graft_entry__._builder()
+    fake = tmp_path / "nvcc"  # writes its output file
+    fake.write_text('#!/bin/sh\nwhile [ $# -gt 0 ]; do [ "$1" = -o ] && echo > "$2"; shift; done\n')
+    fake.chmod(0o755)
+    for name, path in (("BUILD", "obj"), ("LIB", "libqa.so"), ("BINDING", "_binding.so")):
+        monkeypatch.setattr(_build, name, str(tmp_path / path))
+    monkeypatch.setattr(_build, "nvcc", lambda: str(fake))
+    monkeypatch.setattr("importlib.util.find_spec", lambda name: None)
+    for _ in range(2):  # again with the library there
+        with pytest.raises(RuntimeError, match="torch"):
+            _build.build()
+        assert os.path.exists(_build.LIB) and not os.path.exists(_build.BINDING)
