@@ -609,6 +609,95 @@ def test_step_graph_replay_grows_the_cache():
     assert (d["lens"].cpu().numpy() == w["lens"] + 20).all() and qa.qa_device_status() == 0
 
 
+def grown(seed, lens, tokens, axes):
+    """A layer's cache of `lens` tokens with room for `tokens` more, and the new rows of each of them."""
+    rng = np.random.default_rng(seed)
+    B = len(lens)
+    table, pages = _kvq.page_table(rng, np.asarray(lens) + tokens)
+    w = dict(table=table, k_pages=_kvq.random_pool(rng, pages, 8), v_pages=_kvq.random_pool(rng, pages, 8))
+    w["rows"] = [{n: wl.normal_bf16(rng, (B, h, 128)) for n, h in (("q", 16), ("k", 8), ("v", 8))} for _ in range(tokens)]
+    for n in ("q_gain", "k_gain"):
+        w[n] = wl.bf16_to_f64(wl.bf16_bits(rng.uniform(0.5, 1.5, size=128).astype(np.float32))).astype(np.float32)
+    w["positions"] = rng.integers(0, 1 << 18, size=(tokens, axes, B)).astype(np.int32) if axes else None
+    w["pair_axis"] = rng.integers(0, axes, size=64).astype(np.uint8) if axes else None
+    return w
+
+
+@pytest.mark.parametrize("read_back", [False, True])
+@pytest.mark.parametrize("axes", [0, 3])
+@pytest.mark.parametrize("level", [1, 2])
+def test_chained_steps_at_stable_metadata_levels(level, axes, read_back):
+    """Six tokens through two layers' caches, queued without a host synchronise, rings filled and angles computed before
+    the call before is done: every output, every row read back and the pools are those of calls made one at a time at
+    level 0, and those are right."""
+    lens, tokens = np.array([5000, 0, 13, 15, 16, 700]), 6
+    layers = [grown(seed, lens, tokens, axes) for seed in (80, 81)]
+    dev = [[{n: to_dev(x) for n, x in row.items()} for row in w["rows"]] for w in layers]
+    fixed = [{n: to_dev(w[n]) for n in ("q_gain", "k_gain", "table")} for w in layers]
+    pos = [None if w["positions"] is None else [to_dev(x) for x in w["positions"]] for w in layers]
+    n_of = [(lens + 1 + i).astype(np.int32) for i in range(tokens)]
+    dn, last = [to_dev(n) for n in n_of], [to_dev(n - 1) for n in n_of]
+    cu = torch.arange(len(lens) + 1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(qa.qa_kvq_decode_workspace_size(len(lens), 0), dtype=torch.uint8, device="cuda")
+
+    def run(level, after):
+        pools = [{n: to_dev(w[n]) for n in ("k_pages", "v_pages")} for w in layers]
+        torch.cuda.synchronize()
+        got = []
+        for i in range(tokens):
+            for j, w in enumerate(layers):
+                r, f, p = dev[j][i], fixed[j], pools[j]
+                out = qa.qa_kvq_decode_step(r["q"], r["k"], r["v"], f["q_gain"], f["k_gain"], f["table"], dn[i], p["k_pages"],
+                                            p["v_pages"], positions=pos[j] and pos[j][i], pair_axis=w["pair_axis"],
+                                            workspace=ws, stable_metadata=level)
+                got.append(out)
+                if read_back:
+                    got += qa.qa_kvq_read(p["k_pages"], p["v_pages"], f["table"], cu, len(lens), n_past=last[i],
+                                          stable_metadata=level)
+                after(i, j, p, out)
+        torch.cuda.synchronize()
+        return got + [p[n] for p in pools for n in p]
+
+    def right(i, j, p, out):
+        w = layers[j]
+        at = (n_of[i] - 1)[None] if w["positions"] is None else w["positions"][i]
+        q, _ = _kvq.rope(wl.bf16_to_f64(w["rows"][i]["q"]), at, w["q_gain"], w["pair_axis"])
+        k, size = _kvq.rope(wl.bf16_to_f64(w["rows"][i]["k"]), at, w["k_gain"], w["pair_axis"])
+        now = dict(table=w["table"], lens=n_of[i], **{n: x.cpu().numpy() for n, x in p.items()})
+        check(out, now, f"token {i} layer {j}", q=wl.bf16_to_f64(wl.bf16_bits(q.astype(np.float32)).reshape(q.shape)))
+        v_codes, v_sm = _kvq.quantise(w["rows"][i]["v"])
+        for b, n in enumerate(n_of[i]):
+            s, m, c = (x[:, 0] for x in _kvq.rows(now["v_pages"], w["table"][b], n - 1, 1, False))
+            np.testing.assert_array_equal(c, v_codes[b])
+            np.testing.assert_array_equal(s[:, ::32], wl.bf16_to_f64(v_sm[b][..., 0]))
+            np.testing.assert_array_equal(m[:, ::32], wl.bf16_to_f64(v_sm[b][..., 1]))
+            s, m, c = (x[:, 0] for x in _kvq.rows(now["k_pages"], w["table"][b], n - 1, 1, True))
+            # as in check_step: half a step of s, s itself within 2^-8, and K's rounding to bf16
+            assert (np.abs(m + s * c - k[b]) <= s * (0.5 + 15 * 2.0 ** -8) + 2.0 ** -8 * np.abs(k[b]) + 2.0 ** -18 * size[b]).all()
+
+    want = run(0, right)
+    for _ in range(3):
+        got = run(level, lambda *a: None)
+        assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert qa.qa_device_status() == 0
+
+
+@pytest.mark.parametrize("lens, hq, hkv", [((5000, 3), 16, 8), ((9000, 40, 1, 4000), 16, 8), ((70,) * 300, 16, 8),
+                                           ((16000, 12000), 2, 1), ((3000, 257), 6, 3), ((0, 0), 16, 8)])
+def test_counters_are_zero_after_every_call(lens, hq, hkv):
+    """Those of requests and those of the groups that merge requests over more than 16 workers, on a workspace whose
+    partials are of other sizes every time."""
+    ws = torch.zeros(qa.qa_kvq_decode_workspace_size(300, 0), dtype=torch.uint8, device="cuda")
+    w = setup(47, lens, hq, hkv)
+    for _ in range(2):
+        check(attn(w, workspace=ws), w, "attention")
+        assert not ws[:4096 * 8 * 4].any()
+    if min(lens) > 0:
+        w = step_setup(48, lens, hq, hkv)
+        check_step(w, "step", workspace=ws)
+        assert not ws[:4096 * 8 * 4].any()
+
+
 # ------------------------------------------------------------------ served together
 
 def test_serving_run():
