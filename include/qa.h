@@ -505,8 +505,11 @@ int qa_rope_axes(const int *sections, int n_axes, int interleaved, int head_dim,
  *   z[i] = y[i] cos a_i - y[i + D/2] sin a_i,  z[i + D/2] = y[i] sin a_i + y[i + D/2] cos a_i
  *
  * for every head of row t of q and of k, in fp32, rounded to bf16 once.  Each
- * angle is reduced to a fraction of a turn exactly before the hardware sine
- * and cosine (within 2^-20.5).
+ * angle is reduced to a fraction of a turn (within 2^-24) before the hardware
+ * sine and cosine (within 2^-20.5).  One ladder of frequencies runs over all
+ * D/2 pairs, whatever their axis, as in decoders of text with images in it;
+ * encoders that begin the ladder anew for each axis have another rotation,
+ * which this call does not do.
  *
  *   q, q_out   bf16, row t's [n_q_heads][head_dim] at t * ldq, t * ldq_out
  *   k, k_out   bf16, row t's [n_kv_heads][head_dim] at t * ldk, t * ldk_out;
@@ -538,7 +541,8 @@ qa_status qa_rope_rows(const void *q, long long ldq, const void *k, long long ld
  * group reads back exactly).  A group whose range is not a finite fp32
  * number (an infinity or NaN in it) reads back as NaN in all 32 dims; other
  * groups and tokens are untouched by it.  The largest error of a value is
- * about half of s, a thirtieth of the group's range.
+ * about half of s, a thirtieth of the group's range (the largest finite bf16
+ * may come back as infinity: m + 15 s with s rounded up).
  *
  * Bytes inside a head's part of a page, token t in 0..15, little-endian:
  *   K codes   dim 32 g + 8 c + j: nibble j of the 4-byte word at
@@ -592,7 +596,10 @@ qa_status qa_kvq_read(const void *k_pages, const void *v_pages, const int32_t *p
  *
  *   out[b][h] = softmax_j(q[b][h] . K_b[j] * scale) V_b[j]
  *
- * with K and V rows m + s n as stored, never rounded to bf16.  Slots past
+ * with K and V rows m + s n as stored, never rounded to bf16.  Scores, softmax
+ * and sums are fp32; in the product of probabilities and codes a probability
+ * times s is rounded to fp16, by 2^-11 of itself, or by 2^-36 of the largest
+ * one of its group and head where it is below 2^-25 of that.  Slots past
  * seq_lens[b] may hold any bytes.  batch * max_pages_per_seq is at most 2^30;
  * queries (in the step: normed and rotated ones) of 2^115 and more in size
  * give NaN or infinities. */

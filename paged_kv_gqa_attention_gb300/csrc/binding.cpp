@@ -5,7 +5,9 @@
 // These calls are made once a layer and token, and a small one's kernel is
 // done in 2 to 7 us.  Marshalled in Python, eight tensors' attributes, the
 // structs and the ctypes call take 13 to 18 us on a Grace core; here a call
-// takes about 4, most of it the launch.  Nothing is kept between calls.
+// takes about 4, most of it the launch.  Nothing of a call's arguments is
+// kept for the next one (the library keeps the frequency table of a thread's
+// last rope theta, rope.cu).
 //
 // A function returns its outputs, or the status as an int where the call was
 // refused.  Arguments of the wrong kind raise TypeError or ValueError.

@@ -8,7 +8,7 @@
 // The codes lie so that each lane's share of a page is whole 16-byte words,
 // neighbouring lanes read neighbouring words, and the two halves of a
 // 32-bit word are one register's two k: masking one nibble of both halves
-// and ORing the bf16 bits of 128 gives the register, without a shuffle.
+// gives the register, a pair of fp16 subnormals, without a shuffle.
 #pragma once
 
 #include <float.h>

@@ -149,8 +149,12 @@ constexpr int kMaxStages = 5;         // pages in a warp's ring
 // A stage: K codes, V codes, K parameters, V parameters, so that lane l copies
 // 16 bytes at 16 l of each 512.
 constexpr int kStageBytes = 2 * kKvqHeadBytes;
-constexpr int kAlignedBatch = 256;    // requests up to which a split may follow their boundaries
-constexpr int kAlignedPages = 16;     // of a worker on average, up to which it may
+constexpr int kAlignedBatch = 256;    // requests up to which a split may follow their boundaries: one a thread
+// Pages of a worker on average up to which it may.  Requests of 200..2000
+// tokens, even split and this one: 16 of them (4 pages) 12.8 and 11.4 us, 32
+// (7) 16.4 and 13.6, 64 (14) 21.0 and 19.5, 80 (18) 23.2 and 22.0, 96 (22) 27.7
+// and 27.1, 128 (28) 34.7 and 36.1, 200 (45) 47.5 and 48.2.
+constexpr int kAlignedPages = 24;
 constexpr int kMinPages = 3;          // of a worker (one request of 257 tokens: 1 page 7.3 us, 2 6.4, 3 6.2, 4 6.8)
 constexpr int kMergeMost = 8;         // partials merged in one round of loads, workers of a group (10 and 12 spill)
 constexpr int kAtV = kKvqCodeBytes, kAtKp = 2 * kKvqCodeBytes, kAtVp = kAtKp + kKvqHeadBytes - kKvqCodeBytes;

@@ -11,9 +11,11 @@
 //
 // Both move 512 bytes of rows and 160 of pages a token and KV head.  35032
 // rows of 8 heads (188 MB) are written in 38.4 us, 4.9 TB/s, 72 % of the copy
-// rate: 640 instructions a warp of K or V (issue slots 58 % full, ALU 48 %)
-// and the chain from cu_seqlens to the rows keep it below.  56691 rows (305
-// MB) are read back in 48.7 us, 6.26 TB/s, 92 %.  Warps that walk over pages
+// rate.  Nothing is full (640 instructions a warp of K or V, issue slots 58 %,
+// ALU 48 %, DRAM 60 %): a CTA of one page begins its chain from cu_seqlens to
+// the rows with nothing in flight.  56691 rows (305 MB) are read back in 48.7
+// us, 6.26 TB/s, 92 %; few rows wait on the loop's loads, each behind the
+// stores before it (16 requests of 53..430 4.96 us).  Warps that walk over pages
 // with the next rows on their way into shared memory were slower (written and
 // read back 77..81 us against 72.7): fewer fit, and it is warps that cover the
 // chains of the quantiser.
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(256, 4) kvq_write_kernel(const __grid_constant
     else write_v(a, j, h, lane, params[h]);
 }
 
-// Two values (codes in nibble positions 0 and 4 of `pair`) of a group.
+// The value of code n of a group.
 __device__ __forceinline__ float kvq_value(uint32_t n, float s, float m) { return fmaf(s, (float)n, m); }
 
 __global__ void __launch_bounds__(256) kvq_read_kernel(const __grid_constant__ PagesArgs a) {
