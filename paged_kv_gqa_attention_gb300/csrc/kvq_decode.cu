@@ -9,10 +9,10 @@
 // 80 of V); below that the latency of a page's chain at 16 warps an SM
 // (about 245 instructions a page and head, issue slots 50 % full, ALU 48 %,
 // tensor pipe 26 %).  64 requests of 2000..16000 tokens (651 MB) take 100..105
-// us, 6.2..6.5 TB/s, 91..96 % of the copy rate; 32 of 200..2000 (48 MB) 14.4
+// us, 6.2..6.5 TB/s, 91..96 % of the copy rate; 32 of 200..2000 (48 MB) 14.2
 // us, of which 7 are the bytes: the rest is the launch, the first pages' round
 // trip and the merging of split requests.  A step of 128 requests of 100..4000
-// tokens takes 61 us, 5 more than its attention.
+// tokens takes 61 us, 4 more than its attention.
 //
 // Work split.  The pages of all requests form one flat list (request-major),
 // cut into contiguous ranges (Split), one a worker.  A worker is one warp for
@@ -242,7 +242,7 @@ inline int workers_to_group(int batch, int workers, int hkv) {
 // workers of its own, one for up to `most` pages, if that takes no more than
 // there are: a worker with the end of one request and the start of another
 // pays twice for beginning and for settling, about 2 us (32 requests of
-// 200..2000 tokens 16.9 -> 14.4 us, 4 of 500 9.4 -> 7.3 us), which a few
+// 200..2000 tokens 16.4 -> 13.6 us, 4 of 500 9.4 -> 7.3 us), which a few
 // pages' imbalance costs less than.
 struct Split {
     int total, nv;

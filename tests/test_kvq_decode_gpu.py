@@ -153,14 +153,14 @@ def params_view(pool, hkv=8):
 
 def place_score(w, b, pos, nats):
     """Gives request b's token `pos` constant key groups whose score is the largest of its head's others plus `nats`,
-    for both query heads of every KV head (q . K = sum_g m_g sum_{d in g} q_d: two equations for four minima)."""
+    for the query heads of every KV head (q . K = sum_g m_g sum_{d in g} q_d: an equation each for four minima)."""
     n = int(w["lens"][b])
     ks, km, kn = _kvq.rows(w["k_pages"], w["table"][b], 0, n, True)
-    q = wl.bf16_to_f64(w["q"])[b].reshape(8, 2, 128)
+    q = wl.bf16_to_f64(w["q"])[b].reshape(8, -1, 128)
     sc = np.einsum("hgd,htd->hgt", q, km + ks * kn)
     sc[..., pos] = -np.inf
     want = sc.max(-1) + nats * 128 ** 0.5
-    sums = q.reshape(8, 2, 4, 32).sum(-1)
+    sums = q.reshape(8, -1, 4, 32).sum(-1)
     sm = np.zeros((8, 4, 2), np.float32)
     for h in range(8):
         sm[h, :, 1] = np.linalg.lstsq(sums[h], want[h], rcond=None)[0]
@@ -169,10 +169,11 @@ def place_score(w, b, pos, nats):
 
 @pytest.mark.parametrize("where", ["first", "middle", "last"])
 @pytest.mark.parametrize("log2_ratio", [17, 24, 60])
-def test_a_huge_value_of_no_weight(where, log2_ratio):
+@pytest.mark.parametrize("hq", [16, 8])
+def test_a_huge_value_of_no_weight(where, log2_ratio, hq):
     """A token whose values are 2^17 and more times the others' and whose probability is e^-60 of the largest: the
     others' part of the output stays exact to the bound, in its own group and the rest."""
-    w = setup(42, (700, 41, 5000))
+    w = setup(42, (700, 41, 5000), hq)
     for b, n in enumerate(w["lens"]):
         pos = {"first": 0, "middle": int(n) // 2, "last": int(n) - 1}[where]
         place_score(w, b, pos, -60.0)
@@ -182,10 +183,11 @@ def test_a_huge_value_of_no_weight(where, log2_ratio):
 
 
 @pytest.mark.parametrize("where", ["first", "middle", "last"])
-def test_a_sink_without_a_value(where):
+@pytest.mark.parametrize("hq", [16, 8])
+def test_a_sink_without_a_value(where, hq):
     """A token that takes nearly all of the softmax and whose value groups are 0 + 2^-30 n: the output is what the
     others' probabilities of e^-19 give, all alike, so that their roundings would not average out."""
-    w = setup(43, (700, 41, 3000))
+    w = setup(43, (700, 41, 3000), hq)
     for n in ("k_pages", "v_pages"):
         params_view(w[n])[...] = wl.bf16_bits(np.array([0.0, 0.0] if n == "k_pages" else [0.171875, -1.25], np.float32))
     for b, n in enumerate(w["lens"]):
