@@ -90,6 +90,7 @@ typedef enum qa_status {
                                        not ending at total_tokens               */
 #define QA_DEVICE_TIMEOUT 0x8u      /* a bounded wait inside a kernel expired    */
 #define QA_DEVICE_BAD_POSITION 0x10u /* rotary position outside [0, 2^18)        */
+#define QA_DEVICE_BAD_TREE 0x20u     /* a row's parent outside [-1, the row)     */
 
 typedef struct qa_attn_params {
     int abi_version;       /* set by qa_attn_default_params()                    */
@@ -628,6 +629,140 @@ qa_status qa_kvq_decode_attn(const void *q, const void *k_pages, const void *v_p
 qa_status qa_kvq_decode_step(const void *q, long long ldq, const void *k, const void *v, long long ldkv,
                              const qa_rope *rope, void *k_pages, void *v_pages, const int32_t *page_table,
                              const int32_t *seq_lens, int batch, void *out, const qa_attn_params *params);
+
+/* ------------------------------------------------------------------------
+ * Drafted tokens over the paged bf16 cache, and cross attention.
+ *
+ * A step that checks drafted tokens takes, a layer, qa_append_rows (the
+ * drafted rows normed, rotated and written behind the cached positions) and
+ * qa_tree_attn (every drafted row over the cache and its own ancestors), and
+ * at its end one qa_tree_accept, which finds the path of drafted tokens that
+ * the model agrees with and moves its rows, in every layer, to where a plain
+ * continuation would have put them.  qa_cross_attn attends packed rows to
+ * paged states of another length (an encoder's, which qa_append_rows lays
+ * into pages).
+ *
+ * A tree is one array over the packed rows: parents[t] is the row that row t
+ * continues, counted within its request; -1: it continues the cache (a
+ * request may have several such rows).  A parent comes before its rows:
+ * parents[t] < t's own number.  parents NULL: every row continues the one
+ * before it.  A parent outside [-1, own number) counts as -1 and sets
+ * QA_DEVICE_BAD_TREE.  A row's depth is the number of its ancestors.
+ *
+ * In these calls cu_seqlens[batch] may be less than total_rows: rows behind
+ * the last request are left as they were, so that a captured call serves any
+ * number of rows up to its total.
+ * ------------------------------------------------------------------------ */
+
+/* Appends rows to the paged bf16 cache, normed and rotated on the way:
+ *
+ *   q, k, v    bf16, row t's heads at t * ldq, t * ldk, t * ldv (elements,
+ *              multiples of 8; 0 = packed): they may lie in the rows of one
+ *              fused projection.  q may be NULL (keys and values only)
+ *   cu_seqlens int32 [batch + 1]: request r owns rows [cu[r], cu[r+1])
+ *   n_past     int32 [batch] (device) or NULL (all 0): row i of request r is
+ *              position n_past[r] + i of its cache
+ *   parents    int32 [total_rows] (device) or NULL, as above; used only
+ *              for positions
+ *   page_table int32 [batch][max_pages_per_seq]
+ *   k_pages, v_pages  pools (layout as in qa_decode_attn): the row's slot
+ *              receives k normed and rotated as in qa_rope_rows, and v bit
+ *              for bit
+ *   q_out      bf16, row t's at t * ldq_out: q normed and rotated; may be q
+ *              itself (same stride), must not overlap an input otherwise
+ *   rope       as in qa_rope_rows; positions [n_axes][total_rows], or NULL
+ *              with n_axes 1: n_past[r] plus the row's depth.  NULL: no norm
+ *              and no rotation (k is written, and q copied, bit for bit)
+ *
+ * Device checks: as in qa_prefill_chunk_attn's page write (a request whose
+ * n_past is outside [0, max_pages_per_seq * 16] is skipped, rows past the
+ * page-table row are not written: QA_DEVICE_BAD_LENGTH; pages outside
+ * [0, num_pages): QA_DEVICE_BAD_PAGE; malformed cu_seqlens:
+ * QA_DEVICE_BAD_SEGMENTS).  A row with a position outside [0, 2^18) is not
+ * written, nor is its q_out (QA_DEVICE_BAD_POSITION).  Where only the page
+ * or the place in it is bad, q_out is written all the same.  No slot may be
+ * written twice in a call.  Supported: head_dim 128, page_size 16,
+ * n_kv_heads in [1, 8], n_q_heads / n_kv_heads in {1, 2}.  stable_metadata
+ * >= 1 covers cu_seqlens, n_past, parents, page_table, positions and gains. */
+qa_status qa_append_rows(const void *q, long long ldq, const void *k, long long ldk, const void *v, long long ldv,
+                         const int32_t *cu_seqlens, const int32_t *n_past, const int32_t *parents, int batch,
+                         int total_rows, const int32_t *page_table, void *k_pages, void *v_pages, void *q_out,
+                         long long ldq_out, const qa_rope *rope, const qa_attn_params *params);
+
+/* Bytes of device workspace (256-byte aligned) for qa_tree_attn and
+ * qa_cross_attn calls of up to max_rows rows a request on the CURRENT
+ * device: fp32 partial results.  It need not be cleared; calls sharing one
+ * workspace must be ordered (one stream).  Of params the head counts matter.
+ * Returns 0 on invalid arguments and sets qa_last_error(). */
+size_t qa_rows_attn_workspace_size(int max_rows, const qa_attn_params *params);
+
+/* Attention of drafted tokens over the cache:
+ *
+ *   out[t][h] = softmax_j(q[t][h] . K_r[j] * scale) V_r[j]
+ *
+ * over j < n_past[r] (every cached position) and j = n_past[r] + i' for the
+ * row itself and its ancestors i'.  The rows' own keys and values are read
+ * from their pages (qa_append_rows).
+ *
+ *   q          bf16, row t's [n_q_heads][128] at t * ldq (a multiple of 8;
+ *              0 = packed)
+ *   cu_seqlens, n_past, parents, page_table, k_pages, v_pages  as above
+ *   max_rows   the most rows of a request, 1..64 (host): what the kernel is
+ *              chosen by
+ *   out        bf16 [total_rows][n_q_heads][128], packed
+ *
+ * Slots past n_past[r] + rows may hold anything, NaN included, and so may
+ * the keys and values of rows that are not a row's ancestors.  A visible
+ * infinity gives an infinity or NaN.  Scores, softmax and sums are fp32;
+ * probabilities enter the product with V as two bf16 terms (about 16 bits).
+ * Device checks: a request with more than max_rows rows, n_past < 0 or
+ * n_past + rows beyond its page-table row has zero rows in out
+ * (QA_DEVICE_BAD_LENGTH); pages outside [0, num_pages) are left out
+ * (QA_DEVICE_BAD_PAGE); rows of malformed segments are not written
+ * (QA_DEVICE_BAD_SEGMENTS).  Supported: batch up to 1024, head_dim 128,
+ * page_size 16, n_kv_heads in [1, 8], n_q_heads / n_kv_heads in {1, 2}; needs
+ * params->workspace of qa_rows_attn_workspace_size().  stable_metadata >= 1
+ * covers cu_seqlens, n_past, parents and page_table (2 acts as 1). */
+qa_status qa_tree_attn(const void *q, long long ldq, const int32_t *cu_seqlens, const int32_t *n_past,
+                       const int32_t *parents, int batch, int total_rows, int max_rows, const int32_t *page_table,
+                       const void *k_pages, const void *v_pages, void *out, const qa_attn_params *params);
+
+/* Cross attention: row t of request r attends to all of the request's
+ * seq_lens[r] paged states, without an order; a request without states has
+ * zero rows.  Arguments, workspace, precision and device checks as in
+ * qa_tree_attn (seq_lens outside [0, max_pages_per_seq * 16] is a bad
+ * length), with any max_rows >= 1. */
+qa_status qa_cross_attn(const void *q, long long ldq, const int32_t *cu_seqlens, const int32_t *seq_lens, int batch,
+                        int total_rows, int max_rows, const int32_t *page_table, const void *k_pages,
+                        const void *v_pages, void *out, const qa_attn_params *params);
+
+/* Settles a step of drafted tokens.  Row 0 of a request (its token was
+ * chosen before the step) is accepted; then, from the accepted row i, the
+ * first row c with parents[c] = i and draft[c] = target[i], and so on:
+ *
+ *   draft, target  int32 [total_rows]: the token each row stands for, and the
+ *              one the model chose after it
+ *   n_accepted int32 [batch]: accepted rows (0 for a request without rows)
+ *   path       int32 [batch][max_rows]: their numbers in the request, -1
+ *              behind them
+ *   next_token int32 [batch]: target of the last accepted row (-1 without
+ *              rows)
+ *   k_pages, v_pages  HOST arrays of n_layers device pointers (0..64 layers):
+ *              in each pool, the row at n_past + path[j] is copied to
+ *              n_past + j; other slots keep what they hold
+ *
+ * parents, cu_seqlens, n_past, page_table, max_rows (1..64) as in
+ * qa_tree_attn; the outputs may not overlap the inputs.  n_past is not
+ * advanced: the next step's is n_past + n_accepted.  Device checks as there;
+ * a request with a bad length has n_accepted 0, next_token -1 and nothing
+ * moved; a row whose source or destination page is bad is not moved.  No two
+ * requests may write one page, nor may one stand twice in a request's row of
+ * the table.  stable_metadata >= 1 covers cu_seqlens, n_past, parents and
+ * page_table. */
+qa_status qa_tree_accept(const int32_t *draft, const int32_t *target, const int32_t *parents,
+                         const int32_t *cu_seqlens, const int32_t *n_past, int batch, int total_rows, int max_rows,
+                         const int32_t *page_table, int n_layers, void *const *k_pages, void *const *v_pages,
+                         int32_t *n_accepted, int32_t *path, int32_t *next_token, const qa_attn_params *params);
 
 /* Synchronises `stream` (cudaStream_t, NULL = legacy default), then reads and
  * clears the device status word of the current device.  Returns its bits

@@ -76,10 +76,11 @@ qa_status launch_result(cudaError_t e, const char *fn) {
 qa_status debug_status(unsigned int bits, cudaError_t e, const char *fn) {
     if (e != cudaSuccess) return fail(QA_STATUS_LAUNCH_FAILED, "%s: CUDA error %s", fn, cudaGetErrorString(e));
     if (bits)
-        return fail(QA_STATUS_DEVICE_ERROR, "%s: device status 0x%x (%s%s%s%s%s)", fn, bits,
+        return fail(QA_STATUS_DEVICE_ERROR, "%s: device status 0x%x (%s%s%s%s%s%s)", fn, bits,
                     bits & QA_DEVICE_BAD_PAGE ? "bad page id " : "", bits & QA_DEVICE_BAD_LENGTH ? "bad length " : "",
                     bits & QA_DEVICE_BAD_SEGMENTS ? "bad segments " : "",
-                    bits & QA_DEVICE_BAD_POSITION ? "bad position " : "", bits & QA_DEVICE_TIMEOUT ? "timeout" : "");
+                    bits & QA_DEVICE_BAD_POSITION ? "bad position " : "", bits & QA_DEVICE_BAD_TREE ? "bad tree " : "",
+                    bits & QA_DEVICE_TIMEOUT ? "timeout" : "");
     return QA_STATUS_OK;
 }
 
@@ -455,11 +456,12 @@ QA_API qa_status qa_layer_norm(const void *x, int t, int d, const void *gain, co
 QA_API int qa_device_status(void *stream) {
     clear_error();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e[8];
+    cudaError_t e[10];
     const unsigned int bits = qa::status_read_clear_decode(s, &e[0]) | qa::status_read_clear_prefill(s, &e[1]) |
                               qa::status_read_clear_window(s, &e[2]) | qa::status_read_clear_append(s, &e[3]) |
                               qa::status_read_clear_gemm(s, &e[4]) | qa::status_read_clear_rope(s, &e[5]) |
-                              qa::status_read_clear_kvq_pages(s, &e[6]) | qa::status_read_clear_kvq_decode(s, &e[7]);
+                              qa::status_read_clear_kvq_pages(s, &e[6]) | qa::status_read_clear_kvq_decode(s, &e[7]) |
+                              qa::status_read_clear_rows_attn(s, &e[8]) | qa::status_read_clear_tree_accept(s, &e[9]);
     for (cudaError_t ei : e)
         if (ei != cudaSuccess) {
             fail(QA_STATUS_LAUNCH_FAILED, "qa_device_status: CUDA error %s", cudaGetErrorString(ei));

@@ -1,0 +1,632 @@
+// Attention of packed rows over paged states (qa_tree_attn, qa_cross_attn):
+// the kernel for few rows a request, the merge of both kernels' split jobs,
+// and the launch.  The kernel for many rows is rows_tiles.cu.
+//
+//   out[t][h] = softmax_j(q[t][h] . K_r[j] scale) V_r[j]
+//
+// over the request's n_past positions and the row's own ancestors in the tree
+// behind them (tree), or over all its states (cross).
+//
+// Few rows (rows x group up to 32).  Bound by HBM: every key and value is
+// read once, for all rows of its request and both query heads of its KV head.
+// As in the single-token decode a persistent grid cuts the list of all pages
+// into equal ranges (rows_attn.cuh) and a producer warp streams whole pages,
+// all KV heads of 16 tokens, through a ring in shared memory.  The pages come
+// as boxes of a tensor map that puts the heads outermost and swizzles the
+// rows of 64 dims, so that 8 tokens of one head are read by one ldmatrix
+// without a bank conflict.  One consumer warp a KV head: its rows (a query
+// row's heads in turn) are the M of mma.sync m16n8k16, so that S stays in
+// registers as the A operand of P V.  A tcgen05 tile would be 128 rows for
+// these 16 or 32, and its S would have to come back from TMEM for the softmax;
+// the tensor pipe is not what bounds.
+//
+// P enters P V as two bf16 terms (p truncated, and the rest rounded): about
+// 16 bits of each probability, with fp32 statistics.  The running max of a
+// row moves only when a page exceeds it by 2^8 (log2 units 8), so that the
+// accumulator is seldom rescaled; the result does not depend on the
+// reference.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "async.cuh"
+#include "rows_attn.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+
+namespace qa {
+namespace {
+
+__device__ unsigned int g_status;
+
+constexpr int kPage = 16;
+constexpr int kMaxStages = 8;
+constexpr float kSlack = 8.f;
+constexpr int kMergeThreads = 256;
+constexpr int kMaxWorkers = 1024;
+
+// Bytes of a stage: K and V of one page, each two halves of 64 dims.
+__host__ __device__ constexpr uint32_t half_bytes(int hkv) { return (uint32_t)hkv * kPage * 128; }
+__host__ __device__ constexpr uint32_t stage_bytes(int hkv) { return 4 * half_bytes(hkv); }
+
+// CTAs an SM that few KV heads leave room for, and the ring's stages.
+constexpr int ctas_per_sm(int hkv) { return hkv >= 5 ? 1 : hkv >= 3 ? 2 : 4; }
+constexpr int stages_of(int hkv) {
+    const int n = (int)(216u * 1024u / ctas_per_sm(hkv) / stage_bytes(hkv));
+    return n < kMaxStages ? n : kMaxStages;
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void grid_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// RT: blocks of 16 rows.
+template <int RT>
+__global__ void __launch_bounds__(288, 1)
+    few_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    const __grid_constant__ RowsArgs a, int stages) {
+    constexpr unsigned kAll = 0xffffffffu;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), ring = (raw + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hkv = a.hkv;
+    const uint32_t half = half_bytes(hkv), stage_size = stage_bytes(hkv);
+    const uint32_t full_k = ring + stages * stage_size, full_v = full_k + 8 * kMaxStages, empty = full_v + 8 * kMaxStages;
+    int *page_ok = reinterpret_cast<int *>(smem_raw + (empty + 8 * kMaxStages - raw));
+    int *prefix = page_ok + kMaxStages;
+    const int worker = blockIdx.x;
+    if (!a.early) grid_wait();
+    if (warp == 0) {
+        count_tiles<kPage>(a, prefix, a.max_rows, worker == 0 ? &g_status : nullptr);
+        if (lane == 0) {
+            for (int s = 0; s < stages; ++s) {
+                mbar_init(full_k + 8 * s, 1);
+                mbar_init(full_v + 8 * s, 1);
+                mbar_init(empty + 8 * s, hkv);
+            }
+            fence_mbar_init();
+        }
+    }
+    __syncthreads();
+    const int total = prefix[a.batch], per = (total + a.workers - 1) / a.workers;
+    const int lo = (int)min(worker * (long long)per, (long long)total), hi = min(lo + per, total);
+    const int b0 = lo < hi ? request_at(prefix, a.batch, lo) : 0, b_last = lo < hi ? request_at(prefix, a.batch, hi - 1) : -1;
+    int first_ids = -1;
+    if (warp == hkv && lo < hi) {
+        const int p0 = prefix[b0], j = lo - p0 + lane;
+        if (j < min(hi, prefix[b0 + 1]) - p0) first_ids = a.page_table[(size_t)b0 * a.max_pages + j];
+    }
+    if (a.early) grid_wait();
+    zero_rows(a, prefix, worker, threadIdx.x, blockDim.x);
+
+    if (warp == hkv) {
+        // the producer: lanes fetch page ids, lane 0 issues the copies
+        if (lane == 0) {
+            Split s = {0, 0, 0, 0};
+            if (lo < hi && prefix[b_last] >= lo && prefix[b_last + 1] > hi) {
+                const Request r = request_of(a, b_last, nullptr);
+                s.count = (prefix[b_last + 1] - 1) / per - worker + 1;
+                s.first_slot = 2 * worker + (prefix[b_last] > lo);
+                s.out_row = r.first;
+                s.rows = r.rows * a.group;
+            }
+            a.splits[worker] = s;
+            tc::prefetch_tmap(&tk);
+            tc::prefetch_tmap(&tv);
+        }
+        int stage = 0, phase = 0;
+        for (int b = b0; b <= b_last; ++b) {
+            const int p0 = prefix[b], p1 = prefix[b + 1];
+            if (p0 == p1) continue;
+            const int j0 = max(lo, p0) - p0, j1 = min(hi, p1) - p0;
+            const int32_t *row = a.page_table + (size_t)b * a.max_pages;
+            for (int jb = j0; jb < j1; jb += 32) {
+                const int mine = b == b0 && jb == j0 ? first_ids : jb + lane < j1 ? row[jb + lane] : -1;
+                for (int j = jb; j < min(jb + 32, j1); ++j) {
+                    const int id = __shfl_sync(kAll, mine, j - jb);
+                    if (lane == 0) {
+                        mbar_wait(empty + 8 * stage, phase ^ 1, &g_status);
+                        const bool ok = id >= 0 && id < a.num_pages;
+                        page_ok[stage] = ok;
+                        if (ok) {
+                            const uint32_t k = ring + stage * stage_size, v = k + 2 * half;
+                            mbar_arrive_expect_tx(full_k + 8 * stage, 2 * half);
+                            tc::tma_load_3d(k, &tk, 0, id * kPage, 0, full_k + 8 * stage);
+                            tc::tma_load_3d(k + half, &tk, 64, id * kPage, 0, full_k + 8 * stage);
+                            mbar_arrive_expect_tx(full_v + 8 * stage, 2 * half);
+                            tc::tma_load_3d(v, &tv, 0, id * kPage, 0, full_v + 8 * stage);
+                            tc::tma_load_3d(v + half, &tv, 64, id * kPage, 0, full_v + 8 * stage);
+                        } else {
+                            atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
+                            mbar_arrive(full_k + 8 * stage);
+                            mbar_arrive(full_v + 8 * stage);
+                        }
+                    }
+                    if (++stage == stages) stage = 0, phase ^= 1;
+                }
+            }
+        }
+        return;
+    }
+
+    const int G = a.group, quad = lane >> 2, pair = 2 * (lane & 3);
+    // a lane's rows of ldmatrix: K, 8 keys by 8 dims each (keys 0..7, two chunks; keys 8..15); V, transposed, the other way round
+    const uint32_t at_k = warp * 2048 + ((lane >> 4) * 8 + (lane & 7)) * 128, chunk_k = (lane >> 3) & 1;
+    const uint32_t at_v = warp * 2048 + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128, chunk_v = lane >> 4;
+    int stage = 0, phase = 0;
+    for (int b = b0; b <= b_last; ++b) {
+        const int p0 = prefix[b], p1 = prefix[b + 1];
+        if (p0 == p1) continue;
+        const int j0 = max(lo, p0) - p0, j1 = min(hi, p1) - p0;
+        const Request r = request_of(a, b, nullptr);
+        const int rows = r.rows * G;
+        uint32_t qf[RT][8][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = rt * 16 + quad + 8 * e;
+                const bool live = row < rows;
+                const uint16_t *src = a.q + (r.first + (G == 2 ? row >> 1 : row)) * a.ldq + (warp * G + (G == 2 ? row & 1 : 0)) * 128 + pair;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    qf[rt][kk][e] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * kk) : 0u;
+                    qf[rt][kk][e + 2] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * kk + 8) : 0u;
+                }
+            }
+        // the rows that each of the lane's rows sees among the drafted ones: ancestors double their reach every round
+        uint32_t seen[RT][2];
+        if (a.tree && j1 * kPage > r.past) {
+            int up = lane < r.rows ? parent_of(a, r.first, lane, &g_status) : -1;
+            uint32_t mine = 1u << lane;
+            if (!a.parents) {
+                mine = 0xffffffffu >> (31 - lane);
+            } else {
+#pragma unroll
+                for (int n = 0; n < 5; ++n) {
+                    const uint32_t theirs = __shfl_sync(kAll, mine, up & 31);
+                    const int next = __shfl_sync(kAll, up, up & 31);
+                    if (up >= 0) mine |= theirs, up = next;
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) seen[rt][e] = __shfl_sync(kAll, mine, ((rt * 16 + quad + 8 * e) >> (G - 1)) & 31);
+        }
+        float o[RT][16][4], m[RT][2], l[RT][2];
+        bool odd = false;  // a drafted value that is not finite was met
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            m[rt][0] = m[rt][1] = -INFINITY, l[rt][0] = l[rt][1] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) o[rt][n][0] = o[rt][n][1] = o[rt][n][2] = o[rt][n][3] = 0.f;
+        }
+        for (int j = j0; j < j1; ++j) {
+            const uint32_t k = ring + stage * stage_size, v = k + 2 * half;
+            mbar_wait(full_k + 8 * stage, phase, &g_status);
+            const bool ok = page_ok[stage];
+            bool wrote = false;
+            float s[RT][2][4];
+            if (ok) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) s[rt][n][0] = s[rt][n][1] = s[rt][n][2] = s[rt][n][3] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    uint32_t f[4];
+                    ldmatrix4(f, k + (kk >> 2) * half + at_k + (((2 * (kk & 3) + chunk_k) ^ (lane & 7)) << 4));
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        mma16816(s[rt][0], qf[rt][kk], f[0], f[1]);
+                        mma16816(s[rt][1], qf[rt][kk], f[2], f[3]);
+                    }
+                }
+                const int behind = r.past - j * kPage;  // keys of this page that every row sees
+                if (behind < kPage) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const int t = n * 8 + pair + (x & 1), d = t - behind;
+                                if (d >= 0 && !(a.tree && d < r.rows && (seen[rt][x >> 1] >> d & 1))) s[rt][n][x] = -INFINITY;
+                            }
+                }
+                uint32_t hi_p[RT][4], lo_p[RT][4];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    float alpha[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(fmaxf(s[rt][0][2 * e], s[rt][0][2 * e + 1]), fmaxf(s[rt][1][2 * e], s[rt][1][2 * e + 1]));
+                        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2)) * a.scale_log2;
+                        const float next = mx > m[rt][e] + kSlack ? mx : m[rt][e];
+                        alpha[e] = next == m[rt][e] ? 1.f : exp2_approx(m[rt][e] - next);
+                        m[rt][e] = next;
+                        const float ref = next == -INFINITY ? 0.f : next;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int x = 2 * e; x < 2 * e + 2; ++x) s[rt][n][x] = exp2_approx(fmaf(s[rt][n][x], a.scale_log2, -ref));
+                        l[rt][e] = l[rt][e] * alpha[e] + ((s[rt][0][2 * e] + s[rt][0][2 * e + 1]) + (s[rt][1][2 * e] + s[rt][1][2 * e + 1]));
+                    }
+                    if (__any_sync(kAll, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) {
+                            o[rt][n][0] *= alpha[0], o[rt][n][1] *= alpha[0];
+                            o[rt][n][2] *= alpha[1], o[rt][n][3] *= alpha[1];
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = s[rt][n][2 * e], y = s[rt][n][2 * e + 1];
+                            const uint32_t w = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+                            hi_p[rt][2 * n + e] = w;
+                            lo_p[rt][2 * n + e] = pack_bf16x2(x - bf16lo(w), y - bf16hi(w));
+                        }
+                }
+                mbar_wait(full_v + 8 * stage, phase, &g_status);
+                if (behind < kPage) {
+                    // Slots that hold no key are zeroed, and of drafted values what is not finite, so that a probability
+                    // of 0 meets nothing that it would not cancel; the rows that see such a value get it at the end.
+                    const int n_keys = r.keys - j * kPage;
+                    for (int c = max(behind, 0) * 16 + lane; c < kPage * 16; c += 32) {
+                        const int t = c >> 4;
+                        const uint32_t addr = v + (c >> 3 & 1) * half + warp * 2048 + t * 128 + (c & 7) * 16;
+                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        if (t < n_keys) {
+                            const uint4 x = lds128(addr);
+                            w = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+                            if (w.x == x.x && w.y == x.y && w.z == x.z && w.w == x.w) continue;
+                            odd = true;
+                        }
+                        tc::st_shared_v4(addr, w.x, w.y, w.z, w.w);
+                    }
+                    wrote = true;
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                    uint32_t f[4];
+                    ldmatrix4_trans(f, v + (c >> 3) * half + at_v + ((((c & 7) + chunk_v) ^ (lane & 7)) << 4));
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        mma16816(o[rt][c], hi_p[rt], f[0], f[1]);
+                        mma16816(o[rt][c + 1], hi_p[rt], f[2], f[3]);
+                        mma16816(o[rt][c], lo_p[rt], f[0], f[1]);
+                        mma16816(o[rt][c + 1], lo_p[rt], f[2], f[3]);
+                    }
+                }
+            } else {
+                mbar_wait(full_v + 8 * stage, phase, &g_status);
+            }
+            if (wrote) tc::fence_proxy_async_smem();  // before the next copy into these bytes
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * stage);
+            if (++stage == stages) stage = 0, phase ^= 1;
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[rt][e] += __shfl_xor_sync(kAll, l[rt][e], 1);
+                l[rt][e] += __shfl_xor_sync(kAll, l[rt][e], 2);
+            }
+        if (__any_sync(kAll, odd)) {
+            const int32_t *row = a.page_table + (size_t)b * a.max_pages;
+            for (int pos = max(r.past, j0 * kPage); pos < min(r.keys, j1 * kPage); ++pos) {
+                const int id = row[pos >> 4];
+                if (id < 0 || id >= a.num_pages) continue;
+                const uint16_t *src = a.v_pages + (((size_t)id * kPage + (pos & 15)) * hkv + warp) * 128 + pair;
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    const uint32_t w = not_finite(*reinterpret_cast<const uint32_t *>(src + 8 * n));
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (seen[rt][x >> 1] >> (pos - r.past) & 1) o[rt][n][x] += x & 1 ? bf16hi(w) : bf16lo(w);
+                }
+            }
+        }
+        const bool whole = lo <= p0 && p1 <= hi;
+        const int slot = 2 * worker + (p0 > lo);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = rt * 16 + quad + 8 * e;
+                if (row >= rows) continue;
+                if (whole) {
+                    const float inv = l[rt][e] > 0.f ? 1.f / l[rt][e] : l[rt][e];
+                    uint16_t *dst = a.out + ((size_t)(r.first + (row >> (G - 1))) * a.hq + warp * G + (row & (G - 1))) * 128 + pair;
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+                        *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack_bf16x2(o[rt][n][2 * e] * inv, o[rt][n][2 * e + 1] * inv);
+                } else {
+                    const size_t at = ((size_t)slot * hkv + warp) * a.block_rows + row;
+                    float *dst = a.acc + at * 128 + pair;
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+                        *reinterpret_cast<float2 *>(dst + 8 * n) = make_float2(o[rt][n][2 * e], o[rt][n][2 * e + 1]);
+                    if (pair == 0) *reinterpret_cast<float2 *>(a.ml + 2 * at) = make_float2(m[rt][e], l[rt][e]);
+                }
+            }
+    }
+}
+
+// Merges the jobs that span several workers: rows of up to 8 partials by a
+// warp each, rows of more by a CTA, whose warps take every eighth.  Partials
+// are added in the order of their workers, 4 loads in flight a lane.
+__global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const __grid_constant__ RowsArgs a) {
+    constexpr unsigned kAll = 0xffffffffu;
+    constexpr int kWarps = kMergeThreads / 32, kEach = kMaxWorkers / kMergeThreads;
+    __shared__ int start[kMaxWorkers + 1], sums[kWarps];
+    __shared__ float4 s_acc[kWarps][32];
+    __shared__ float2 s_ml[kWarps];
+    grid_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // steps of a CTA that each split job takes, and their prefix sums
+    int steps[kEach], mine = 0;
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+        const int w = threadIdx.x * kEach + x;
+        steps[x] = 0;
+        if (w < a.workers) {
+            const Split s = a.splits[w];
+            const int n = s.rows * a.hkv;
+            steps[x] = s.count == 0 ? 0 : s.count <= kWarps ? (n + kWarps - 1) / kWarps : n;
+        }
+        mine += steps[x];
+    }
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kAll, before, o);
+        if (lane >= o) before += u;
+    }
+    if (lane == 31) sums[warp] = before;
+    __syncthreads();
+    before -= mine;
+    for (int x = 0; x < warp; ++x) before += sums[x];
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+        start[threadIdx.x * kEach + x] = before;
+        before += steps[x];
+    }
+    if (threadIdx.x == kMergeThreads - 1) start[kMaxWorkers] = before;
+    __syncthreads();
+    const int total = start[kMaxWorkers];
+    for (int step = blockIdx.x; step < total; step += gridDim.x) {
+        int l = 0, r = kMaxWorkers - 1;
+        while (l < r) {  // the split that has this step
+            const int mid = (l + r) >> 1;
+            if (start[mid + 1] > step) r = mid; else l = mid + 1;
+        }
+        const Split s = a.splits[l];
+        const bool team = s.count > kWarps;
+        const int item = team ? step - start[l] : (step - start[l]) * kWarps + warp;
+        const bool live = item < s.rows * a.hkv;
+        const int head = live ? item / s.rows : 0, row = live ? item % s.rows : 0;
+        const int first = team ? warp : 0, by = team ? kWarps : 1;
+        const auto at = [&](int i) {
+            const size_t slot = i == 0 ? s.first_slot : 2 * (l + i);
+            return (slot * a.hkv + head) * a.block_rows + row;
+        };
+        float m = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const auto add = [&](float2 ml, float4 v) {
+            const float next = fmaxf(m, ml.x);
+            if (next == -INFINITY) return;  // a worker that saw no key of this row
+            const float old = m == -INFINITY ? 0.f : exp2_approx(m - next), now = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - next);
+            sum = sum * old + ml.y * now;
+            acc.x = acc.x * old + v.x * now, acc.y = acc.y * old + v.y * now;
+            acc.z = acc.z * old + v.z * now, acc.w = acc.w * old + v.w * now;
+            m = next;
+        };
+        if (live)
+            for (int i = first; i < s.count; i += 4 * by) {
+                float2 ml[4];
+                float4 v[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (i + x * by < s.count) {
+                        const size_t p = at(i + x * by);
+                        ml[x] = __ldcg(reinterpret_cast<const float2 *>(a.ml) + p);
+                        v[x] = __ldcg(reinterpret_cast<const float4 *>(a.acc) + p * 32 + lane);
+                    }
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (i + x * by < s.count) add(ml[x], v[x]);
+            }
+        if (team) {
+            s_acc[warp][lane] = acc;
+            if (lane == 0) s_ml[warp] = make_float2(m, sum);
+            __syncthreads();
+            if (warp == 0) {
+                m = -INFINITY, sum = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int x = 0; x < kWarps; ++x) add(s_ml[x], s_acc[x][lane]);
+            }
+            __syncthreads();
+        }
+        if (live && (!team || warp == 0)) {
+            const float inv = sum > 0.f ? 1.f / sum : sum;
+            uint16_t *dst = a.out + ((size_t)(s.out_row + row / a.group) * a.hq + head * a.group + row % a.group) * 128;
+            reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        }
+    }
+}
+
+struct Plan {
+    bool few;
+    int workers, block_rows;
+    size_t acc, ml, splits, total;
+};
+
+// Rows times group up to which the rows of a request are few.
+constexpr int kFewRows = 32;
+
+int sm_count() {
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+bool plan_of(int max_rows, int hq, int hkv, Plan *p) {
+    const int group = hq / hkv, sms = sm_count();
+    if (sms <= 0) return false;
+    p->few = (long long)max_rows * group <= kFewRows;
+    p->workers = p->few ? sms * ctas_per_sm(hkv) : rows_tiles_workers(hkv);
+    if (p->workers > kMaxWorkers) p->workers = kMaxWorkers;
+    p->block_rows = p->few ? (max_rows * group <= 16 ? 16 : 32) : 128;
+    const size_t rows = (size_t)2 * p->workers * hkv * p->block_rows;
+    p->splits = 0;
+    p->ml = (sizeof(Split) * p->workers + 255) & ~(size_t)255;
+    p->acc = p->ml + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
+    p->total = p->acc + rows * 128 * sizeof(float);
+    return true;
+}
+
+// Pools as {dims, token slots, KV heads}: a box is one page's 64 dims of all
+// heads (heads: 1 for one), the rows of 16 tokens of a head together.
+bool make_pool_tmap(CUtensorMap *map, const void *base, int hkv, long long slots, int heads) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {128, (cuuint64_t)slots, (cuuint64_t)hkv};
+    cuuint64_t strides[2] = {(cuuint64_t)hkv * 256, 256};
+    cuuint32_t box[3] = {64, 16, (cuuint32_t)heads}, estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Packed query rows as {dims, heads, rows}: a box is 64 dims of a KV head's
+// `group` heads in 128 / group rows.
+bool make_query_tmap(CUtensorMap *map, const void *base, int hq, long long rows, long long ld, int group) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {128, (cuuint64_t)hq, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {256, (cuuint64_t)ld * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)}, estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// Enough for calls of max_rows or fewer, whichever kernel they take.
+size_t rows_attn_workspace_bytes(int max_rows, int n_q_heads, int n_kv_heads) {
+    const int group = n_q_heads / n_kv_heads, steps[3] = {16 / group, kFewRows / group, max_rows};
+    size_t most = 0;
+    for (int n : steps) {
+        Plan p;
+        if (!plan_of(n < max_rows ? n : max_rows, n_q_heads, n_kv_heads, &p)) return 0;
+        if (p.total > most) most = p.total;
+    }
+    return most;
+}
+
+cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float scale, cudaStream_t stream) {
+    Plan plan;
+    if (!plan_of(x.max_rows, p.n_q_heads, p.n_kv_heads, &plan)) return cudaErrorInvalidDevice;
+    RowsArgs a = {};
+    uint8_t *ws = static_cast<uint8_t *>(p.workspace);
+    a.q = static_cast<const uint16_t *>(x.q);
+    a.v_pages = static_cast<const uint16_t *>(x.v_pages);
+    a.out = static_cast<uint16_t *>(x.out);
+    a.ldq = x.ldq ? x.ldq : (long long)p.n_q_heads * 128;
+    a.cu = x.cu_seqlens;
+    a.past = x.past;
+    a.parents = x.parents;
+    a.page_table = x.page_table;
+    a.acc = reinterpret_cast<float *>(ws + plan.acc);
+    a.ml = reinterpret_cast<float *>(ws + plan.ml);
+    a.splits = reinterpret_cast<Split *>(ws + plan.splits);
+    a.batch = x.batch;
+    a.rows = x.rows;
+    a.max_rows = x.max_rows;
+    a.hq = p.n_q_heads;
+    a.hkv = p.n_kv_heads;
+    a.group = p.n_q_heads / p.n_kv_heads;
+    a.max_pages = p.max_pages_per_seq;
+    a.num_pages = p.num_pages;
+    a.block_rows = plan.block_rows;
+    a.workers = plan.workers;
+    a.tree = x.tree;
+    a.early = (p.abi_version >= 2 && p.stable_metadata >= 1) ? 1 : 0;
+    a.scale_log2 = scale * kLog2e;
+    CUtensorMap tk, tv;
+    const long long slots = (long long)p.num_pages * kPage;
+    const int box_heads = plan.few ? a.hkv : 1;
+    if (!make_pool_tmap(&tk, x.k_pages, a.hkv, slots, box_heads) || !make_pool_tmap(&tv, x.v_pages, a.hkv, slots, box_heads))
+        return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e;
+    if (plan.few) {
+        const int stages = stages_of(a.hkv);
+        cfg.gridDim = dim3((unsigned)plan.workers);
+        cfg.blockDim = dim3((a.hkv + 1) * 32);
+        cfg.dynamicSmemBytes = 1024 + stages * stage_bytes(a.hkv) + 3 * 8 * kMaxStages + 4 * kMaxStages + 4 * (x.batch + 1);
+        const auto kernel = plan.block_rows == 16 ? few_rows_kernel<1> : few_rows_kernel<2>;
+        // the most of any call, so that host threads' calls cannot lower one another's
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return e;
+        e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, a, stages);
+    } else {
+        CUtensorMap tq;
+        if (!make_query_tmap(&tq, x.q, a.hq, x.rows, a.ldq, a.group)) return cudaErrorInvalidValue;
+        e = launch_rows_tiles(a, tq, tk, tv, stream);
+    }
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(2 * sm_count()));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, merge_rows_kernel, a);
+}
+
+unsigned int status_read_clear_rows_attn(cudaStream_t stream, cudaError_t *err) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status, sizeof v, 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && v) e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) {
+        if (err) *err = e;
+        return v;
+    }
+    return v | status_read_clear_rows_tiles(stream, err);
+}
+
+}  // namespace qa
