@@ -20,6 +20,13 @@ Rotary positions with several axes, and a KV cache held in 4 bits:
     qa_kvq_read          cached rows back as bf16
     qa_kvq_decode_attn   paged GQA decode over the 4-bit pages
     qa_kvq_decode_step   norm, rotation, quantised append and decode of one token
+
+Drafted tokens over the paged bf16 cache, and cross attention:
+
+    qa_append_rows       rows normed, rotated and written to their pages
+    qa_tree_attn         a tree of drafted rows over the cache
+    qa_cross_attn        packed rows over paged states of another length
+    qa_tree_accept       the accepted path, its rows moved behind the cache
 """
 from __future__ import annotations
 
@@ -36,13 +43,14 @@ __all__ = [
     "qa_encoder_workspace_size", "qa_encoder_layer", "qa_linear", "qa_layer_norm", "ENCODER_WEIGHT_NAMES",
     "qa_rope_axes", "qa_rope_rows", "qa_kvq_page_bytes", "qa_kvq_write", "qa_kvq_read",
     "qa_kvq_decode_workspace_size", "qa_kvq_decode_attn", "qa_kvq_decode_step",
+    "qa_append_rows", "qa_rows_attn_workspace_size", "qa_tree_attn", "qa_cross_attn", "qa_tree_accept",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_PKG, "libqa.so")
 
 DEVICE_STATUS_BITS = {0x1: "bad page id", 0x2: "bad length", 0x4: "bad segments", 0x8: "timeout",
-                      0x10: "bad position"}
+                      0x10: "bad position", 0x20: "bad tree"}
 
 
 class QAError(RuntimeError):
@@ -153,6 +161,16 @@ def _load():
     lib.qa_kvq_decode_attn.argtypes = [P, P, P, P, P, I, P, PP]
     lib.qa_kvq_decode_step.restype = I
     lib.qa_kvq_decode_step.argtypes = [P, L, P, P, L, PR, P, P, P, P, I, P, PP]
+    lib.qa_append_rows.restype = I
+    lib.qa_append_rows.argtypes = [P, L, P, L, P, L, P, P, P, I, I, P, P, P, P, L, PR, PP]
+    lib.qa_rows_attn_workspace_size.restype = S
+    lib.qa_rows_attn_workspace_size.argtypes = [I, PP]
+    lib.qa_tree_attn.restype = I
+    lib.qa_tree_attn.argtypes = [P, L, P, P, P, I, I, I, P, P, P, P, PP]
+    lib.qa_cross_attn.restype = I
+    lib.qa_cross_attn.argtypes = [P, L, P, P, I, I, I, P, P, P, P, PP]
+    lib.qa_tree_accept.restype = I
+    lib.qa_tree_accept.argtypes = [P, P, P, P, P, I, I, I, P, I, PA, PA, P, P, P, PP]
     lib.qa_device_status.restype = I
     lib.qa_device_status.argtypes = [P]
     lib.qa_check_bounded_wait.restype = I
@@ -730,6 +748,75 @@ def qa_kvq_decode_step(q, k, v, q_gain, k_gain, page_table, seq_lens, k_pages, v
     return _done("qa_kvq_decode_step", _fast().kvq_decode_step(
         q, k_pages, v_pages, page_table, seq_lens, out, workspace, scale, stream, debug_checks, stable_metadata, k, v,
         q_gain, k_gain, positions, pair_axis, rms_eps, rope_theta))
+
+
+def qa_append_rows(q, k, v, cu_seqlens, page_table, k_pages, v_pages, q_out=None, *, n_past=None, parents=None,
+                   positions=None, q_gain=None, k_gain=None, rms_eps=1e-6, rope_theta=1e6, pair_axis=None, rotate=True,
+                   stream=None, debug_checks=False, stable_metadata=False):
+    """Writes key and value rows to their pages, the keys normed (gains
+    float32 [128], both or neither) and rotated on the way, and gives the
+    queries normed and rotated.  q bf16 [T,Hq,128] or None; k/v bf16
+    [T,Hkv,128] (rows may lie apart); cu_seqlens int32 [B+1]; page_table int32
+    [B,max_pages]; pools bf16 [P,16,Hkv,128], written in place; n_past int32
+    [B]: request r's row i is cached at n_past[r] + i (default 0).  The rotary
+    position is positions (int32 [T] or [n_axes,T], with pair_axis as for
+    qa_rope_rows), or n_past[r] plus the row's depth: parents int32 [T], the
+    row of its request that each row continues, -1 for one that continues the
+    cache (None: the row before).  rotate=False: no norm and no rotation.
+    q_out=q works in place.  Returns q_out (None without q)."""
+    return _done("qa_append_rows", _fast().append_rows(
+        q, k, v, cu_seqlens, page_table, k_pages, v_pages, q_out, n_past, parents, positions, q_gain, k_gain, rms_eps,
+        rope_theta, pair_axis, rotate, stream, debug_checks, stable_metadata))
+
+
+def qa_rows_attn_workspace_size(max_rows: int, *, n_q_heads=16, n_kv_heads=8) -> int:
+    """Bytes of workspace that qa_tree_attn and qa_cross_attn need for
+    requests of up to max_rows rows on the current device."""
+    p = _lib.qa_attn_default_params()
+    p.n_q_heads, p.n_kv_heads, p.num_pages, p.max_pages_per_seq = n_q_heads, n_kv_heads, 1, 1
+    n = _lib.qa_rows_attn_workspace_size(int(max_rows), ctypes.byref(p))
+    if n == 0:
+        raise QAError("qa_rows_attn_workspace_size", -1, qa_last_error())
+    return int(n)
+
+
+def qa_tree_attn(q, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, out=None, *, parents=None,
+                 workspace=None, scale=0.0, stream=None, debug_checks=False, stable_metadata=False):
+    """Attention of drafted rows over the cache: row i of request r attends to
+    its n_past[r] cached positions, to itself and to its ancestors, the rows
+    being cached at n_past[r] + i (qa_append_rows).  q bf16 [T,Hq,128] (rows
+    may lie apart); cu_seqlens, n_past, parents, page_table and pools as for
+    qa_append_rows; max_rows: the most rows of a request, up to 64.
+    workspace: uint8, qa_rows_attn_workspace_size(max_rows, ...) bytes
+    (allocated here if omitted), reusable across calls on one stream.  Returns
+    out bf16 [T,Hq,128]; rows from cu_seqlens[-1] on are left as they were."""
+    return _done("qa_tree_attn", _fast().tree_attn(
+        q, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, out, parents, workspace, scale, stream,
+        debug_checks, stable_metadata))
+
+
+def qa_cross_attn(q, cu_seqlens, seq_lens, page_table, k_pages, v_pages, max_rows, out=None, *, workspace=None,
+                  scale=0.0, stream=None, debug_checks=False, stable_metadata=False):
+    """Cross attention: every row of request r attends to its seq_lens[r]
+    paged states (written by qa_append_rows with rotate=False, for example).
+    Any max_rows >= 1; the rest as for qa_tree_attn."""
+    return _done("qa_cross_attn", _fast().cross_attn(
+        q, cu_seqlens, seq_lens, page_table, k_pages, v_pages, max_rows, out, None, workspace, scale, stream,
+        debug_checks, stable_metadata))
+
+
+def qa_tree_accept(draft, target, parents, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, n_accepted=None,
+                   path=None, next_token=None, *, stream=None, debug_checks=False, stable_metadata=False):
+    """Settles a step of drafted tokens: from row 0 of each request on, the
+    first row whose parent is accepted and whose token (draft int32 [T]) is
+    the one the model chose there (target int32 [T]) is accepted too, and the
+    accepted rows are moved in every pool to n_past and on.  k_pages and
+    v_pages: lists of the layers' pools (up to 64, of one shape).  Returns
+    (n_accepted int32 [B], path int32 [B,max_rows] with -1 behind it,
+    next_token int32 [B])."""
+    return _done("qa_tree_accept", _fast().tree_accept(
+        draft, target, parents, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, n_accepted, path, next_token,
+        stream, debug_checks, stable_metadata))
 
 
 def qa_check_bounded_wait(limit_us=20000, stream=None) -> None:

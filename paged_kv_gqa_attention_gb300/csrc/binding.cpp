@@ -1,6 +1,6 @@
-// Python binding of the rotary-position and 4-bit-cache calls: reads torch
-// tensors, checks them and passes addresses, sizes and the current stream to
-// the qa_* entry point of the same name (qa.h).
+// Python binding of the rotary-position, 4-bit-cache and drafted-row calls:
+// reads torch tensors, checks them and passes addresses, sizes and the
+// current stream to the qa_* entry point of the same name (qa.h).
 //
 // These calls are made once a layer and token, and a small one's kernel is
 // done in 2 to 7 us.  Marshalled in Python, eight tensors' attributes, the
@@ -448,6 +448,174 @@ PyObject *decode(PyObject *const *a, bool step) {
 PyObject *kvq_decode_attn(PyObject *const *a) { return decode(a, false); }
 PyObject *kvq_decode_step(PyObject *const *a) { return decode(a, true); }
 
+// bf16 pools [num_pages, 16, n_kv_heads, 128] of one shape.
+Pools bf16_pools(PyObject *ko, PyObject *vo, int device) {
+    const at::Tensor &k = tensor(ko, "k_pages"), &v = tensor(vo, "v_pages");
+    void *kp = address(k, "k_pages", at::kBFloat16, 4, device), *vp = address(v, "v_pages", at::kBFloat16, 4, device);
+    if (k.size(1) != 16 || k.size(3) != 128 || k.sizes() != v.sizes())
+        refuse(PyExc_ValueError, "pools must be bfloat16 [num_pages, 16, n_kv_heads, 128], of one shape");
+    return {kp, vp, k.size(0), k.size(2)};
+}
+
+const int32_t *parents_of(PyObject *o, int64_t n_rows, int device) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, "parents");
+    const int32_t *p = static_cast<const int32_t *>(address(t, "parents", at::kInt, 1, device));
+    if (t.size(0) != n_rows) refuse(PyExc_ValueError, "parents must be [total_rows]");
+    return p;
+}
+
+// (q, k, v, cu_seqlens, page_table, k_pages, v_pages, q_out, n_past, parents, positions, q_gain, k_gain, rms_eps, rope_theta,
+// pair_axis, rotate, stream, debug_checks, stable_metadata)
+PyObject *append_rows(PyObject *const *a) {
+    const int device = current_device();
+    const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const Rows rk = rows(k, "k", device), rv = rows(v, "v", device);
+    const int64_t T = k.size(0), Hkv = k.size(1), D = k.size(2);
+    const Pools pools = bf16_pools(a[5], a[6], device);
+    if (k.sizes() != v.sizes() || Hkv != pools.hkv || D != 128) refuse(PyExc_ValueError, "inconsistent append shapes");
+    const RowArgs r = row_args(a[3], a[8], a[4], device);
+    const int32_t *parents = parents_of(a[9], T, device);
+    const Stream s = stream_of(a[17], device);
+    Rows rq = {nullptr, 0}, ro = {nullptr, 0};
+    at::Tensor q_made;
+    int64_t Hq = Hkv;
+    if (a[0] != Py_None) {
+        const at::Tensor &q = tensor(a[0], "q");
+        rq = rows(q, "q", device);
+        Hq = q.size(1);
+        if (!shape_is(q, T, Hq, D)) refuse(PyExc_ValueError, "inconsistent append shapes");
+        if (a[7] == Py_None) {
+            q_made = made(s, {T, Hq, D}, at::kBFloat16, device);
+            ro = {q_made.data_ptr(), 0};
+        } else {
+            const at::Tensor &t = tensor(a[7], "q_out");
+            ro = rows(t, "q_out", device);
+            if (!shape_is(t, T, Hq, D)) refuse(PyExc_ValueError, "q_out must have q's shape");
+        }
+    } else if (a[7] != Py_None) {
+        refuse(PyExc_ValueError, "q_out is given without q");
+    }
+    Rope rope;
+    const bool rotate = as_bool(a[16], "rotate");
+    if (rotate) rope_of(rope, a[10], T, a[11], a[12], a[15], D, a[13], a[14], device);
+    else if (a[10] != Py_None || a[11] != Py_None || a[12] != Py_None || a[15] != Py_None)
+        refuse(PyExc_ValueError, "positions, gains and pair_axis are given without rotation");
+    const qa_attn_params p = params_of(Hq, Hkv, D, pools.pages, r.width, 0.0, s.raw, a[18], a[19]);
+    const int n = as_int(T, "total_rows"), batch = as_int(r.batch, "batch");
+    const qa_status st = call([&]() noexcept {
+        return qa_append_rows(rq.p, rq.ld, rk.p, rk.ld, rv.p, rv.ld, r.cu, r.past, parents, batch, n, r.table, pools.k, pools.v,
+                              ro.p, ro.ld, rotate ? &rope.r : nullptr, &p);
+    });
+    if (st != QA_STATUS_OK) return PyLong_FromLong(st);
+    if (a[0] == Py_None) Py_RETURN_NONE;
+    return object_of(a[7], std::move(q_made));
+}
+
+// (q, cu_seqlens, n_past or seq_lens, page_table, k_pages, v_pages, max_rows, out, parents, workspace, scale, stream,
+// debug_checks, stable_metadata)
+PyObject *rows_attn(PyObject *const *a, bool tree) {
+    const int device = current_device();
+    const at::Tensor &q = tensor(a[0], "q");
+    const Rows rq = rows(q, "q", device);
+    const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2);
+    const Pools pools = bf16_pools(a[4], a[5], device);
+    if (a[2] == Py_None) refuse(PyExc_TypeError, "%s must be a torch.Tensor", tree ? "n_past" : "seq_lens");
+    const RowArgs r = row_args(a[1], a[2], a[3], device);
+    const int32_t *parents = parents_of(a[8], T, device);
+    const int max_rows = as_int(as_long(a[6], "max_rows"), "max_rows");
+    const Stream s = stream_of(a[11], device);
+    at::Tensor out_made, ws_made;
+    void *out;
+    if (a[7] == Py_None) {
+        out_made = made(s, {T, Hq, D}, at::kBFloat16, device);
+        out = out_made.data_ptr();
+    } else {
+        const at::Tensor &t = tensor(a[7], "out");
+        out = address(t, "out", at::kBFloat16, 3, device);
+        if (!shape_is(t, T, Hq, D)) refuse(PyExc_ValueError, "out must have q's shape");
+    }
+    qa_attn_params p = params_of(Hq, pools.hkv, D, pools.pages, r.width, as_double(a[10], "scale"), s.raw, a[12], a[13]);
+    const int n = as_int(T, "total_rows"), batch = as_int(r.batch, "batch");
+    if (a[9] == Py_None) {
+        const size_t need = qa_rows_attn_workspace_size(max_rows, &p);
+        if (!need) return PyLong_FromLong(QA_STATUS_INVALID_PARAMS);
+        ws_made = made(s, {(int64_t)need}, at::kByte, device);
+        p.workspace = ws_made.data_ptr();
+        p.workspace_bytes = need;
+    } else {
+        const at::Tensor &t = tensor(a[9], "workspace");
+        on_device(t, "workspace", device);
+        if (!t.is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+        p.workspace = t.data_ptr();
+        p.workspace_bytes = (size_t)t.nbytes();
+    }
+    const qa_status st = call([&]() noexcept {
+        return tree ? qa_tree_attn(rq.p, rq.ld, r.cu, r.past, parents, batch, n, max_rows, r.table, pools.k, pools.v, out, &p)
+                    : qa_cross_attn(rq.p, rq.ld, r.cu, r.past, batch, n, max_rows, r.table, pools.k, pools.v, out, &p);
+    });
+    if (st != QA_STATUS_OK) return PyLong_FromLong(st);
+    return object_of(a[7], std::move(out_made));
+}
+PyObject *tree_attn(PyObject *const *a) { return rows_attn(a, true); }
+PyObject *cross_attn(PyObject *const *a) { return rows_attn(a, false); }
+
+PyObject *pool_list(PyObject *o, const char *name) {
+    if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(PyExc_TypeError, "%s must be a list or tuple of pools", name);
+    return o;
+}
+
+// (draft, target, parents, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, n_accepted, path, next_token, stream,
+// debug_checks, stable_metadata)
+PyObject *tree_accept(PyObject *const *a) {
+    const int device = current_device();
+    const at::Tensor &draft = tensor(a[0], "draft"), &target = tensor(a[1], "target");
+    const int32_t *dp = static_cast<const int32_t *>(address(draft, "draft", at::kInt, 1, device));
+    const int32_t *tp = static_cast<const int32_t *>(address(target, "target", at::kInt, 1, device));
+    const int64_t T = draft.size(0);
+    if (target.size(0) != T) refuse(PyExc_ValueError, "target must have draft's shape");
+    const int32_t *parents = parents_of(a[2], T, device);
+    if (a[4] == Py_None) refuse(PyExc_TypeError, "n_past must be a torch.Tensor");
+    const RowArgs r = row_args(a[3], a[4], a[5], device);
+    PyObject *ks = pool_list(a[6], "k_pages"), *vs = pool_list(a[7], "v_pages");
+    const Py_ssize_t layers = PySequence_Fast_GET_SIZE(ks);
+    if (PySequence_Fast_GET_SIZE(vs) != layers || layers > 64)
+        refuse(PyExc_ValueError, "k_pages and v_pages must be as long as each other, at most 64");
+    void *kp[64], *vp[64];
+    int64_t pages = 1, hkv = 1;
+    for (Py_ssize_t i = 0; i < layers; ++i) {
+        const Pools p = bf16_pools(PySequence_Fast_GET_ITEM(ks, i), PySequence_Fast_GET_ITEM(vs, i), device);
+        if (i > 0 && (p.pages != pages || p.hkv != hkv)) refuse(PyExc_ValueError, "the layers' pools must have one shape");
+        pages = p.pages, hkv = p.hkv, kp[i] = p.k, vp[i] = p.v;
+    }
+    const int max_rows = as_int(as_long(a[8], "max_rows"), "max_rows"), batch = as_int(r.batch, "batch"), n = as_int(T, "total_rows");
+    const Stream s = stream_of(a[12], device);
+    at::Tensor made_out[3];
+    int32_t *out[3];
+    const char *const names[3] = {"n_accepted", "path", "next_token"};
+    for (int i = 0; i < 3; ++i) {
+        if (a[9 + i] == Py_None) {
+            made_out[i] = i == 1 ? made(s, {r.batch, max_rows}, at::kInt, device) : made(s, {r.batch}, at::kInt, device);
+            out[i] = static_cast<int32_t *>(made_out[i].data_ptr());
+        } else {
+            const at::Tensor &t = tensor(a[9 + i], names[i]);
+            out[i] = static_cast<int32_t *>(address(t, names[i], at::kInt, i == 1 ? 2 : 1, device));
+            if (t.size(0) != r.batch || (i == 1 && t.size(1) != max_rows))
+                refuse(PyExc_ValueError, "n_accepted and next_token must be [batch], path [batch, max_rows]");
+        }
+    }
+    const qa_attn_params p = params_of(hkv, hkv, 128, pages, r.width, 0.0, s.raw, a[13], a[14]);
+    const qa_status st = call([&]() noexcept {
+        return qa_tree_accept(dp, tp, parents, r.cu, r.past, batch, n, max_rows, r.table, (int)layers, kp, vp, out[0], out[1], out[2], &p);
+    });
+    if (st != QA_STATUS_OK) return PyLong_FromLong(st);
+    PyObject *o[3], *t = nullptr;
+    for (int i = 0; i < 3; ++i) o[i] = object_of(a[9 + i], std::move(made_out[i]));
+    if (o[0] && o[1] && o[2]) t = PyTuple_Pack(3, o[0], o[1], o[2]);
+    for (PyObject *x : o) Py_XDECREF(x);
+    return t;
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != N) {
@@ -466,7 +634,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(rope_rows, 13), ENTRY(kvq_write, 10), ENTRY(kvq_read, 11), ENTRY(kvq_decode_attn, 11),
-                         ENTRY(kvq_decode_step, 19), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(kvq_decode_step, 19), ENTRY(append_rows, 20), ENTRY(tree_attn, 14), ENTRY(cross_attn, 14),
+                         ENTRY(tree_accept, 15), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
