@@ -7,7 +7,7 @@
 // over the request's n_past positions and the row's own ancestors in the tree
 // behind them (tree), or over all its states (cross).
 //
-// Few rows (rows x group up to 32).  Bound by HBM: every key and value is
+// Few rows (rows x group up to 16).  Bound by HBM: every key and value is
 // read once, for all rows of its request and both query heads of its KV head.
 // As in the single-token decode a persistent grid cuts the list of all pages
 // into equal ranges (rows_attn.cuh) and a producer warp streams whole pages,
@@ -17,7 +17,7 @@
 // without a bank conflict.  One consumer warp a KV head: its rows (a query
 // row's heads in turn) are the M of mma.sync m16n8k16, so that S stays in
 // registers as the A operand of P V.  A tcgen05 tile would be 128 rows for
-// these 16 or 32, and its S would have to come back from TMEM for the softmax;
+// these 16, and its S would have to come back from TMEM for the softmax;
 // the tensor pipe is not what bounds.
 //
 // P enters P V as two bf16 terms (p truncated, and the rest rounded): about
@@ -78,8 +78,6 @@ __device__ __forceinline__ void grid_wait() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// RT: blocks of 16 rows.
-template <int RT>
 __global__ void __launch_bounds__(288, 1)
     few_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const __grid_constant__ RowsArgs a, int stages) {
@@ -166,10 +164,10 @@ __global__ void __launch_bounds__(288, 1)
         return;
     }
 
-    const int G = a.group, quad = lane >> 2, pair = 2 * (lane & 3);
+    const int G = a.group, quad = lane >> 2, pair = 2 * (lane & 3), head = warp;
     // a lane's rows of ldmatrix: K, 8 keys by 8 dims each (keys 0..7, two chunks; keys 8..15); V, transposed, the other way round
-    const uint32_t at_k = warp * 2048 + ((lane >> 4) * 8 + (lane & 7)) * 128, chunk_k = (lane >> 3) & 1;
-    const uint32_t at_v = warp * 2048 + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128, chunk_v = lane >> 4;
+    const uint32_t at_k = head * 2048 + ((lane >> 4) * 8 + (lane & 7)) * 128, chunk_k = (lane >> 3) & 1;
+    const uint32_t at_v = head * 2048 + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128, chunk_v = lane >> 4;
     int stage = 0, phase = 0;
     for (int b = b0; b <= b_last; ++b) {
         const int p0 = prefix[b], p1 = prefix[b + 1];
@@ -177,133 +175,115 @@ __global__ void __launch_bounds__(288, 1)
         const int j0 = max(lo, p0) - p0, j1 = min(hi, p1) - p0;
         const Request r = request_of(a, b, nullptr);
         const int rows = r.rows * G;
-        uint32_t qf[RT][8][4];
+        uint32_t qf[8][4];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int e = 0; e < 2; ++e) {
+            const int row = quad + 8 * e;
+            const bool live = row < rows;
+            const uint16_t *src = a.q + (r.first + (row >> (G - 1))) * a.ldq + (head * G + (row & (G - 1))) * 128 + pair;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = rt * 16 + quad + 8 * e;
-                const bool live = row < rows;
-                const uint16_t *src = a.q + (r.first + (G == 2 ? row >> 1 : row)) * a.ldq + (warp * G + (G == 2 ? row & 1 : 0)) * 128 + pair;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    qf[rt][kk][e] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * kk) : 0u;
-                    qf[rt][kk][e + 2] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * kk + 8) : 0u;
-                }
+            for (int kk = 0; kk < 8; ++kk) {
+                qf[kk][e] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * kk) : 0u;
+                qf[kk][e + 2] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * kk + 8) : 0u;
             }
-        // the rows that each of the lane's rows sees among the drafted ones: ancestors double their reach every round
-        uint32_t seen[RT][2];
+        }
+        // the rows that each of the lane's two rows sees among the drafted ones (bit j: row j); reach doubles every round
+        uint32_t seen[2] = {0, 0};
         if (a.tree && j1 * kPage > r.past) {
             int up = lane < r.rows ? parent_of(a, r.first, lane, &g_status) : -1;
-            uint32_t mine = 1u << lane;
-            if (!a.parents) {
-                mine = 0xffffffffu >> (31 - lane);
-            } else {
-#pragma unroll
-                for (int n = 0; n < 5; ++n) {
+            uint32_t mine = a.parents ? 1u << lane : 0xffffffffu >> (31 - lane);
+            if (a.parents)
+                for (int n = 0; n < 4; ++n) {
                     const uint32_t theirs = __shfl_sync(kAll, mine, up & 31);
                     const int next = __shfl_sync(kAll, up, up & 31);
                     if (up >= 0) mine |= theirs, up = next;
                 }
-            }
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) seen[rt][e] = __shfl_sync(kAll, mine, ((rt * 16 + quad + 8 * e) >> (G - 1)) & 31);
+            for (int e = 0; e < 2; ++e) seen[e] = __shfl_sync(kAll, mine, (quad + 8 * e) >> (G - 1));
         }
-        float o[RT][16][4], m[RT][2], l[RT][2];
+        float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         bool odd = false;  // a drafted value that is not finite was met
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            m[rt][0] = m[rt][1] = -INFINITY, l[rt][0] = l[rt][1] = 0.f;
-#pragma unroll
-            for (int n = 0; n < 16; ++n) o[rt][n][0] = o[rt][n][1] = o[rt][n][2] = o[rt][n][3] = 0.f;
-        }
+        for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         for (int j = j0; j < j1; ++j) {
             const uint32_t k = ring + stage * stage_size, v = k + 2 * half;
             mbar_wait(full_k + 8 * stage, phase, &g_status);
             const bool ok = page_ok[stage];
             bool wrote = false;
-            float s[RT][2][4];
             if (ok) {
+                float s[2][4];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) s[rt][n][0] = s[rt][n][1] = s[rt][n][2] = s[rt][n][3] = 0.f;
+                for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
                     uint32_t f[4];
                     ldmatrix4(f, k + (kk >> 2) * half + at_k + (((2 * (kk & 3) + chunk_k) ^ (lane & 7)) << 4));
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        mma16816(s[rt][0], qf[rt][kk], f[0], f[1]);
-                        mma16816(s[rt][1], qf[rt][kk], f[2], f[3]);
-                    }
+                    mma16816(s[0], qf[kk], f[0], f[1]);
+                    mma16816(s[1], qf[kk], f[2], f[3]);
                 }
                 const int behind = r.past - j * kPage;  // keys of this page that every row sees
                 if (behind < kPage) {
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const int t = n * 8 + pair + (x & 1), d = t - behind;
-                                if (d >= 0 && !(a.tree && d < r.rows && (seen[rt][x >> 1] >> d & 1))) s[rt][n][x] = -INFINITY;
-                            }
-                }
-                uint32_t hi_p[RT][4], lo_p[RT][4];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    float alpha[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(fmaxf(s[rt][0][2 * e], s[rt][0][2 * e + 1]), fmaxf(s[rt][1][2 * e], s[rt][1][2 * e + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2)) * a.scale_log2;
-                        const float next = mx > m[rt][e] + kSlack ? mx : m[rt][e];
-                        alpha[e] = next == m[rt][e] ? 1.f : exp2_approx(m[rt][e] - next);
-                        m[rt][e] = next;
-                        const float ref = next == -INFINITY ? 0.f : next;
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int x = 2 * e; x < 2 * e + 2; ++x) s[rt][n][x] = exp2_approx(fmaf(s[rt][n][x], a.scale_log2, -ref));
-                        l[rt][e] = l[rt][e] * alpha[e] + ((s[rt][0][2 * e] + s[rt][0][2 * e + 1]) + (s[rt][1][2 * e] + s[rt][1][2 * e + 1]));
-                    }
-                    if (__any_sync(kAll, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-                        for (int n = 0; n < 16; ++n) {
-                            o[rt][n][0] *= alpha[0], o[rt][n][1] *= alpha[0];
-                            o[rt][n][2] *= alpha[1], o[rt][n][3] *= alpha[1];
+                        for (int x = 0; x < 4; ++x) {
+                            const int t = n * 8 + pair + (x & 1), d = t - behind;
+                            if (d >= 0 && !(a.tree && d < r.rows && (seen[x >> 1] >> d & 1))) s[n][x] = -INFINITY;
                         }
-                    }
+                }
+                uint32_t hi_p[4], lo_p[4];
+                float alpha[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2)) * a.scale_log2;
+                    const float next = mx > m[e] + kSlack ? mx : m[e];
+                    alpha[e] = next == m[e] ? 1.f : exp2_approx(m[e] - next);
+                    m[e] = next;
+                    const float ref = next == -INFINITY ? 0.f : next;
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = s[rt][n][2 * e], y = s[rt][n][2 * e + 1];
-                            const uint32_t w = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-                            hi_p[rt][2 * n + e] = w;
-                            lo_p[rt][2 * n + e] = pack_bf16x2(x - bf16lo(w), y - bf16hi(w));
-                        }
+                        for (int x = 2 * e; x < 2 * e + 2; ++x) s[n][x] = exp2_approx(fmaf(s[n][x], a.scale_log2, -ref));
+                    l[e] = l[e] * alpha[e] + ((s[0][2 * e] + s[0][2 * e + 1]) + (s[1][2 * e] + s[1][2 * e + 1]));
                 }
+                if (__any_sync(kAll, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                    for (int n = 0; n < 16; ++n) {
+                        o[n][0] *= alpha[0], o[n][1] *= alpha[0];
+                        o[n][2] *= alpha[1], o[n][3] *= alpha[1];
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = s[n][2 * e], y = s[n][2 * e + 1];
+                        const uint32_t w = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+                        hi_p[2 * n + e] = w;
+                        lo_p[2 * n + e] = pack_bf16x2(x - bf16lo(w), y - bf16hi(w));
+                    }
                 mbar_wait(full_v + 8 * stage, phase, &g_status);
                 if (behind < kPage) {
                     // Slots that hold no key are zeroed, and of drafted values what is not finite, so that a probability
                     // of 0 meets nothing that it would not cancel; the rows that see such a value get it at the end.
-                    const int n_keys = r.keys - j * kPage;
-                    for (int c = max(behind, 0) * 16 + lane; c < kPage * 16; c += 32) {
-                        const int t = c >> 4;
-                        const uint32_t addr = v + (c >> 3 & 1) * half + warp * 2048 + t * 128 + (c & 7) * 16;
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (t < n_keys) {
-                            const uint4 x = lds128(addr);
-                            w = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
-                            if (w.x == x.x && w.y == x.y && w.z == x.z && w.w == x.w) continue;
-                            odd = true;
+                    const int n_keys = r.keys - j * kPage, from = max(behind, 0) * 16 + lane;
+                    const auto chunk = [&](int c) { return v + (c >> 3 & 1) * half + head * 2048 + (c >> 4) * 128 + (c & 7) * 16; };
+                    bool here = false;
+                    for (int c = from; c < min(n_keys, kPage) * 16; c += 32) {
+                        const uint4 x = lds128(chunk(c));
+                        here |= not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
+                    }
+                    here = __any_sync(kAll, here);
+                    odd |= here;
+                    for (int c = here ? from : max(n_keys, 0) * 16 + lane; c < kPage * 16; c += 32) {
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        if (c >> 4 < n_keys) {
+                            x = lds128(chunk(c));
+                            x = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
                         }
-                        tc::st_shared_v4(addr, w.x, w.y, w.z, w.w);
+                        tc::st_shared_v4(chunk(c), x.x, x.y, x.z, x.w);
                     }
                     wrote = true;
                     __syncwarp();
@@ -312,13 +292,10 @@ __global__ void __launch_bounds__(288, 1)
                 for (int c = 0; c < 16; c += 2) {
                     uint32_t f[4];
                     ldmatrix4_trans(f, v + (c >> 3) * half + at_v + ((((c & 7) + chunk_v) ^ (lane & 7)) << 4));
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        mma16816(o[rt][c], hi_p[rt], f[0], f[1]);
-                        mma16816(o[rt][c + 1], hi_p[rt], f[2], f[3]);
-                        mma16816(o[rt][c], lo_p[rt], f[0], f[1]);
-                        mma16816(o[rt][c + 1], lo_p[rt], f[2], f[3]);
-                    }
+                    mma16816(o[c], hi_p, f[0], f[1]);
+                    mma16816(o[c + 1], hi_p, f[2], f[3]);
+                    mma16816(o[c], lo_p, f[0], f[1]);
+                    mma16816(o[c + 1], lo_p, f[2], f[3]);
                 }
             } else {
                 mbar_wait(full_v + 8 * stage, phase, &g_status);
@@ -329,52 +306,45 @@ __global__ void __launch_bounds__(288, 1)
             if (++stage == stages) stage = 0, phase ^= 1;
         }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[rt][e] += __shfl_xor_sync(kAll, l[rt][e], 1);
-                l[rt][e] += __shfl_xor_sync(kAll, l[rt][e], 2);
-            }
-        if (__any_sync(kAll, odd)) {
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(kAll, l[e], 1);
+            l[e] += __shfl_xor_sync(kAll, l[e], 2);
+        }
+        if (odd) {
             const int32_t *row = a.page_table + (size_t)b * a.max_pages;
             for (int pos = max(r.past, j0 * kPage); pos < min(r.keys, j1 * kPage); ++pos) {
                 const int id = row[pos >> 4];
                 if (id < 0 || id >= a.num_pages) continue;
-                const uint16_t *src = a.v_pages + (((size_t)id * kPage + (pos & 15)) * hkv + warp) * 128 + pair;
+                const uint16_t *src = a.v_pages + (((size_t)id * kPage + (pos & 15)) * hkv + head) * 128 + pair;
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
                     const uint32_t w = not_finite(*reinterpret_cast<const uint32_t *>(src + 8 * n));
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (seen[rt][x >> 1] >> (pos - r.past) & 1) o[rt][n][x] += x & 1 ? bf16hi(w) : bf16lo(w);
+                    for (int x = 0; x < 4; ++x)
+                        if (seen[x >> 1] >> (pos - r.past) & 1) o[n][x] += x & 1 ? bf16hi(w) : bf16lo(w);
                 }
             }
         }
         const bool whole = lo <= p0 && p1 <= hi;
         const int slot = 2 * worker + (p0 > lo);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int e = 0; e < 2; ++e) {
+            const int row = quad + 8 * e;
+            if (row >= rows) continue;
+            if (whole) {
+                const float inv = l[e] > 0.f ? 1.f / l[e] : l[e];
+                uint16_t *dst = a.out + ((size_t)(r.first + (row >> (G - 1))) * a.hq + head * G + (row & (G - 1))) * 128 + pair;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = rt * 16 + quad + 8 * e;
-                if (row >= rows) continue;
-                if (whole) {
-                    const float inv = l[rt][e] > 0.f ? 1.f / l[rt][e] : l[rt][e];
-                    uint16_t *dst = a.out + ((size_t)(r.first + (row >> (G - 1))) * a.hq + warp * G + (row & (G - 1))) * 128 + pair;
+                for (int n = 0; n < 16; ++n)
+                    *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack_bf16x2(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
+            } else {
+                const size_t at = ((size_t)slot * hkv + head) * a.block_rows + row;
+                float *dst = a.acc + at * 128 + pair;
 #pragma unroll
-                    for (int n = 0; n < 16; ++n)
-                        *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack_bf16x2(o[rt][n][2 * e] * inv, o[rt][n][2 * e + 1] * inv);
-                } else {
-                    const size_t at = ((size_t)slot * hkv + warp) * a.block_rows + row;
-                    float *dst = a.acc + at * 128 + pair;
-#pragma unroll
-                    for (int n = 0; n < 16; ++n)
-                        *reinterpret_cast<float2 *>(dst + 8 * n) = make_float2(o[rt][n][2 * e], o[rt][n][2 * e + 1]);
-                    if (pair == 0) *reinterpret_cast<float2 *>(a.ml + 2 * at) = make_float2(m[rt][e], l[rt][e]);
-                }
+                for (int n = 0; n < 16; ++n) *reinterpret_cast<float2 *>(dst + 8 * n) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
+                if (pair == 0) *reinterpret_cast<float2 *>(a.ml + 2 * at) = make_float2(m[e], l[e]);
             }
+        }
     }
 }
 
@@ -486,8 +456,13 @@ struct Plan {
     size_t acc, ml, splits, total;
 };
 
-// Rows times group up to which the rows of a request are few.
-constexpr int kFewRows = 32;
+// Rows times group up to which the rows of a request are few: one m16 block.
+// With two blocks (32 rows, 32 requests of 200..2000 positions) mma.sync took
+// 45.3 us against 42.8 of rows_tiles.cu, with eight (128 rows, 24 requests of
+// 500..8000) 322 us against 102: 48 products a page, head and block at a
+// measured 2048 multiply-adds in 4.7 clocks an SM are slower than HBM from two
+// blocks on.
+constexpr int kFewRows = 16;
 
 int sm_count() {
     int device = 0, sms = 0;
@@ -500,10 +475,11 @@ int sm_count() {
 bool plan_of(int max_rows, int hq, int hkv, Plan *p) {
     const int group = hq / hkv, sms = sm_count();
     if (sms <= 0) return false;
+    *p = {};
     p->few = (long long)max_rows * group <= kFewRows;
     p->workers = p->few ? sms * ctas_per_sm(hkv) : rows_tiles_workers(hkv);
+    p->block_rows = p->few ? 16 : 128;
     if (p->workers > kMaxWorkers) p->workers = kMaxWorkers;
-    p->block_rows = p->few ? (max_rows * group <= 16 ? 16 : 32) : 128;
     const size_t rows = (size_t)2 * p->workers * hkv * p->block_rows;
     p->splits = 0;
     p->ml = (sizeof(Split) * p->workers + 255) & ~(size_t)255;
@@ -542,9 +518,9 @@ bool make_query_tmap(CUtensorMap *map, const void *base, int hq, long long rows,
 
 // Enough for calls of max_rows or fewer, whichever kernel they take.
 size_t rows_attn_workspace_bytes(int max_rows, int n_q_heads, int n_kv_heads) {
-    const int group = n_q_heads / n_kv_heads, steps[3] = {16 / group, kFewRows / group, max_rows};
+    const int group = n_q_heads / n_kv_heads;
     size_t most = 0;
-    for (int n : steps) {
+    for (int n : {kFewRows / group, max_rows}) {
         Plan p;
         if (!plan_of(n < max_rows ? n : max_rows, n_q_heads, n_kv_heads, &p)) return 0;
         if (p.total > most) most = p.total;
@@ -599,11 +575,10 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
         cfg.gridDim = dim3((unsigned)plan.workers);
         cfg.blockDim = dim3((a.hkv + 1) * 32);
         cfg.dynamicSmemBytes = 1024 + stages * stage_bytes(a.hkv) + 3 * 8 * kMaxStages + 4 * kMaxStages + 4 * (x.batch + 1);
-        const auto kernel = plan.block_rows == 16 ? few_rows_kernel<1> : few_rows_kernel<2>;
         // the most of any call, so that host threads' calls cannot lower one another's
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        e = cudaFuncSetAttribute(few_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
-        e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, a, stages);
+        e = cudaLaunchKernelEx(&cfg, few_rows_kernel, tk, tv, a, stages);
     } else {
         CUtensorMap tq;
         if (!make_query_tmap(&tq, x.q, a.hq, x.rows, a.ldq, a.group)) return cudaErrorInvalidValue;
