@@ -73,6 +73,37 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// prefix[b] = pages of the requests before b, by one warp.
+__device__ __forceinline__ void count_pages(const RowsArgs &a, int *prefix, unsigned int *report) {
+    const int lane = threadIdx.x & 31;
+    int carry = 0;
+    if (lane == 0) prefix[0] = 0;
+    for (int base = 0; base < a.batch; base += 32) {
+        const int b = base + lane;
+        int v = 0;
+        if (b < a.batch) {
+            v = (request_of(a, b, report).keys + kPage - 1) / kPage;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (b < a.batch) prefix[b + 1] = carry + v;
+        carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+}
+
+// First request whose pages reach past page x.
+__device__ __forceinline__ int request_at(const int *prefix, int batch, int x) {
+    int l = 0, r = batch - 1;
+    while (l < r) {
+        const int mid = (l + r) >> 1;
+        if (prefix[mid + 1] > x) r = mid; else l = mid + 1;
+    }
+    return l;
+}
+
 __device__ __forceinline__ void grid_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -92,7 +123,7 @@ __global__ void __launch_bounds__(288, 1)
     const int worker = blockIdx.x;
     if (!a.early) grid_wait();
     if (warp == 0) {
-        count_tiles<kPage>(a, prefix, a.max_rows, worker == 0 ? &g_status : nullptr);
+        count_pages(a, prefix, worker == 0 ? &g_status : nullptr);
         if (lane == 0) {
             for (int s = 0; s < stages; ++s) {
                 mbar_init(full_k + 8 * s, 1);
@@ -112,7 +143,8 @@ __global__ void __launch_bounds__(288, 1)
         if (j < min(hi, prefix[b0 + 1]) - p0) first_ids = a.page_table[(size_t)b0 * a.max_pages + j];
     }
     if (a.early) grid_wait();
-    zero_rows(a, prefix, worker, threadIdx.x, blockDim.x);
+    for (int b = worker; b < a.batch; b += a.workers)
+        if (prefix[b + 1] == prefix[b]) zero_rows(a, request_of(a, b, nullptr), threadIdx.x, blockDim.x);
 
     if (warp == hkv) {
         // the producer: lanes fetch page ids, lane 0 issues the copies

@@ -68,49 +68,12 @@ __device__ __forceinline__ Request request_of(const RowsArgs &a, int b, unsigned
     return r;
 }
 
-// prefix[b] = key tiles of the requests before b, by one warp.
-template <int TILE>
-__device__ __forceinline__ void count_tiles(const RowsArgs &a, int *prefix, int rows_a_block, unsigned int *report) {
-    const int lane = threadIdx.x & 31;
-    int carry = 0;
-    if (lane == 0) prefix[0] = 0;
-    for (int base = 0; base < a.batch; base += 32) {
-        const int b = base + lane;
-        int v = 0;
-        if (b < a.batch) {
-            const Request r = request_of(a, b, report);
-            v = (r.keys + TILE - 1) / TILE * ((r.rows + rows_a_block - 1) / rows_a_block);
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
-        }
-        if (b < a.batch) prefix[b + 1] = carry + v;
-        carry += __shfl_sync(0xffffffffu, v, 31);
-    }
-}
-
-// First request whose tiles reach past tile x.
-__device__ __forceinline__ int request_at(const int *prefix, int batch, int x) {
-    int l = 0, r = batch - 1;
-    while (l < r) {
-        const int mid = (l + r) >> 1;
-        if (prefix[mid + 1] > x) r = mid; else l = mid + 1;
-    }
-    return l;
-}
-
-// Zero rows of requests with nothing to attend to, by every worker's share.
-__device__ __forceinline__ void zero_rows(const RowsArgs &a, const int *prefix, int worker, int thread, int threads) {
-    for (int b = worker; b < a.batch; b += a.workers) {
-        if (prefix[b + 1] != prefix[b]) continue;
-        const Request r = request_of(a, b, nullptr);
-        if (!r.valid) continue;
-        uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)r.first * a.hq * 128);
-        const long long n = (long long)r.rows * a.hq * 16;
-        for (long long i = thread; i < n; i += threads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
+// A request with nothing to attend to has zero rows.
+__device__ __forceinline__ void zero_rows(const RowsArgs &a, const Request &r, int thread, int threads) {
+    if (!r.valid || r.keys > 0) return;
+    uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)r.first * a.hq * 128);
+    const long long n = (long long)r.rows * a.hq * 16;
+    for (long long i = thread; i < n; i += threads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Row i's parent in its request's tree, checked.

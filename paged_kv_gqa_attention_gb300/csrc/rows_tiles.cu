@@ -2,23 +2,29 @@
 // rows a request (rows_attn.cu says what is computed and when it is taken).
 //
 // A job is 128 rows, 128 / group query rows with the heads of one KV head in
-// turn, over its request's keys, 64 at a time.  Two CTAs an SM, a group of
+// turn, over its request's keys, 128 at a time.  One CTA an SM, a group of
 // hkv CTAs a worker: the group's CTAs take the same key tiles of each KV head,
 // so that whole token rows are asked of HBM at about the same time.
 //
-//   warp 4     producer: Q once a job, then K and V of each tile, page by
-//              page (boxes of 16 tokens by 64 dims), two slots each
-//   warp 5     issues S = Q K^T (M 128, N 64) into one of two buffers in TMEM
-//              and O += P V (N 128), P from TMEM.  S of the next tile is
-//              issued before P V of this one, so the tensor core has work
-//              while the softmax has it
-//   warps 0-3  softmax, a row a thread: the row's 64 scores in registers, the
-//              lazy running max (log2 slack 8: O is rescaled only when it
-//              moves), P written over its scores as two bf16 terms of 16
-//              columns each for every 32 keys; then the epilogue
+//   warp 8     producer: Q once a job (two buffers), K and V of each tile,
+//              page by page (boxes of 16 tokens by 64 dims), into one ring of
+//              five slots in the order they are used
+//   warp 9     issues S = Q K^T (M 128, N 128) into one of two buffers in TMEM
+//              and, for each half of the tile's keys, O_h += P_h V_h (N 128),
+//              P from TMEM.  S of the next tile, of the next job too, is
+//              issued before P V of this one
+//   warps 0-7  softmax: warps 0-3 have the first 64 keys of every tile, warps
+//              4-7 the others, a row a thread: 64 scores in registers, a lazy
+//              running max (log2 slack 8: O is rescaled only when it moves),
+//              P written over its scores as two bf16 terms of 16 columns each
+//              for every 32 keys.  The halves have maxima, sums and
+//              accumulators of their own, which meet at the job's end; Q is
+//              shared by both, which leaves the room for the ring
 //
 // Two terms of P make P V two products: 16 bits of each probability, as in
-// the prefill kernels.
+// the prefill kernels.  The tensor core needs 514 clocks for S and 1028 for
+// P V of a tile (measured: 64.2 an instruction; N = 64 would take 48), the
+// softmax of a half about 1050 with both at work.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -32,45 +38,83 @@ namespace {
 __device__ unsigned int g_status;
 
 constexpr int kPage = 16;
-constexpr int kTile = 64;
-constexpr int kThreads = 192;
+constexpr int kTile = 128;
+constexpr int kThreads = 320;
+constexpr int kSlots = 5;
 constexpr float kSlack = 8.f;
-constexpr uint32_t kHalf = kTile * 128;            // 64 dims of a tile's rows
-constexpr uint32_t kSlot = 2 * kHalf;              // K or V of a tile
-constexpr uint32_t kQ = 0;                         // two halves of 128 rows
-constexpr uint32_t kK = kQ + 2 * tc::kSubTileBytes;
-constexpr uint32_t kV = kK + 2 * kSlot;
-constexpr uint32_t kBar = kV + 2 * kSlot;
-enum : uint32_t { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2,
-                  kSFull = kVEmpty + 2, kPFull = kSFull + 2, kDone = kPFull + 2, kOFull, kOFree, kBars };
-constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kPrefix = kAbort + 4;
-constexpr uint32_t kColO = 128;  // TMEM: S / P in [0, 64) and [64, 128), O in [128, 256)
+constexpr uint32_t kQBytes = 2 * tc::kSubTileBytes;  // two halves of 64 dims of 128 rows; K and V of a tile too
+constexpr uint32_t kRing = 2 * kQBytes;
+constexpr uint32_t kBar = kRing + kSlots * kQBytes;
+enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots,
+                  kPFull = kSFull + 2, kDone = kPFull + 4, kOFull, kBars };  // kPFull: [half][buffer]
+constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 16;
+constexpr uint32_t kSmem = kStats + 2 * 128 * 8;  // kStats: [half][row] max and sum
+static_assert(kSmem <= 227 * 1024, "shared memory");
+constexpr uint32_t kColO = 256;  // TMEM: S / P in [0, 128) and [128, 256), O of the halves in [256, 384) and [384, 512)
 
-// The tiles of one job that are the worker's: the walk of every role.
+// A call's tiles, and the request of the worker's first one, by one warp.
+struct Start {
+    int total, b, base;  // base: the tiles before request b
+};
+__device__ __forceinline__ int tiles_of(const RowsArgs &a, const Request &r, int rows_a_block) {
+    return (r.keys + kTile - 1) / kTile * ((r.rows + rows_a_block - 1) / rows_a_block);
+}
+__device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, int rows_a_block, unsigned int *report) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    int sum = 0, first = 0;  // first: of the first 32 requests
+    for (int b = lane; b < a.batch; b += 32) {
+        const int v = tiles_of(a, request_of(a, b, report), rows_a_block);
+        if (b < 32) first = v;
+        sum += v;
+    }
+    Start s = {__reduce_add_sync(kAll, sum), 0, 0};
+    const int per = (s.total + a.workers - 1) / a.workers;
+    const long long lo = (long long)worker * per;
+    if (lo >= s.total) return s;
+    for (int begin = 0, carry = 0; begin < a.batch; begin += 32) {
+        const int b = begin + lane;
+        const int v = begin == 0 ? first : b < a.batch ? tiles_of(a, request_of(a, b, nullptr), rows_a_block) : 0;
+        int up_to = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kAll, up_to, o);
+            if (lane >= o) up_to += u;
+        }
+        const unsigned past = __ballot_sync(kAll, carry + up_to > lo);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            s.b = begin + l;
+            s.base = carry + __shfl_sync(kAll, up_to - v, l);
+            return s;
+        }
+        carry += __shfl_sync(kAll, up_to, 31);
+    }
+    return s;
+}
+
+// The jobs of a worker, one after another: the walk of every role.
 struct Walk {
     const RowsArgs &a;
-    const int *prefix;
-    int at, hi, b;
+    int at, hi, b, base, rows_a_block;
     int block, t0, t1;  // the segment: rows block, tiles [t0, t1) of `tiles`
     int tiles;
     Request r;
-    __device__ Walk(const RowsArgs &args, const int *p, int lo, int end) : a(args), prefix(p), at(lo), hi(end), b(-1) {
-        t0 = t1 = 0;
+    __device__ Walk(const RowsArgs &args, const Start &s, int lo, int end, int rab)
+        : a(args), at(lo), hi(end), b(s.b), base(s.base), rows_a_block(rab), t0(0), t1(0) {
+        if (lo < end) load();
     }
     __device__ bool next() {
         at += t1 - t0;
         if (at >= hi) return false;
-        if (b < 0) b = request_at(prefix, a.batch, at), load();
-        else if (at >= prefix[b + 1]) {
-            do ++b; while (prefix[b + 1] == prefix[b]);
-            load();
-        }
-        const int x = at - prefix[b];
+        for (int n = mine(); at >= base + n; n = mine()) base += n, ++b, load();
+        const int x = at - base;
         block = x / tiles;
         t0 = x - block * tiles;
         t1 = min(tiles, t0 + hi - at);
         return true;
     }
+    __device__ int mine() const { return tiles * ((r.rows + rows_a_block - 1) / rows_a_block); }
     __device__ void load() {
         r = request_of(a, b, nullptr);
         tiles = (r.keys + kTile - 1) / kTile;
@@ -94,9 +138,9 @@ struct Waits {
     }
 };
 
-__device__ __forceinline__ bool any_of_rows(bool x) {  // the 128 threads that own rows
+__device__ __forceinline__ bool any_of_rows(bool x) {  // the 256 threads that own rows
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
                  : "r"((uint32_t)x)
                  : "memory");
@@ -142,17 +186,15 @@ __device__ __forceinline__ void ancestors(const RowsArgs &a, const Request &r, u
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     rows_tiles_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ RowsArgs a) {
     constexpr unsigned kAll = 0xffffffffu;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw), sb = (raw + 1023u) & ~1023u;
-    uint8_t *smem = smem_raw + (sb - raw);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.hkv, worker = blockIdx.x / a.hkv;
     const int rows_a_block = 128 / a.group;
-    int *prefix = reinterpret_cast<int *>(smem + kPrefix);
     const Waits wait{reinterpret_cast<volatile int *>(smem + kAbort)};
     const auto bar = [&](uint32_t i) { return sb + kBar + 8 * i; };
     const auto grid_wait = [] {
@@ -161,140 +203,159 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     if (!a.early) grid_wait();
     if (warp == 0) {
-        count_tiles<kTile>(a, prefix, rows_a_block, blockIdx.x == 0 ? &g_status : nullptr);
-    } else if (warp == 4) {
-        if (lane == 0) {
-            for (uint32_t i = 0; i < kBars; ++i) {
-                const bool rows = i == kOFree || i == kPFull || i == kPFull + 1;  // an arrival of each of four warps
-                mbar_init(bar(i), rows ? 4 : 1);
-            }
-            *wait.abort = 0;
-            fence_mbar_init();
-            tc::prefetch_tmap(&tq);
-            tc::prefetch_tmap(&tk);
-            tc::prefetch_tmap(&tv);
-        }
-    } else if (warp == 5) {
-        tc::tmem_alloc(sb + kTmem, 256);
+        const Start s = find_start(a, worker, rows_a_block, blockIdx.x == 0 ? &g_status : nullptr);
+        if (lane == 0) *reinterpret_cast<Start *>(smem + kStart) = s;
+    } else if (warp == 8 && lane == 0) {
+        for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + 4 ? 4 : 1);
+        *wait.abort = 0;
+        fence_mbar_init();
+        tc::prefetch_tmap(&tq);
+        tc::prefetch_tmap(&tk);
+        tc::prefetch_tmap(&tv);
     }
+    // TMEM only once the kernel before has ended: one that starts its successors before it allocates could wait for
+    // columns that this one holds while it waits for that kernel
+    if (a.early) grid_wait();
+    if (warp == 9) tc::tmem_alloc(sb + kTmem, 512);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kTmem);
-    const int total = prefix[a.batch], per = (total + a.workers - 1) / a.workers;
+    const Start start = *reinterpret_cast<const Start *>(smem + kStart);
+    const int total = start.total, per = (total + a.workers - 1) / a.workers;
     const int lo = (int)min(worker * (long long)per, (long long)total), hi = min(lo + per, total);
-    if (a.early) grid_wait();
-    if (head == 0) zero_rows(a, prefix, worker, threadIdx.x, kThreads);
-    Walk w(a, prefix, lo, hi);
+    if (head == 0)
+        for (int b = worker; b < a.batch; b += a.workers) zero_rows(a, request_of(a, b, nullptr), threadIdx.x, kThreads);
+    Walk w(a, start, lo, hi, rows_a_block);
 
-    if (warp == 4) {
-        if (head == 0 && lane == 0) {
-            Split s = {0, 0, 0, 0};
-            if (lo < hi) {
-                const int b = request_at(prefix, a.batch, hi - 1);
-                const Request r = request_of(a, b, nullptr);
-                const int tiles = (r.keys + kTile - 1) / kTile, block = (hi - 1 - prefix[b]) / tiles;
-                const int p0 = prefix[b] + block * tiles, p1 = p0 + tiles;  // the job that holds the last tile
-                if (p0 >= lo && p1 > hi) {
-                    s.count = (p1 - 1) / per - worker + 1;
-                    s.first_slot = 2 * worker + (p0 > lo);
-                    s.out_row = r.first + block * rows_a_block;
-                    s.rows = min(rows_a_block, r.rows - block * rows_a_block) * a.group;
-                }
-            }
-            a.splits[worker] = s;
-        }
-        __syncwarp();
-        // K of a tile goes out before V of the tile before it (which waits for an earlier P V)
-        const int p = lane >> 1, sd = lane & 1;
-        int n = 0, job = 0, id_before = -1;
-        const auto load = [&](const CUtensorMap *map, uint32_t slots, uint32_t full, uint32_t empty, int i, int id) {
-            const int slot = i & 1;
-            wait(bar(empty + slot), ((i >> 1) & 1) ^ 1);
+    if (warp == 8) {
+        // ring order K 0, K 1, V 0, K 2, V 1, ...
+        const int p = (lane >> 1) & 7, sd = lane & 1;
+        int slot = 0, phase = 1, job = 0, id_before = -1;
+        bool any = false;
+        Split split = {0, 0, 0, 0};
+        const auto load = [&](const CUtensorMap *map, int id) {
+            wait(bar(kEmpty + slot), phase);
             const unsigned boxes = __ballot_sync(kAll, id >= 0);
-            if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), __popc(boxes) * kPage * 128);
+            if (lane == 0) mbar_arrive_expect_tx(bar(kFull + slot), __popc(boxes) * kPage * 128);
             __syncwarp();
-            if (id >= 0) tc::tma_load_3d(sb + slots + slot * kSlot + sd * kHalf + p * kPage * 128, map, sd * 64, id * kPage, head, bar(full + slot));
+            if (id >= 0)
+                tc::tma_load_3d(sb + kRing + slot * kQBytes + sd * tc::kSubTileBytes + p * kPage * 128, map, sd * 64, id * kPage, head,
+                                bar(kFull + slot));
+            if (++slot == kSlots) slot = 0, phase ^= 1;
         };
         while (w.next()) {
             const int32_t *row = a.page_table + (size_t)w.b * a.max_pages;
             const int pages = (w.r.keys + kPage - 1) / kPage;
-            if (n > 0) load(&tv, kV, kVFull, kVEmpty, n - 1, id_before);
-            wait(bar(kQEmpty), (job & 1) ^ 1);
+            const uint32_t q = sb + (job & 1) * kQBytes;
+            wait(bar(kQEmpty + (job & 1)), ((job >> 1) & 1) ^ 1);
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar(kQFull), 2 * tc::kSubTileBytes);
+                mbar_arrive_expect_tx(bar(kQFull + (job & 1)), kQBytes);
                 for (int i = 0; i < 2; ++i)
-                    tc::tma_load_3d(sb + kQ + i * tc::kSubTileBytes, &tq, i * 64, head * a.group, w.r.first + w.block * rows_a_block, bar(kQFull));
+                    tc::tma_load_3d(q + i * tc::kSubTileBytes, &tq, i * 64, head * a.group, w.r.first + w.block * rows_a_block,
+                                    bar(kQFull + (job & 1)));
             }
             __syncwarp();
             ++job;
             int ids = -1, chunk = -1;
-            for (int t = w.t0; t < w.t1; ++t, ++n) {
-                if (t >> 3 != chunk) {  // 32 page ids at a time
-                    chunk = t >> 3;
+            for (int t = w.t0; t < w.t1; ++t) {
+                if (t >> 2 != chunk) {  // 32 page ids at a time
+                    chunk = t >> 2;
                     ids = chunk * 32 + lane < pages ? row[chunk * 32 + lane] : -1;
-                    const bool bad = chunk * 32 + lane < pages && (ids < 0 || ids >= a.num_pages);
-                    if (bad) {
-                        const int tile = chunk * 8 + (lane >> 2);
+                    if (chunk * 32 + lane < pages && (ids < 0 || ids >= a.num_pages)) {
+                        const int tile = chunk * 4 + (lane >> 3);
                         if (tile >= w.t0 && tile < w.t1) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
                         ids = -1;
                     }
                 }
-                int id = __shfl_sync(kAll, ids, (4 * t + (p & 3)) & 31);
-                if (lane >= 8) id = -1;
-                load(&tk, kK, kKFull, kKEmpty, n, id);
-                if (t > w.t0) load(&tv, kV, kVFull, kVEmpty, n - 1, id_before);
+                int id = __shfl_sync(kAll, ids, (8 * t + p) & 31);
+                if (lane >= 16) id = -1;
+                load(&tk, id);
+                if (any) load(&tv, id_before);
                 id_before = id;
+                any = true;
+            }
+            const int p0 = w.at - w.t0, p1 = p0 + w.tiles;  // the job's tiles
+            if (p0 >= lo && p1 > hi) {
+                split.count = (p1 - 1) / per - worker + 1;
+                split.first_slot = 2 * worker + (p0 > lo);
+                split.out_row = w.r.first + w.block * rows_a_block;
+                split.rows = min(rows_a_block, w.r.rows - w.block * rows_a_block) * a.group;
             }
         }
-        if (n > 0) load(&tv, kV, kVFull, kVEmpty, n - 1, id_before);
-    } else if (warp == 5) {
+        if (any) load(&tv, id_before);
+        if (head == 0 && lane == 0) a.splits[worker] = split;
+    } else if (warp == 9) {
         if (lane == 0) {
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, kTile, false), idesc_o = tc::idesc_bf16(128, 128, true);
-            int n = 0, job = 0;
-            // S of tile i takes the buffer that P V of tile i - 2 has read.  Within a job that is the newest P V but one;
-            // at a job's first tile P V of tile i - 1 is out already, and is waited for: a parity names two phases.
-            const auto issue_s = [&](int i, bool first) {
-                wait(bar(kKFull + (i & 1)), (i >> 1) & 1);
-                if (i >= 2 || (first && i >= 1)) wait(bar(kDone), (first ? i + 1 : i) & 1);
+            int n = 0, job = -1, slot = 0, phase = 0;  // of the next S: its tile, job, ring slot
+            bool first_s = false, last_s = false;      // the newest S is its job's first, last
+            int left = 0;                              // of its job's tiles
+            const auto use = [&] {
+                wait(bar(kFull + slot), phase);
                 tc::fence_after();
-                const uint32_t k = sb + kK + (i & 1) * kSlot;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_bf16(tmem + (i & 1) * kTile, tc::sw128_desc(sb + kQ + (kk >> 2) * tc::kSubTileBytes + (kk & 3) * 32),
-                                 tc::sw128_desc(k + (kk >> 2) * kHalf + (kk & 3) * 32), idesc_s, kk > 0);
-                tc::mma_commit(bar(kSFull + (i & 1)));
-                tc::mma_commit(bar(kKEmpty + (i & 1)));
+                return sb + kRing + slot * kQBytes;
             };
-            while (w.next()) {
-                wait(bar(kQFull), job & 1);
-                issue_s(n, true);
-                for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    if (t + 1 < w.t1) issue_s(n + 1, false);
-                    else tc::mma_commit(bar(kQEmpty));
-                    wait(bar(kPFull + (n & 1)), (n >> 1) & 1);
-                    wait(bar(kVFull + (n & 1)), (n >> 1) & 1);
-                    if (t == w.t0 && job > 0) wait(bar(kOFree), (job - 1) & 1);
-                    tc::fence_after();
-                    const uint32_t p = tmem + (n & 1) * kTile, v = sb + kV + (n & 1) * kSlot;
+            const auto done = [&] {
+                tc::mma_commit(bar(kEmpty + slot));
+                if (++slot == kSlots) slot = 0, phase ^= 1;
+            };
+            const auto issue_s = [&]() -> bool {
+                first_s = left == 0;
+                if (first_s) {
+                    if (!w.next()) return false;
+                    ++job;
+                    left = w.t1 - w.t0;
+                    wait(bar(kQFull + (job & 1)), (job >> 1) & 1);
+                }
+                const uint32_t k = use(), q = sb + (job & 1) * kQBytes, s = tmem + (n & 1) * kTile;
+                if (n >= 2) wait(bar(kDone), n & 1);  // P V of tile n - 2 has read this buffer; the newest one out is n - 2
+                tc::fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t off = (kk >> 2) * tc::kSubTileBytes + (kk & 3) * 32;
+                    tc::mma_bf16(s, tc::sw128_desc(q + off), tc::sw128_desc(k + off), idesc_s, kk > 0);
+                }
+                tc::mma_commit(bar(kSFull + (n & 1)));
+                done();
+                last_s = --left == 0;
+                if (last_s) tc::mma_commit(bar(kQEmpty + (job & 1)));
+                ++n;
+                return true;
+            };
+            bool more = issue_s();
+            while (more) {
+                const int u = n - 1;  // the tile whose P V comes next
+                const bool first = first_s, last = last_s;
+                more = issue_s();
+                wait(bar(kPFull + (u & 1)), (u >> 1) & 1);
+                if (first) wait(bar(kPFull + 2 + (u & 1)), (u >> 1) & 1);  // both halves have read the job before's O
+                const uint32_t v = use();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1) {
+                        wait(bar(kPFull + 2 + (u & 1)), (u >> 1) & 1);
+                        tc::fence_after();
+                    }
+                    const uint32_t p = tmem + (u & 1) * kTile + h * 64, o = tmem + kColO + h * 128;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint32_t hi_p = p + (kk >> 1) * 32 + (kk & 1) * 8;
-                        const uint64_t vdesc = tc::sw128_desc_mn(v + kk * 2048, kHalf);
-                        tc::mma_bf16_ts(tmem + kColO, hi_p, vdesc, idesc_o, t > w.t0 || kk > 0);
-                        tc::mma_bf16_ts(tmem + kColO, hi_p + 16, vdesc, idesc_o, 1u);
+                        const uint64_t vdesc = tc::sw128_desc_mn(v + h * 8192 + kk * 2048, tc::kSubTileBytes);
+                        tc::mma_bf16_ts(o, hi_p, vdesc, idesc_o, !first || kk > 0);
+                        tc::mma_bf16_ts(o, hi_p + 16, vdesc, idesc_o, 1u);
                     }
-                    tc::mma_commit(bar(kVEmpty + (n & 1)));
-                    tc::mma_commit(bar(kDone));
                 }
+                done();
+                tc::mma_commit(bar(kDone));
                 // the job's own barrier: a row's thread may be two P V ahead here, more than kDone's parity tells apart
-                tc::mma_commit(bar(kOFull));
-                ++job;
+                if (last) tc::mma_commit(bar(kOFull));
             }
         }
     } else {
-        const int row = threadIdx.x;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16, t_o = tmem + kColO + lanes;
+        const int h = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, t_o = tmem + kColO + h * 128 + lanes;
+        float2 *stats = reinterpret_cast<float2 *>(smem + kStats);
         int n = 0, job = 0;
         while (w.next()) {
             const Request &r = w.r;
@@ -309,15 +370,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint64_t s0 = __shfl_sync(kAll, all[0], node & 31), s1 = __shfl_sync(kAll, all[1], node & 31);
                 seen = node >= r.rows ? 0 : node < 32 ? s0 : s1;
             }
-            const auto ids_ok = [&](int t) -> uint32_t {  // which of tile t's four pages can be read
-                const int page = 4 * t + (lane & 3), id = t < w.t1 && page < pages ? table[page] : 0;
+            const auto ids_ok = [&](int t) -> uint32_t {  // which of the half's four pages can be read
+                const int page = 8 * t + 4 * h + (lane & 3), id = t < w.t1 && page < pages ? table[page] : 0;
                 return __ballot_sync(kAll, id >= 0 && id < a.num_pages) & 15u;
             };
             float m = -INFINITY, l = 0.f;
             bool odd = false;
             uint32_t next_ok = ids_ok(w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const uint32_t ok = next_ok, s = tmem + (n & 1) * kTile + lanes;
+                const uint32_t ok = next_ok, s = tmem + (n & 1) * kTile + h * 64 + lanes;
                 next_ok = ids_ok(t + 1);
                 wait(bar(kSFull + (n & 1)), (n >> 1) & 1);
                 __syncwarp();
@@ -327,11 +388,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tc::tmem_ld32_issue(s + 32, sc[1]);
                 tc::tmem_ld32_wait(sc[0]);
                 tc::tmem_ld32_wait(sc[1]);
-                const int behind = r.past - t * kTile;  // keys of this tile that every row sees
-                const bool masked = behind < kTile || ok != 15u;
+                const int key0 = t * kTile + h * 64, behind = r.past - key0;  // keys of this half that every row sees
+                const bool masked = behind < 64 || ok != 15u;
                 if (masked) {
-                    uint64_t vis = behind >= kTile ? ~0ull : behind > 0 ? ~(~0ull << behind) : 0ull;
-                    if (behind < kTile && behind > -kTile) vis |= behind >= 0 ? seen << behind : seen >> -behind;
+                    uint64_t vis = behind >= 64 ? ~0ull : behind > 0 ? ~(~0ull << behind) : 0ull;
+                    if (behind < 64 && behind > -64) vis |= behind >= 0 ? seen << behind : seen >> -behind;
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
                         if (!(ok >> p & 1)) vis &= ~(0xffffull << 16 * p);
@@ -390,9 +451,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     // Slots that hold no key (or were not loaded) are zeroed, and of drafted values what is not finite, so
                     // that a probability of 0 meets nothing that it would not cancel; rows that see such a value get it at
                     // the end.  Two threads a key.
-                    wait(bar(kVFull + (n & 1)), (n >> 1) & 1);
-                    const int key = row >> 1, pos = t * kTile + key;
-                    uint8_t *v = smem + kV + (n & 1) * kSlot + (row & 1) * kHalf + key * 128;
+                    // the ring's pieces are K 0, K 1, V 0, K 2, V 1, ..., and V of the last tile follows V of the one before
+                    const int piece = 2 * n + (w.at + t + 1 - w.t0 == hi ? 1 : 2), v_slot = piece % kSlots;
+                    wait(bar(kFull + v_slot), piece / kSlots & 1);
+                    const int key = row >> 1, pos = key0 + key;
+                    uint8_t *v = smem + kRing + v_slot * kQBytes + (row & 1) * tc::kSubTileBytes + (h * 64 + key) * 128;
                     const bool live = pos < r.keys && (ok >> (key >> 4) & 1);
                     if (!live || pos >= r.past) {
 #pragma unroll
@@ -414,29 +477,41 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tc::tmem_wait_st();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kPFull + (n & 1)));
+                if (lane == 0) mbar_arrive(bar(kPFull + 2 * h + (n & 1)));
             }
-            const bool any_odd = drafted && any_of_rows(odd);
+            stats[h * 128 + row] = make_float2(m, l);
+            const bool any_odd = any_of_rows(odd);  // both halves' statistics are there too
+            const float2 other = stats[(h ^ 1) * 128 + row];
+            named_barrier(1, 256);  // read before the next job's are written
+            const float top = fmaxf(m, other.x);
+            const float w_mine = m == -INFINITY ? 0.f : exp2_approx(m - top), w_other = other.x == -INFINITY ? 0.f : exp2_approx(other.x - top);
+            const float sum = l * w_mine + other.y * w_other;
+            const float w0 = h == 0 ? w_mine : w_other, w1 = h == 0 ? w_other : w_mine;
             wait(bar(kOFull), job & 1);
             ++job;
             __syncwarp();
             tc::fence_after();
+            // the half's warps give 64 of the dims, of both accumulators
             const bool whole = w.t0 == 0 && w.t1 == w.tiles;
             const int left = (r.rows - w.block * rows_a_block) * a.group;  // rows from this block's first on
             const int slot = 2 * worker + (w.at > lo);
             const size_t part = ((size_t)slot * a.hkv + head) * 128 + row;
-            const float inv = l > 0.f ? 1.f / l : l;
+            const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : sum;
             uint16_t *dst = a.out + ((size_t)(r.first + w.block * rows_a_block + row / a.group) * a.hq + head * a.group + row % a.group) * 128;
             const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float o[32];
-                tc::tmem_ld32(t_o + c * 32, o);
+            for (int c = 0; c < 2; ++c) {
+                const int dim = h * 64 + c * 32;
+                float o[32], o1[32];
+                tc::tmem_ld32(tmem + kColO + lanes + dim, o);
+                tc::tmem_ld32(tmem + kColO + 128 + lanes + dim, o1);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = (o[j] * w0 + o1[j] * w1) * inv;
                 if (any_odd) {
                     for (int pos = max(r.past, w.t0 * kTile); pos < min(r.keys, w.t1 * kTile); ++pos) {
                         const int id = table[pos >> 4];
                         if (id < 0 || id >= a.num_pages || !(seen >> (pos - r.past) & 1)) continue;
-                        const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_pages + (((size_t)id * kPage + (pos & 15)) * a.hkv + head) * 128 + c * 32);
+                        const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_pages + (((size_t)id * kPage + (pos & 15)) * a.hkv + head) * 128 + dim);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const uint32_t x = not_finite(v[j]);
@@ -448,32 +523,30 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (whole) {
                         uint32_t y[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) y[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+                        for (int j = 0; j < 16; ++j) y[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
                         if (wide) {
-                            store32(reinterpret_cast<float *>(dst + c * 32), reinterpret_cast<const float *>(y));
-                            store32(reinterpret_cast<float *>(dst + c * 32 + 16), reinterpret_cast<const float *>(y + 8));
+                            store32(reinterpret_cast<float *>(dst + dim), reinterpret_cast<const float *>(y));
+                            store32(reinterpret_cast<float *>(dst + dim + 16), reinterpret_cast<const float *>(y + 8));
                         } else {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                *reinterpret_cast<uint4 *>(dst + c * 32 + 8 * j) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                                *reinterpret_cast<uint4 *>(dst + dim + 8 * j) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) store32(a.acc + part * 128 + c * 32 + 8 * j, o + 8 * j);
+                        for (int j = 0; j < 4; ++j) store32(a.acc + part * 128 + dim + 8 * j, o + 8 * j);
                     }
                 }
                 __syncwarp();
             }
-            if (!whole && row < left) *reinterpret_cast<float2 *>(a.ml + 2 * part) = make_float2(m, l);
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kOFree));
+            if (!whole && h == 0 && row < left) *reinterpret_cast<float2 *>(a.ml + 2 * part) = make_float2(top, sum);
+            tc::fence_before();  // before the next job's P is handed over
         }
     }
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 9) {
         tc::fence_after();
-        tc::tmem_dealloc(tmem, 256);
+        tc::tmem_dealloc(tmem, 512);
     }
 }
 
@@ -484,17 +557,12 @@ int rows_tiles_workers(int hkv) {
     if (cudaGetDevice(&device) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
         return 0;
-    return 2 * sms / hkv;
+    return sms / hkv;
 }
 
 cudaError_t launch_rows_tiles(const RowsArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                               cudaStream_t stream) {
-    const uint32_t bytes = 1024 + kPrefix + 4 * (a.batch + 1);
-    // the most of any call, so that host threads' calls cannot lower one another's
-    cudaError_t e = cudaFuncSetAttribute(rows_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(1024 + kPrefix + 4 * (kRowsMaxBatch + 1)));
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(rows_tiles_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
+    cudaError_t e = cudaFuncSetAttribute(rows_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -502,7 +570,7 @@ cudaError_t launch_rows_tiles(const RowsArgs &a, const CUtensorMap &tq, const CU
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.workers * a.hkv));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
