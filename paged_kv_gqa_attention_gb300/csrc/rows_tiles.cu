@@ -9,10 +9,11 @@
 //   warp 8     producer: Q once a job (two buffers), K and V of each tile,
 //              page by page (boxes of 16 tokens by 64 dims), into one ring of
 //              five slots in the order they are used
-//   warp 9     issues S = Q K^T (M 128, N 128) into one of two buffers in TMEM
-//              and, for each half of the tile's keys, O_h += P_h V_h (N 128),
-//              P from TMEM.  S of the next tile, of the next job too, is
-//              issued before P V of this one
+//   warp 9     issues S = Q K^T (M 128, N 128) into one of two buffers in
+//              TMEM, up to a tile ahead, into the next job too
+//   warp 10    issues, for each half of the tile's keys, O_h += P_h V_h (N
+//              128), P from TMEM; a thread for both products would let the
+//              tensor core run dry at every barrier that it waits on
 //   warps 0-7  softmax: warps 0-3 have the first 64 keys of every tile, warps
 //              4-7 the others, a row a thread: 64 scores in registers, a lazy
 //              running max (log2 slack 8: O is rescaled only when it moves),
@@ -39,14 +40,14 @@ __device__ unsigned int g_status;
 
 constexpr int kPage = 16;
 constexpr int kTile = 128;
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kSlots = 5;
 constexpr float kSlack = 8.f;
 constexpr uint32_t kQBytes = 2 * tc::kSubTileBytes;  // two halves of 64 dims of 128 rows; K and V of a tile too
 constexpr uint32_t kRing = 2 * kQBytes;
 constexpr uint32_t kBar = kRing + kSlots * kQBytes;
 enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots,
-                  kPFull = kSFull + 2, kDone = kPFull + 4, kOFull, kBars };  // kPFull: [half][buffer]
+                  kPFull = kSFull + 2, kDone = kPFull + 4, kOFull = kDone + 2, kBars };  // kPFull: [half][buffer]
 constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 16;
 constexpr uint32_t kSmem = kStats + 2 * 128 * 8;  // kStats: [half][row] max and sum
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -120,6 +121,10 @@ struct Walk {
         tiles = (r.keys + kTile - 1) / kTile;
     }
 };
+
+// The ring's pieces are K 0, K 1, V 0, K 2, V 1, ...: the place of V of tile n
+// of `tiles`, the last of which follows V of the one before.
+__device__ __forceinline__ int v_piece(int n, int tiles) { return n + 1 < tiles ? 2 * n + 2 : 2 * n + 1; }
 
 // Waits that give up: one that runs out ends every later one that would block.
 struct Waits {
@@ -287,69 +292,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (head == 0 && lane == 0) a.splits[worker] = split;
     } else if (warp == 9) {
         if (lane == 0) {
-            constexpr uint32_t idesc_s = tc::idesc_bf16(128, kTile, false), idesc_o = tc::idesc_bf16(128, 128, true);
-            int n = 0, job = -1, slot = 0, phase = 0;  // of the next S: its tile, job, ring slot
-            bool first_s = false, last_s = false;      // the newest S is its job's first, last
-            int left = 0;                              // of its job's tiles
-            const auto use = [&] {
-                wait(bar(kFull + slot), phase);
-                tc::fence_after();
-                return sb + kRing + slot * kQBytes;
-            };
-            const auto done = [&] {
-                tc::mma_commit(bar(kEmpty + slot));
-                if (++slot == kSlots) slot = 0, phase ^= 1;
-            };
-            const auto issue_s = [&]() -> bool {
-                first_s = left == 0;
-                if (first_s) {
-                    if (!w.next()) return false;
-                    ++job;
-                    left = w.t1 - w.t0;
-                    wait(bar(kQFull + (job & 1)), (job >> 1) & 1);
-                }
-                const uint32_t k = use(), q = sb + (job & 1) * kQBytes, s = tmem + (n & 1) * kTile;
-                if (n >= 2) wait(bar(kDone), n & 1);  // P V of tile n - 2 has read this buffer; the newest one out is n - 2
-                tc::fence_after();
+            constexpr uint32_t idesc_s = tc::idesc_bf16(128, kTile, false);
+            int n = 0, job = 0;
+            while (w.next()) {
+                const uint32_t q = sb + (job & 1) * kQBytes;
+                wait(bar(kQFull + (job & 1)), (job >> 1) & 1);
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const int piece = n == 0 ? 0 : 2 * n - 1, slot = piece % kSlots;
+                    wait(bar(kFull + slot), piece / kSlots & 1);
+                    if (n >= 2) wait(bar(kDone + (n & 1)), ((n >> 1) - 1) & 1);  // P V of tile n - 2 has read this buffer
+                    tc::fence_after();
+                    const uint32_t k = sb + kRing + slot * kQBytes, d = tmem + (n & 1) * kTile;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t off = (kk >> 2) * tc::kSubTileBytes + (kk & 3) * 32;
-                    tc::mma_bf16(s, tc::sw128_desc(q + off), tc::sw128_desc(k + off), idesc_s, kk > 0);
-                }
-                tc::mma_commit(bar(kSFull + (n & 1)));
-                done();
-                last_s = --left == 0;
-                if (last_s) tc::mma_commit(bar(kQEmpty + (job & 1)));
-                ++n;
-                return true;
-            };
-            bool more = issue_s();
-            while (more) {
-                const int u = n - 1;  // the tile whose P V comes next
-                const bool first = first_s, last = last_s;
-                more = issue_s();
-                wait(bar(kPFull + (u & 1)), (u >> 1) & 1);
-                if (first) wait(bar(kPFull + 2 + (u & 1)), (u >> 1) & 1);  // both halves have read the job before's O
-                const uint32_t v = use();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1) {
-                        wait(bar(kPFull + 2 + (u & 1)), (u >> 1) & 1);
-                        tc::fence_after();
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t off = (kk >> 2) * tc::kSubTileBytes + (kk & 3) * 32;
+                        tc::mma_bf16(d, tc::sw128_desc(q + off), tc::sw128_desc(k + off), idesc_s, kk > 0);
                     }
-                    const uint32_t p = tmem + (u & 1) * kTile + h * 64, o = tmem + kColO + h * 128;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t hi_p = p + (kk >> 1) * 32 + (kk & 1) * 8;
-                        const uint64_t vdesc = tc::sw128_desc_mn(v + h * 8192 + kk * 2048, tc::kSubTileBytes);
-                        tc::mma_bf16_ts(o, hi_p, vdesc, idesc_o, !first || kk > 0);
-                        tc::mma_bf16_ts(o, hi_p + 16, vdesc, idesc_o, 1u);
-                    }
+                    tc::mma_commit(bar(kSFull + (n & 1)));
+                    tc::mma_commit(bar(kEmpty + slot));
                 }
-                done();
-                tc::mma_commit(bar(kDone));
-                // the job's own barrier: a row's thread may be two P V ahead here, more than kDone's parity tells apart
-                if (last) tc::mma_commit(bar(kOFull));
+                tc::mma_commit(bar(kQEmpty + (job & 1)));
+                ++job;
+            }
+        }
+    } else if (warp == 10) {
+        if (lane == 0) {
+            constexpr uint32_t idesc_o = tc::idesc_bf16(128, 128, true);
+            int n = 0;
+            while (w.next()) {
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const int piece = v_piece(n, hi - lo), slot = piece % kSlots;
+                    wait(bar(kFull + slot), piece / kSlots & 1);
+                    wait(bar(kPFull + (n & 1)), (n >> 1) & 1);
+                    if (t == w.t0) wait(bar(kPFull + 2 + (n & 1)), (n >> 1) & 1);  // both halves have read the job before's O
+                    tc::fence_after();
+                    const uint32_t v = sb + kRing + slot * kQBytes;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1) {
+                            wait(bar(kPFull + 2 + (n & 1)), (n >> 1) & 1);
+                            tc::fence_after();
+                        }
+                        const uint32_t p = tmem + (n & 1) * kTile + h * 64, o = tmem + kColO + h * 128;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t hi_p = p + (kk >> 1) * 32 + (kk & 1) * 8;
+                            const uint64_t vdesc = tc::sw128_desc_mn(v + h * 8192 + kk * 2048, tc::kSubTileBytes);
+                            tc::mma_bf16_ts(o, hi_p, vdesc, idesc_o, t > w.t0 || kk > 0);
+                            tc::mma_bf16_ts(o, hi_p + 16, vdesc, idesc_o, 1u);
+                        }
+                    }
+                    tc::mma_commit(bar(kEmpty + slot));
+                    tc::mma_commit(bar(kDone + (n & 1)));
+                }
+                tc::mma_commit(bar(kOFull));
             }
         }
     } else {
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = next;
                 const float ref = next == -INFINITY ? 0.f : next;
                 if (t > w.t0 && __any_sync(kAll, alpha != 1.f)) {
-                    wait(bar(kDone), (n - 1) & 1);  // P V of the tile before has written O
+                    wait(bar(kDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1);  // P V of the tile before has written O
                     __syncwarp();
                     tc::fence_after();
 #pragma unroll
@@ -451,8 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Slots that hold no key (or were not loaded) are zeroed, and of drafted values what is not finite, so
                     // that a probability of 0 meets nothing that it would not cancel; rows that see such a value get it at
                     // the end.  Two threads a key.
-                    // the ring's pieces are K 0, K 1, V 0, K 2, V 1, ..., and V of the last tile follows V of the one before
-                    const int piece = 2 * n + (w.at + t + 1 - w.t0 == hi ? 1 : 2), v_slot = piece % kSlots;
+                    const int piece = v_piece(n, hi - lo), v_slot = piece % kSlots;
                     wait(bar(kFull + v_slot), piece / kSlots & 1);
                     const int key = row >> 1, pos = key0 + key;
                     uint8_t *v = smem + kRing + v_slot * kQBytes + (row & 1) * tc::kSubTileBytes + (h * 64 + key) * 128;
