@@ -43,6 +43,7 @@ constexpr int kPage = 16;
 constexpr int kMaxStages = 8;
 constexpr float kSlack = 8.f;
 constexpr int kMergeThreads = 256;
+constexpr int kMergeCtas = 2;  // an SM
 constexpr int kMaxWorkers = 1024;
 
 // Bytes of a stage: K and V of one page, each two halves of 64 dims.
@@ -521,14 +522,29 @@ bool plan_of(int max_rows, int hq, int hkv, Plan *p) {
 }
 
 // Pools as {dims, token slots, KV heads}: a box is one page's 64 dims of all
-// heads (heads: 1 for one), the rows of 16 tokens of a head together.
-bool make_pool_tmap(CUtensorMap *map, const void *base, int hkv, long long slots, int heads) {
+// heads, the rows of 16 tokens of a head together.
+bool make_pool_tmap(CUtensorMap *map, const void *base, int hkv, long long slots) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {128, (cuuint64_t)slots, (cuuint64_t)hkv};
     cuuint64_t strides[2] = {(cuuint64_t)hkv * 256, 256};
-    cuuint32_t box[3] = {64, 16, (cuuint32_t)heads}, estr[3] = {1, 1, 1};
+    cuuint32_t box[3] = {64, 16, (cuuint32_t)hkv}, estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pools as {64 dims, 8 tokens, halves of the dims, groups of 8 tokens, KV
+// heads}: a box is one page of a head, its groups one after another, of each
+// the first 64 dims and then the others.
+bool make_head_tmap(CUtensorMap *map, const void *base, int hkv, long long slots) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t row = (cuuint64_t)hkv * 256;
+    cuuint64_t dims[5] = {64, 8, 2, (cuuint64_t)slots / 8, (cuuint64_t)hkv};
+    cuuint64_t strides[4] = {row, 128, 8 * row, 256};
+    cuuint32_t box[5] = {64, 8, 2, 2, 1}, estr[5] = {1, 1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -591,9 +607,8 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
     a.scale_log2 = scale * kLog2e;
     CUtensorMap tk, tv;
     const long long slots = (long long)p.num_pages * kPage;
-    const int box_heads = plan.few ? a.hkv : 1;
-    if (!make_pool_tmap(&tk, x.k_pages, a.hkv, slots, box_heads) || !make_pool_tmap(&tv, x.v_pages, a.hkv, slots, box_heads))
-        return cudaErrorInvalidValue;
+    const auto make = plan.few ? make_pool_tmap : make_head_tmap;
+    if (!make(&tk, x.k_pages, a.hkv, slots) || !make(&tv, x.v_pages, a.hkv, slots)) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -617,7 +632,7 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
         e = launch_rows_tiles(a, tq, tk, tv, stream);
     }
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(2 * sm_count()));
+    cfg.gridDim = dim3((unsigned)(kMergeCtas * sm_count()));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, merge_rows_kernel, a);

@@ -7,20 +7,24 @@
 // so that whole token rows are asked of HBM at about the same time.
 //
 //   warp 8     producer: Q once a job (two buffers), K and V of each tile,
-//              page by page (boxes of 16 tokens by 64 dims), into one ring of
-//              five slots in the order they are used
-//   warp 9     issues S = Q K^T (M 128, N 128) into one of two buffers in
-//              TMEM, up to a tile ahead, into the next job too
-//   warp 10    issues, for each half of the tile's keys, O_h += P_h V_h (N
-//              128), P from TMEM; a thread for both products would let the
-//              tensor core run dry at every barrier that it waits on
+//              page by page, into one ring of five slots in the order they
+//              are used.  A page's 16 tokens of a head are one box, of 8 keys
+//              by 64 dims four times: as two boxes of 16 keys by 64 dims the
+//              copies came at 25 bytes a clock (80 clocks a box), which was
+//              what bounded
+//   warp 9     issues S = Q K^T (M 128, N 128) into one of three buffers in
+//              TMEM, up to two tiles ahead, into the next job too
+//   warp 10    issues O += P V (N 128), P from TMEM; a thread for both
+//              products would let the tensor core run dry at every barrier
+//              that it waits on
 //   warps 0-7  softmax: warps 0-3 have the first 64 keys of every tile, warps
 //              4-7 the others, a row a thread: 64 scores in registers, a lazy
 //              running max (log2 slack 8: O is rescaled only when it moves),
 //              P written over its scores as two bf16 terms of 16 columns each
-//              for every 32 keys.  The halves have maxima, sums and
-//              accumulators of their own, which meet at the job's end; Q is
-//              shared by both, which leaves the room for the ring
+//              for every 32 keys.  A row's halves share its reference: a
+//              barrier a tile says whether any row's moves, and only then do
+//              they exchange maxima.  So one O serves both, which leaves TMEM
+//              for the third buffer of S
 //
 // Two terms of P make P V two products: 16 bits of each probability, as in
 // the prefill kernels.  The tensor core needs 514 clocks for S and 1028 for
@@ -42,16 +46,18 @@ constexpr int kPage = 16;
 constexpr int kTile = 128;
 constexpr int kThreads = 352;
 constexpr int kSlots = 5;
+constexpr int kBufs = 3;
 constexpr float kSlack = 8.f;
 constexpr uint32_t kQBytes = 2 * tc::kSubTileBytes;  // two halves of 64 dims of 128 rows; K and V of a tile too
+constexpr uint32_t kAtom = 1024, kGroup = 2 * kAtom;    // of K and V: 8 keys' first 64 dims, then their others
 constexpr uint32_t kRing = 2 * kQBytes;
 constexpr uint32_t kBar = kRing + kSlots * kQBytes;
 enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots,
-                  kPFull = kSFull + 2, kDone = kPFull + 4, kOFull = kDone + 2, kBars };  // kPFull: [half][buffer]
+                  kPFull = kSFull + kBufs, kDone = kPFull + kBufs, kOFull = kDone + kBufs, kBars };
 constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 16;
-constexpr uint32_t kSmem = kStats + 2 * 128 * 8;  // kStats: [half][row] max and sum
+constexpr uint32_t kSmem = kStats + 2 * 2 * 128 * 4;  // kStats: [half][row] of maxima, then of sums
 static_assert(kSmem <= 227 * 1024, "shared memory");
-constexpr uint32_t kColO = 256;  // TMEM: S / P in [0, 128) and [128, 256), O of the halves in [256, 384) and [384, 512)
+constexpr uint32_t kColO = kBufs * kTile;  // TMEM: three buffers of S / P, then O
 
 // A call's tiles, and the request of the worker's first one, by one warp.
 struct Start {
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Start s = find_start(a, worker, rows_a_block, blockIdx.x == 0 ? &g_status : nullptr);
         if (lane == 0) *reinterpret_cast<Start *>(smem + kStart) = s;
     } else if (warp == 8 && lane == 0) {
-        for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + 4 ? 4 : 1);
+        for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + kBufs ? 8 : 1);
         *wait.abort = 0;
         fence_mbar_init();
         tc::prefetch_tmap(&tq);
@@ -235,18 +241,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 8) {
         // ring order K 0, K 1, V 0, K 2, V 1, ...
-        const int p = (lane >> 1) & 7, sd = lane & 1;
+        const int p = lane & 7;
         int slot = 0, phase = 1, job = 0, id_before = -1;
         bool any = false;
         Split split = {0, 0, 0, 0};
         const auto load = [&](const CUtensorMap *map, int id) {
             wait(bar(kEmpty + slot), phase);
             const unsigned boxes = __ballot_sync(kAll, id >= 0);
-            if (lane == 0) mbar_arrive_expect_tx(bar(kFull + slot), __popc(boxes) * kPage * 128);
+            if (lane == 0) mbar_arrive_expect_tx(bar(kFull + slot), __popc(boxes) * 2 * kGroup);
             __syncwarp();
-            if (id >= 0)
-                tc::tma_load_3d(sb + kRing + slot * kQBytes + sd * tc::kSubTileBytes + p * kPage * 128, map, sd * 64, id * kPage, head,
-                                bar(kFull + slot));
+            if (id >= 0) tc::tma_load_5d(sb + kRing + slot * kQBytes + p * 2 * kGroup, map, 0, 0, 0, 2 * id, head, bar(kFull + slot));
             if (++slot == kSlots) slot = 0, phase ^= 1;
         };
         while (w.next()) {
@@ -262,11 +266,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             ++job;
-            int ids = -1, chunk = -1;
+            // 32 page ids at a time, the next ones on their way
+            const auto page_ids = [&](int chunk) { return chunk * 32 + lane < pages ? row[chunk * 32 + lane] : -1; };
+            int ids = -1, ids_next = page_ids(w.t0 >> 2);
             for (int t = w.t0; t < w.t1; ++t) {
-                if (t >> 2 != chunk) {  // 32 page ids at a time
-                    chunk = t >> 2;
-                    ids = chunk * 32 + lane < pages ? row[chunk * 32 + lane] : -1;
+                if (t == w.t0 || (t & 3) == 0) {
+                    const int chunk = t >> 2;
+                    ids = ids_next;
+                    ids_next = page_ids(chunk + 1);
                     if (chunk * 32 + lane < pages && (ids < 0 || ids >= a.num_pages)) {
                         const int tile = chunk * 4 + (lane >> 3);
                         if (tile >= w.t0 && tile < w.t1) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 int id = __shfl_sync(kAll, ids, (8 * t + p) & 31);
-                if (lane >= 16) id = -1;
+                if (lane >= 8) id = -1;
                 load(&tk, id);
                 if (any) load(&tv, id_before);
                 id_before = id;
@@ -293,23 +300,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
         if (lane == 0) {
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, kTile, false);
-            int n = 0, job = 0;
+            int n = 0, job = 0, buf = 0, phase = 0;
             while (w.next()) {
                 const uint32_t q = sb + (job & 1) * kQBytes;
                 wait(bar(kQFull + (job & 1)), (job >> 1) & 1);
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
                     const int piece = n == 0 ? 0 : 2 * n - 1, slot = piece % kSlots;
                     wait(bar(kFull + slot), piece / kSlots & 1);
-                    if (n >= 2) wait(bar(kDone + (n & 1)), ((n >> 1) - 1) & 1);  // P V of tile n - 2 has read this buffer
+                    if (n >= kBufs) wait(bar(kDone + buf), phase ^ 1);  // P V of tile n - 3 has read this buffer
                     tc::fence_after();
-                    const uint32_t k = sb + kRing + slot * kQBytes, d = tmem + (n & 1) * kTile;
+                    const uint32_t k = sb + kRing + slot * kQBytes, d = tmem + buf * kTile;
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
                         const uint32_t off = (kk >> 2) * tc::kSubTileBytes + (kk & 3) * 32;
-                        tc::mma_bf16(d, tc::sw128_desc(q + off), tc::sw128_desc(k + off), idesc_s, kk > 0);
+                        tc::mma_bf16(d, tc::sw128_desc(q + off), tc::sw128_desc(k + (kk >> 2) * kAtom + (kk & 3) * 32, kGroup, 0), idesc_s, kk > 0);
                     }
-                    tc::mma_commit(bar(kSFull + (n & 1)));
+                    tc::mma_commit(bar(kSFull + buf));
                     tc::mma_commit(bar(kEmpty + slot));
+                    if (++buf == kBufs) buf = 0, phase ^= 1;
                 }
                 tc::mma_commit(bar(kQEmpty + (job & 1)));
                 ++job;
@@ -318,41 +326,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 10) {
         if (lane == 0) {
             constexpr uint32_t idesc_o = tc::idesc_bf16(128, 128, true);
-            int n = 0;
+            int n = 0, buf = 0, phase = 0;
             while (w.next()) {
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
                     const int piece = v_piece(n, hi - lo), slot = piece % kSlots;
                     wait(bar(kFull + slot), piece / kSlots & 1);
-                    wait(bar(kPFull + (n & 1)), (n >> 1) & 1);
-                    if (t == w.t0) wait(bar(kPFull + 2 + (n & 1)), (n >> 1) & 1);  // both halves have read the job before's O
+                    wait(bar(kPFull + buf), phase);
                     tc::fence_after();
-                    const uint32_t v = sb + kRing + slot * kQBytes;
+                    const uint32_t v = sb + kRing + slot * kQBytes, p = tmem + buf * kTile;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h == 1) {
-                            wait(bar(kPFull + 2 + (n & 1)), (n >> 1) & 1);
-                            tc::fence_after();
-                        }
-                        const uint32_t p = tmem + (n & 1) * kTile + h * 64, o = tmem + kColO + h * 128;
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint32_t hi_p = p + (kk >> 1) * 32 + (kk & 1) * 8;
-                            const uint64_t vdesc = tc::sw128_desc_mn(v + h * 8192 + kk * 2048, tc::kSubTileBytes);
-                            tc::mma_bf16_ts(o, hi_p, vdesc, idesc_o, t > w.t0 || kk > 0);
-                            tc::mma_bf16_ts(o, hi_p + 16, vdesc, idesc_o, 1u);
-                        }
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t hi_p = p + (kk >> 1) * 32 + (kk & 1) * 8;
+                        const uint64_t vdesc = tc::sw128_desc(v + kk * 2 * kGroup, kGroup, kAtom);
+                        tc::mma_bf16_ts(tmem + kColO, hi_p, vdesc, idesc_o, t > w.t0 || kk > 0);
+                        tc::mma_bf16_ts(tmem + kColO, hi_p + 16, vdesc, idesc_o, 1u);
                     }
                     tc::mma_commit(bar(kEmpty + slot));
-                    tc::mma_commit(bar(kDone + (n & 1)));
+                    tc::mma_commit(bar(kDone + buf));
+                    if (++buf == kBufs) buf = 0, phase ^= 1;
                 }
                 tc::mma_commit(bar(kOFull));
             }
         }
     } else {
         const int h = warp >> 2, row = threadIdx.x & 127;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21, t_o = tmem + kColO + h * 128 + lanes;
-        float2 *stats = reinterpret_cast<float2 *>(smem + kStats);
-        int n = 0, job = 0;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, t_o = tmem + kColO + h * 64 + lanes;
+        float *maxima = reinterpret_cast<float *>(smem + kStats), *sums = maxima + 256;
+        int n = 0, job = 0, buf = 0, phase = 0;
         while (w.next()) {
             const Request &r = w.r;
             const int32_t *table = a.page_table + (size_t)w.b * a.max_pages;
@@ -366,17 +366,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t s0 = __shfl_sync(kAll, all[0], node & 31), s1 = __shfl_sync(kAll, all[1], node & 31);
                 seen = node >= r.rows ? 0 : node < 32 ? s0 : s1;
             }
-            const auto ids_ok = [&](int t) -> uint32_t {  // which of the half's four pages can be read
-                const int page = 8 * t + 4 * h + (lane & 3), id = t < w.t1 && page < pages ? table[page] : 0;
-                return __ballot_sync(kAll, id >= 0 && id < a.num_pages) & 15u;
+            const auto page_id = [&](int t) {  // of the half's four pages, the lane's; a tile ahead of its use
+                const int page = 8 * t + 4 * h + (lane & 3);
+                return t < w.t1 && page < pages ? table[page] : 0;
             };
             float m = -INFINITY, l = 0.f;
             bool odd = false;
-            uint32_t next_ok = ids_ok(w.t0);
+            int id = page_id(w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const uint32_t ok = next_ok, s = tmem + (n & 1) * kTile + h * 64 + lanes;
-                next_ok = ids_ok(t + 1);
-                wait(bar(kSFull + (n & 1)), (n >> 1) & 1);
+                const uint32_t ok = __ballot_sync(kAll, id >= 0 && id < a.num_pages) & 15u;  // the pages that can be read
+                const uint32_t s = tmem + buf * kTile + h * 64 + lanes;
+                id = page_id(t + 1);
+                wait(bar(kSFull + buf), phase);
                 __syncwarp();
                 tc::fence_after();
                 uint32_t sc[2][32];
@@ -406,23 +407,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; j += 2)
                         mx4[(j >> 1) & 3] = fmax3(mx4[(j >> 1) & 3], __uint_as_float(sc[c][j]), __uint_as_float(sc[c][j + 1]));
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-                const float next = mx > m + kSlack ? mx : m;
-                const float alpha = next == m ? 1.f : exp2_approx(m - next);
-                m = next;
-                const float ref = next == -INFINITY ? 0.f : next;
-                if (t > w.t0 && __any_sync(kAll, alpha != 1.f)) {
-                    wait(bar(kDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1);  // P V of the tile before has written O
-                    __syncwarp();
-                    tc::fence_after();
+                // one reference a row, for both halves: where a row's moves, its halves agree on the larger maximum
+                float alpha = 1.f;
+                if (any_of_rows(mx > m + kSlack)) {
+                    maxima[h * 128 + row] = mx;
+                    named_barrier(1, 256);
+                    const float top = fmaxf(mx, maxima[(h ^ 1) * 128 + row]), next = top > m + kSlack ? top : m;
+                    alpha = next == m ? 1.f : exp2_approx(m - next);
+                    m = next;
+                    if (t > w.t0 && __any_sync(kAll, alpha != 1.f)) {
+                        // P V of the tile before has written O, of which each half scales 64 dims
+                        wait(bar(kDone + (buf == 0 ? kBufs - 1 : buf - 1)), buf == 0 ? phase ^ 1 : phase);
+                        __syncwarp();
+                        tc::fence_after();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float o[32];
-                        tc::tmem_ld32(t_o + c * 32, o);
+                        for (int c = 0; c < 2; ++c) {
+                            float o[32];
+                            tc::tmem_ld32(t_o + c * 32, o);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] *= alpha;
-                        tc::tmem_st32(t_o + c * 32, o);
+                            for (int j = 0; j < 32; ++j) o[j] *= alpha;
+                            tc::tmem_st32(t_o + c * 32, o);
+                        }
                     }
                 }
+                const float ref = m == -INFINITY ? 0.f : m;
                 const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
                 float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int piece = v_piece(n, hi - lo), v_slot = piece % kSlots;
                     wait(bar(kFull + v_slot), piece / kSlots & 1);
                     const int key = row >> 1, pos = key0 + key;
-                    uint8_t *v = smem + kRing + v_slot * kQBytes + (row & 1) * tc::kSubTileBytes + (h * 64 + key) * 128;
+                    uint8_t *v = smem + kRing + v_slot * kQBytes + (8 * h + (key >> 3)) * kGroup + (row & 1) * kAtom + (key & 7) * 128;
                     const bool live = pos < r.keys && (ok >> (key >> 4) & 1);
                     if (!live || pos >= r.past) {
 #pragma unroll
@@ -472,21 +480,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tmem_wait_st();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kPFull + 2 * h + (n & 1)));
+                if (lane == 0) mbar_arrive(bar(kPFull + buf));
+                if (++buf == kBufs) buf = 0, phase ^= 1;
             }
-            stats[h * 128 + row] = make_float2(m, l);
-            const bool any_odd = any_of_rows(odd);  // both halves' statistics are there too
-            const float2 other = stats[(h ^ 1) * 128 + row];
-            named_barrier(1, 256);  // read before the next job's are written
-            const float top = fmaxf(m, other.x);
-            const float w_mine = m == -INFINITY ? 0.f : exp2_approx(m - top), w_other = other.x == -INFINITY ? 0.f : exp2_approx(other.x - top);
-            const float sum = l * w_mine + other.y * w_other;
-            const float w0 = h == 0 ? w_mine : w_other, w1 = h == 0 ? w_other : w_mine;
+            sums[h * 128 + row] = l;
+            const bool any_odd = any_of_rows(odd);  // both halves' sums are there too
+            const float sum = l + sums[(h ^ 1) * 128 + row];
             wait(bar(kOFull), job & 1);
             ++job;
             __syncwarp();
             tc::fence_after();
-            // the half's warps give 64 of the dims, of both accumulators
+            // each half's warps give 64 of the dims
             const bool whole = w.t0 == 0 && w.t1 == w.tiles;
             const int left = (r.rows - w.block * rows_a_block) * a.group;  // rows from this block's first on
             const int slot = 2 * worker + (w.at > lo);
@@ -497,11 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int dim = h * 64 + c * 32;
-                float o[32], o1[32];
-                tc::tmem_ld32(tmem + kColO + lanes + dim, o);
-                tc::tmem_ld32(tmem + kColO + 128 + lanes + dim, o1);
+                float o[32];
+                tc::tmem_ld32(t_o + c * 32, o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = (o[j] * w0 + o1[j] * w1) * inv;
+                for (int j = 0; j < 32; ++j) o[j] *= inv;
                 if (any_odd) {
                     for (int pos = max(r.past, w.t0 * kTile); pos < min(r.keys, w.t1 * kTile); ++pos) {
                         const int id = table[pos >> 4];
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (!whole && h == 0 && row < left) *reinterpret_cast<float2 *>(a.ml + 2 * part) = make_float2(top, sum);
+            if (!whole && h == 0 && row < left) *reinterpret_cast<float2 *>(a.ml + 2 * part) = make_float2(m, sum);
             tc::fence_before();  // before the next job's P is handed over
         }
     }

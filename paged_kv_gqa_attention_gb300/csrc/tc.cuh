@@ -31,6 +31,14 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
            ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
+// The same with other strides: group_stride bytes between consecutive groups
+// of 8 rows and, for an MN-major operand wider than 64 elements, mn_stride
+// bytes between its swizzle atoms (0: none).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t group_stride, uint32_t mn_stride) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(mn_stride ? (mn_stride >> 4) & 0x3FFFu : 1u) << 16) |
+           ((uint64_t)((group_stride >> 4) & 0x3FFFu) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
 // The same for an MN-major operand wider than one 128-byte swizzle atom in
 // its MN dimension (N = 128 of a V tile held as two 64-wide sub-tiles): the
 // leading-dimension byte offset is the distance between consecutive atoms
@@ -235,6 +243,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
         "[%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// Tiled TMA load of a 5-D box into shared memory, completing on an mbarrier.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+        "[%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
         : "memory");
 }
 
