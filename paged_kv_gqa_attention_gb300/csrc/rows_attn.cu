@@ -43,7 +43,6 @@ constexpr int kPage = 16;
 constexpr int kMaxStages = 8;
 constexpr float kSlack = 8.f;
 constexpr int kMergeThreads = 256;
-constexpr int kMergeCtas = 2;  // an SM
 constexpr int kMaxWorkers = 1024;
 
 // Bytes of a stage: K and V of one page, each two halves of 64 dims.
@@ -381,18 +380,92 @@ __global__ void __launch_bounds__(288, 1)
     }
 }
 
-// Merges the jobs that span several workers: rows of up to 8 partials by a
-// warp each, rows of more by a CTA, whose warps take every eighth.  Partials
-// are added in the order of their workers, 4 loads in flight a lane.
-__global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const __grid_constant__ RowsArgs a) {
+// A running merge of partials: the lane's four dims of one row.
+struct Merge {
+    float m = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ void add(float2 ml, float4 v) {
+        const float next = fmaxf(m, ml.x);
+        if (next == -INFINITY) return;  // a worker that saw no key of this row
+        const float old = m == -INFINITY ? 0.f : exp2_approx(m - next), now = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - next);
+        sum = sum * old + ml.y * now;
+        acc.x = acc.x * old + v.x * now, acc.y = acc.y * old + v.y * now;
+        acc.z = acc.z * old + v.z * now, acc.w = acc.w * old + v.w * now;
+        m = next;
+    }
+};
+
+// Merges rows item0, item0 + step, .. (NI of them, a head's rows in turn) of
+// worker w's split over partials first, first + by, .., in this order, FLIGHT
+// of each row in flight.
+template <int NI, int FLIGHT>
+__device__ __forceinline__ void merge_items(const RowsArgs &a, const Split &s, int w, int item0, int step, int first, int by,
+                                            Merge (&g)[NI]) {
+    const int lane = threadIdx.x & 31, n = s.rows * a.hkv;
+    size_t at[NI];
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+        const int item = min(item0 + k * step, n - 1);
+        at[k] = (size_t)(item / s.rows) * a.block_rows + item % s.rows;
+    }
+    for (int i = first; i < s.count; i += FLIGHT * by) {
+        float2 ml[NI][FLIGHT];
+        float4 v[NI][FLIGHT];
+#pragma unroll
+        for (int x = 0; x < FLIGHT; ++x)
+            if (i + x * by < s.count) {
+                const size_t slot = i + x * by == 0 ? s.first_slot : 2 * (w + i + x * by), base = slot * a.hkv * a.block_rows;
+#pragma unroll
+                for (int k = 0; k < NI; ++k) {
+                    ml[k][x] = __ldcg(reinterpret_cast<const float2 *>(a.ml) + base + at[k]);
+                    v[k][x] = __ldcg(reinterpret_cast<const float4 *>(a.acc) + (base + at[k]) * 32 + lane);
+                }
+            }
+#pragma unroll
+        for (int x = 0; x < FLIGHT; ++x)
+            if (i + x * by < s.count) {
+#pragma unroll
+                for (int k = 0; k < NI; ++k) g[k].add(ml[k][x], v[k][x]);
+            }
+    }
+}
+
+__device__ __forceinline__ void store_item(const RowsArgs &a, const Split &s, int item, const Merge &g) {
+    if (item >= s.rows * a.hkv) return;
+    const int head = item / s.rows, row = item % s.rows;
+    const float inv = g.sum > 0.f ? 1.f / g.sum : g.sum;
+    uint16_t *dst = a.out + ((size_t)(s.out_row + row / a.group) * a.hq + head * a.group + row % a.group) * 128;
+    reinterpret_cast<uint2 *>(dst)[threadIdx.x & 31] =
+        make_uint2(pack_bf16x2(g.acc.x * inv, g.acc.y * inv), pack_bf16x2(g.acc.z * inv, g.acc.w * inv));
+}
+
+// A row of many partials by a CTA, whose warps take every eighth.
+__device__ __forceinline__ void merge_by_cta(const RowsArgs &a, const Split &s, int w, int item) {
+    constexpr int kWarps = kMergeThreads / 32;
+    __shared__ float4 s_acc[kWarps][32];
+    __shared__ float2 s_ml[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Merge g[1];
+    merge_items<1, 4>(a, s, w, item, 0, warp, kWarps, g);
+    s_acc[warp][lane] = g[0].acc;
+    if (lane == 0) s_ml[warp] = make_float2(g[0].m, g[0].sum);
+    __syncthreads();
+    if (warp == 0) {
+        Merge all;
+        for (int x = 0; x < kWarps; ++x) all.add(s_ml[x], s_acc[x][lane]);
+        store_item(a, s, item, all);
+    }
+    __syncthreads();
+}
+
+// The merge behind few_rows_kernel, with many workers and few rows a split:
+// every CTA sums up the steps that all splits take and takes its share.
+__global__ void __launch_bounds__(kMergeThreads) merge_few_kernel(const __grid_constant__ RowsArgs a) {
     constexpr unsigned kAll = 0xffffffffu;
     constexpr int kWarps = kMergeThreads / 32, kEach = kMaxWorkers / kMergeThreads;
     __shared__ int start[kMaxWorkers + 1], sums[kWarps];
-    __shared__ float4 s_acc[kWarps][32];
-    __shared__ float2 s_ml[kWarps];
     grid_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // steps of a CTA that each split job takes, and their prefix sums
     int steps[kEach], mine = 0;
 #pragma unroll
     for (int x = 0; x < kEach; ++x) {
@@ -424,61 +497,39 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const __grid_
     __syncthreads();
     const int total = start[kMaxWorkers];
     for (int step = blockIdx.x; step < total; step += gridDim.x) {
-        int l = 0, r = kMaxWorkers - 1;
-        while (l < r) {  // the split that has this step
-            const int mid = (l + r) >> 1;
-            if (start[mid + 1] > step) r = mid; else l = mid + 1;
+        int w = 0, r = kMaxWorkers - 1;
+        while (w < r) {  // the split that has this step
+            const int mid = (w + r) >> 1;
+            if (start[mid + 1] > step) r = mid; else w = mid + 1;
         }
-        const Split s = a.splits[l];
-        const bool team = s.count > kWarps;
-        const int item = team ? step - start[l] : (step - start[l]) * kWarps + warp;
-        const bool live = item < s.rows * a.hkv;
-        const int head = live ? item / s.rows : 0, row = live ? item % s.rows : 0;
-        const int first = team ? warp : 0, by = team ? kWarps : 1;
-        const auto at = [&](int i) {
-            const size_t slot = i == 0 ? s.first_slot : 2 * (l + i);
-            return (slot * a.hkv + head) * a.block_rows + row;
-        };
-        float m = -INFINITY, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        const auto add = [&](float2 ml, float4 v) {
-            const float next = fmaxf(m, ml.x);
-            if (next == -INFINITY) return;  // a worker that saw no key of this row
-            const float old = m == -INFINITY ? 0.f : exp2_approx(m - next), now = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - next);
-            sum = sum * old + ml.y * now;
-            acc.x = acc.x * old + v.x * now, acc.y = acc.y * old + v.y * now;
-            acc.z = acc.z * old + v.z * now, acc.w = acc.w * old + v.w * now;
-            m = next;
-        };
-        if (live)
-            for (int i = first; i < s.count; i += 4 * by) {
-                float2 ml[4];
-                float4 v[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (i + x * by < s.count) {
-                        const size_t p = at(i + x * by);
-                        ml[x] = __ldcg(reinterpret_cast<const float2 *>(a.ml) + p);
-                        v[x] = __ldcg(reinterpret_cast<const float4 *>(a.acc) + p * 32 + lane);
-                    }
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (i + x * by < s.count) add(ml[x], v[x]);
-            }
-        if (team) {
-            s_acc[warp][lane] = acc;
-            if (lane == 0) s_ml[warp] = make_float2(m, sum);
-            __syncthreads();
-            if (warp == 0) {
-                m = -INFINITY, sum = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int x = 0; x < kWarps; ++x) add(s_ml[x], s_acc[x][lane]);
-            }
-            __syncthreads();
+        const Split s = a.splits[w];
+        if (s.count > kWarps) {
+            merge_by_cta(a, s, w, step - start[w]);
+        } else {
+            const int item = (step - start[w]) * kWarps + warp;
+            Merge g[1];
+            merge_items<1, 4>(a, s, w, item, 0, 0, 1, g);
+            store_item(a, s, item, g[0]);
         }
-        if (live && (!team || warp == 0)) {
-            const float inv = sum > 0.f ? 1.f / sum : sum;
-            uint16_t *dst = a.out + ((size_t)(s.out_row + row / a.group) * a.hq + head * a.group + row % a.group) * 128;
-            reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+}
+
+// The merge behind rows_tiles_kernel, with few workers and many rows a split:
+// a worker's CTAs take the rows of its split in turn, a warp two at a time.
+__global__ void __launch_bounds__(kMergeThreads) merge_tiles_kernel(const __grid_constant__ RowsArgs a) {
+    constexpr int kWarps = kMergeThreads / 32;
+    grid_wait();
+    const int w = blockIdx.y, n_warps = gridDim.x * kWarps;
+    const Split s = a.splits[w];
+    const int n = s.count ? s.rows * a.hkv : 0;
+    if (s.count > kWarps) {
+        for (int item = blockIdx.x; item < n; item += gridDim.x) merge_by_cta(a, s, w, item);
+    } else {
+        for (int item = blockIdx.x * kWarps + (threadIdx.x >> 5); item < n; item += 2 * n_warps) {
+            Merge g[2];
+            merge_items<2, 3>(a, s, w, item, n_warps, 0, 1, g);
+            store_item(a, s, item, g[0]);
+            store_item(a, s, item + n_warps, g[1]);
         }
     }
 }
@@ -632,10 +683,14 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
         e = launch_rows_tiles(a, tq, tk, tv, stream);
     }
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(kMergeCtas * sm_count()));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, merge_rows_kernel, a);
+    if (plan.few) {
+        cfg.gridDim = dim3((unsigned)(2 * sm_count()));
+        return cudaLaunchKernelEx(&cfg, merge_few_kernel, a);
+    }
+    cfg.gridDim = dim3((unsigned)(4 * a.hkv), (unsigned)plan.workers);  // up to 128 rows a head: two rounds of two a warp
+    return cudaLaunchKernelEx(&cfg, merge_tiles_kernel, a);
 }
 
 unsigned int status_read_clear_rows_attn(cudaStream_t stream, cudaError_t *err) {

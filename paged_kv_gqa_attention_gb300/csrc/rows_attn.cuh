@@ -50,8 +50,7 @@ struct Request {
     bool valid;  // its rows are its own: they may be written
 };
 
-__device__ __forceinline__ Request request_of(const RowsArgs &a, int b, unsigned int *report) {
-    const int first = a.cu[b], end = a.cu[b + 1], past = a.past[b];
+__device__ __forceinline__ Request request_of(const RowsArgs &a, int first, int end, int past, unsigned int *report) {
     Request r = {first, 0, 0, 0, first >= 0 && end >= first && end <= a.rows};
     if (!r.valid) {
         if (report) atomicOr(report, QA_DEVICE_BAD_SEGMENTS);
@@ -66,6 +65,9 @@ __device__ __forceinline__ Request request_of(const RowsArgs &a, int b, unsigned
     r.past = past;
     r.keys = r.rows > 0 ? (int)keys : 0;
     return r;
+}
+__device__ __forceinline__ Request request_of(const RowsArgs &a, int b, unsigned int *report) {
+    return request_of(a, a.cu[b], a.cu[b + 1], a.past[b], report);
 }
 
 // A request with nothing to attend to has zero rows.

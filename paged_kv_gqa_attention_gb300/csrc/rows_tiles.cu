@@ -107,9 +107,12 @@ struct Walk {
     int block, t0, t1;  // the segment: rows block, tiles [t0, t1) of `tiles`
     int tiles;
     Request r;
+    int first_next, end_next, past_next;  // of request b + 1
     __device__ Walk(const RowsArgs &args, const Start &s, int lo, int end, int rab)
         : a(args), at(lo), hi(end), b(s.b), base(s.base), rows_a_block(rab), t0(0), t1(0) {
-        if (lo < end) load();
+        if (lo >= end) return;
+        first_next = a.cu[b], end_next = a.cu[b + 1], past_next = a.past[b];
+        load();
     }
     __device__ bool next() {
         at += t1 - t0;
@@ -122,9 +125,10 @@ struct Walk {
         return true;
     }
     __device__ int mine() const { return tiles * ((r.rows + rows_a_block - 1) / rows_a_block); }
-    __device__ void load() {
-        r = request_of(a, b, nullptr);
+    __device__ void load() {  // the request whose numbers are here, and asks for the next one's
+        r = request_of(a, first_next, end_next, past_next, nullptr);
         tiles = (r.keys + kTile - 1) / kTile;
+        if (b + 1 < a.batch) first_next = end_next, end_next = a.cu[b + 2], past_next = a.past[b + 1];
     }
 };
 
@@ -167,22 +171,13 @@ __device__ __forceinline__ void store32(float *dst, const float *v) {  // 32-byt
 
 // The rows that row i sees among the drafted ones (bit j: row j), by a warp
 // for all 64 rows, two a lane: reach doubles every round.
-__device__ __forceinline__ void ancestors(const RowsArgs &a, const Request &r, uint64_t (&seen)[2]) {
+__device__ __forceinline__ void ancestors(const RowsArgs &a, int (&up)[2], uint64_t (&seen)[2]) {
     constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
-    int up[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int i = lane + 32 * x;
-        if (!a.parents) {
-            seen[x] = ~0ull >> (63 - i);
-            continue;
-        }
-        up[x] = i < r.rows ? parent_of(a, r.first, i, &g_status) : -1;
-        seen[x] = 1ull << i;
-    }
+    for (int x = 0; x < 2; ++x) seen[x] = a.parents ? 1ull << (lane + 32 * x) : ~0ull >> (63 - lane - 32 * x);
     if (!a.parents) return;
-    for (int n = 0; n < 6; ++n) {
+    while (__any_sync(kAll, up[0] >= 0 || up[1] >= 0)) {
         uint64_t theirs[2];
         int next[2];
 #pragma unroll
@@ -358,14 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t *table = a.page_table + (size_t)w.b * a.max_pages;
             const int pages = (r.keys + kPage - 1) / kPage;
             const bool drafted = a.tree && w.t1 * kTile > r.past;
-            uint64_t seen = 0;
-            if (drafted) {
-                uint64_t all[2];
-                ancestors(a, r, all);
-                const int node = row / a.group;
-                const uint64_t s0 = __shfl_sync(kAll, all[0], node & 31), s1 = __shfl_sync(kAll, all[1], node & 31);
-                seen = node >= r.rows ? 0 : node < 32 ? s0 : s1;
+            uint64_t seen = 0;  // of the drafted rows, found where the first of them comes
+            int up[2] = {-1, -1};
+            if (drafted && a.parents) {
+                if (lane < r.rows) up[0] = a.parents[r.first + lane];
+                if (lane + 32 < r.rows) up[1] = a.parents[r.first + lane + 32];
             }
+            bool found = !drafted;
             const auto page_id = [&](int t) {  // of the half's four pages, the lane's; a tile ahead of its use
                 const int page = 8 * t + 4 * h + (lane & 3);
                 return t < w.t1 && page < pages ? table[page] : 0;
@@ -388,6 +382,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key0 = t * kTile + h * 64, behind = r.past - key0;  // keys of this half that every row sees
                 const bool masked = behind < 64 || ok != 15u;
                 if (masked) {
+                    if (!found) {
+                        uint64_t all[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (up[x] < -1 || up[x] >= lane + 32 * x) atomicOr(&g_status, QA_DEVICE_BAD_TREE), up[x] = -1;
+                        ancestors(a, up, all);
+                        const int node = row / a.group;
+                        const uint64_t s0 = __shfl_sync(kAll, all[0], node & 31), s1 = __shfl_sync(kAll, all[1], node & 31);
+                        seen = node >= r.rows ? 0 : node < 32 ? s0 : s1;
+                        found = true;
+                    }
                     uint64_t vis = behind >= 64 ? ~0ull : behind > 0 ? ~(~0ull << behind) : 0ull;
                     if (behind < 64 && behind > -64) vis |= behind >= 0 ? seen << behind : seen >> -behind;
 #pragma unroll
@@ -462,8 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool live = pos < r.keys && (ok >> (key >> 4) & 1);
                     if (!live || pos >= r.past) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            uint4 *at = reinterpret_cast<uint4 *>(v) + c;
+                        for (int c = 0; c < 8; ++c) {  // a key's lanes begin at chunks of their own: no bank twice
+                            uint4 *at = reinterpret_cast<uint4 *>(v) + ((c + key) & 7);
                             uint4 z = make_uint4(0u, 0u, 0u, 0u);
                             if (live) {
                                 const uint4 x = *at;
