@@ -44,7 +44,11 @@ __device__ unsigned int g_status;
 
 constexpr int kPage = 16;
 constexpr int kTile = 128;
-constexpr int kThreads = 352;
+constexpr int kParts = 4;               // of a tile's keys, each a warpgroup's
+constexpr int kKeys = kTile / kParts;   // of a thread
+constexpr int kRows = kParts * 128;     // threads that own rows
+constexpr int kProducer = kParts * 4, kIssueS = kProducer + 1, kIssueO = kIssueS + 1;  // warps
+constexpr int kThreads = (kIssueO + 1) * 32;
 constexpr int kSlots = 5;
 constexpr int kBufs = 3;
 constexpr float kSlack = 8.f;
@@ -55,7 +59,7 @@ constexpr uint32_t kBar = kRing + kSlots * kQBytes;
 enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots,
                   kPFull = kSFull + kBufs, kDone = kPFull + kBufs, kOFull = kDone + kBufs, kBars };
 constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 16;
-constexpr uint32_t kSmem = kStats + 2 * 2 * 128 * 4;  // kStats: [half][row] of maxima, then of sums
+constexpr uint32_t kSmem = kStats + kParts * 128 * 4;  // kStats: [part][row]
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kColO = kBufs * kTile;  // TMEM: three buffers of S / P, then O
 
@@ -153,11 +157,11 @@ struct Waits {
     }
 };
 
-__device__ __forceinline__ bool any_of_rows(bool x) {  // the 256 threads that own rows
+__device__ __forceinline__ bool any_of_rows(bool x) {  // the threads that own rows
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"((uint32_t)x)
+                 : "r"((uint32_t)x), "n"(kRows)
                  : "memory");
     return r != 0;
 }
@@ -211,8 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         const Start s = find_start(a, worker, rows_a_block, blockIdx.x == 0 ? &g_status : nullptr);
         if (lane == 0) *reinterpret_cast<Start *>(smem + kStart) = s;
-    } else if (warp == 8 && lane == 0) {
-        for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + kBufs ? 8 : 1);
+    } else if (warp == kProducer && lane == 0) {
+        for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + kBufs ? kParts * 4 : 1);
         *wait.abort = 0;
         fence_mbar_init();
         tc::prefetch_tmap(&tq);
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // TMEM only once the kernel before has ended: one that starts its successors before it allocates could wait for
     // columns that this one holds while it waits for that kernel
     if (a.early) grid_wait();
-    if (warp == 9) tc::tmem_alloc(sb + kTmem, 512);
+    if (warp == kIssueS) tc::tmem_alloc(sb + kTmem, 512);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = worker; b < a.batch; b += a.workers) zero_rows(a, request_of(a, b, nullptr), threadIdx.x, kThreads);
     Walk w(a, start, lo, hi, rows_a_block);
 
-    if (warp == 8) {
+    if (warp == kProducer) {
         // ring order K 0, K 1, V 0, K 2, V 1, ...
         const int p = lane & 7;
         int slot = 0, phase = 1, job = 0, id_before = -1;
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (any) load(&tv, id_before);
         if (head == 0 && lane == 0) a.splits[worker] = split;
-    } else if (warp == 9) {
+    } else if (warp == kIssueS) {
         if (lane == 0) {
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, kTile, false);
             int n = 0, job = 0, buf = 0, phase = 0;
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++job;
             }
         }
-    } else if (warp == 10) {
+    } else if (warp == kIssueO) {
         if (lane == 0) {
             constexpr uint32_t idesc_o = tc::idesc_bf16(128, 128, true);
             int n = 0, buf = 0, phase = 0;
@@ -345,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         const int h = warp >> 2, row = threadIdx.x & 127;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21, t_o = tmem + kColO + h * 64 + lanes;
-        float *maxima = reinterpret_cast<float *>(smem + kStats), *sums = maxima + 256;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, t_o = tmem + kColO + h * kKeys + lanes;  // of O, the part's share of the dims
+        float *stats = reinterpret_cast<float *>(smem + kStats) + row;  // [part][row]
         int n = 0, job = 0, buf = 0, phase = 0;
         while (w.next()) {
             const Request &r = w.r;
@@ -360,46 +364,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane + 32 < r.rows) up[1] = a.parents[r.first + lane + 32];
             }
             bool found = !drafted;
-            const auto page_id = [&](int t) {  // of the half's four pages, the lane's; a tile ahead of its use
-                const int page = 8 * t + 4 * h + (lane & 3);
+            const auto find = [&] {
+                uint64_t all[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (up[x] < -1 || up[x] >= lane + 32 * x) atomicOr(&g_status, QA_DEVICE_BAD_TREE), up[x] = -1;
+                ancestors(a, up, all);
+                const int node = row / a.group;
+                const uint64_t s0 = __shfl_sync(kAll, all[0], node & 31), s1 = __shfl_sync(kAll, all[1], node & 31);
+                seen = node >= r.rows ? 0 : node < 32 ? s0 : s1;
+                found = true;
+            };
+            constexpr int kPages = kKeys / kPage;
+            const auto page_id = [&](int t) {  // of the part's pages, the lane's; a tile ahead of its use
+                const int page = 8 * t + kPages * h + lane % kPages;
                 return t < w.t1 && page < pages ? table[page] : 0;
             };
             float m = -INFINITY, l = 0.f;
             bool odd = false;
             int id = page_id(w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const uint32_t ok = __ballot_sync(kAll, id >= 0 && id < a.num_pages) & 15u;  // the pages that can be read
-                const uint32_t s = tmem + buf * kTile + h * 64 + lanes;
+                const uint32_t ok = __ballot_sync(kAll, id >= 0 && id < a.num_pages) & ((1u << kPages) - 1);  // pages that can be read
+                const uint32_t s = tmem + buf * kTile + h * kKeys + lanes;
                 id = page_id(t + 1);
                 wait(bar(kSFull + buf), phase);
                 __syncwarp();
                 tc::fence_after();
-                uint32_t sc[2][32];
-                tc::tmem_ld32_issue(s, sc[0]);
-                tc::tmem_ld32_issue(s + 32, sc[1]);
-                tc::tmem_ld32_wait(sc[0]);
-                tc::tmem_ld32_wait(sc[1]);
-                const int key0 = t * kTile + h * 64, behind = r.past - key0;  // keys of this half that every row sees
-                const bool masked = behind < 64 || ok != 15u;
-                if (masked) {
-                    if (!found) {
-                        uint64_t all[2];
+                uint32_t sc[kKeys / 32][32];
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            if (up[x] < -1 || up[x] >= lane + 32 * x) atomicOr(&g_status, QA_DEVICE_BAD_TREE), up[x] = -1;
-                        ancestors(a, up, all);
-                        const int node = row / a.group;
-                        const uint64_t s0 = __shfl_sync(kAll, all[0], node & 31), s1 = __shfl_sync(kAll, all[1], node & 31);
-                        seen = node >= r.rows ? 0 : node < 32 ? s0 : s1;
-                        found = true;
-                    }
+                for (int c = 0; c < kKeys / 32; ++c) tc::tmem_ld32_issue(s + 32 * c, sc[c]);
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c) tc::tmem_ld32_wait(sc[c]);
+                const int key0 = t * kTile + h * kKeys, behind = r.past - key0;  // keys of this part that every row sees
+                const bool masked = behind < kKeys || ok != (1u << kPages) - 1;
+                if (masked) {
+                    if (!found) find();
                     uint64_t vis = behind >= 64 ? ~0ull : behind > 0 ? ~(~0ull << behind) : 0ull;
                     if (behind < 64 && behind > -64) vis |= behind >= 0 ? seen << behind : seen >> -behind;
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
+                    for (int p = 0; p < kPages; ++p)
                         if (!(ok >> p & 1)) vis &= ~(0xffffull << 16 * p);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < kKeys / 32; ++c) {
                         const uint32_t v = (uint32_t)(vis >> 32 * c);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) sc[c][j] = v >> j & 1 ? sc[c][j] : __float_as_uint(-INFINITY);
@@ -407,26 +413,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < kKeys / 32; ++c)
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)
                         mx4[(j >> 1) & 3] = fmax3(mx4[(j >> 1) & 3], __uint_as_float(sc[c][j]), __uint_as_float(sc[c][j + 1]));
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-                // one reference a row, for both halves: where a row's moves, its halves agree on the larger maximum
+                // one reference a row, for all parts: where a row's moves, they agree on the largest maximum
                 float alpha = 1.f;
                 if (any_of_rows(mx > m + kSlack)) {
-                    maxima[h * 128 + row] = mx;
-                    named_barrier(1, 256);
-                    const float top = fmaxf(mx, maxima[(h ^ 1) * 128 + row]), next = top > m + kSlack ? top : m;
+                    stats[h * 128] = mx;
+                    named_barrier(1, kRows);
+                    float top = stats[0];
+#pragma unroll
+                    for (int x = 1; x < kParts; ++x) top = fmaxf(top, stats[x * 128]);
+                    const float next = top > m + kSlack ? top : m;
                     alpha = next == m ? 1.f : exp2_approx(m - next);
                     m = next;
                     if (t > w.t0 && __any_sync(kAll, alpha != 1.f)) {
-                        // P V of the tile before has written O, of which each half scales 64 dims
+                        // P V of the tile before has written O, of which each part scales its share of the dims
                         wait(bar(kDone + (buf == 0 ? kBufs - 1 : buf - 1)), buf == 0 ? phase ^ 1 : phase);
                         __syncwarp();
                         tc::fence_after();
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
+                        for (int c = 0; c < kKeys / 32; ++c) {
                             float o[32];
                             tc::tmem_ld32(t_o + c * 32, o);
 #pragma unroll
@@ -439,36 +448,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
                 float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t ph[16], pl[16];
+                for (int c = 0; c < kKeys / 16; ++c) {
+                    uint32_t ph[8], pl[8];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 x = ffma2(make_float2(__uint_as_float(sc[c][j]), __uint_as_float(sc[c][j + 1])), scale2, ref2);
+                    for (int jj = 0; jj < 16; jj += 2) {
+                        const int j = (c & 1) * 16 + jj;
+                        const float2 x = ffma2(make_float2(__uint_as_float(sc[c / 2][j]), __uint_as_float(sc[c / 2][j + 1])), scale2, ref2);
                         const float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                         sum[(j >> 1) & 3] = fadd2(sum[(j >> 1) & 3], p);
                         const uint32_t b0 = __float_as_uint(p.x), b1 = __float_as_uint(p.y);
-                        ph[j >> 1] = __byte_perm(b0, b1, 0x7632);
+                        ph[jj >> 1] = __byte_perm(b0, b1, 0x7632);
                         const float2 rest = fsub2(p, make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)));
-                        pl[j >> 1] = pack_bf16x2(rest.x, rest.y);
+                        pl[jj >> 1] = pack_bf16x2(rest.x, rest.y);
                     }
-                    tc::tmem_st16(s + c * 32, ph);
-                    tc::tmem_st16(s + c * 32 + 16, pl);
+                    tc::tmem_st8(s + (c >> 1) * 32 + (c & 1) * 8, ph);
+                    tc::tmem_st8(s + (c >> 1) * 32 + 16 + (c & 1) * 8, pl);
                 }
                 const float2 both = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
                 l = l * alpha + (both.x + both.y);
                 if (masked) {
                     // Slots that hold no key (or were not loaded) are zeroed, and of drafted values what is not finite, so
                     // that a probability of 0 meets nothing that it would not cancel; rows that see such a value get it at
-                    // the end.  Two threads a key.
+                    // the end.
                     const int piece = v_piece(n, hi - lo), v_slot = piece % kSlots;
                     wait(bar(kFull + v_slot), piece / kSlots & 1);
-                    const int key = row >> 1, pos = key0 + key;
-                    uint8_t *v = smem + kRing + v_slot * kQBytes + (8 * h + (key >> 3)) * kGroup + (row & 1) * kAtom + (key & 7) * 128;
+                    constexpr int kEach = 128 / kKeys, kChunks = 16 / kEach;  // threads of a key, 16-byte pieces of a thread
+                    const int key = row / kEach, piece0 = row % kEach * kChunks, pos = key0 + key;
+                    uint8_t *v = smem + kRing + v_slot * kQBytes + (kKeys / 8 * h + (key >> 3)) * kGroup + (piece0 >> 3) * kAtom + (key & 7) * 128;
                     const bool live = pos < r.keys && (ok >> (key >> 4) & 1);
                     if (!live || pos >= r.past) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {  // a key's lanes begin at chunks of their own: no bank twice
-                            uint4 *at = reinterpret_cast<uint4 *>(v) + ((c + key) & 7);
+                        for (int c = 0; c < kChunks; ++c) {  // keys begin at pieces of their own: fewer bank conflicts
+                            uint4 *at = reinterpret_cast<uint4 *>(v) + (piece0 & 7) + (c + key) % kChunks;
                             uint4 z = make_uint4(0u, 0u, 0u, 0u);
                             if (live) {
                                 const uint4 x = *at;
@@ -488,14 +499,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(bar(kPFull + buf));
                 if (++buf == kBufs) buf = 0, phase ^= 1;
             }
-            sums[h * 128 + row] = l;
-            const bool any_odd = any_of_rows(odd);  // both halves' sums are there too
-            const float sum = l + sums[(h ^ 1) * 128 + row];
+            named_barrier(1, kRows);  // maxima that were exchanged have been read
+            stats[h * 128] = l;
+            const bool any_odd = any_of_rows(odd);  // all parts' sums are there too
+            if (any_odd && !found) find();  // the part's own keys were all behind
+            float sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) sum += stats[x * 128];
             wait(bar(kOFull), job & 1);
             ++job;
             __syncwarp();
             tc::fence_after();
-            // each half's warps give 64 of the dims
+            // each part's warps give their share of the dims
             const bool whole = w.t0 == 0 && w.t1 == w.tiles;
             const int left = (r.rows - w.block * rows_a_block) * a.group;  // rows from this block's first on
             const int slot = 2 * worker + (w.at > lo);
@@ -504,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint16_t *dst = a.out + ((size_t)(r.first + w.block * rows_a_block + row / a.group) * a.hq + head * a.group + row % a.group) * 128;
             const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int dim = h * 64 + c * 32;
+            for (int c = 0; c < kKeys / 32; ++c) {
+                const int dim = h * kKeys + c * 32;
                 float o[32];
                 tc::tmem_ld32(t_o + c * 32, o);
 #pragma unroll
@@ -547,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssueS) {
         tc::fence_after();
         tc::tmem_dealloc(tmem, 512);
     }

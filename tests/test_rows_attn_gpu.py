@@ -172,9 +172,10 @@ def test_scale():
 
 
 @pytest.mark.parametrize("hq, rows", [(16, [8, 3]), (8, [16, 3]), (16, [16, 9]), (16, [64, 30]), (8, [64, 30])])
-def test_hidden_rows_may_hold_anything(hq, rows):
+@pytest.mark.parametrize("past", [50, 0, 125, 300])
+def test_hidden_rows_may_hold_anything(hq, rows, past):
     """NaN and infinities in a drafted row's key or value reach that row and those behind it in the tree, no other."""
-    c = Case(17, rows, [50, 0], hq, 8, "tree")
+    c = Case(17, rows, [past, 0], hq, 8, "tree")
     c.parents[:rows[0]] = [-1, 0, 0, 1] + [2] * (rows[0] - 4)
     clean, bound = c.reference()
     at = c.past[0] + 1  # row 1: its row and row 3's see it
@@ -182,7 +183,7 @@ def test_hidden_rows_may_hold_anything(hq, rows):
     behind = [1, 3]
     others = [i for i in range(sum(rows)) if i not in behind]
     for what in ("value inf", "value nan", "key nan", "key inf", "value -inf in one dim"):
-        d = Case(17, rows, [50, 0], hq, 8, "tree")
+        d = Case(17, rows, [past, 0], hq, 8, "tree")
         d.parents = c.parents
         if what == "value inf":
             d.v[page, slot] = INF
