@@ -456,12 +456,13 @@ QA_API qa_status qa_layer_norm(const void *x, int t, int d, const void *gain, co
 QA_API int qa_device_status(void *stream) {
     clear_error();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e[10];
+    cudaError_t e[11];
     const unsigned int bits = qa::status_read_clear_decode(s, &e[0]) | qa::status_read_clear_prefill(s, &e[1]) |
                               qa::status_read_clear_window(s, &e[2]) | qa::status_read_clear_append(s, &e[3]) |
                               qa::status_read_clear_gemm(s, &e[4]) | qa::status_read_clear_rope(s, &e[5]) |
                               qa::status_read_clear_kvq_pages(s, &e[6]) | qa::status_read_clear_kvq_decode(s, &e[7]) |
-                              qa::status_read_clear_rows_attn(s, &e[8]) | qa::status_read_clear_tree_accept(s, &e[9]);
+                              qa::status_read_clear_rows_attn(s, &e[8]) | qa::status_read_clear_tree_accept(s, &e[9]) |
+                              qa::status_read_clear_append_rows(s, &e[10]);
     for (cudaError_t ei : e)
         if (ei != cudaSuccess) {
             fail(QA_STATUS_LAUNCH_FAILED, "qa_device_status: CUDA error %s", cudaGetErrorString(ei));

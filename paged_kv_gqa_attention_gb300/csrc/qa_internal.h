@@ -83,17 +83,6 @@ cudaError_t launch_encoder_layer(const void *x, const int32_t *cu_windows, int n
 cudaError_t launch_rope_rows(const void *q, long long ldq, const void *k, long long ldk, int rows, void *q_out,
                              long long ldq_out, void *k_out, long long ldk_out, const qa_rope &rope,
                              const qa_attn_params &p, cudaStream_t stream);
-// rows normed, rotated and written to their pages; rope NULL: written as they are
-struct AppendRows {
-    const void *q, *k, *v;
-    long long ldq, ldk, ldv;
-    const int32_t *cu_seqlens, *n_past, *parents, *page_table;
-    int batch, rows;
-    void *k_pages, *v_pages, *q_out;
-    long long ldq_out;
-    const qa_rope *rope;
-};
-cudaError_t launch_append_rows(const AppendRows &x, const qa_attn_params &p, cudaStream_t stream);
 // theta^(-2i/D) / 2 pi of the D/2 pairs (turns a position), computed in fp64, as fp32 hi + lo parts
 void rope_frequencies(float theta, int head_dim, float *hi, float *lo);
 unsigned int status_read_clear_rope(cudaStream_t stream, cudaError_t *err);
@@ -118,6 +107,20 @@ cudaError_t launch_kvq_decode(const void *q, long long ldq, void *k_pages, void 
                               const int32_t *seq_lens, int batch, void *out, const qa_attn_params &p, float scale,
                               int ctas, cudaStream_t stream, const KvqAppend *app);
 unsigned int status_read_clear_kvq_decode(cudaStream_t stream, cudaError_t *err);
+
+// ---- rows normed, rotated and written to their pages (append_rows.cu); rope
+// NULL: written as they are
+struct AppendRows {
+    const void *q, *k, *v;
+    long long ldq, ldk, ldv;
+    const int32_t *cu_seqlens, *n_past, *parents, *page_table;
+    int batch, rows;
+    void *k_pages, *v_pages, *q_out;
+    long long ldq_out;
+    const qa_rope *rope;
+};
+cudaError_t launch_append_rows(const AppendRows &x, const qa_attn_params &p, cudaStream_t stream);
+unsigned int status_read_clear_append_rows(cudaStream_t stream, cudaError_t *err);
 
 // ---- packed rows over paged states (rows_attn.cu): a tree of drafted rows
 // behind n_past positions, or (tree false) every row over `past` states

@@ -1,6 +1,5 @@
 // Per-head QK-norm and rotary positions with up to four axes over packed
-// query and key rows (qa_rope_rows), and the same with the keys, and the
-// values beside them, written to their pages (qa_append_rows).
+// query and key rows (qa_rope_rows).
 //
 //   y = x / sqrt(mean x^2 + eps) * gain;  a_i = positions[axis(i)][t] theta^(-2i/D)
 //   z_i = y_i cos a_i - y_{i+D/2} sin a_i,  z_{i+D/2} = y_i sin a_i + y_{i+D/2} cos a_i
@@ -63,92 +62,8 @@ struct RopeArgs {
     float freq_hi[kMaxHalf], freq_lo[kMaxHalf];
 };
 
-// Of the rows that go to pages; heads counts the values' too, behind the keys'.
-struct AppendArgs : RopeArgs {
-    const uint16_t *v;
-    long long ldv;
-    uint16_t *k_pages, *v_pages;
-    const int32_t *cu, *past, *parents, *page_table;
-    int batch, hkv, max_pages, num_pages;
-    int turned;  // the heads before this one are rotated: hq + hkv, or none
-};
-
-// Where a row goes, and what it is turned by.
-struct Place {
-    int pos;       // lane x: the position on axis x
-    long long at;  // the row's number in the pools, -1: no place in them
-    bool live;     // the row belongs to a request
-};
-
-// A warp's search for row t's request: the last one that begins at or before
-// it (32 boundaries a round), then its place and, without explicit positions,
-// its depth in the tree.  The parents of the 64 rows up to t come with two
-// loads a lane; a walk that leaves these goes on in memory.
-__device__ __forceinline__ Place place_of(const AppendArgs &a, long long t) {
-    constexpr unsigned kAll = 0xffffffffu;
-    const int lane = threadIdx.x & 31;
-    Place p = {0, -1, false};
-    if (t >= a.rows) return p;
-    const int row = (int)t;
-    if (a.positions && lane < a.n_axes) p.pos = a.positions[(size_t)lane * a.rows + row];
-    int r = 0;
-    for (int n = a.batch;;) {
-        const int step = (n + 31) / 32, i = lane * step;
-        const unsigned before = __ballot_sync(kAll, i < n && a.cu[r + i] <= row);
-        if (before == 0) return p;
-        const int k = 31 - __clz(before);
-        r += k * step;
-        n = min(step, n - k * step);
-        if (step == 1) break;
-    }
-    const int first = a.cu[r], end = a.cu[r + 1];
-    if (first < 0 || end > a.rows || row >= end) return p;
-    const int i = row - first;
-    const long long past = a.past ? a.past[r] : 0, cap = (long long)a.max_pages * 16;
-    if (past < 0 || past > cap) {
-        if (lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_LENGTH);
-        return p;
-    }
-    p.live = true;
-    const long long at = past + i;
-    if (at < cap) {
-        const int page = a.page_table[(size_t)r * a.max_pages + (int)(at >> 4)];
-        if (page >= 0 && page < a.num_pages) p.at = (long long)page * 16 + (at & 15);
-        else if (lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
-    } else if (lane == 0) {
-        atomicOr(&g_status, QA_DEVICE_BAD_LENGTH);
-    }
-    if (!a.positions && a.turned) {
-        int depth = i;
-        if (a.parents) {
-            const int base = max(0, i - 63);
-            auto parent = [&](int node) {
-                const int up = a.parents[first + node];
-                if (up >= -1 && up < node) return up;
-                atomicOr(&g_status, QA_DEVICE_BAD_TREE);
-                return -1;
-            };
-            const int low = base + lane <= i ? parent(base + lane) : -1;
-            const int high = base + 32 + lane <= i ? parent(base + 32 + lane) : -1;
-            depth = -1;
-            for (int node = i; node >= 0; ++depth) {
-                if (node >= base) {
-                    const int x = __shfl_sync(kAll, low, (node - base) & 31), y = __shfl_sync(kAll, high, (node - base) & 31);
-                    node = node - base < 32 ? x : y;
-                } else {
-                    node = parent(node);
-                }
-            }
-        }
-        const long long pos = past + depth;
-        p.pos = lane == 0 ? (pos < kMaxPos ? (int)pos : kMaxPos) : 0;
-    }
-    return p;
-}
-
-template <int D, int PASSES, bool NORM, bool PAGED>
-__global__ void __launch_bounds__(kThreads)
-    rope_rows_kernel(const __grid_constant__ std::conditional_t<PAGED, AppendArgs, RopeArgs> a) {
+template <int D, int PASSES, bool NORM>
+__global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int HALF = D / 2;
     constexpr int LANES = D / 16;        // lanes of a head
     constexpr int HEADS = 32 / LANES;    // of a pass
@@ -173,8 +88,6 @@ __global__ void __launch_bounds__(kThreads)
     }
     // where the lane's head of pass p lies in a row: its first pass's place as a query or as a key, p HEADS D further
     const int at_q = h0 * D + 8 * l, at_k = (h0 - a.hq) * D + 8 * l;
-    [[maybe_unused]] int first_v, at_v;  // the first head of the values, and where the lane's lies
-    if constexpr (PAGED) first_v = a.hq + a.hkv, at_v = at_k - a.hkv * D;
     auto fetch = [&](long long row, int stage) {  // a row's copies, or nothing past the last: a group either way
         if (row < a.rows) {
             const uint16_t *q = a.q + row * a.ldq + at_q, *k = a.k + row * a.ldk + at_k;
@@ -183,8 +96,6 @@ __global__ void __launch_bounds__(kThreads)
                 const int h = h0 + p * HEADS;
                 if (h < a.heads) {
                     const uint16_t *src = (h < a.hq ? q : k) + p * (HEADS * D);
-                    if constexpr (PAGED)
-                        if (h >= first_v) src = a.v + row * a.ldv + at_v + p * (HEADS * D);
                     copy16(ring + stage * STAGE + p * 1024, src);
                     copy16(ring + stage * STAGE + p * 1024 + 512, src + HALF);
                 }
@@ -192,38 +103,24 @@ __global__ void __launch_bounds__(kThreads)
         }
         copy_commit();
     };
-    auto place = [&](long long row) -> Place {
-        if constexpr (PAGED) return place_of(a, row);
-        else return {row < a.rows && lane < a.n_axes ? a.positions[(size_t)lane * a.rows + row] : 0, -1, true};
+    auto position = [&](long long row) -> int {  // lane x: the row's position on axis x
+        return row < a.rows && lane < a.n_axes ? a.positions[(size_t)lane * a.rows + row] : 0;
     };
     const auto wait = [] {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     };
     if (!a.early) wait();
-    Place next;
-    if constexpr (PAGED) {  // the rows' own copies are on their way while their places are found
-        if (a.early) next = place(t), wait();
-        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
-            bool wrong = false;
-            for (int r = lane; r < a.batch; r += 32) wrong |= a.cu[r] < 0 || a.cu[r] > a.cu[r + 1] || a.cu[r + 1] > a.rows;
-            if (__any_sync(0xffffffffu, wrong) && lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_SEGMENTS);
-        }
-    } else {
-        next = place(t);
-        if (a.early) wait();
-    }
+    int pos_next = position(t);
+    if (a.early) wait();
 #pragma unroll
     for (int n = 0; n < kStages; ++n) fetch(t + (long long)n * stride, n);
-    if (PAGED && !a.early) next = place(t);
     int stage = 0;
     for (; t < a.rows; t += stride) {
-        const Place here = next;
-        const int pos = here.pos;
-        next = place((long long)t + stride);
-        bool bad = __any_sync(0xffffffffu, pos < 0 || pos >= kMaxPos);
-        if (bad && here.live && lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_POSITION);
-        bad |= !here.live;
+        const int pos = pos_next;
+        pos_next = position((long long)t + stride);
+        const bool bad = __any_sync(0xffffffffu, pos < 0 || pos >= kMaxPos);
+        if (bad && lane == 0) atomicOr(&g_status, QA_DEVICE_BAD_POSITION);
         float c_own[OWN], s_own[OWN];
         float2 c[4], s[4];
 #pragma unroll
@@ -248,14 +145,7 @@ __global__ void __launch_bounds__(kThreads)
             }
         };
         factors(h0 < a.hq);
-        uint16_t *q_out = a.q_out + (long long)t * a.ldq_out + at_q, *k_out;
-        [[maybe_unused]] uint16_t *v_out;
-        if constexpr (PAGED) {
-            const long long width = (long long)a.hkv * D;
-            k_out = a.k_pages + here.at * width + at_k, v_out = a.v_pages + here.at * width + at_v;
-        } else {
-            k_out = a.k_out + (long long)t * a.ldk_out + at_k;
-        }
+        uint16_t *q_out = a.q_out + (long long)t * a.ldq_out + at_q, *k_out = a.k_out + (long long)t * a.ldk_out + at_k;
         copy_wait<kStages - 1>();
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
@@ -291,15 +181,9 @@ __global__ void __launch_bounds__(kThreads)
                 if (NORM) lo = fmul2(lo, rr), hi = fmul2(hi, rr);
                 z[i] = pack_bf16x2(lo.x, lo.y);
                 u[i] = pack_bf16x2(hi.x, hi.y);
-                if constexpr (PAGED)
-                    if (h >= a.turned) z[i] = wx[i], u[i] = wy[i];
             }
-            bool out = h < a.heads && !bad;
-            if constexpr (PAGED) out &= h < a.hq || here.at >= 0;
-            if (out) {
+            if (h < a.heads && !bad) {
                 uint16_t *dst = (h < a.hq ? q_out : k_out) + p * (HEADS * D);
-                if constexpr (PAGED)
-                    if (h >= first_v) dst = v_out + p * (HEADS * D);
                 *reinterpret_cast<uint4 *>(dst) = make_uint4(z[0], z[1], z[2], z[3]);
                 *reinterpret_cast<uint4 *>(dst + HALF) = make_uint4(u[0], u[1], u[2], u[3]);
             }
@@ -330,37 +214,6 @@ void rope_frequencies(float theta, int head_dim, float *hi, float *lo) {
     memcpy(lo, t_lo, half * sizeof(float));
 }
 
-namespace {
-
-// The grid of `rows` rows of `heads` head vectors, and its launch.
-template <typename Launch>
-cudaError_t launch_items(int rows, int heads, int head_dim, cudaStream_t stream, Launch launch) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int device = 0, sms = 0;
-    if (cudaGetDevice(&device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
-        return cudaErrorInvalidDevice;
-    const auto pick = [&](auto n) {
-        constexpr int N = decltype(n)::value;
-        const int heads_an_item = 512 / head_dim * N, chunks = (heads + heads_an_item - 1) / heads_an_item;
-        const int ctas = (rows + kThreads / 32 - 1) / (kThreads / 32), most = (sms * kCtasPerSm + chunks - 1) / chunks;
-        cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most), (unsigned)chunks);
-        cfg.dynamicSmemBytes = (kThreads / 32) * kStages * N * 1024;
-        return launch(n, cfg);
-    };
-    if ((long long)rows * heads <= kFewHeads) return pick(std::integral_constant<int, 1>());
-    return pick(std::integral_constant<int, 2>());
-}
-
-}  // namespace
-
 cudaError_t launch_rope_rows(const void *q, long long ldq, const void *k, long long ldk, int rows, void *q_out,
                              long long ldq_out, void *k_out, long long ldk_out, const qa_rope &rope,
                              const qa_attn_params &p, cudaStream_t stream) {
@@ -386,56 +239,30 @@ cudaError_t launch_rope_rows(const void *q, long long ldq, const void *k, long l
     if (rope.pair_axis) memcpy(a.pair_axis, rope.pair_axis, p.head_dim / 2);
     rope_frequencies(rope.theta, p.head_dim, a.freq_hi, a.freq_lo);
 
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     const bool wide = p.head_dim == 128, norm = rope.q_gain != nullptr;
-    return launch_items(rows, a.heads, p.head_dim, stream, [&](auto n, const cudaLaunchConfig_t &cfg) {
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
+        return cudaErrorInvalidDevice;
+    const auto pick = [&](auto n) {
         constexpr int N = decltype(n)::value;
-        return norm ? cudaLaunchKernelEx(&cfg, wide ? rope_rows_kernel<128, N, true, false> : rope_rows_kernel<64, N, true, false>, a)
-                    : cudaLaunchKernelEx(&cfg, wide ? rope_rows_kernel<128, N, false, false> : rope_rows_kernel<64, N, false, false>, a);
-    });
-}
-
-cudaError_t launch_append_rows(const AppendRows &x, const qa_attn_params &p, cudaStream_t stream) {
-    AppendArgs a = {};
-    const long long wq = (long long)p.n_q_heads * 128, wk = (long long)p.n_kv_heads * 128;
-    a.q = static_cast<const uint16_t *>(x.q);
-    a.k = static_cast<const uint16_t *>(x.k);
-    a.v = static_cast<const uint16_t *>(x.v);
-    a.q_out = static_cast<uint16_t *>(x.q_out);
-    a.k_pages = static_cast<uint16_t *>(x.k_pages);
-    a.v_pages = static_cast<uint16_t *>(x.v_pages);
-    a.ldq = x.ldq ? x.ldq : wq;
-    a.ldk = x.ldk ? x.ldk : wk;
-    a.ldv = x.ldv ? x.ldv : wk;
-    a.ldq_out = x.ldq_out ? x.ldq_out : wq;
-    a.cu = x.cu_seqlens;
-    a.past = x.n_past;
-    a.parents = x.parents;
-    a.page_table = x.page_table;
-    a.rows = x.rows;
-    a.batch = x.batch;
-    a.hq = x.q ? p.n_q_heads : 0;
-    a.hkv = p.n_kv_heads;
-    a.heads = a.hq + 2 * a.hkv;
-    a.turned = x.rope ? a.hq + a.hkv : 0;
-    a.max_pages = p.max_pages_per_seq;
-    a.num_pages = p.num_pages;
-    a.early = (p.abi_version >= 2 && p.stable_metadata >= 1) ? 1 : 0;
-    a.n_axes = 1;
-    bool norm = false;
-    if (x.rope) {
-        a.q_gain = x.rope->q_gain;
-        a.k_gain = x.rope->k_gain;
-        a.positions = x.rope->positions;
-        a.n_axes = x.rope->n_axes;
-        a.eps = x.rope->rms_eps;
-        norm = a.q_gain != nullptr;
-        if (x.rope->pair_axis) memcpy(a.pair_axis, x.rope->pair_axis, 64);
-        rope_frequencies(x.rope->theta, 128, a.freq_hi, a.freq_lo);
-    }
-    return launch_items(x.rows, a.heads, 128, stream, [&](auto n, const cudaLaunchConfig_t &cfg) {
-        constexpr int N = decltype(n)::value;
-        return cudaLaunchKernelEx(&cfg, norm ? rope_rows_kernel<128, N, true, true> : rope_rows_kernel<128, N, false, true>, a);
-    });
+        const int heads_an_item = 512 / p.head_dim * N, chunks = (a.heads + heads_an_item - 1) / heads_an_item;
+        const int ctas = (rows + kThreads / 32 - 1) / (kThreads / 32), most = (sms * kCtasPerSm + chunks - 1) / chunks;
+        cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most), (unsigned)chunks);
+        cfg.dynamicSmemBytes = (kThreads / 32) * kStages * N * 1024;
+        return norm ? cudaLaunchKernelEx(&cfg, wide ? rope_rows_kernel<128, N, true> : rope_rows_kernel<64, N, true>, a)
+                    : cudaLaunchKernelEx(&cfg, wide ? rope_rows_kernel<128, N, false> : rope_rows_kernel<64, N, false>, a);
+    };
+    if ((long long)rows * a.heads <= kFewHeads) return pick(std::integral_constant<int, 1>());
+    return pick(std::integral_constant<int, 2>());
 }
 
 unsigned int status_read_clear_rope(cudaStream_t stream, cudaError_t *err) {

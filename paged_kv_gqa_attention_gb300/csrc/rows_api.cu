@@ -93,7 +93,7 @@ QA_API qa_status qa_append_rows(const void *q, long long ldq, const void *k, lon
     st = launched(qa::launch_append_rows(x, *p, stream), fn);
     if (st != QA_STATUS_OK || !p->debug_checks) return st;
     cudaError_t e;
-    const unsigned int bits = qa::status_read_clear_rope(stream, &e);
+    const unsigned int bits = qa::status_read_clear_append_rows(stream, &e);
     return qa::report_device_status(bits, e, fn);
 }
 
