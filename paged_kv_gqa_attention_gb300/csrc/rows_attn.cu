@@ -43,7 +43,7 @@ constexpr int kPage = 16;
 constexpr int kMaxStages = 8;
 constexpr float kSlack = 8.f;
 constexpr int kMergeThreads = 256;
-constexpr int kMaxWorkers = 1024;
+constexpr int kFewEach = 5, kMaxWorkers = 32 * 20;  // workers of a lane of the merge, and all
 
 // Bytes of a stage: K and V of one page, each two halves of 64 dims.
 __host__ __device__ constexpr uint32_t half_bytes(int hkv) { return (uint32_t)hkv * kPage * 128; }
@@ -121,6 +121,10 @@ __global__ void __launch_bounds__(288, 1)
     int *page_ok = reinterpret_cast<int *>(smem_raw + (empty + 8 * kMaxStages - raw));
     int *prefix = page_ok + kMaxStages;
     const int worker = blockIdx.x;
+    if (warp == hkv && lane == 0) {
+        tc::prefetch_tmap(&tk);
+        tc::prefetch_tmap(&tv);
+    }
     if (!a.early) grid_wait();
     if (warp == 0) {
         count_pages(a, prefix, worker == 0 ? &g_status : nullptr);
@@ -158,8 +162,6 @@ __global__ void __launch_bounds__(288, 1)
                 s.rows = r.rows * a.group;
             }
             a.splits[worker] = s;
-            tc::prefetch_tmap(&tk);
-            tc::prefetch_tmap(&tv);
         }
         int stage = 0, phase = 0;
         for (int b = b0; b <= b_last; ++b) {
@@ -459,17 +461,18 @@ __device__ __forceinline__ void merge_by_cta(const RowsArgs &a, const Split &s, 
 }
 
 // The merge behind few_rows_kernel, with many workers and few rows a split:
-// every CTA sums up the steps that all splits take and takes its share.
+// every warp sums up the steps that all splits take, EACH workers a lane, and
+// the CTAs take them in turn.
+template <int EACH>
 __global__ void __launch_bounds__(kMergeThreads) merge_few_kernel(const __grid_constant__ RowsArgs a) {
     constexpr unsigned kAll = 0xffffffffu;
-    constexpr int kWarps = kMergeThreads / 32, kEach = kMaxWorkers / kMergeThreads;
-    __shared__ int start[kMaxWorkers + 1], sums[kWarps];
+    constexpr int kWarps = kMergeThreads / 32;
     grid_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int steps[kEach], mine = 0;
+    int steps[EACH], mine = 0;
 #pragma unroll
-    for (int x = 0; x < kEach; ++x) {
-        const int w = threadIdx.x * kEach + x;
+    for (int x = 0; x < EACH; ++x) {
+        const int w = lane * EACH + x;
         steps[x] = 0;
         if (w < a.workers) {
             const Split s = a.splits[w];
@@ -484,29 +487,23 @@ __global__ void __launch_bounds__(kMergeThreads) merge_few_kernel(const __grid_c
         const int u = __shfl_up_sync(kAll, before, o);
         if (lane >= o) before += u;
     }
-    if (lane == 31) sums[warp] = before;
-    __syncthreads();
+    const int total = __shfl_sync(kAll, before, 31);
     before -= mine;
-    for (int x = 0; x < warp; ++x) before += sums[x];
-#pragma unroll
-    for (int x = 0; x < kEach; ++x) {
-        start[threadIdx.x * kEach + x] = before;
-        before += steps[x];
-    }
-    if (threadIdx.x == kMergeThreads - 1) start[kMaxWorkers] = before;
-    __syncthreads();
-    const int total = start[kMaxWorkers];
     for (int step = blockIdx.x; step < total; step += gridDim.x) {
-        int w = 0, r = kMaxWorkers - 1;
-        while (w < r) {  // the split that has this step
-            const int mid = (w + r) >> 1;
-            if (start[mid + 1] > step) r = mid; else w = mid + 1;
+        // the last lane that starts at or before the step, and which of its workers has it
+        const int l = 31 - __clz(__ballot_sync(kAll, before <= step));
+        int w = lane * EACH, begin = before, at = before;
+#pragma unroll
+        for (int x = 0; x < EACH; ++x) {
+            if (steps[x] > 0 && at <= step) w = lane * EACH + x, begin = at;
+            at += steps[x];
         }
+        w = __shfl_sync(kAll, w, l), begin = __shfl_sync(kAll, begin, l);
         const Split s = a.splits[w];
         if (s.count > kWarps) {
-            merge_by_cta(a, s, w, step - start[w]);
+            merge_by_cta(a, s, w, step - begin);
         } else {
-            const int item = (step - start[w]) * kWarps + warp;
+            const int item = (step - begin) * kWarps + warp;
             Merge g[1];
             merge_items<1, 4>(a, s, w, item, 0, 0, 1, g);
             store_item(a, s, item, g[0]);
@@ -687,7 +684,7 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
     cfg.dynamicSmemBytes = 0;
     if (plan.few) {
         cfg.gridDim = dim3((unsigned)(2 * sm_count()));
-        return cudaLaunchKernelEx(&cfg, merge_few_kernel, a);
+        return cudaLaunchKernelEx(&cfg, plan.workers <= 32 * kFewEach ? merge_few_kernel<kFewEach> : merge_few_kernel<kMaxWorkers / 32>, a);
     }
     cfg.gridDim = dim3((unsigned)(4 * a.hkv), (unsigned)plan.workers);  // up to 128 rows a head: two rounds of two a warp
     return cudaLaunchKernelEx(&cfg, merge_tiles_kernel, a);

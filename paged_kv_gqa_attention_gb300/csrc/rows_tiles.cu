@@ -58,14 +58,15 @@ constexpr uint32_t kRing = 2 * kQBytes;
 constexpr uint32_t kBar = kRing + kSlots * kQBytes;
 enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots,
                   kPFull = kSFull + kBufs, kDone = kPFull + kBufs, kOFull = kDone + kBufs, kBars };
-constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 16;
+constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 24;
 constexpr uint32_t kSmem = kStats + kParts * 128 * 4;  // kStats: [part][row]
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kColO = kBufs * kTile;  // TMEM: three buffers of S / P, then O
 
 // A call's tiles, and the request of the worker's first one, by one warp.
 struct Start {
-    int total, b, base;  // base: the tiles before request b
+    int total, b, base;   // base: the tiles before request b
+    int first, end, past; // request b's numbers
 };
 __device__ __forceinline__ int tiles_of(const RowsArgs &a, const Request &r, int rows_a_block) {
     return (r.keys + kTile - 1) / kTile * ((r.rows + rows_a_block - 1) / rows_a_block);
@@ -79,7 +80,7 @@ __device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, int r
         if (b < 32) first = v;
         sum += v;
     }
-    Start s = {__reduce_add_sync(kAll, sum), 0, 0};
+    Start s = {__reduce_add_sync(kAll, sum), 0, 0, 0, 0, 0};
     const int per = (s.total + a.workers - 1) / a.workers;
     const long long lo = (long long)worker * per;
     if (lo >= s.total) return s;
@@ -97,6 +98,7 @@ __device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, int r
             const int l = __ffs(past) - 1;
             s.b = begin + l;
             s.base = carry + __shfl_sync(kAll, up_to - v, l);
+            s.first = a.cu[s.b], s.end = a.cu[s.b + 1], s.past = a.past[s.b];
             return s;
         }
         carry += __shfl_sync(kAll, up_to, 31);
@@ -115,7 +117,7 @@ struct Walk {
     __device__ Walk(const RowsArgs &args, const Start &s, int lo, int end, int rab)
         : a(args), at(lo), hi(end), b(s.b), base(s.base), rows_a_block(rab), t0(0), t1(0) {
         if (lo >= end) return;
-        first_next = a.cu[b], end_next = a.cu[b + 1], past_next = a.past[b];
+        first_next = s.first, end_next = s.end, past_next = s.past;
         load();
     }
     __device__ bool next() {
@@ -211,6 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     };
+    if (warp == kProducer && lane == 0) {
+        tc::prefetch_tmap(&tq);
+        tc::prefetch_tmap(&tk);
+        tc::prefetch_tmap(&tv);
+    }
     if (!a.early) grid_wait();
     if (warp == 0) {
         const Start s = find_start(a, worker, rows_a_block, blockIdx.x == 0 ? &g_status : nullptr);
@@ -219,9 +226,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + kBufs ? kParts * 4 : 1);
         *wait.abort = 0;
         fence_mbar_init();
-        tc::prefetch_tmap(&tq);
-        tc::prefetch_tmap(&tk);
-        tc::prefetch_tmap(&tv);
     }
     // TMEM only once the kernel before has ended: one that starts its successors before it allocates could wait for
     // columns that this one holds while it waits for that kernel
