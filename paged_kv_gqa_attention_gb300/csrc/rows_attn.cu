@@ -42,7 +42,7 @@ __device__ unsigned int g_status;
 constexpr int kPage = 16;
 constexpr int kMaxStages = 8;
 constexpr float kSlack = 8.f;
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 256, kMergeCtas = 2;  // CTAs: an SM
 constexpr int kFewEach = 5, kMaxWorkers = 32 * 20;  // workers of a lane of the merge, and all
 
 // Bytes of a stage: K and V of one page, each two halves of 64 dims.
@@ -397,43 +397,33 @@ struct Merge {
     }
 };
 
-// Merges rows item0, item0 + step, .. (NI of them, a head's rows in turn) of
-// worker w's split over partials first, first + by, .., in this order, FLIGHT
-// of each row in flight.
-template <int NI, int FLIGHT>
-__device__ __forceinline__ void merge_items(const RowsArgs &a, const Split &s, int w, int item0, int step, int first, int by,
-                                            Merge (&g)[NI]) {
-    const int lane = threadIdx.x & 31, n = s.rows * a.hkv;
-    size_t at[NI];
+// Merges row `item` (a head's rows in turn) of worker w's split over the
+// partials first, first + by, .., in this order, four loads in flight.  Two
+// rows of three, or three CTAs an SM, were no faster: 32 requests of eight
+// drafted rows 40.1 and 38.2 us in all against 38.3.
+__device__ __forceinline__ Merge merge_item(const RowsArgs &a, const Split &s, int w, int item, int first, int by) {
+    constexpr int kFlight = 4;
+    const int lane = threadIdx.x & 31;
+    const size_t row = (size_t)(item / s.rows) * a.block_rows + item % s.rows;
+    Merge g;
+    for (int i = first; i < s.count; i += kFlight * by) {
+        float2 ml[kFlight];
+        float4 v[kFlight];
 #pragma unroll
-    for (int k = 0; k < NI; ++k) {
-        const int item = min(item0 + k * step, n - 1);
-        at[k] = (size_t)(item / s.rows) * a.block_rows + item % s.rows;
-    }
-    for (int i = first; i < s.count; i += FLIGHT * by) {
-        float2 ml[NI][FLIGHT];
-        float4 v[NI][FLIGHT];
-#pragma unroll
-        for (int x = 0; x < FLIGHT; ++x)
+        for (int x = 0; x < kFlight; ++x)
             if (i + x * by < s.count) {
-                const size_t slot = i + x * by == 0 ? s.first_slot : 2 * (w + i + x * by), base = slot * a.hkv * a.block_rows;
-#pragma unroll
-                for (int k = 0; k < NI; ++k) {
-                    ml[k][x] = __ldcg(reinterpret_cast<const float2 *>(a.ml) + base + at[k]);
-                    v[k][x] = __ldcg(reinterpret_cast<const float4 *>(a.acc) + (base + at[k]) * 32 + lane);
-                }
+                const size_t slot = i + x * by == 0 ? s.first_slot : 2 * (w + i + x * by), at = slot * a.hkv * a.block_rows + row;
+                ml[x] = __ldcg(reinterpret_cast<const float2 *>(a.ml) + at);
+                v[x] = __ldcg(reinterpret_cast<const float4 *>(a.acc) + at * 32 + lane);
             }
 #pragma unroll
-        for (int x = 0; x < FLIGHT; ++x)
-            if (i + x * by < s.count) {
-#pragma unroll
-                for (int k = 0; k < NI; ++k) g[k].add(ml[k][x], v[k][x]);
-            }
+        for (int x = 0; x < kFlight; ++x)
+            if (i + x * by < s.count) g.add(ml[x], v[x]);
     }
+    return g;
 }
 
 __device__ __forceinline__ void store_item(const RowsArgs &a, const Split &s, int item, const Merge &g) {
-    if (item >= s.rows * a.hkv) return;
     const int head = item / s.rows, row = item % s.rows;
     const float inv = g.sum > 0.f ? 1.f / g.sum : g.sum;
     uint16_t *dst = a.out + ((size_t)(s.out_row + row / a.group) * a.hq + head * a.group + row % a.group) * 128;
@@ -447,10 +437,9 @@ __device__ __forceinline__ void merge_by_cta(const RowsArgs &a, const Split &s, 
     __shared__ float4 s_acc[kWarps][32];
     __shared__ float2 s_ml[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Merge g[1];
-    merge_items<1, 4>(a, s, w, item, 0, warp, kWarps, g);
-    s_acc[warp][lane] = g[0].acc;
-    if (lane == 0) s_ml[warp] = make_float2(g[0].m, g[0].sum);
+    const Merge g = merge_item(a, s, w, item, warp, kWarps);
+    s_acc[warp][lane] = g.acc;
+    if (lane == 0) s_ml[warp] = make_float2(g.m, g.sum);
     __syncthreads();
     if (warp == 0) {
         Merge all;
@@ -460,11 +449,10 @@ __device__ __forceinline__ void merge_by_cta(const RowsArgs &a, const Split &s, 
     __syncthreads();
 }
 
-// The merge behind few_rows_kernel, with many workers and few rows a split:
-// every warp sums up the steps that all splits take, EACH workers a lane, and
-// the CTAs take them in turn.
+// The merge of both kernels' splits: every warp sums up the steps that all
+// splits take, EACH workers a lane, and the CTAs take them in turn.
 template <int EACH>
-__global__ void __launch_bounds__(kMergeThreads) merge_few_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kMergeThreads, kMergeCtas) merge_rows_kernel(const __grid_constant__ RowsArgs a) {
     constexpr unsigned kAll = 0xffffffffu;
     constexpr int kWarps = kMergeThreads / 32;
     grid_wait();
@@ -504,29 +492,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_few_kernel(const __grid_c
             merge_by_cta(a, s, w, step - begin);
         } else {
             const int item = (step - begin) * kWarps + warp;
-            Merge g[1];
-            merge_items<1, 4>(a, s, w, item, 0, 0, 1, g);
-            store_item(a, s, item, g[0]);
-        }
-    }
-}
-
-// The merge behind rows_tiles_kernel, with few workers and many rows a split:
-// a worker's CTAs take the rows of its split in turn, a warp two at a time.
-__global__ void __launch_bounds__(kMergeThreads) merge_tiles_kernel(const __grid_constant__ RowsArgs a) {
-    constexpr int kWarps = kMergeThreads / 32;
-    grid_wait();
-    const int w = blockIdx.y, n_warps = gridDim.x * kWarps;
-    const Split s = a.splits[w];
-    const int n = s.count ? s.rows * a.hkv : 0;
-    if (s.count > kWarps) {
-        for (int item = blockIdx.x; item < n; item += gridDim.x) merge_by_cta(a, s, w, item);
-    } else {
-        for (int item = blockIdx.x * kWarps + (threadIdx.x >> 5); item < n; item += 2 * n_warps) {
-            Merge g[2];
-            merge_items<2, 3>(a, s, w, item, n_warps, 0, 1, g);
-            store_item(a, s, item, g[0]);
-            store_item(a, s, item + n_warps, g[1]);
+            if (item < s.rows * a.hkv) store_item(a, s, item, merge_item(a, s, w, item, 0, 1));
         }
     }
 }
@@ -682,12 +648,8 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
     if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    if (plan.few) {
-        cfg.gridDim = dim3((unsigned)(2 * sm_count()));
-        return cudaLaunchKernelEx(&cfg, plan.workers <= 32 * kFewEach ? merge_few_kernel<kFewEach> : merge_few_kernel<kMaxWorkers / 32>, a);
-    }
-    cfg.gridDim = dim3((unsigned)(4 * a.hkv), (unsigned)plan.workers);  // up to 128 rows a head: two rounds of two a warp
-    return cudaLaunchKernelEx(&cfg, merge_tiles_kernel, a);
+    cfg.gridDim = dim3((unsigned)(kMergeCtas * sm_count()));
+    return cudaLaunchKernelEx(&cfg, plan.workers <= 32 * kFewEach ? merge_rows_kernel<kFewEach> : merge_rows_kernel<kMaxWorkers / 32>, a);
 }
 
 unsigned int status_read_clear_rows_attn(cudaStream_t stream, cudaError_t *err) {
