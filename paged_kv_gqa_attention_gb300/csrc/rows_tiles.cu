@@ -6,30 +6,41 @@
 // hkv CTAs a worker: the group's CTAs take the same key tiles of each KV head,
 // so that whole token rows are asked of HBM at about the same time.
 //
-//   warp 8     producer: Q once a job (two buffers), K and V of each tile,
+//   warp 16    producer: Q once a job (two buffers), K and V of each tile,
 //              page by page, into one ring of five slots in the order they
 //              are used.  A page's 16 tokens of a head are one box, of 8 keys
 //              by 64 dims four times: as two boxes of 16 keys by 64 dims the
 //              copies came at 25 bytes a clock (80 clocks a box), which was
 //              what bounded
-//   warp 9     issues S = Q K^T (M 128, N 128) into one of three buffers in
+//   warp 17    issues S = Q K^T (M 128, N 128) into one of three buffers in
 //              TMEM, up to two tiles ahead, into the next job too
-//   warp 10    issues O += P V (N 128), P from TMEM; a thread for both
+//   warp 18    issues O += P V (N 128), P from TMEM; a thread for both
 //              products would let the tensor core run dry at every barrier
 //              that it waits on
-//   warps 0-7  softmax: warps 0-3 have the first 64 keys of every tile, warps
-//              4-7 the others, a row a thread: 64 scores in registers, a lazy
-//              running max (log2 slack 8: O is rescaled only when it moves),
-//              P written over its scores as two bf16 terms of 16 columns each
-//              for every 32 keys.  A row's halves share its reference: a
-//              barrier a tile says whether any row's moves, and only then do
-//              they exchange maxima.  So one O serves both, which leaves TMEM
-//              for the third buffer of S
+//   warp 19    the scout: a job ahead, whether any of its pages is bad, and
+//              which drafted rows each row sees
+//   warps 0-15 softmax, a row a thread: a warpgroup has 32 of each tile's keys.
+//              32 scores in registers, a lazy running max (log2 slack 8: O is
+//              rescaled only when it moves), P written over its scores as two
+//              bf16 terms of 16 columns each.  A row's four parts share its
+//              reference: a barrier a tile says whether any row's moves, and
+//              only then do they exchange maxima.  So one O serves all, which
+//              leaves TMEM for the third buffer of S
 //
 // Two terms of P make P V two products: 16 bits of each probability, as in
-// the prefill kernels.  The tensor core needs 514 clocks for S and 1028 for
-// P V of a tile (measured: 64.2 an instruction; N = 64 would take 48), the
-// softmax of a half about 1050 with both at work.
+// the prefill kernels.
+//
+// What bounds: the tensor core needs 514 clocks for S and 1028 for P V of a
+// tile (measured: 64.2 an instruction; N = 64 would take 48), shared memory as
+// many (Q, K and twice V read, K and V written, at 128 bytes a clock); a tile
+// takes 1.2 us where its pages come from L2, about 2300 clocks, so that the
+// tensor core works two thirds of the time.  Four parts or two of 64 keys: 44.0
+// and 45.1 us for 64 requests of 16 to 64 rows over 500 to 2000 positions (16
+// heads on 8); that call's floor by its bytes is 21.8 us.  A job's switch costs
+// 2 to 4 us (its last tile waits for V, then O is given back), which is what
+// such a call of a few tiles a job pays; 8 requests of 100 to 448 rows over
+// 2000 to 15600 positions, 230 us, read K and V again for each 64 query rows,
+// 1.33 GB, 5.7 TB/s.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -47,8 +58,8 @@ constexpr int kTile = 128;
 constexpr int kParts = 4;               // of a tile's keys, each a warpgroup's
 constexpr int kKeys = kTile / kParts;   // of a thread
 constexpr int kRows = kParts * 128;     // threads that own rows
-constexpr int kProducer = kParts * 4, kIssueS = kProducer + 1, kIssueO = kIssueS + 1;  // warps
-constexpr int kThreads = (kIssueO + 1) * 32;
+constexpr int kProducer = kParts * 4, kIssueS = kProducer + 1, kIssueO = kIssueS + 1, kScout = kIssueO + 1;  // warps
+constexpr int kThreads = (kScout + 1) * 32;
 constexpr int kSlots = 5;
 constexpr int kBufs = 3;
 constexpr float kSlack = 8.f;
@@ -57,9 +68,15 @@ constexpr uint32_t kAtom = 1024, kGroup = 2 * kAtom;    // of K and V: 8 keys' f
 constexpr uint32_t kRing = 2 * kQBytes;
 constexpr uint32_t kBar = kRing + kSlots * kQBytes;
 enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots,
-                  kPFull = kSFull + kBufs, kDone = kPFull + kBufs, kOFull = kDone + kBufs, kBars };
+                  kPFull = kSFull + kBufs, kDone = kPFull + kBufs, kOFull = kDone + kBufs,
+                  kInfoFull, kInfoFree, kBars };
 constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 24;
-constexpr uint32_t kSmem = kStats + kParts * 128 * 4;  // kStats: [part][row]
+// What the scout finds of a job.
+struct Info {
+    uint64_t seen[64];  // the drafted rows that a row sees (bit j: row j)
+    int bad;            // a page of the job's tiles cannot be read
+};
+constexpr uint32_t kInfo = kStats + kParts * 128 * 4, kSmem = kInfo + sizeof(Info);  // kStats: [part][row]
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kColO = kBufs * kTile;  // TMEM: three buffers of S / P, then O
 
@@ -138,9 +155,10 @@ struct Walk {
     }
 };
 
-// The ring's pieces are K 0, K 1, V 0, K 2, V 1, ...: the place of V of tile n
-// of `tiles`, the last of which follows V of the one before.
-__device__ __forceinline__ int v_piece(int n, int tiles) { return n + 1 < tiles ? 2 * n + 2 : 2 * n + 1; }
+// The ring's pieces are, of each job, K 0, K 1, V 0, K 2, V 1, .., V of the
+// last tile: the places of a tile's among the job's.
+__device__ __forceinline__ int k_piece(int tile) { return tile == 0 ? 0 : 2 * tile - 1; }
+__device__ __forceinline__ int v_piece(int tile, int tiles) { return tile + 1 < tiles ? 2 * tile + 2 : 2 * tile + 1; }
 
 // Waits that give up: one that runs out ends every later one that would block.
 struct Waits {
@@ -223,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Start s = find_start(a, worker, rows_a_block, blockIdx.x == 0 ? &g_status : nullptr);
         if (lane == 0) *reinterpret_cast<Start *>(smem + kStart) = s;
     } else if (warp == kProducer && lane == 0) {
-        for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + kBufs ? kParts * 4 : 1);
+        for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), (i >= kPFull && i < kPFull + kBufs) || i == kInfoFree ? kParts * 4 : 1);
         *wait.abort = 0;
         fence_mbar_init();
     }
@@ -243,10 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w(a, start, lo, hi, rows_a_block);
 
     if (warp == kProducer) {
-        // ring order K 0, K 1, V 0, K 2, V 1, ...
         const int p = lane & 7;
-        int slot = 0, phase = 1, job = 0, id_before = -1;
-        bool any = false;
+        int slot = 0, phase = 1, job = 0;
         Split split = {0, 0, 0, 0};
         const auto load = [&](const CUtensorMap *map, int id) {
             wait(bar(kEmpty + slot), phase);
@@ -256,49 +272,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (id >= 0) tc::tma_load_5d(sb + kRing + slot * kQBytes + p * 2 * kGroup, map, 0, 0, 0, 2 * id, head, bar(kFull + slot));
             if (++slot == kSlots) slot = 0, phase ^= 1;
         };
-        while (w.next()) {
-            const int32_t *row = a.page_table + (size_t)w.b * a.max_pages;
-            const int pages = (w.r.keys + kPage - 1) / kPage;
-            const uint32_t q = sb + (job & 1) * kQBytes;
+        // a job's numbers; the next job's are taken, and its first page ids asked for, before this one's copies go out
+        struct Job {
+            const int32_t *row;
+            int pages, t0, t1, q_row;
+        };
+        const auto page_ids = [&](const Job &j, int chunk) { return chunk * 32 + lane < j.pages ? j.row[chunk * 32 + lane] : -1; };
+        Job next = {};
+        int next_ids = -1;
+        const auto take = [&] {
+            if (!w.next()) return false;
+            next = {a.page_table + (size_t)w.b * a.max_pages, (w.r.keys + kPage - 1) / kPage, w.t0, w.t1, w.r.first + w.block * rows_a_block};
+            next_ids = page_ids(next, w.t0 >> 2);
+            const int first = w.at - w.t0, last = first + w.tiles - 1;  // the job's tiles
+            if (first >= lo && last >= hi) {
+                split.count = last / per - worker + 1;
+                split.first_slot = 2 * worker + (first > lo);
+                split.out_row = next.q_row;
+                split.rows = min(rows_a_block, w.r.rows - w.block * rows_a_block) * a.group;
+            }
+            return true;
+        };
+        for (bool more = take(); more; ++job) {
+            const Job j = next;
+            int ids = -1, ids_next = next_ids, id_before = -1;
+            more = take();
             wait(bar(kQEmpty + (job & 1)), ((job >> 1) & 1) ^ 1);
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar(kQFull + (job & 1)), kQBytes);
                 for (int i = 0; i < 2; ++i)
-                    tc::tma_load_3d(q + i * tc::kSubTileBytes, &tq, i * 64, head * a.group, w.r.first + w.block * rows_a_block,
+                    tc::tma_load_3d(sb + (job & 1) * kQBytes + i * tc::kSubTileBytes, &tq, i * 64, head * a.group, j.q_row,
                                     bar(kQFull + (job & 1)));
             }
             __syncwarp();
-            ++job;
-            // 32 page ids at a time, the next ones on their way
-            const auto page_ids = [&](int chunk) { return chunk * 32 + lane < pages ? row[chunk * 32 + lane] : -1; };
-            int ids = -1, ids_next = page_ids(w.t0 >> 2);
-            for (int t = w.t0; t < w.t1; ++t) {
-                if (t == w.t0 || (t & 3) == 0) {
+            for (int t = j.t0; t < j.t1; ++t) {
+                if (t == j.t0 || (t & 3) == 0) {  // 32 page ids at a time, the next ones on their way
                     const int chunk = t >> 2;
                     ids = ids_next;
-                    ids_next = page_ids(chunk + 1);
-                    if (chunk * 32 + lane < pages && (ids < 0 || ids >= a.num_pages)) {
+                    ids_next = page_ids(j, chunk + 1);
+                    if (chunk * 32 + lane < j.pages && (ids < 0 || ids >= a.num_pages)) {
                         const int tile = chunk * 4 + (lane >> 3);
-                        if (tile >= w.t0 && tile < w.t1) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
+                        if (tile >= j.t0 && tile < j.t1) atomicOr(&g_status, QA_DEVICE_BAD_PAGE);
                         ids = -1;
                     }
                 }
                 int id = __shfl_sync(kAll, ids, (8 * t + p) & 31);
                 if (lane >= 8) id = -1;
                 load(&tk, id);
-                if (any) load(&tv, id_before);
+                if (t > j.t0) load(&tv, id_before);
                 id_before = id;
-                any = true;
             }
-            const int p0 = w.at - w.t0, p1 = p0 + w.tiles;  // the job's tiles
-            if (p0 >= lo && p1 > hi) {
-                split.count = (p1 - 1) / per - worker + 1;
-                split.first_slot = 2 * worker + (p0 > lo);
-                split.out_row = w.r.first + w.block * rows_a_block;
-                split.rows = min(rows_a_block, w.r.rows - w.block * rows_a_block) * a.group;
-            }
+            load(&tv, id_before);
         }
-        if (any) load(&tv, id_before);
         if (head == 0 && lane == 0) a.splits[worker] = split;
     } else if (warp == kIssueS) {
         if (lane == 0) {
@@ -308,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t q = sb + (job & 1) * kQBytes;
                 wait(bar(kQFull + (job & 1)), (job >> 1) & 1);
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    const int piece = n == 0 ? 0 : 2 * n - 1, slot = piece % kSlots;
+                    const int piece = 2 * (n - (t - w.t0)) + k_piece(t - w.t0), slot = piece % kSlots;
                     wait(bar(kFull + slot), piece / kSlots & 1);
                     if (n >= kBufs) wait(bar(kDone + buf), phase ^ 1);  // P V of tile n - 3 has read this buffer
                     tc::fence_after();
@@ -332,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 0, buf = 0, phase = 0;
             while (w.next()) {
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    const int piece = v_piece(n, hi - lo), slot = piece % kSlots;
+                    const int piece = 2 * (n - (t - w.t0)) + v_piece(t - w.t0, w.t1 - w.t0), slot = piece % kSlots;
                     wait(bar(kFull + slot), piece / kSlots & 1);
                     wait(bar(kPFull + buf), phase);
                     tc::fence_after();
@@ -351,6 +376,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mma_commit(bar(kOFull));
             }
         }
+    } else if (warp == kScout) {
+        Info &info = *reinterpret_cast<Info *>(smem + kInfo);
+        for (int job = 0; w.next(); ++job) {
+            const int32_t *table = a.page_table + (size_t)w.b * a.max_pages;
+            const int end = min(w.t1 * (kTile / kPage), (w.r.keys + kPage - 1) / kPage);
+            bool bad = false;
+            for (int j = w.t0 * (kTile / kPage) + lane; j < end; j += 32) {
+                const int id = table[j];
+                bad |= id < 0 || id >= a.num_pages;
+            }
+            bad = __any_sync(kAll, bad);
+            uint64_t seen[2] = {0, 0};
+            if (a.tree && w.t1 * kTile > w.r.past) {
+                int up[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) up[y] = lane + 32 * y < w.r.rows ? parent_of(a, w.r.first, lane + 32 * y, &g_status) : -1;
+                ancestors(a, up, seen);
+            }
+            wait(bar(kInfoFree), (job & 1) ^ 1);
+            info.seen[lane] = seen[0], info.seen[lane + 32] = seen[1];
+            if (lane == 0) info.bad = bad;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kInfoFull));
+        }
     } else {
         const int h = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21, t_o = tmem + kColO + h * kKeys + lanes;  // of O, the part's share of the dims
@@ -359,38 +408,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (w.next()) {
             const Request &r = w.r;
             const int32_t *table = a.page_table + (size_t)w.b * a.max_pages;
-            const int pages = (r.keys + kPage - 1) / kPage;
             const bool drafted = a.tree && w.t1 * kTile > r.past;
-            uint64_t seen = 0;  // of the drafted rows, found where the first of them comes
-            int up[2] = {-1, -1};
-            if (drafted && a.parents) {
-                if (lane < r.rows) up[0] = a.parents[r.first + lane];
-                if (lane + 32 < r.rows) up[1] = a.parents[r.first + lane + 32];
-            }
-            bool found = !drafted;
-            const auto find = [&] {
-                uint64_t all[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (up[x] < -1 || up[x] >= lane + 32 * x) atomicOr(&g_status, QA_DEVICE_BAD_TREE), up[x] = -1;
-                ancestors(a, up, all);
-                const int node = row / a.group;
-                const uint64_t s0 = __shfl_sync(kAll, all[0], node & 31), s1 = __shfl_sync(kAll, all[1], node & 31);
-                seen = node >= r.rows ? 0 : node < 32 ? s0 : s1;
-                found = true;
-            };
+            const Info &info = *reinterpret_cast<const Info *>(smem + kInfo);
+            wait(bar(kInfoFull), job & 1);
+            const bool holes = info.bad;  // then each tile looks which of its pages are there
+            const uint64_t seen = drafted && row / a.group < r.rows ? info.seen[row / a.group] : 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kInfoFree));
             constexpr int kPages = kKeys / kPage;
-            const auto page_id = [&](int t) {  // of the part's pages, the lane's; a tile ahead of its use
-                const int page = 8 * t + kPages * h + lane % kPages;
-                return t < w.t1 && page < pages ? table[page] : 0;
+            const auto pages_of = [&](int t) -> uint32_t {  // which of the part's pages can be read
+                const int page = 8 * t + kPages * h + lane % kPages, id = page * kPage < r.keys ? table[page] : 0;
+                return __ballot_sync(kAll, id >= 0 && id < a.num_pages) & ((1u << kPages) - 1);
             };
             float m = -INFINITY, l = 0.f;
             bool odd = false;
-            int id = page_id(w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const uint32_t ok = __ballot_sync(kAll, id >= 0 && id < a.num_pages) & ((1u << kPages) - 1);  // pages that can be read
+                const uint32_t ok = holes ? pages_of(t) : (1u << kPages) - 1;
                 const uint32_t s = tmem + buf * kTile + h * kKeys + lanes;
-                id = page_id(t + 1);
                 wait(bar(kSFull + buf), phase);
                 __syncwarp();
                 tc::fence_after();
@@ -402,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key0 = t * kTile + h * kKeys, behind = r.past - key0;  // keys of this part that every row sees
                 const bool masked = behind < kKeys || ok != (1u << kPages) - 1;
                 if (masked) {
-                    if (!found) find();
                     uint64_t vis = behind >= 64 ? ~0ull : behind > 0 ? ~(~0ull << behind) : 0ull;
                     if (behind < 64 && behind > -64) vis |= behind >= 0 ? seen << behind : seen >> -behind;
 #pragma unroll
@@ -474,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Slots that hold no key (or were not loaded) are zeroed, and of drafted values what is not finite, so
                     // that a probability of 0 meets nothing that it would not cancel; rows that see such a value get it at
                     // the end.
-                    const int piece = v_piece(n, hi - lo), v_slot = piece % kSlots;
+                    const int piece = 2 * (n - (t - w.t0)) + v_piece(t - w.t0, w.t1 - w.t0), v_slot = piece % kSlots;
                     wait(bar(kFull + v_slot), piece / kSlots & 1);
                     constexpr int kEach = 128 / kKeys, kChunks = 16 / kEach;  // threads of a key, 16-byte pieces of a thread
                     const int key = row / kEach, piece0 = row % kEach * kChunks, pos = key0 + key;
@@ -506,12 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_barrier(1, kRows);  // maxima that were exchanged have been read
             stats[h * 128] = l;
             const bool any_odd = any_of_rows(odd);  // all parts' sums are there too
-            if (any_odd && !found) find();  // the part's own keys were all behind
             float sum = 0.f;
 #pragma unroll
             for (int x = 0; x < kParts; ++x) sum += stats[x * 128];
             wait(bar(kOFull), job & 1);
-            ++job;
             __syncwarp();
             tc::fence_after();
             // each part's warps give their share of the dims
@@ -563,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!whole && h == 0 && row < left) *reinterpret_cast<float2 *>(a.ml + 2 * part) = make_float2(m, sum);
             tc::fence_before();  // before the next job's P is handed over
+            ++job;
         }
     }
     __syncthreads();
