@@ -589,6 +589,7 @@ PyObject *tree_accept(PyObject *const *a) {
         pages = p.pages, hkv = p.hkv, kp[i] = p.k, vp[i] = p.v;
     }
     const int max_rows = as_int(as_long(a[8], "max_rows"), "max_rows"), batch = as_int(r.batch, "batch"), n = as_int(T, "total_rows");
+    if (max_rows < 1 || max_rows > 64) refuse(PyExc_ValueError, "max_rows %d is outside [1, 64]", max_rows);
     const Stream s = stream_of(a[12], device);
     at::Tensor made_out[3];
     int32_t *out[3];

@@ -35,12 +35,13 @@
 // many (Q, K and twice V read, K and V written, at 128 bytes a clock); a tile
 // takes 1.2 us where its pages come from L2, about 2300 clocks, so that the
 // tensor core works two thirds of the time.  Four parts or two of 64 keys: 44.0
-// and 45.1 us for 64 requests of 16 to 64 rows over 500 to 2000 positions (16
-// heads on 8); that call's floor by its bytes is 21.8 us.  A job's switch costs
-// 2 to 4 us (its last tile waits for V, then O is given back), which is what
-// such a call of a few tiles a job pays; 8 requests of 100 to 448 rows over
-// 2000 to 15600 positions, 230 us, read K and V again for each 64 query rows,
-// 1.33 GB, 5.7 TB/s.
+// and 45.1 us for 32 requests of 9 to 16 rows over 200 to 2000 positions (16
+// heads on 8), now 43.5; that call's floor by its bytes is 21.8 us.  A job's
+// switch costs 2 to 4 us (its last tile waits for V, then O is given back),
+// which is what such a call of a few tiles a job pays.  24 requests of 33 to 64
+// rows over 500 to 8000 positions: 97 us, 4.8 TB/s, floor 68.6 us.  8 requests
+// of 100 to 448 rows over 2000 to 15600 positions: 235 us; K and V are read
+// again for each 64 query rows, 1.33 GB, 5.7 TB/s.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
