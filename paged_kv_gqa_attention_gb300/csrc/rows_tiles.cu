@@ -70,7 +70,7 @@ constexpr uint32_t kRing = 2 * kQBytes;
 constexpr uint32_t kBar = kRing + kSlots * kQBytes;
 enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots,
                   kPFull = kSFull + kBufs, kDone = kPFull + kBufs, kOFull = kDone + kBufs,
-                  kInfoFull, kInfoFree, kBars };
+                  kInfoFull, kInfoFree, kDrained, kBars };
 constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 24;
 // What the scout finds of a job.
 struct Info {
@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Start s = find_start(a, worker, rows_a_block, blockIdx.x == 0 ? &g_status : nullptr);
         if (lane == 0) *reinterpret_cast<Start *>(smem + kStart) = s;
     } else if (warp == kProducer && lane == 0) {
-        for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), (i >= kPFull && i < kPFull + kBufs) || i == kInfoFree ? kParts * 4 : 1);
+        for (uint32_t i = 0; i < kBars; ++i)
+            mbar_init(bar(i), (i >= kPFull && i < kPFull + kBufs) || i == kInfoFree ? kParts * 4 : i == kDrained ? 2 : 1);
         *wait.abort = 0;
         fence_mbar_init();
     }
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (head == 0)
         for (int b = worker; b < a.batch; b += a.workers) zero_rows(a, request_of(a, b, nullptr), threadIdx.x, kThreads);
     Walk w(a, start, lo, hi, rows_a_block);
+    int pieces = 0, jobs = 0;  // whose copies the producer has asked for
 
     if (warp == kProducer) {
         const int p = lane & 7;
@@ -267,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Split split = {0, 0, 0, 0};
         const auto load = [&](const CUtensorMap *map, int id) {
             wait(bar(kEmpty + slot), phase);
+            if (__any_sync(kAll, *wait.abort)) return;  // the slot may still be read
+            ++pieces;
             const unsigned boxes = __ballot_sync(kAll, id >= 0);
             if (lane == 0) mbar_arrive_expect_tx(bar(kFull + slot), __popc(boxes) * 2 * kGroup);
             __syncwarp();
@@ -299,6 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int ids = -1, ids_next = next_ids, id_before = -1;
             more = take();
             wait(bar(kQEmpty + (job & 1)), ((job >> 1) & 1) ^ 1);
+            if (__any_sync(kAll, *wait.abort)) break;
+            ++jobs;
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar(kQFull + (job & 1)), kQBytes);
                 for (int i = 0; i < 2; ++i)
@@ -599,6 +605,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
+    if (*wait.abort) {  // a wait ran out: what is still under way writes shared memory and TMEM
+        if (warp == kProducer && lane == 0) {
+            for (int i = max(0, pieces - kSlots); i < pieces; ++i) mbar_wait(bar(kFull + i % kSlots), i / kSlots & 1, &g_status);
+            for (int i = max(0, jobs - 2); i < jobs; ++i) mbar_wait(bar(kQFull + (i & 1)), i >> 1 & 1, &g_status);
+        } else if ((warp == kIssueS || warp == kIssueO) && lane == 0) {
+            tc::mma_commit(bar(kDrained));
+            mbar_wait(bar(kDrained), 0, &g_status);
+        }
+        __syncthreads();
+    }
     if (warp == kIssueS) {
         tc::fence_after();
         tc::tmem_dealloc(tmem, 512);
