@@ -14,9 +14,8 @@
 //              what bounded
 //   warp 17    issues S = Q K^T (M 128, N 128) into one of three buffers in
 //              TMEM, up to two tiles ahead, into the next job too
-//   warp 18    issues O += P V (N 128), P from TMEM; a thread for both
-//              products would let the tensor core run dry at every barrier
-//              that it waits on
+//   warp 18    issues O += P V (N 128), P from TMEM; one thread for both
+//              products was slower, 1.98 us a tile against 1.30
 //   warp 19    the scout: a job ahead, whether any of its pages is bad, and
 //              which drafted rows each row sees
 //   warps 0-15 softmax, a row a thread: a warpgroup has 32 of each tile's keys.
@@ -30,18 +29,22 @@
 // Two terms of P make P V two products: 16 bits of each probability, as in
 // the prefill kernels.
 //
-// What bounds: the tensor core needs 514 clocks for S and 1028 for P V of a
-// tile (measured: 64.2 an instruction; N = 64 would take 48), shared memory as
-// many (Q, K and twice V read, K and V written, at 128 bytes a clock); a tile
-// takes 1.2 us where its pages come from L2, about 2300 clocks, so that the
-// tensor core works two thirds of the time.  Four parts or two of 64 keys: 44.0
-// and 45.1 us for 32 requests of 9 to 16 rows over 200 to 2000 positions (16
-// heads on 8), now 43.5; that call's floor by its bytes is 21.8 us.  A job's
-// switch costs 2 to 4 us (its last tile waits for V, then O is given back),
-// which is what such a call of a few tiles a job pays.  24 requests of 33 to 64
-// rows over 500 to 8000 positions: 97 us, 4.8 TB/s, floor 68.6 us.  8 requests
-// of 100 to 448 rows over 2000 to 15600 positions: 235 us; K and V are read
-// again for each 64 query rows, 1.33 GB, 5.7 TB/s.
+// What bounds.  One request of 4000 rows over 15600 states that stay in L2 (16
+// heads on 8): 530 us, 1.3 us a tile, 1.43 PFLOP/s with both terms of P, 76 %
+// of the measured peak.  The tensor core needs 514 clocks for S and 1028 for
+// P V of a tile (measured: 64.2 an instruction; N = 64 would take 48), shared
+// memory as many; P waits for the products, not they for it.  Not faster were
+// two teams of softmax warps with two buffers of S and an O each (1.47 us a
+// tile), two blocks of rows for each tile's K and V (1.38), pairs of workers on
+// two blocks of a request, which halve what is read from HBM (8 requests of 448
+// rows over 8000 states 313 us against 265; an odd block idles a worker).
+// 24 requests of 33 to 64 rows over 500 to 8000 positions: 94 us, 4.9 TB/s,
+// floor 68.6 us by their bytes.  32 requests of 9 to 16 rows over 200 to 2000:
+// 40.7 us, floor 21.8: jobs are a few tiles long, and each costs 2 to 4 us
+// beside them (the last tile waits for V, then O is given back); four parts or
+// two of 64 keys there: 44.0 and 45.1 us.  8 requests of 100 to 448 rows over
+// 2000 to 15600 states: 230 us, where K and V are read again for each 64 rows,
+// 1.33 GB.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -68,7 +71,7 @@ constexpr uint32_t kQBytes = 2 * tc::kSubTileBytes;  // two halves of 64 dims of
 constexpr uint32_t kAtom = 1024, kGroup = 2 * kAtom;    // of K and V: 8 keys' first 64 dims, then their others
 constexpr uint32_t kRing = 2 * kQBytes;
 constexpr uint32_t kBar = kRing + kSlots * kQBytes;
-enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kEmpty = kFull + kSlots, kSFull = kEmpty + kSlots,
+enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kSFull = kFull + kSlots,
                   kPFull = kSFull + kBufs, kDone = kPFull + kBufs, kOFull = kDone + kBufs,
                   kInfoFull, kInfoFree, kDrained, kBars };
 constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 24;
@@ -187,6 +190,18 @@ __device__ __forceinline__ bool any_of_rows(bool x) {  // the threads that own r
     return r != 0;
 }
 
+// One lane of a whole warp, in a form that lets the products' operands be
+// kept in uniform registers.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+template <class T>
+__device__ __forceinline__ T same_in_warp(T x) {
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
 __device__ __forceinline__ void store32(float *dst, const float *v) {  // 32-byte aligned
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(__float_as_uint(v[0])),
                  "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])),
@@ -265,17 +280,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kProducer) {
         const int p = lane & 7;
-        int slot = 0, phase = 1, job = 0;
+        int slot = 0, job = 0, tile = 0;
+        int ends[kSlots];  // of the last pieces, newest first: the barrier that says that its slot is free, and its parity
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) ends[i] = -1;
         Split split = {0, 0, 0, 0};
-        const auto load = [&](const CUtensorMap *map, int id) {
-            wait(bar(kEmpty + slot), phase);
+        const auto load = [&](const CUtensorMap *map, int id, uint32_t end, int of) {
+            if (ends[kSlots - 1] >= 0) wait(bar(ends[kSlots - 1] >> 1), ends[kSlots - 1] & 1);
+#pragma unroll
+            for (int i = kSlots - 1; i > 0; --i) ends[i] = ends[i - 1];
+            ends[0] = 2 * (end + of % kBufs) + (of / kBufs & 1);
             if (__any_sync(kAll, *wait.abort)) return;  // the slot may still be read
             ++pieces;
             const unsigned boxes = __ballot_sync(kAll, id >= 0);
             if (lane == 0) mbar_arrive_expect_tx(bar(kFull + slot), __popc(boxes) * 2 * kGroup);
             __syncwarp();
             if (id >= 0) tc::tma_load_5d(sb + kRing + slot * kQBytes + p * 2 * kGroup, map, 0, 0, 0, 2 * id, head, bar(kFull + slot));
-            if (++slot == kSlots) slot = 0, phase ^= 1;
+            if (++slot == kSlots) slot = 0;
         };
         // a job's numbers; the next job's are taken, and its first page ids asked for, before this one's copies go out
         struct Job {
@@ -325,62 +346,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 int id = __shfl_sync(kAll, ids, (8 * t + p) & 31);
                 if (lane >= 8) id = -1;
-                load(&tk, id);
-                if (t > j.t0) load(&tv, id_before);
+                load(&tk, id, kSFull, tile);
+                if (t > j.t0) load(&tv, id_before, kDone, tile - 1);
                 id_before = id;
+                ++tile;
             }
-            load(&tv, id_before);
+            load(&tv, id_before, kDone, tile - 1);
         }
         if (head == 0 && lane == 0) a.splits[worker] = split;
     } else if (warp == kIssueS) {
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = tc::idesc_bf16(128, kTile, false);
-            int n = 0, job = 0, buf = 0, phase = 0;
-            while (w.next()) {
-                const uint32_t q = sb + (job & 1) * kQBytes;
-                wait(bar(kQFull + (job & 1)), (job >> 1) & 1);
-                for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    const int piece = 2 * (n - (t - w.t0)) + k_piece(t - w.t0), slot = piece % kSlots;
-                    wait(bar(kFull + slot), piece / kSlots & 1);
-                    if (n >= kBufs) wait(bar(kDone + buf), phase ^ 1);  // P V of tile n - 3 has read this buffer
-                    tc::fence_after();
-                    const uint32_t k = sb + kRing + slot * kQBytes, d = tmem + buf * kTile;
+        constexpr uint32_t idesc_s = tc::idesc_bf16(128, kTile, false);
+        int n = 0, job = 0, buf = 0, phase = 0;
+        while (w.next()) {
+            const uint32_t q = sb + (job & 1) * kQBytes;
+            wait(bar(kQFull + (job & 1)), (job >> 1) & 1);
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const int piece = 2 * (n - (t - w.t0)) + k_piece(t - w.t0), slot = piece % kSlots;
+                wait(bar(kFull + slot), piece / kSlots & 1);
+                if (n >= kBufs) wait(bar(kDone + buf), phase ^ 1);  // P V of tile n - 3 has read this buffer
+                __syncwarp();
+                tc::fence_after();
+                const uint64_t qd = same_in_warp(tc::sw128_desc(q)), kd = same_in_warp(tc::sw128_desc(sb + kRing + slot * kQBytes, kGroup, 0));
+                const uint32_t d = same_in_warp(tmem + buf * kTile);
+                if (elected()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t off = (kk >> 2) * tc::kSubTileBytes + (kk & 3) * 32;
-                        tc::mma_bf16(d, tc::sw128_desc(q + off), tc::sw128_desc(k + (kk >> 2) * kAtom + (kk & 3) * 32, kGroup, 0), idesc_s, kk > 0);
-                    }
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc::mma_bf16(d, qd + ((kk >> 2) * tc::kSubTileBytes + (kk & 3) * 32) / 16, kd + ((kk >> 2) * kAtom + (kk & 3) * 32) / 16, idesc_s, kk > 0);
                     tc::mma_commit(bar(kSFull + buf));
-                    tc::mma_commit(bar(kEmpty + slot));
-                    if (++buf == kBufs) buf = 0, phase ^= 1;
+                    if (t + 1 == w.t1) tc::mma_commit(bar(kQEmpty + (job & 1)));
                 }
-                tc::mma_commit(bar(kQEmpty + (job & 1)));
-                ++job;
+                __syncwarp();
+                if (++buf == kBufs) buf = 0, phase ^= 1;
             }
+            ++job;
         }
     } else if (warp == kIssueO) {
-        if (lane == 0) {
-            constexpr uint32_t idesc_o = tc::idesc_bf16(128, 128, true);
-            int n = 0, buf = 0, phase = 0;
-            while (w.next()) {
-                for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    const int piece = 2 * (n - (t - w.t0)) + v_piece(t - w.t0, w.t1 - w.t0), slot = piece % kSlots;
-                    wait(bar(kFull + slot), piece / kSlots & 1);
-                    wait(bar(kPFull + buf), phase);
-                    tc::fence_after();
-                    const uint32_t v = sb + kRing + slot * kQBytes, p = tmem + buf * kTile;
+        constexpr uint32_t idesc_o = tc::idesc_bf16(128, 128, true);
+        int n = 0, buf = 0, phase = 0;
+        while (w.next()) {
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const int piece = 2 * (n - (t - w.t0)) + v_piece(t - w.t0, w.t1 - w.t0), slot = piece % kSlots;
+                wait(bar(kFull + slot), piece / kSlots & 1);
+                wait(bar(kPFull + buf), phase);
+                __syncwarp();
+                tc::fence_after();
+                const uint64_t vd = same_in_warp(tc::sw128_desc(sb + kRing + slot * kQBytes, kGroup, kAtom));
+                const uint32_t p = same_in_warp(tmem + buf * kTile), o = same_in_warp(tmem + kColO);
+                if (elected()) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
                         const uint32_t hi_p = p + (kk >> 1) * 32 + (kk & 1) * 8;
-                        const uint64_t vdesc = tc::sw128_desc(v + kk * 2 * kGroup, kGroup, kAtom);
-                        tc::mma_bf16_ts(tmem + kColO, hi_p, vdesc, idesc_o, t > w.t0 || kk > 0);
-                        tc::mma_bf16_ts(tmem + kColO, hi_p + 16, vdesc, idesc_o, 1u);
+                        tc::mma_bf16_ts(o, hi_p, vd + kk * 2 * kGroup / 16, idesc_o, t > w.t0 || kk > 0);
+                        tc::mma_bf16_ts(o, hi_p + 16, vd + kk * 2 * kGroup / 16, idesc_o, 1u);
                     }
-                    tc::mma_commit(bar(kEmpty + slot));
                     tc::mma_commit(bar(kDone + buf));
-                    if (++buf == kBufs) buf = 0, phase ^= 1;
+                    if (t + 1 == w.t1) tc::mma_commit(bar(kOFull));
                 }
-                tc::mma_commit(bar(kOFull));
+                __syncwarp();
+                if (++buf == kBufs) buf = 0, phase ^= 1;
             }
         }
     } else if (warp == kScout) {
@@ -609,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kProducer && lane == 0) {
             for (int i = max(0, pieces - kSlots); i < pieces; ++i) mbar_wait(bar(kFull + i % kSlots), i / kSlots & 1, &g_status);
             for (int i = max(0, jobs - 2); i < jobs; ++i) mbar_wait(bar(kQFull + (i & 1)), i >> 1 & 1, &g_status);
-        } else if ((warp == kIssueS || warp == kIssueO) && lane == 0) {
+        } else if ((warp == kIssueS || warp == kIssueO) && elected()) {
             tc::mma_commit(bar(kDrained));
             mbar_wait(bar(kDrained), 0, &g_status);
         }
