@@ -38,13 +38,13 @@
 // tile), two blocks of rows for each tile's K and V (1.38), pairs of workers on
 // two blocks of a request, which halve what is read from HBM (8 requests of 448
 // rows over 8000 states 313 us against 265; an odd block idles a worker).
-// 24 requests of 33 to 64 rows over 500 to 8000 positions: 94 us, 4.9 TB/s,
+// 24 requests of 33 to 64 rows over 500 to 8000 positions: 92.5 us, 5.0 TB/s,
 // floor 68.6 us by their bytes.  32 requests of 9 to 16 rows over 200 to 2000:
-// 40.7 us, floor 21.8: jobs are a few tiles long, and each costs 2 to 4 us
+// 39.5 us, floor 21.8: jobs are a few tiles long, and each costs 2 to 4 us
 // beside them (the last tile waits for V, then O is given back); four parts or
-// two of 64 keys there: 44.0 and 45.1 us.  8 requests of 100 to 448 rows over
-// 2000 to 15600 states: 230 us, where K and V are read again for each 64 rows,
-// 1.33 GB.
+// two of 64 keys there: 44.0 and 45.1 us before that.  8 requests of 100 to 448
+// rows over 2000 to 15600 states: 224 us, where K and V are read again for each
+// 64 rows, 1.33 GB.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -84,20 +84,30 @@ constexpr uint32_t kInfo = kStats + kParts * 128 * 4, kSmem = kInfo + sizeof(Inf
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kColO = kBufs * kTile;  // TMEM: three buffers of S / P, then O
 
-// A call's tiles, and the request of the worker's first one, by one warp.
+// The list of a call's places, of which every worker gets as many: a job's
+// tiles, and kSwitch places before them for what a job costs beside its tiles.
+// With 0, 1, 2, 3, 5 places: 64 requests of 32 rows over 550 positions 59.7,
+// 55.8, 51.9, 51.2, 50.5 us; 32 of 9 to 16 over 200 to 2000 43.4, 40.5, 40.0,
+// 39.5, 40.0; one of 4000 over 15600 531, 534, 538, 538, 537.
+constexpr int kSwitch = 3;
+
+// The places of a call, and the request of the worker's first one, by one warp.
 struct Start {
-    int total, b, base;   // base: the tiles before request b
+    int total, b, base;   // base: the places before request b
     int first, end, past; // request b's numbers
 };
-__device__ __forceinline__ int tiles_of(const RowsArgs &a, const Request &r, int rows_a_block) {
-    return (r.keys + kTile - 1) / kTile * ((r.rows + rows_a_block - 1) / rows_a_block);
+__device__ __forceinline__ int places_of(int tiles, int rows, int rows_a_block) {
+    return tiles == 0 ? 0 : (tiles + kSwitch) * ((rows + rows_a_block - 1) / rows_a_block);
+}
+__device__ __forceinline__ int places_of(const Request &r, int rows_a_block) {
+    return places_of((r.keys + kTile - 1) / kTile, r.rows, rows_a_block);
 }
 __device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, int rows_a_block, unsigned int *report) {
     constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     int sum = 0, first = 0;  // first: of the first 32 requests
     for (int b = lane; b < a.batch; b += 32) {
-        const int v = tiles_of(a, request_of(a, b, report), rows_a_block);
+        const int v = places_of(request_of(a, b, report), rows_a_block);
         if (b < 32) first = v;
         sum += v;
     }
@@ -107,7 +117,7 @@ __device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, int r
     if (lo >= s.total) return s;
     for (int begin = 0, carry = 0; begin < a.batch; begin += 32) {
         const int b = begin + lane;
-        const int v = begin == 0 ? first : b < a.batch ? tiles_of(a, request_of(a, b, nullptr), rows_a_block) : 0;
+        const int v = begin == 0 ? first : b < a.batch ? places_of(request_of(a, b, nullptr), rows_a_block) : 0;
         int up_to = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -133,25 +143,30 @@ struct Walk {
     int at, hi, b, base, rows_a_block;
     int block, t0, t1;  // the segment: rows block, tiles [t0, t1) of `tiles`
     int tiles;
+    int first, end;     // the places of the job's tile 0, and behind the segment
     Request r;
     int first_next, end_next, past_next;  // of request b + 1
     __device__ Walk(const RowsArgs &args, const Start &s, int lo, int end, int rab)
-        : a(args), at(lo), hi(end), b(s.b), base(s.base), rows_a_block(rab), t0(0), t1(0) {
+        : a(args), at(lo), hi(end), b(s.b), base(s.base), rows_a_block(rab), end(lo) {
         if (lo >= end) return;
         first_next = s.first, end_next = s.end, past_next = s.past;
         load();
     }
     __device__ bool next() {
-        at += t1 - t0;
-        if (at >= hi) return false;
-        for (int n = mine(); at >= base + n; n = mine()) base += n, ++b, load();
-        const int x = at - base;
-        block = x / tiles;
-        t0 = x - block * tiles;
-        t1 = min(tiles, t0 + hi - at);
+        do {
+            at = end;
+            if (at >= hi) return false;
+            for (int n = mine(); at >= base + n; n = mine()) base += n, ++b, load();
+            const int job = tiles + kSwitch;
+            block = (at - base) / job;
+            first = base + block * job + kSwitch;
+            end = min(first + tiles, hi);
+            t0 = max(at - first, 0);
+            t1 = end - first;
+        } while (t0 >= t1);
         return true;
     }
-    __device__ int mine() const { return tiles * ((r.rows + rows_a_block - 1) / rows_a_block); }
+    __device__ int mine() const { return places_of(tiles, r.rows, rows_a_block); }
     __device__ void load() {  // the request whose numbers are here, and asks for the next one's
         r = request_of(a, first_next, end_next, past_next, nullptr);
         tiles = (r.keys + kTile - 1) / kTile;
@@ -310,10 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!w.next()) return false;
             next = {a.page_table + (size_t)w.b * a.max_pages, (w.r.keys + kPage - 1) / kPage, w.t0, w.t1, w.r.first + w.block * rows_a_block};
             next_ids = page_ids(next, w.t0 >> 2);
-            const int first = w.at - w.t0, last = first + w.tiles - 1;  // the job's tiles
-            if (first >= lo && last >= hi) {
+            const int last = w.first + w.tiles - 1;  // the place of the job's last tile
+            if (w.t0 == 0 && last >= hi) {
                 split.count = last / per - worker + 1;
-                split.first_slot = 2 * worker + (first > lo);
+                split.first_slot = 2 * worker + (w.at > lo);
                 split.out_row = next.q_row;
                 split.rows = min(rows_a_block, w.r.rows - w.block * rows_a_block) * a.group;
             }
