@@ -18,7 +18,10 @@
 // row's heads in turn) are the M of mma.sync m16n8k16, so that S stays in
 // registers as the A operand of P V.  A tcgen05 tile would be 128 rows for
 // these 16, and its S would have to come back from TMEM for the softmax;
-// the tensor pipe is not what bounds.
+// the tensor pipe is not what bounds.  64 requests of 4 to 8 rows over 2000 to
+// 16000 positions (16 heads on 8): 345 us, 6.8 TB/s; 1 request of 8 over 257:
+// 9.4 us, of which the pages are 0.2: a launch, lengths, page ids and a page one
+// after another (5.5 us), the end of the grid and the merge.
 //
 // P enters P V as two bf16 terms (p truncated, and the rest rounded): about
 // 16 bits of each probability, with fp32 statistics.  The running max of a
@@ -73,7 +76,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// prefix[b] = pages of the requests before b, by one warp.
+// Places of the list that a request takes before its pages, for its queries
+// and its partial result.  With 0, 1, 2, 3 places: 32 requests of 8 rows over
+// 200 to 2000 positions 38.3, 38.3, 36.6, 36.2 us, 16 over 100 to 500 18.0,
+// 15.9, 15.9, 14.7, 5 of 1 to 4 over 13 to 390 7.3, 7.4, 7.6, 7.9, 64 of 4 to 8
+// over 2000 to 16000 345, 347, 344, 349 (16 heads on 8; the third 8 on 8).
+constexpr int kSwitch = 2;
+
+// prefix[b] = places of the requests before b, by one warp.
 __device__ __forceinline__ void count_pages(const RowsArgs &a, int *prefix, unsigned int *report) {
     const int lane = threadIdx.x & 31;
     int carry = 0;
@@ -83,6 +93,7 @@ __device__ __forceinline__ void count_pages(const RowsArgs &a, int *prefix, unsi
         int v = 0;
         if (b < a.batch) {
             v = (request_of(a, b, report).keys + kPage - 1) / kPage;
+            if (v > 0) v += kSwitch;
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -94,7 +105,7 @@ __device__ __forceinline__ void count_pages(const RowsArgs &a, int *prefix, unsi
     }
 }
 
-// First request whose pages reach past page x.
+// First request whose places reach past place x.
 __device__ __forceinline__ int request_at(const int *prefix, int batch, int x) {
     int l = 0, r = batch - 1;
     while (l < r) {
@@ -143,7 +154,7 @@ __global__ void __launch_bounds__(288, 1)
     const int b0 = lo < hi ? request_at(prefix, a.batch, lo) : 0, b_last = lo < hi ? request_at(prefix, a.batch, hi - 1) : -1;
     int first_ids = -1;
     if (warp == hkv && lo < hi) {
-        const int p0 = prefix[b0], j = lo - p0 + lane;
+        const int p0 = prefix[b0] + kSwitch, j = max(lo - p0, 0) + lane;
         if (j < min(hi, prefix[b0 + 1]) - p0) first_ids = a.page_table[(size_t)b0 * a.max_pages + j];
     }
     if (a.early) grid_wait();
@@ -154,7 +165,8 @@ __global__ void __launch_bounds__(288, 1)
         // the producer: lanes fetch page ids, lane 0 issues the copies
         if (lane == 0) {
             Split s = {0, 0, 0, 0};
-            if (lo < hi && prefix[b_last] >= lo && prefix[b_last + 1] > hi) {
+            const int p0 = lo < hi ? prefix[b_last] + kSwitch : hi;
+            if (p0 >= lo && p0 < hi && prefix[b_last + 1] > hi) {
                 const Request r = request_of(a, b_last, nullptr);
                 s.count = (prefix[b_last + 1] - 1) / per - worker + 1;
                 s.first_slot = 2 * worker + (prefix[b_last] > lo);
@@ -165,9 +177,9 @@ __global__ void __launch_bounds__(288, 1)
         }
         int stage = 0, phase = 0;
         for (int b = b0; b <= b_last; ++b) {
-            const int p0 = prefix[b], p1 = prefix[b + 1];
-            if (p0 == p1) continue;
+            const int p0 = prefix[b] + kSwitch, p1 = prefix[b + 1];
             const int j0 = max(lo, p0) - p0, j1 = min(hi, p1) - p0;
+            if (j0 >= j1) continue;
             const int32_t *row = a.page_table + (size_t)b * a.max_pages;
             for (int jb = j0; jb < j1; jb += 32) {
                 const int mine = b == b0 && jb == j0 ? first_ids : jb + lane < j1 ? row[jb + lane] : -1;
@@ -204,9 +216,9 @@ __global__ void __launch_bounds__(288, 1)
     const uint32_t at_v = head * 2048 + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128, chunk_v = lane >> 4;
     int stage = 0, phase = 0;
     for (int b = b0; b <= b_last; ++b) {
-        const int p0 = prefix[b], p1 = prefix[b + 1];
-        if (p0 == p1) continue;
+        const int p0 = prefix[b] + kSwitch, p1 = prefix[b + 1];
         const int j0 = max(lo, p0) - p0, j1 = min(hi, p1) - p0;
+        if (j0 >= j1) continue;
         const Request r = request_of(a, b, nullptr);
         const int rows = r.rows * G;
         uint32_t qf[8][4];
@@ -360,7 +372,7 @@ __global__ void __launch_bounds__(288, 1)
             }
         }
         const bool whole = lo <= p0 && p1 <= hi;
-        const int slot = 2 * worker + (p0 > lo);
+        const int slot = 2 * worker + (prefix[b] > lo);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = quad + 8 * e;

@@ -4,8 +4,9 @@
 //
 // Work split.  A job is a request's block of query rows (up to `rows_a_block`
 // of them); its key tiles run over the request's positions.  All jobs' tiles
-// form one list, requests in order and a request's blocks in order, and
-// worker w of n takes the tiles [w per, (w + 1) per), per = ceil(total / n).
+// form one list, requests in order and a request's blocks in order, with a few
+// places before a job's tiles for what it costs beside them; worker w of n
+// takes the places [w per, (w + 1) per), per = ceil(total / n).
 // A job inside one worker is finished by it.  Of a job that spans several,
 // each leaves fp32 (max, sum, accumulator) rows in a slot of its own, 2 w for
 // the first job of its range and 2 w + 1 for one that begins inside it and
