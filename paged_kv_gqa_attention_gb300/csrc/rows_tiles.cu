@@ -96,18 +96,19 @@ struct Start {
     int total, b, base;   // base: the places before request b
     int first, end, past; // request b's numbers
 };
-__device__ __forceinline__ int places_of(int tiles, int rows, int rows_a_block) {
-    return tiles == 0 ? 0 : (tiles + kSwitch) * ((rows + rows_a_block - 1) / rows_a_block);
+__device__ __forceinline__ int block_shift(const RowsArgs &a) { return 8 - a.group; }  // a block is 128 / group rows, group 1 or 2
+__device__ __forceinline__ int places_of(int tiles, int rows, int shift) {
+    return tiles == 0 ? 0 : (tiles + kSwitch) * ((rows + (1 << shift) - 1) >> shift);
 }
-__device__ __forceinline__ int places_of(const Request &r, int rows_a_block) {
-    return places_of((r.keys + kTile - 1) / kTile, r.rows, rows_a_block);
+__device__ __forceinline__ int places_of(const RowsArgs &a, const Request &r) {
+    return places_of((r.keys + kTile - 1) / kTile, r.rows, block_shift(a));
 }
-__device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, int rows_a_block, unsigned int *report) {
+__device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, unsigned int *report) {
     constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     int sum = 0, first = 0;  // first: of the first 32 requests
     for (int b = lane; b < a.batch; b += 32) {
-        const int v = places_of(request_of(a, b, report), rows_a_block);
+        const int v = places_of(a, request_of(a, b, report));
         if (b < 32) first = v;
         sum += v;
     }
@@ -117,7 +118,7 @@ __device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, int r
     if (lo >= s.total) return s;
     for (int begin = 0, carry = 0; begin < a.batch; begin += 32) {
         const int b = begin + lane;
-        const int v = begin == 0 ? first : b < a.batch ? places_of(request_of(a, b, nullptr), rows_a_block) : 0;
+        const int v = begin == 0 ? first : b < a.batch ? places_of(a, request_of(a, b, nullptr)) : 0;
         int up_to = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -140,14 +141,14 @@ __device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, int r
 // The jobs of a worker, one after another: the walk of every role.
 struct Walk {
     const RowsArgs &a;
-    int at, hi, b, base, rows_a_block;
+    int at, hi, b, base;
     int block, t0, t1;  // the segment: rows block, tiles [t0, t1) of `tiles`
     int tiles;
     int first, end;     // the places of the job's tile 0, and behind the segment
     Request r;
     int first_next, end_next, past_next;  // of request b + 1
-    __device__ Walk(const RowsArgs &args, const Start &s, int lo, int end, int rab)
-        : a(args), at(lo), hi(end), b(s.b), base(s.base), rows_a_block(rab), end(lo) {
+    __device__ Walk(const RowsArgs &args, const Start &s, int lo, int end)
+        : a(args), at(lo), hi(end), b(s.b), base(s.base), end(lo) {
         if (lo >= end) return;
         first_next = s.first, end_next = s.end, past_next = s.past;
         load();
@@ -157,8 +158,8 @@ struct Walk {
             at = end;
             if (at >= hi) return false;
             for (int n = mine(); at >= base + n; n = mine()) base += n, ++b, load();
-            const int job = tiles + kSwitch;
-            block = (at - base) / job;
+            const int job = tiles + kSwitch, x = at - base;
+            block = x < job ? 0 : x / job;
             first = base + block * job + kSwitch;
             end = min(first + tiles, hi);
             t0 = max(at - first, 0);
@@ -166,7 +167,7 @@ struct Walk {
         } while (t0 >= t1);
         return true;
     }
-    __device__ int mine() const { return places_of(tiles, r.rows, rows_a_block); }
+    __device__ int mine() const { return places_of(tiles, r.rows, block_shift(a)); }
     __device__ void load() {  // the request whose numbers are here, and asks for the next one's
         r = request_of(a, first_next, end_next, past_next, nullptr);
         tiles = (r.keys + kTile - 1) / kTile;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.hkv, worker = blockIdx.x / a.hkv;
-    const int rows_a_block = 128 / a.group;
+    const int rows_a_block = 1 << block_shift(a), by = a.group - 1;  // a tile's row i is query row i >> by, head i & by
     const Waits wait{reinterpret_cast<volatile int *>(smem + kAbort)};
     const auto bar = [&](uint32_t i) { return sb + kBar + 8 * i; };
     const auto grid_wait = [] {
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!a.early) grid_wait();
     if (warp == 0) {
-        const Start s = find_start(a, worker, rows_a_block, blockIdx.x == 0 ? &g_status : nullptr);
+        const Start s = find_start(a, worker, blockIdx.x == 0 ? &g_status : nullptr);
         if (lane == 0) *reinterpret_cast<Start *>(smem + kStart) = s;
     } else if (warp == kProducer && lane == 0) {
         for (uint32_t i = 0; i < kBars; ++i)
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lo = (int)min(worker * (long long)per, (long long)total), hi = min(lo + per, total);
     if (head == 0)
         for (int b = worker; b < a.batch; b += a.workers) zero_rows(a, request_of(a, b, nullptr), threadIdx.x, kThreads);
-    Walk w(a, start, lo, hi, rows_a_block);
+    Walk w(a, start, lo, hi);
     int pieces = 0, jobs = 0;  // whose copies the producer has asked for
 
     if (warp == kProducer) {
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Info &info = *reinterpret_cast<const Info *>(smem + kInfo);
             wait(bar(kInfoFull), job & 1);
             const bool holes = info.bad;  // then each tile looks which of its pages are there
-            const uint64_t seen = drafted && row / a.group < r.rows ? info.seen[row / a.group] : 0;
+            const uint64_t seen = drafted && (row >> by) < r.rows ? info.seen[row >> by] : 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kInfoFree));
             constexpr int kPages = kKeys / kPage;
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int slot = 2 * worker + (w.at > lo);
             const size_t part = ((size_t)slot * a.hkv + head) * 128 + row;
             const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : sum;
-            uint16_t *dst = a.out + ((size_t)(r.first + w.block * rows_a_block + row / a.group) * a.hq + head * a.group + row % a.group) * 128;
+            uint16_t *dst = a.out + ((size_t)(r.first + w.block * rows_a_block + (row >> by)) * a.hq + head * a.group + (row & by)) * 128;
             const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
             for (int c = 0; c < kKeys / 32; ++c) {
