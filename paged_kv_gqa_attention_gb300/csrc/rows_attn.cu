@@ -409,6 +409,10 @@ struct Merge {
     }
 };
 
+// item / rows for fewer than 2^12 of each: half a row more keeps the quotient
+// 2^-13 from a whole number, the approximate division is within 2^-21 of it.
+__device__ __forceinline__ int head_of(const Split &s, int item) { return (int)__fdividef((float)item + 0.5f, (float)s.rows); }
+
 // Merges row `item` (a head's rows in turn) of worker w's split over the
 // partials first, first + by, .., in this order, four loads in flight.  Two
 // rows of three, or three CTAs an SM, were no faster: 32 requests of eight
@@ -416,7 +420,8 @@ struct Merge {
 __device__ __forceinline__ Merge merge_item(const RowsArgs &a, const Split &s, int w, int item, int first, int by) {
     constexpr int kFlight = 4;
     const int lane = threadIdx.x & 31;
-    const size_t row = (size_t)(item / s.rows) * a.block_rows + item % s.rows;
+    const int head = head_of(s, item);
+    const size_t row = (size_t)head * a.block_rows + (item - head * s.rows);
     Merge g;
     for (int i = first; i < s.count; i += kFlight * by) {
         float2 ml[kFlight];
@@ -436,9 +441,9 @@ __device__ __forceinline__ Merge merge_item(const RowsArgs &a, const Split &s, i
 }
 
 __device__ __forceinline__ void store_item(const RowsArgs &a, const Split &s, int item, const Merge &g) {
-    const int head = item / s.rows, row = item % s.rows;
+    const int head = head_of(s, item), row = item - head * s.rows, by = a.group - 1;  // group is 1 or 2
     const float inv = g.sum > 0.f ? 1.f / g.sum : g.sum;
-    uint16_t *dst = a.out + ((size_t)(s.out_row + row / a.group) * a.hq + head * a.group + row % a.group) * 128;
+    uint16_t *dst = a.out + ((size_t)(s.out_row + (row >> by)) * a.hq + head * a.group + (row & by)) * 128;
     reinterpret_cast<uint2 *>(dst)[threadIdx.x & 31] =
         make_uint2(pack_bf16x2(g.acc.x * inv, g.acc.y * inv), pack_bf16x2(g.acc.z * inv, g.acc.w * inv));
 }

@@ -74,7 +74,7 @@ constexpr uint32_t kBar = kRing + kSlots * kQBytes;
 enum : uint32_t { kQFull, kQEmpty = kQFull + 2, kFull = kQEmpty + 2, kSFull = kFull + kSlots,
                   kPFull = kSFull + kBufs, kDone = kPFull + kBufs, kOFull = kDone + kBufs,
                   kInfoFull, kInfoFree, kDrained, kBars };
-constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 24;
+constexpr uint32_t kTmem = kBar + 8 * kBars, kAbort = kTmem + 4, kStart = kAbort + 4, kStats = kStart + 32;
 // What the scout finds of a job.
 struct Info {
     uint64_t seen[64];  // the drafted rows that a row sees (bit j: row j)
@@ -95,6 +95,7 @@ constexpr int kSwitch = 3;
 struct Start {
     int total, b, base;   // base: the places before request b
     int first, end, past; // request b's numbers
+    int per;              // places a worker
 };
 __device__ __forceinline__ int block_shift(const RowsArgs &a) { return 8 - a.group; }  // a block is 128 / group rows, group 1 or 2
 __device__ __forceinline__ int places_of(int tiles, int rows, int shift) {
@@ -112,9 +113,9 @@ __device__ __forceinline__ Start find_start(const RowsArgs &a, int worker, unsig
         if (b < 32) first = v;
         sum += v;
     }
-    Start s = {__reduce_add_sync(kAll, sum), 0, 0, 0, 0, 0};
-    const int per = (s.total + a.workers - 1) / a.workers;
-    const long long lo = (long long)worker * per;
+    Start s = {__reduce_add_sync(kAll, sum), 0, 0, 0, 0, 0, 0};
+    s.per = (s.total + a.workers - 1) / a.workers;
+    const long long lo = (long long)worker * s.per;
     if (lo >= s.total) return s;
     for (int begin = 0, carry = 0; begin < a.batch; begin += 32) {
         const int b = begin + lane;
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kTmem);
     const Start start = *reinterpret_cast<const Start *>(smem + kStart);
-    const int total = start.total, per = (total + a.workers - 1) / a.workers;
+    const int total = start.total, per = start.per;
     const int lo = (int)min(worker * (long long)per, (long long)total), hi = min(lo + per, total);
     if (head == 0)
         for (int b = worker; b < a.batch; b += a.workers) zero_rows(a, request_of(a, b, nullptr), threadIdx.x, kThreads);
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return __ballot_sync(kAll, id >= 0 && id < a.num_pages) & ((1u << kPages) - 1);
             };
             float m = -INFINITY, l = 0.f;
-            bool odd = false;
+            bool odd = false, agreed = false;
             for (int t = w.t0; t < w.t1; ++t, ++n) {
                 const uint32_t ok = holes ? pages_of(t) : (1u << kPages) - 1;
                 const uint32_t s = tmem + buf * kTile + h * kKeys + lanes;
@@ -503,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
                 // one reference a row, for all parts: where a row's moves, they agree on the largest maximum
                 float alpha = 1.f;
-                if (any_of_rows(mx > m + kSlack)) {
+                agreed = any_of_rows(mx > m + kSlack);
+                if (agreed) {
                     stats[h * 128] = mx;
                     named_barrier(1, kRows);
                     float top = stats[0];
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(bar(kPFull + buf));
                 if (++buf == kBufs) buf = 0, phase ^= 1;
             }
-            named_barrier(1, kRows);  // maxima that were exchanged have been read
+            if (agreed) named_barrier(1, kRows);  // the last tile's maxima have been read
             stats[h * 128] = l;
             const bool any_odd = any_of_rows(odd);  // all parts' sums are there too
             float sum = 0.f;
