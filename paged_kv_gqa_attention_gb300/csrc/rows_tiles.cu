@@ -429,9 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t *table = a.page_table + (size_t)w.b * a.max_pages;
             const int end = min(w.t1 * (kTile / kPage), (w.r.keys + kPage - 1) / kPage);
             bool bad = false;
-            for (int j = w.t0 * (kTile / kPage) + lane; j < end; j += 32) {
-                const int id = table[j];
-                bad |= id < 0 || id >= a.num_pages;
+            for (int j = w.t0 * (kTile / kPage) + lane; j < end; j += 8 * 32) {
+                int id[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) id[x] = j + 32 * x < end ? table[j + 32 * x] : 0;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) bad |= id[x] < 0 || id[x] >= a.num_pages;
             }
             bad = __any_sync(kAll, bad);
             uint64_t seen[2] = {0, 0};
@@ -452,10 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21, t_o = tmem + kColO + h * kKeys + lanes;  // of O, the part's share of the dims
         float *stats = reinterpret_cast<float *>(smem + kStats) + row;  // [part][row]
         int n = 0, job = 0, buf = 0, phase = 0;
-        while (w.next()) {
-            const Request &r = w.r;
+        for (bool more = w.next(); more; ++job) {
+            const Request r = w.r;
+            const int t0 = w.t0, t1 = w.t1;
             const int32_t *table = a.page_table + (size_t)w.b * a.max_pages;
-            const bool drafted = a.tree && w.t1 * kTile > r.past;
+            const bool drafted = a.tree && t1 * kTile > r.past;
             const Info &info = *reinterpret_cast<const Info *>(smem + kInfo);
             wait(bar(kInfoFull), job & 1);
             const bool holes = info.bad;  // then each tile looks which of its pages are there
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             float m = -INFINITY, l = 0.f;
             bool odd = false, agreed = false;
-            for (int t = w.t0; t < w.t1; ++t, ++n) {
+            for (int t = t0; t < t1; ++t, ++n) {
                 const uint32_t ok = holes ? pages_of(t) : (1u << kPages) - 1;
                 const uint32_t s = tmem + buf * kTile + h * kKeys + lanes;
                 wait(bar(kSFull + buf), phase);
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float next = top > m + kSlack ? top : m;
                     alpha = next == m ? 1.f : exp2_approx(m - next);
                     m = next;
-                    if (t > w.t0 && __any_sync(kAll, alpha != 1.f)) {
+                    if (t > t0 && __any_sync(kAll, alpha != 1.f)) {
                         // P V of the tile before has written O, of which each part scales its share of the dims
                         wait(bar(kDone + (buf == 0 ? kBufs - 1 : buf - 1)), buf == 0 ? phase ^ 1 : phase);
                         __syncwarp();
@@ -555,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Slots that hold no key (or were not loaded) are zeroed, and of drafted values what is not finite, so
                     // that a probability of 0 meets nothing that it would not cancel; rows that see such a value get it at
                     // the end.
-                    const int piece = 2 * (n - (t - w.t0)) + v_piece(t - w.t0, w.t1 - w.t0), v_slot = piece % kSlots;
+                    const int piece = 2 * (n - (t - t0)) + v_piece(t - t0, t1 - t0), v_slot = piece % kSlots;
                     wait(bar(kFull + v_slot), piece / kSlots & 1);
                     constexpr int kEach = 128 / kKeys, kChunks = 16 / kEach;  // threads of a key, 16-byte pieces of a thread
                     const int key = row / kEach, piece0 = row % kEach * kChunks, pos = key0 + key;
@@ -590,16 +594,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             float sum = 0.f;
 #pragma unroll
             for (int x = 0; x < kParts; ++x) sum += stats[x * 128];
+            // each part's warps give their share of the dims
+            const bool whole = t0 == 0 && t1 == w.tiles;
+            const int left = (r.rows - w.block * rows_a_block) * a.group;  // rows from this block's first on
+            const int q_row = r.first + w.block * rows_a_block, slot = 2 * worker + (w.at > lo);
+            more = w.next();  // while the last P V runs
             wait(bar(kOFull), job & 1);
             __syncwarp();
             tc::fence_after();
-            // each part's warps give their share of the dims
-            const bool whole = w.t0 == 0 && w.t1 == w.tiles;
-            const int left = (r.rows - w.block * rows_a_block) * a.group;  // rows from this block's first on
-            const int slot = 2 * worker + (w.at > lo);
             const size_t part = ((size_t)slot * a.hkv + head) * 128 + row;
             const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : sum;
-            uint16_t *dst = a.out + ((size_t)(r.first + w.block * rows_a_block + (row >> by)) * a.hq + head * a.group + (row & by)) * 128;
+            uint16_t *dst = a.out + ((size_t)(q_row + (row >> by)) * a.hq + head * a.group + (row & by)) * 128;
             const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
             for (int c = 0; c < kKeys / 32; ++c) {
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] *= inv;
                 if (any_odd) {
-                    for (int pos = max(r.past, w.t0 * kTile); pos < min(r.keys, w.t1 * kTile); ++pos) {
+                    for (int pos = max(r.past, t0 * kTile); pos < min(r.keys, t1 * kTile); ++pos) {
                         const int id = table[pos >> 4];
                         if (id < 0 || id >= a.num_pages || !(seen >> (pos - r.past) & 1)) continue;
                         const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_pages + (((size_t)id * kPage + (pos & 15)) * a.hkv + head) * 128 + dim);
@@ -642,7 +647,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!whole && h == 0 && row < left) *reinterpret_cast<float2 *>(a.ml + 2 * part) = make_float2(m, sum);
             tc::fence_before();  // before the next job's P is handed over
-            ++job;
         }
     }
     __syncthreads();
