@@ -38,13 +38,15 @@
 // tile), two blocks of rows for each tile's K and V (1.38), pairs of workers on
 // two blocks of a request, which halve what is read from HBM (8 requests of 448
 // rows over 8000 states 313 us against 265; an odd block idles a worker).
-// 24 requests of 33 to 64 rows over 500 to 8000 positions: 92.5 us, 5.0 TB/s,
+// 24 requests of 33 to 64 rows over 500 to 8000 positions: 89 us, 5.2 TB/s,
 // floor 68.6 us by their bytes.  32 requests of 9 to 16 rows over 200 to 2000:
-// 39.5 us, floor 21.8: jobs are a few tiles long, and each costs 2 to 4 us
+// 36.7 us, floor 21.8: jobs are a few tiles long, and each costs 2 to 4 us
 // beside them (the last tile waits for V, then O is given back); four parts or
 // two of 64 keys there: 44.0 and 45.1 us before that.  8 requests of 100 to 448
 // rows over 2000 to 15600 states: 224 us, where K and V are read again for each
-// 64 rows, 1.33 GB.
+// 64 rows, 1.33 GB at 6.4 TB/s.  Putting a job's end off until the next one's
+// first P is there costs registers in the loop: 45.5 us for the second of these
+// calls, against 39.4 at the time.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -135,6 +135,21 @@ def test_largest_batch(rows):
     c.check(c.call())
 
 
+@pytest.mark.parametrize("kind, most, group", [("tree", 8, 2), ("tree", 16, 1), ("tree", 64, 2), ("cross", 300, 2), ("cross", 300, 1)])
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_mixed_lengths(kind, most, group, seed):
+    """Lengths at the borders of pages and tiles between long ones and none at all, so that ranges of workers begin and
+    end on, before and behind a job's first and last tile."""
+    rng = np.random.default_rng(seed)
+    border = [0, 1, 15, 16, 17, 127, 128, 129, 255, 256, 257, 400]
+    n = int(rng.integers(20, 60))
+    keys = [int(rng.choice(border)) if rng.random() < 0.8 else int(rng.integers(300, 3000)) for _ in range(n)]
+    rows = [int(rng.choice([0, 1, most, int(rng.integers(1, most + 1))])) for _ in range(n)]
+    rows[0] = most
+    c = Case(100 + seed, rows, keys, 4 * group, 4, kind)
+    c.check(c.call())
+
+
 @pytest.mark.parametrize("rows", [8, 32, 64])
 def test_deep_and_flat_trees(rows):
     for parents in ([-1] * rows, [-1] + [0] * (rows - 1), [i - 1 for i in range(rows)], [i // 2 - 1 if i < 2 else (i - 1) // 2 for i in range(rows)]):
