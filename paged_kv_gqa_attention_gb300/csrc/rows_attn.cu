@@ -45,7 +45,8 @@ __device__ unsigned int g_status;
 constexpr int kPage = 16;
 constexpr int kMaxStages = 8;
 constexpr float kSlack = 8.f;
-constexpr int kMergeThreads = 256, kMergeCtas = 2;  // CTAs: an SM
+constexpr int kMergeThreads = 512;  // of all CTAs of the merge on an SM
+constexpr int kManyParts = 8;       // partials above which a CTA merges a row together
 constexpr int kFewEach = 5, kMaxWorkers = 32 * 20;  // workers of a lane of the merge, and all
 
 // Bytes of a stage: K and V of one page, each two halves of 64 dims.
@@ -448,9 +449,10 @@ __device__ __forceinline__ void store_item(const RowsArgs &a, const Split &s, in
         make_uint2(pack_bf16x2(g.acc.x * inv, g.acc.y * inv), pack_bf16x2(g.acc.z * inv, g.acc.w * inv));
 }
 
-// A row of many partials by a CTA, whose warps take every eighth.
+// A row of many partials by a CTA, whose warps take them in turn.
+template <int THREADS>
 __device__ __forceinline__ void merge_by_cta(const RowsArgs &a, const Split &s, int w, int item) {
-    constexpr int kWarps = kMergeThreads / 32;
+    constexpr int kWarps = THREADS / 32;
     __shared__ float4 s_acc[kWarps][32];
     __shared__ float2 s_ml[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -468,10 +470,18 @@ __device__ __forceinline__ void merge_by_cta(const RowsArgs &a, const Split &s, 
 
 // The merge of both kernels' splits: every warp sums up the steps that all
 // splits take, EACH workers a lane, and the CTAs take them in turn.
-template <int EACH>
-__global__ void __launch_bounds__(kMergeThreads, kMergeCtas) merge_rows_kernel(const __grid_constant__ RowsArgs a) {
+//
+// CTAs of 128 threads find room beside the kernel for few rows, and wait there
+// for its end; of 256, a row of very many partials takes fewer rounds.  128 and
+// 256 threads, 8 rows a request, 16 heads on 8: 32 requests of 1100 positions
+// 34.2 and 35.9 us, 16 of 300 13.2 and 15.3, 4 of 500 11.2 and 12.1, 1 of 257
+// 9.7 and 9.4, 1 of 4000 14.3 and 12.1; 2 heads on 1: 64 of 1100 19.6 and 20.8,
+// 1 of 4000 20.8 and 16.3.  Behind the kernel for many rows, which has few
+// workers: 1 request of 64 rows over 8000 17.4 and 19.0.
+template <int EACH, int THREADS>
+__global__ void __launch_bounds__(THREADS, kMergeThreads / THREADS) merge_rows_kernel(const __grid_constant__ RowsArgs a) {
     constexpr unsigned kAll = 0xffffffffu;
-    constexpr int kWarps = kMergeThreads / 32;
+    constexpr int kWarps = THREADS / 32;
     grid_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int steps[EACH], mine = 0;
@@ -482,7 +492,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas) merge_rows_kernel(c
         if (w < a.workers) {
             const Split s = a.splits[w];
             const int n = s.rows * a.hkv;
-            steps[x] = s.count == 0 ? 0 : s.count <= kWarps ? (n + kWarps - 1) / kWarps : n;
+            steps[x] = s.count == 0 ? 0 : s.count <= kManyParts ? (n + kWarps - 1) / kWarps : n;
         }
         mine += steps[x];
     }
@@ -505,8 +515,8 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas) merge_rows_kernel(c
         }
         w = __shfl_sync(kAll, w, l), begin = __shfl_sync(kAll, begin, l);
         const Split s = a.splits[w];
-        if (s.count > kWarps) {
-            merge_by_cta(a, s, w, step - begin);
+        if (s.count > kManyParts) {
+            merge_by_cta<THREADS>(a, s, w, step - begin);
         } else {
             const int item = (step - begin) * kWarps + warp;
             if (item < s.rows * a.hkv) store_item(a, s, item, merge_item(a, s, w, item, 0, 1));
@@ -663,10 +673,15 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
         e = launch_rows_tiles(a, tq, tk, tv, stream);
     }
     if (e != cudaSuccess) return e;
-    cfg.blockDim = dim3(kMergeThreads);
+    const int threads = plan.few && plan.workers > 16 * x.batch ? 256 : 128;  // workers of a request on average: many partials a row, or not
+    const bool small = plan.workers <= 32 * kFewEach;
+    constexpr int kEach = kMaxWorkers / 32;
+    const auto merge = threads == 256 ? (small ? merge_rows_kernel<kFewEach, 256> : merge_rows_kernel<kEach, 256>)
+                                      : (small ? merge_rows_kernel<kFewEach, 128> : merge_rows_kernel<kEach, 128>);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = 0;
-    cfg.gridDim = dim3((unsigned)(kMergeCtas * sm_count()));
-    return cudaLaunchKernelEx(&cfg, plan.workers <= 32 * kFewEach ? merge_rows_kernel<kFewEach> : merge_rows_kernel<kMaxWorkers / 32>, a);
+    cfg.gridDim = dim3((unsigned)(kMergeThreads / threads * sm_count()));
+    return cudaLaunchKernelEx(&cfg, merge, a);
 }
 
 unsigned int status_read_clear_rows_attn(cudaStream_t stream, cudaError_t *err) {
