@@ -120,15 +120,16 @@ __device__ __forceinline__ Place place_of(const AppendArgs &a, long long t, int 
                 return -1;
             };
             const int up_low = checked(low, max(base + lane, 0)), up_high = checked(high, base + 32 + lane);
-            depth = -1;
-            for (int node = i; node >= 0; ++depth) {
-                if (node >= base) {
-                    const int x = __shfl_sync(kAll, up_low, (node - base) & 31), y = __shfl_sync(kAll, up_high, (node - base) & 31);
-                    node = node - base < 32 ? x : y;
-                } else {
-                    node = checked(a.parents[first + node], node);
-                }
+            // numbered from `base`, 64 where the walk leaves the rows at hand: a shuffle a step
+            const uint32_t both = (uint32_t)(up_low >= base ? up_low - base : 64) | (uint32_t)(up_high >= base ? up_high - base : 64) << 8;
+            int at = i - base;
+            for (depth = 0;; ++depth) {
+                const uint32_t w = __shfl_sync(kAll, both, at & 31), up = at < 32 ? w & 0xffu : w >> 8;
+                if (up == 64) break;
+                at = (int)up;
             }
+            const int x = __shfl_sync(kAll, up_low, at & 31), y = __shfl_sync(kAll, up_high, at & 31);
+            for (int node = at < 32 ? x : y; node >= 0; ++depth) node = checked(a.parents[first + node], node);
         }
         const long long pos = past + depth;
         p.pos = lane == 0 ? (pos < kMaxPos ? (int)pos : kMaxPos) : 0;
