@@ -395,14 +395,16 @@ __global__ void __launch_bounds__(288, 1)
     }
 }
 
-// A running merge of partials: the lane's four dims of one row.
+// A running merge of partials: the lane's four dims of one row.  The maxima
+// pass over NaN, so that a worker whose scores of a row were all NaN leaves
+// -inf beside a sum of NaN, as one that saw no key leaves it beside zeros:
+// equal maxima, -inf too, have the weight 1, and every sum is taken.
 struct Merge {
     float m = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     __device__ void add(float2 ml, float4 v) {
         const float next = fmaxf(m, ml.x);
-        if (next == -INFINITY) return;  // a worker that saw no key of this row
-        const float old = m == -INFINITY ? 0.f : exp2_approx(m - next), now = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - next);
+        const float old = m == next ? 1.f : exp2_approx(m - next), now = ml.x == next ? 1.f : exp2_approx(ml.x - next);
         sum = sum * old + ml.y * now;
         acc.x = acc.x * old + v.x * now, acc.y = acc.y * old + v.y * now;
         acc.z = acc.z * old + v.z * now, acc.w = acc.w * old + v.w * now;
