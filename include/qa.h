@@ -712,9 +712,13 @@ size_t qa_rows_attn_workspace_size(int max_rows, const qa_attn_params *params);
  *   out        bf16 [total_rows][n_q_heads][128], packed
  *
  * Slots past n_past[r] + rows may hold anything, NaN included, and so may
- * the keys and values of rows that are not a row's ancestors.  A visible
- * infinity gives an infinity or NaN.  Scores, softmax and sums are fp32;
- * probabilities enter the product with V as two bf16 terms (about 16 bits).
+ * the keys and values of rows that are not a row's ancestors.  Of what a row
+ * sees: a score of -inf has the weight 0, and a row with such scores only has
+ * zeros, as one without keys has; a score of +inf or NaN (a NaN or opposed
+ * infinities in q or a key) makes the row's head NaN; an infinity in a value
+ * gives an infinity or NaN in its dim, a NaN a NaN.  Scores, softmax and sums
+ * are fp32; probabilities enter the product with V as two bf16 terms (about
+ * 16 bits).
  * Device checks: a request with more than max_rows rows, n_past < 0 or
  * n_past + rows beyond its page-table row has zero rows in out
  * (QA_DEVICE_BAD_LENGTH); pages outside [0, num_pages) are left out
