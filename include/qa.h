@@ -753,7 +753,9 @@ qa_status qa_cross_attn(const void *q, long long ldq, const int32_t *cu_seqlens,
  *              rows)
  *   k_pages, v_pages  HOST arrays of n_layers device pointers (0..64 layers):
  *              in each pool, the row at n_past + path[j] is copied to
- *              n_past + j; other slots keep what they hold
+ *              n_past + j; other slots keep what they hold.  A pool that
+ *              stands there more than once (layers that share a cache) is
+ *              settled once; pools that overlap otherwise are refused
  *
  * parents, cu_seqlens, n_past, page_table, max_rows (1..64) as in
  * qa_tree_attn; the outputs may not overlap the inputs.  n_past is not

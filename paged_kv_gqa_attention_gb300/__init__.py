@@ -811,9 +811,9 @@ def qa_tree_accept(draft, target, parents, cu_seqlens, n_past, page_table, k_pag
     first row whose parent is accepted and whose token (draft int32 [T]) is
     the one the model chose there (target int32 [T]) is accepted too, and the
     accepted rows are moved in every pool to n_past and on.  k_pages and
-    v_pages: lists of the layers' pools (up to 64, of one shape).  Returns
-    (n_accepted int32 [B], path int32 [B,max_rows] with -1 behind it,
-    next_token int32 [B])."""
+    v_pages: lists of the layers' pools (up to 64, of one shape; a pool that
+    layers share may stand there several times).  Returns (n_accepted int32
+    [B], path int32 [B,max_rows] with -1 behind it, next_token int32 [B])."""
     return _done("qa_tree_accept", _fast().tree_accept(
         draft, target, parents, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, n_accepted, path, next_token,
         stream, debug_checks, stable_metadata))

@@ -143,8 +143,9 @@ unsigned int status_read_clear_rows_attn(cudaStream_t stream, cudaError_t *err);
 constexpr int kAcceptMaxLayers = 64;
 struct TreeAccept {
     const int32_t *draft, *target, *parents, *cu_seqlens, *n_past, *page_table;
-    int batch, rows, max_rows, n_layers;
-    void *const *k_pages, *const *v_pages;
+    int batch, rows, max_rows;
+    void *const *pools;  // of all layers, keys and values; no two overlap
+    int n_pools;
     int32_t *n_accepted, *path, *next_token;
 };
 cudaError_t launch_tree_accept(const TreeAccept &x, const qa_attn_params &p, cudaStream_t stream);

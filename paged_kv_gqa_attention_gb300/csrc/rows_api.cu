@@ -4,6 +4,9 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <functional>
+
 #include "api_checks.h"
 #include "qa.h"
 #include "qa_internal.h"
@@ -147,9 +150,18 @@ QA_API qa_status qa_tree_accept(const int32_t *draft, const int32_t *target, con
         if (!k_pages[i] || !v_pages[i]) return invalid(fn, "NULL tensor pointer");
         if (!aligned(k_pages[i], 16) || !aligned(v_pages[i], 16)) return invalid(fn, "tensors must be 16-byte aligned");
     }
+    // Each pool once, in the order of their addresses: two CTAs that move a pool's rows in place would read one another's.
+    void *pools[2 * qa::kAcceptMaxLayers];
+    for (int i = 0; i < n_layers; ++i) pools[2 * i] = k_pages[i], pools[2 * i + 1] = v_pages[i];
+    std::sort(pools, pools + 2 * n_layers, std::less<void *>());
+    const int n_pools = (int)(std::unique(pools, pools + 2 * n_layers) - pools);
+    const uintptr_t bytes = (uintptr_t)p->num_pages * p->page_size * p->n_kv_heads * p->head_dim * sizeof(uint16_t);
+    for (int i = 1; i < n_pools; ++i)
+        if (reinterpret_cast<uintptr_t>(pools[i]) - reinterpret_cast<uintptr_t>(pools[i - 1]) < bytes)
+            return invalid(fn, "two pools overlap without being the same");
     cudaStream_t stream = static_cast<cudaStream_t>(p->stream);
-    const qa::TreeAccept x{draft, target, parents, cu_seqlens, n_past, page_table, batch, total_rows, max_rows, n_layers,
-                           k_pages, v_pages, n_accepted, path, next_token};
+    const qa::TreeAccept x{draft, target, parents, cu_seqlens, n_past, page_table, batch, total_rows, max_rows, pools,
+                           n_pools, n_accepted, path, next_token};
     st = launched(qa::launch_tree_accept(x, *p, stream), fn);
     if (st != QA_STATUS_OK || !p->debug_checks) return st;
     cudaError_t e;

@@ -137,11 +137,8 @@ cudaError_t launch_tree_accept(const TreeAccept &x, const qa_attn_params &p, cud
     a.num_pages = p.num_pages;
     a.row_chunks = p.n_kv_heads * 16;
     a.early = (p.abi_version >= 2 && p.stable_metadata >= 1) ? 1 : 0;
-    a.n_pools = 2 * x.n_layers;
-    for (int i = 0; i < x.n_layers; ++i) {
-        a.pools[2 * i] = static_cast<uint4 *>(x.k_pages[i]);
-        a.pools[2 * i + 1] = static_cast<uint4 *>(x.v_pages[i]);
-    }
+    a.n_pools = x.n_pools;
+    for (int i = 0; i < x.n_pools; ++i) a.pools[i] = static_cast<uint4 *>(x.pools[i]);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -136,6 +136,16 @@ def test_accept_refuses():
     refused(accept(layers=2, kp=(0x1000, 0x1000), vp=(0x1000, 0x1008)), "aligned")
 
 
+def test_accept_refuses_pools_that_overlap():
+    """A pool may be listed several times (layers that share a cache); another one that begins inside it may not."""
+    pages = 3
+    size = pages * 16 * 8 * 128 * 2
+    p = params(num_pages=pages)
+    a = 1 << 30
+    for kp, vp in (((a,), (a + 16,)), ((a,), (a + size - 16,)), ((a, a + 2 * size), (a, a + size + 256)), ((a, a + size), (a - 16, a - size))):
+        refused(accept(layers=len(kp), kp=kp, vp=vp, p=p), "overlap")
+
+
 def test_python_checks():
     torch = pytest.importorskip("torch")
     rows = torch.zeros(4, 8, 128, dtype=torch.bfloat16)

@@ -87,6 +87,31 @@ def test_sixty_four_layers_and_every_head_count():
         c.check(c.call())
 
 
+@pytest.mark.parametrize("batch, layers", [(2, 2), (80, 64)])
+def test_a_pool_listed_several_times_is_settled_once(batch, layers):
+    """Layers that share a cache, and keys and values in one pool.  With 80 requests of 64 layers the CTAs of a pool's
+    later mentions start when those of its first are done."""
+    rows = [24] * batch
+    c = Case(10, rows, [5] * batch, 3, 2)
+    keep = np.arange(24) % 3 != 1  # every path leaves rows out, so that it moves them
+    keep[0] = True
+    last = np.maximum.accumulate(np.where(keep, np.arange(24), 0))
+    one = np.where(np.arange(24) > 0, np.concatenate(([0], last[:-1])), -1)
+    c.parents = np.tile(one, batch).astype(np.int32)
+    tokens = np.where(keep, 1, 2)
+    c.draft = np.tile(tokens, batch).astype(np.int32)
+    c.target = np.ones(24 * batch, np.int32)
+    c.dev = [[to_dev(p) for p in side] for side in c.pools]
+    (a, b, _), (d, e, _) = c.dev
+    ks, vs = ([a, b, a, a] * layers)[:layers], ([d, a, b, e] * layers)[:layers]
+    got = qa.qa_tree_accept(to_dev(c.draft), to_dev(c.target), to_dev(c.parents), to_dev(c.cu), to_dev(np.array(c.past, np.int32)),
+                            to_dev(c.table), ks, vs, 24, debug_checks=True)
+    c.dev = [[a, b], [d, e if layers > 3 else d]]
+    c.pools = [c.pools[0][:2], [c.pools[1][0], c.pools[1][1] if layers > 3 else c.pools[1][0]]]
+    paths = c.check(got)
+    assert paths == [list(np.nonzero(keep)[0])] * batch
+
+
 def test_ties_go_to_the_first_row():
     c = Case(1, [6], [5], 1)
     c.parents = np.array([-1, 0, 0, 0, 2, 2], np.int32)
