@@ -723,10 +723,11 @@ size_t qa_rows_attn_workspace_size(int max_rows, const qa_attn_params *params);
  * n_past + rows beyond its page-table row has zero rows in out
  * (QA_DEVICE_BAD_LENGTH); pages outside [0, num_pages) are left out
  * (QA_DEVICE_BAD_PAGE); rows of malformed segments are not written
- * (QA_DEVICE_BAD_SEGMENTS).  Supported: batch up to 1024, head_dim 128,
- * page_size 16, n_kv_heads in [1, 8], n_q_heads / n_kv_heads in {1, 2}; needs
- * params->workspace of qa_rows_attn_workspace_size().  stable_metadata >= 1
- * covers cu_seqlens, n_past, parents and page_table (2 acts as 1). */
+ * (QA_DEVICE_BAD_SEGMENTS).  Supported: batch up to 1024, max_pages_per_seq
+ * up to 2^27 - 8, head_dim 128, page_size 16, n_kv_heads in [1, 8],
+ * n_q_heads / n_kv_heads in {1, 2}; needs params->workspace of
+ * qa_rows_attn_workspace_size().  stable_metadata >= 1 covers cu_seqlens,
+ * n_past, parents and page_table (2 acts as 1). */
 qa_status qa_tree_attn(const void *q, long long ldq, const int32_t *cu_seqlens, const int32_t *n_past,
                        const int32_t *parents, int batch, int total_rows, int max_rows, const int32_t *page_table,
                        const void *k_pages, const void *v_pages, void *out, const qa_attn_params *params);

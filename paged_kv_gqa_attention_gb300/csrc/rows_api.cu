@@ -17,6 +17,7 @@ using namespace qa::checks;
 
 constexpr int kMaxRows = 1 << 30;
 constexpr int kMaxPoolPages = (1 << 27) - 1;  // token slots are coordinates of 31 bits
+constexpr int kMaxSeqPages = (1 << 27) - 8;   // positions and the ends of their tiles of 128 are counted in 31 bits
 constexpr long long kMaxTiles = 1LL << 30;    // a call's key tiles are numbered in 32 bits
 
 // What every call with packed rows, their requests and pages has.
@@ -47,6 +48,8 @@ qa_status attn_entry(const char *fn, const qa::RowsAttn &x, const qa_attn_params
     if ((st = check_stride(fn, "ldq", x.ldq, (long long)p->n_q_heads * p->head_dim)) != QA_STATUS_OK) return st;
     if (p->num_pages > kMaxPoolPages)
         return reject(QA_STATUS_INVALID_PARAMS, "%s: num_pages %d above %d", fn, p->num_pages, kMaxPoolPages);
+    if (p->max_pages_per_seq > kMaxSeqPages)
+        return reject(QA_STATUS_INVALID_PARAMS, "%s: max_pages_per_seq %d above %d", fn, p->max_pages_per_seq, kMaxSeqPages);
     // rows of a request in blocks of at least 64
     const long long tiles = (long long)x.batch * p->max_pages_per_seq, blocks = ((long long)x.max_rows + 63) / 64;
     if (tiles > kMaxTiles || tiles * blocks > kMaxTiles)

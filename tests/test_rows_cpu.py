@@ -110,6 +110,15 @@ def test_attention_refuses(fn):
     assert "max_pages_per_seq" not in qa.qa_last_error()
 
 
+@pytest.mark.parametrize("fn", [tree_attn, cross_attn])
+def test_positions_whose_tiles_end_past_31_bits_are_refused(fn):
+    """2^31 - 128 positions end a tile of 128 keys below 2^31; one page more does not."""
+    for pages in (2**27 - 7, 2**27 - 1):
+        refused(fn(batch=1, p=params(max_pages_per_seq=pages)), "above 134217720")
+    assert fn(batch=1, p=params(max_pages_per_seq=2**27 - 8)) in (-1, -3)  # no workspace; without a GPU, no device
+    assert "max_pages_per_seq" not in qa.qa_last_error()
+
+
 def test_row_limits():
     refused(tree_attn(max_rows=65), "[1, 64]")
     refused(accept(max_rows=65), "[1, 64]")
