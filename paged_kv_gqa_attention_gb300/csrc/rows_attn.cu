@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(288, 1)
     const uint32_t half = half_bytes(hkv), stage_size = stage_bytes(hkv);
     const uint32_t full_k = ring + stages * stage_size, full_v = full_k + 8 * kMaxStages, empty = full_v + 8 * kMaxStages;
     int *page_ok = reinterpret_cast<int *>(smem_raw + (empty + 8 * kMaxStages - raw));
-    int *prefix = page_ok + kMaxStages;
+    const Waits wait{page_ok + kMaxStages, &g_status, kWaitLimitNs};
+    int *prefix = page_ok + kMaxStages + 1;
     const int worker = blockIdx.x;
     if (warp == hkv && lane == 0) {
         tc::prefetch_tmap(&tk);
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(288, 1)
     if (warp == 0) {
         count_pages(a, prefix, worker == 0 ? &g_status : nullptr);
         if (lane == 0) {
+            *wait.abort = 0;
             for (int s = 0; s < stages; ++s) {
                 mbar_init(full_k + 8 * s, 1);
                 mbar_init(full_v + 8 * s, 1);
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(288, 1)
             }
             a.splits[worker] = s;
         }
-        int stage = 0, phase = 0;
+        int stage = 0, phase = 0, asked = 0;  // asked: pages whose stages were filled
         for (int b = b0; b <= b_last; ++b) {
             const int p0 = prefix[b] + kSwitch, p1 = prefix[b + 1];
             const int j0 = max(lo, p0) - p0, j1 = min(hi, p1) - p0;
@@ -186,8 +188,9 @@ __global__ void __launch_bounds__(288, 1)
                 const int mine = b == b0 && jb == j0 ? first_ids : jb + lane < j1 ? row[jb + lane] : -1;
                 for (int j = jb; j < min(jb + 32, j1); ++j) {
                     const int id = __shfl_sync(kAll, mine, j - jb);
-                    if (lane == 0) {
-                        mbar_wait(empty + 8 * stage, phase ^ 1, &g_status);
+                    if (lane == 0) wait(empty + 8 * stage, phase ^ 1);
+                    if (lane == 0 && !*wait.abort) {  // else the stage may still be read
+                        ++asked;
                         const bool ok = id >= 0 && id < a.num_pages;
                         page_ok[stage] = ok;
                         if (ok) {
@@ -208,6 +211,12 @@ __global__ void __launch_bounds__(288, 1)
                 }
             }
         }
+        named_barrier(1, blockDim.x);
+        if (lane == 0 && *wait.abort)  // a wait ran out: what is still under way writes shared memory
+            for (int i = max(0, asked - stages); i < asked; ++i) {
+                mbar_wait(full_k + 8 * (i % stages), i / stages & 1, &g_status);
+                mbar_wait(full_v + 8 * (i % stages), i / stages & 1, &g_status);
+            }
         return;
     }
 
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(288, 1)
         for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         for (int j = j0; j < j1; ++j) {
             const uint32_t k = ring + stage * stage_size, v = k + 2 * half;
-            mbar_wait(full_k + 8 * stage, phase, &g_status);
+            wait(full_k + 8 * stage, phase);
             const bool ok = page_ok[stage];
             bool wrote = false;
             if (ok) {
@@ -311,7 +320,7 @@ __global__ void __launch_bounds__(288, 1)
                         hi_p[2 * n + e] = w;
                         lo_p[2 * n + e] = pack_bf16x2(x - bf16lo(w), y - bf16hi(w));
                     }
-                mbar_wait(full_v + 8 * stage, phase, &g_status);
+                wait(full_v + 8 * stage, phase);
                 if (behind < kPage) {
                     // Slots that hold no key are zeroed, and of drafted values what is not finite, so that a probability
                     // of 0 meets nothing that it would not cancel; the rows that see such a value get it at the end.
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(288, 1)
                     mma16816(o[c + 1], lo_p, f[2], f[3]);
                 }
             } else {
-                mbar_wait(full_v + 8 * stage, phase, &g_status);
+                wait(full_v + 8 * stage, phase);
             }
             if (wrote) tc::fence_proxy_async_smem();  // before the next copy into these bytes
             __syncwarp();
@@ -393,6 +402,7 @@ __global__ void __launch_bounds__(288, 1)
             }
         }
     }
+    named_barrier(1, blockDim.x);
 }
 
 // A running merge of partials: the lane's four dims of one row.  The maxima
@@ -664,7 +674,7 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
         const int stages = stages_of(a.hkv);
         cfg.gridDim = dim3((unsigned)plan.workers);
         cfg.blockDim = dim3((a.hkv + 1) * 32);
-        cfg.dynamicSmemBytes = 1024 + stages * stage_bytes(a.hkv) + 3 * 8 * kMaxStages + 4 * kMaxStages + 4 * (x.batch + 1);
+        cfg.dynamicSmemBytes = 1024 + stages * stage_bytes(a.hkv) + 3 * 8 * kMaxStages + 4 * (kMaxStages + 1) + 4 * (x.batch + 1);
         // the most of any call, so that host threads' calls cannot lower one another's
         e = cudaFuncSetAttribute(few_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;

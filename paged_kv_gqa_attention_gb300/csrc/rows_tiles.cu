@@ -183,23 +183,6 @@ struct Walk {
 __device__ __forceinline__ int k_piece(int tile) { return tile == 0 ? 0 : 2 * tile - 1; }
 __device__ __forceinline__ int v_piece(int tile, int tiles) { return tile + 1 < tiles ? 2 * tile + 2 : 2 * tile + 1; }
 
-// Waits that give up: one that runs out ends every later one that would block.
-struct Waits {
-    volatile int *abort;
-    __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return;
-        const unsigned long long t0 = globaltimer_ns();
-        while (!mbar_try_wait(bar, parity)) {
-            if (*abort) return;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
-                atomicOr(&g_status, QA_DEVICE_TIMEOUT);
-                *abort = 1;
-                return;
-            }
-        }
-    }
-};
-
 __device__ __forceinline__ bool any_of_rows(bool x) {  // the threads that own rows
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -260,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.hkv, worker = blockIdx.x / a.hkv;
     const int rows_a_block = 1 << block_shift(a), by = a.group - 1;  // a tile's row i is query row i >> by, head i & by
-    const Waits wait{reinterpret_cast<volatile int *>(smem + kAbort)};
+    const Waits wait{reinterpret_cast<volatile int *>(smem + kAbort), &g_status, kWaitLimitNs};
     const auto bar = [&](uint32_t i) { return sb + kBar + 8 * i; };
     const auto grid_wait = [] {
         asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -31,3 +31,16 @@ def test_expired_wait_is_reported_and_the_context_stays_usable():
     torch.cuda.synchronize()
     ref = oracle.decode(w["q"], w["k_pages"], w["v_pages"], w["page_table"], w["seq_lens"])
     assert_close(f64(out), ref, "decode after an expired wait")
+
+
+def test_waits_of_a_cta_give_up_together():
+    """Three of the check's warps wait eight times each: one limit in all, not eight."""
+    limit = 0.4
+    assert qa.qa_device_status() == 0
+    t0 = time.perf_counter()
+    qa.qa_check_bounded_wait(int(limit * 1e6))
+    bits = qa.qa_device_status()
+    elapsed = time.perf_counter() - t0
+    assert bits == 0x8, f"status bits {bits:#x}"
+    assert 0.95 * limit < elapsed < 2 * limit
+    assert qa.qa_device_status() == 0
