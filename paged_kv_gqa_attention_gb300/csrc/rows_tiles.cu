@@ -69,6 +69,10 @@ constexpr int kThreads = (kScout + 1) * 32;
 constexpr int kSlots = 5;
 constexpr int kBufs = 3;
 constexpr float kSlack = 8.f;
+// The scout waits while its warps work through a whole job: this much longer
+// for each of its tiles, 1.3 us when all is well.  (Every other wait is for a
+// tile's time at most, and ends this one too if it runs out.)
+constexpr unsigned long long kScoutTileNs = 20000;
 constexpr uint32_t kQBytes = 2 * tc::kSubTileBytes;  // two halves of 64 dims of 128 rows; K and V of a tile too
 constexpr uint32_t kAtom = 1024, kGroup = 2 * kAtom;    // of K and V: 8 keys' first 64 dims, then their others
 constexpr uint32_t kRing = 2 * kQBytes;
@@ -410,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kScout) {
         Info &info = *reinterpret_cast<Info *>(smem + kInfo);
+        unsigned tiles_before = 0, tiles_last = 0;  // of the job before the last one, which the warps are at, and of the last
         for (int job = 0; w.next(); ++job) {
             const int32_t *table = a.page_table + (size_t)w.b * a.max_pages;
             const int end = min(w.t1 * (kTile / kPage), (w.r.keys + kPage - 1) / kPage);
@@ -429,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int y = 0; y < 2; ++y) up[y] = lane + 32 * y < w.r.rows ? parent_of(a, w.r.first, lane + 32 * y, &g_status) : -1;
                 ancestors(a, up, seen);
             }
-            wait(bar(kInfoFree), (job & 1) ^ 1);
+            wait(bar(kInfoFree), (job & 1) ^ 1, tiles_before * kScoutTileNs);
+            tiles_before = tiles_last, tiles_last = w.t1 - w.t0;
             info.seen[lane] = seen[0], info.seen[lane + 32] = seen[1];
             if (lane == 0) info.bad = bad;
             __syncwarp();

@@ -471,3 +471,24 @@ def test_one_row_equals_the_decode():
     assert (np.abs(f64(got) - f64(ref)) <= 2 * bound).all()
     cross = qa.qa_cross_attn(to_dev(c.q), to_dev(c.cu), lens, to_dev(c.table), to_dev(c.k), to_dev(c.v), 1, debug_checks=True)
     assert np.array_equal(bits(cross), bits(got))
+
+
+def test_a_job_may_take_longer_than_a_wait():
+    """The last worker of 19 has 1.9 million tiles of the first request, 2.4 s of them, before three jobs of one tile: more
+    than the 2 s that a wait inside the kernel lasts.  512 pages with keys of 0 make up that request again and again, but
+    for its last page, whose keys score 181 more: the others' share is below 2^-230, and the result the mean of 16 values."""
+    long_pages, rows, pages = 18 << 20, [1024, 192], 514
+    rng = np.random.default_rng(80)
+    v = wl.normal_bf16(rng, (pages, 16, 8, 128))
+    k = np.zeros(v.shape, np.float32)
+    k[-2:] = 16.0
+    table = (torch.arange(2 * long_pages, dtype=torch.int32, device="cuda") % (pages - 2)).view(2, long_pages)
+    table[0, -1], table[1, 0] = pages - 2, pages - 1
+    keys = torch.tensor([16 * long_pages, 16], dtype=torch.int32, device="cuda")
+    q = torch.ones(sum(rows), 16, 128, dtype=torch.bfloat16, device="cuda")
+    got = qa.qa_cross_attn(q, to_dev(_rows.cumulative(rows)), keys, table, to_dev(wl.bf16_bits(k)), to_dev(v), max(rows), debug_checks=True)
+    mean = np.repeat(wl.bf16_to_f64(v[-2:]).mean(1), 2, axis=1)  # [request, query head, 128]
+    # probabilities of 1, sums of 16 bf16 values in fp32 and one rounding of the result to bf16
+    bound = 2.0 ** -8 * np.abs(mean) + 2.0 ** -18
+    for part, ref, most in zip(torch.split(got, rows), mean, bound):
+        assert (np.abs(f64(part) - ref) <= most).all()
