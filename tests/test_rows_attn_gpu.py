@@ -312,6 +312,45 @@ def test_bad_pages_lengths_and_segments(kind, rows):
     assert bool((out[int(c.cu[2]):] == 9).all())
 
 
+@pytest.mark.parametrize("kind, most", [("tree", 8), ("tree", 50), ("cross", 8), ("cross", 160)])
+@pytest.mark.parametrize("what", ["begins behind its end", "begins below 0", "ends behind the rows", "all three"])
+def test_malformed_segments_leave_the_others_as_they_are(kind, most, what):
+    """Requests whose segments are well formed, and do not overlap, have their results; every other row stays."""
+    cu = {"begins behind its end": [2 + most, 3, 3 + most, 8 + most], "begins below 0": [-1, 4, 4 + most, 9 + most],
+          "ends behind the rows": [0, most, most + 5, 10 ** 6], "all three": [-7, -3, 5, 2 ** 31 - 1]}[what]
+    total, keys = 2 * most + 12, [300, 77, 129]
+    good = {"begins behind its end": [1, 2], "begins below 0": [1, 2], "ends behind the rows": [0, 1], "all three": []}[what]
+    rng = np.random.default_rng(24)
+    # a case of the good requests alone gives the reference; the call has all three
+    rows = [cu[r + 1] - cu[r] if r in good else 0 for r in range(3)]
+    c = Case(25, rows, keys, 16, 8, kind)
+    ref, bound = c.reference()
+    q = wl.normal_bf16(rng, (total, 16, 128))
+    parents, first = np.full(total, -1, np.int32), 0
+    for r, n in enumerate(rows):
+        if n:
+            q[cu[r]:cu[r] + n] = c.q[first:first + n]
+            if kind == "tree":
+                parents[cu[r]:cu[r] + n] = c.parents[first:first + n]
+        first += n
+    out = torch.full((total, 16, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    args = (to_dev(q), to_dev(np.array(cu, np.int32)), to_dev(np.array(keys, np.int32)), to_dev(c.table), to_dev(c.k), to_dev(c.v), most, out)
+    if kind == "cross":
+        qa.qa_cross_attn(*args)
+    else:
+        qa.qa_tree_attn(*args, parents=to_dev(parents))
+    assert qa.qa_device_status() == 0x4
+    got, owned, first = f64(out), np.zeros(total, bool), 0
+    for r, n in enumerate(rows):
+        if n:
+            at = slice(cu[r], cu[r] + n)
+            owned[at] = True
+            assert (np.abs(got[at] - ref[first:first + n]) <= bound[first:first + n]).all(), r
+        first += n
+    assert (got[~owned] == 9).all()
+    assert owned.sum() == sum(rows)
+
+
 @pytest.mark.parametrize("rows", [[8], [50]])
 def test_bad_parents_count_as_roots(rows):
     c = Case(21, rows, [33], 16, 8, "tree")
