@@ -777,14 +777,15 @@ qa_status qa_tree_accept(const int32_t *draft, const int32_t *target, const int3
 int qa_device_status(void *stream);
 
 /* Exercises the failure path of the kernels' waits without a fault: launches
- * one CTA (asynchronous on `stream`) that waits, through the same bounded
- * waits the attention kernels use, on barriers that nothing ever completes:
- * one wait by itself, and several, one behind another, of which the first to
- * run out ends all.  They give up after limit_us microseconds (1 .. 1000000;
- * the kernels themselves give up after 2 s), set QA_DEVICE_TIMEOUT in the
- * device status word and the kernel ends; the context stays usable.  Read the
- * bit with qa_device_status().  INVALID_PARAMS for a limit outside that range,
- * LAUNCH_FAILED on a launch error. */
+ * two CTAs, one after the other (asynchronous on `stream`), that wait, through
+ * the bounded waits the attention kernels use, on barriers that nothing ever
+ * completes: one of them once, the other several times, where the first wait
+ * to run out ends all.  Each gives up after limit_us microseconds (1 ..
+ * 1000000; the kernels themselves give up after 2 s, or 2 s beyond what a wait
+ * takes when all is well), sets QA_DEVICE_TIMEOUT in the device status word
+ * and ends; the context stays usable.  Read the bit with qa_device_status().
+ * INVALID_PARAMS for a limit outside that range, LAUNCH_FAILED on a launch
+ * error. */
 qa_status qa_check_bounded_wait(unsigned int limit_us, void *stream);
 
 /* Thread-local message describing the last failure on this thread; valid

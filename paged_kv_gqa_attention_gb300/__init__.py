@@ -820,10 +820,10 @@ def qa_tree_accept(draft, target, parents, cu_seqlens, n_past, page_table, k_pag
 
 
 def qa_check_bounded_wait(limit_us=20000, stream=None) -> None:
-    """Launches one CTA whose bounded waits (the ones the kernels use, alone and
-    several that end together) give up after limit_us microseconds on barriers
-    that nothing completes, setting QA_DEVICE_TIMEOUT (read it with
-    qa_device_status); the kernel then ends."""
+    """Launches two CTAs, one after the other, whose bounded waits (the ones the
+    kernels use: one alone, and several that end together) give up after
+    limit_us microseconds each on barriers that nothing completes, setting
+    QA_DEVICE_TIMEOUT (read it with qa_device_status); the kernels then end."""
     _check("qa_check_bounded_wait", _lib.qa_check_bounded_wait(int(limit_us), _stream_ptr(stream)))
 
 

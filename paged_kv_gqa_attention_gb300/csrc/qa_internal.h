@@ -137,6 +137,7 @@ constexpr int kRowsMaxBatch = 1024;  // a call's page counts lie in shared memor
 constexpr int kTreeMaxRows = 64;
 size_t rows_attn_workspace_bytes(int max_rows, int n_q_heads, int n_kv_heads);
 cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float scale, cudaStream_t stream);
+cudaError_t launch_shared_waits_check(unsigned int limit_us, cudaStream_t stream);
 unsigned int status_read_clear_rows_attn(cudaStream_t stream, cudaError_t *err);
 
 // ---- the end of a step of drafted rows (tree_accept.cu)

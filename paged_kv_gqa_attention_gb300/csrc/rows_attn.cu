@@ -536,6 +536,23 @@ __global__ void __launch_bounds__(THREADS, kMergeThreads / THREADS) merge_rows_k
     }
 }
 
+// Three warps wait eight times each on barriers that nothing ever completes:
+// one limit in all, not eight (qa_check_bounded_wait).
+constexpr int kCheckThreads = 96, kCheckBars = 8;
+__global__ void shared_waits_check_kernel(unsigned long long limit_ns) {
+    __shared__ __align__(8) unsigned long long bars[kCheckBars];
+    __shared__ int abort;
+    const uint32_t b = smem_u32(bars);
+    if (threadIdx.x == 0) {
+        abort = 0;
+        for (int i = 0; i < kCheckBars; ++i) mbar_init(b + 8 * i, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const Waits wait{&abort, &g_status, limit_ns};
+    for (int i = 0; i < kCheckBars; ++i) wait(b + 8 * i, 0);
+}
+
 struct Plan {
     bool few;
     int workers, block_rows;
@@ -694,6 +711,11 @@ cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float s
     cfg.dynamicSmemBytes = 0;
     cfg.gridDim = dim3((unsigned)(kMergeThreads / threads * sm_count()));
     return cudaLaunchKernelEx(&cfg, merge, a);
+}
+
+cudaError_t launch_shared_waits_check(unsigned int limit_us, cudaStream_t stream) {
+    shared_waits_check_kernel<<<1, kCheckThreads, 0, stream>>>((unsigned long long)limit_us * 1000ull);
+    return cudaGetLastError();
 }
 
 unsigned int status_read_clear_rows_attn(cudaStream_t stream, cudaError_t *err) {

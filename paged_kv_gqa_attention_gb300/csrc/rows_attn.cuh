@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "qa_internal.h"
+#include "waits.cuh"
 
 namespace qa {
 

@@ -34,7 +34,7 @@ def test_expired_wait_is_reported_and_the_context_stays_usable():
 
 
 def test_waits_of_a_cta_give_up_together():
-    """Three of the check's warps wait eight times each: one limit in all, not eight."""
+    """The check's first CTA waits once, three warps of its second one eight times each: two limits in all, not nine."""
     limit = 0.4
     assert qa.qa_device_status() == 0
     t0 = time.perf_counter()
@@ -42,5 +42,5 @@ def test_waits_of_a_cta_give_up_together():
     bits = qa.qa_device_status()
     elapsed = time.perf_counter() - t0
     assert bits == 0x8, f"status bits {bits:#x}"
-    assert 0.95 * limit < elapsed < 2 * limit
+    assert 1.9 * limit < elapsed < 4 * limit
     assert qa.qa_device_status() == 0
