@@ -647,7 +647,11 @@ qa_status qa_kvq_decode_step(const void *q, long long ldq, const void *k, const 
  * request may have several such rows).  A parent comes before its rows:
  * parents[t] < t's own number.  parents NULL: every row continues the one
  * before it.  A parent outside [-1, own number) counts as -1 and sets
- * QA_DEVICE_BAD_TREE.  A row's depth is the number of its ancestors.
+ * QA_DEVICE_BAD_TREE.  A row's depth is the number of its ancestors.  Trees
+ * are meant to be short: qa_tree_attn and qa_tree_accept take up to 64 rows a
+ * request; qa_append_rows takes any number, but where it finds a position from
+ * the depth, each ancestor more than 63 rows back costs the row a load that
+ * waits for the one before (a long line is better given as NULL).
  *
  * In these calls cu_seqlens[batch] may be less than total_rows: rows behind
  * the last request are left as they were, so that a captured call serves any
@@ -708,8 +712,15 @@ size_t qa_rows_attn_workspace_size(int max_rows, const qa_attn_params *params);
  *              0 = packed)
  *   cu_seqlens, n_past, parents, page_table, k_pages, v_pages  as above
  *   max_rows   the most rows of a request, 1..64 (host): what the kernel is
- *              chosen by
- *   out        bf16 [total_rows][n_q_heads][128], packed
+ *              chosen by, for all requests of the call.  Where max_rows *
+ *              n_q_heads / n_kv_heads is up to 16, keys stream past one block
+ *              of 16 rows; above, every request takes tiles of 128 rows,
+ *              however few it has: 64 requests of one row over 200 to 2000
+ *              positions (16 heads on 8) take 51 us with max_rows 8 and 60
+ *              with 9, also if one of them has nine rows (63 in one call and
+ *              it in another: 50 and 11)
+ *   out        bf16 [total_rows][n_q_heads][128], packed; must not overlap
+ *              an input
  *
  * Slots past n_past[r] + rows may hold anything, NaN included, and so may
  * the keys and values of rows that are not a row's ancestors.  Of what a row

@@ -786,10 +786,13 @@ def qa_tree_attn(q, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, 
     its n_past[r] cached positions, to itself and to its ancestors, the rows
     being cached at n_past[r] + i (qa_append_rows).  q bf16 [T,Hq,128] (rows
     may lie apart); cu_seqlens, n_past, parents, page_table and pools as for
-    qa_append_rows; max_rows: the most rows of a request, up to 64.
+    qa_append_rows; max_rows: the most rows of a request, up to 64, which
+    picks the kernel for all of them (with max_rows * Hq / Hkv above 16, a
+    request of few rows costs more than in a call of its own kind).
     workspace: uint8, qa_rows_attn_workspace_size(max_rows, ...) bytes
     (allocated here if omitted), reusable across calls on one stream.  Returns
-    out bf16 [T,Hq,128]; rows from cu_seqlens[-1] on are left as they were."""
+    out bf16 [T,Hq,128], which may not overlap an input; rows from
+    cu_seqlens[-1] on are left as they were."""
     return _done("qa_tree_attn", _fast().tree_attn(
         q, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, out, parents, workspace, scale, stream,
         debug_checks, stable_metadata))

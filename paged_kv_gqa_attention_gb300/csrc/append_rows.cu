@@ -71,7 +71,7 @@ struct Place {
 // it (32 boundaries a round, `probe` the first round's), then its place and,
 // without explicit positions, its depth in the tree.  The parents of the 64
 // rows up to t come with two loads a lane; a walk that leaves these goes on in
-// memory.
+// memory, a load a step.
 __device__ __forceinline__ Place place_of(const AppendArgs &a, long long t, int probe) {
     constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;

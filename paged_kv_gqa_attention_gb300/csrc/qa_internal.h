@@ -133,7 +133,10 @@ struct RowsAttn {
     void *out;
     bool tree;
 };
-constexpr int kRowsMaxBatch = 1024;  // a call's page counts lie in shared memory
+// The kernel for few rows has a call's page counts in shared memory beside its
+// ring; the one for many rows has none, but takes no more requests either, so
+// that max_rows does not decide what a call may be.
+constexpr int kRowsMaxBatch = 1024;
 constexpr int kTreeMaxRows = 64;
 size_t rows_attn_workspace_bytes(int max_rows, int n_q_heads, int n_kv_heads);
 cudaError_t launch_rows_attn(const RowsAttn &x, const qa_attn_params &p, float scale, cudaStream_t stream);

@@ -5,7 +5,7 @@
 //   path[0] = 0;  path[j + 1] = the first c with parents[c] = path[j] and
 //   draft[c] = target[path[j]];  slot n_past + j takes slot n_past + path[j]
 //
-// One CTA a request and pool.  Every CTA walks its request's tree by itself
+// One CTA a request and pool (no two of which overlap).  Every CTA walks its request's tree by itself
 // (a ballot a step over at most 64 rows held two a lane), which is cheaper
 // than a launch, or a wait, between the walk and the moves.  A thread owns 16
 // bytes of a row and goes up the path: path[j] >= j, and it rises, so that a
@@ -13,8 +13,10 @@
 // no thread waits for another.
 //
 // What bounds it is latency: boundaries, then tokens and parents, then page
-// ids, then rows: 3.3 us for 64 requests in four layers (26.5 with the four
-// layers' appends), 2.4 us for one (14.7).
+// ids, then rows: 3.3 us for 64 requests in four layers, 2.4 us for one, as
+// nodes of a graph.  With the four layers' appends before it 26.2 and 14.2 us
+// replayed, and 33.0 and 19.6 called one by one, where five calls on the host
+// bound the small one.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
