@@ -695,8 +695,11 @@ qa_status qa_append_rows(const void *q, long long ldq, const void *k, long long 
 
 /* Bytes of device workspace (256-byte aligned) for qa_tree_attn and
  * qa_cross_attn calls of up to max_rows rows a request on the CURRENT
- * device: fp32 partial results.  It need not be cleared; calls sharing one
- * workspace must be ordered (one stream).  Of params the head counts matter.
+ * device: fp32 partial results.  It need not be cleared, and calls leave the
+ * counters of qa_decode_attn and qa_kvq_decode_attn in it as they are: one
+ * workspace of the largest size, zero-filled once for these, may serve all in
+ * turn.  Calls sharing one workspace must be ordered (one stream).  Of params
+ * the head counts matter.
  * Returns 0 on invalid arguments and sets qa_last_error(). */
 size_t qa_rows_attn_workspace_size(int max_rows, const qa_attn_params *params);
 

@@ -790,7 +790,8 @@ def qa_tree_attn(q, cu_seqlens, n_past, page_table, k_pages, v_pages, max_rows, 
     picks the kernel for all of them (with max_rows * Hq / Hkv above 16, a
     request of few rows costs more than in a call of its own kind).
     workspace: uint8, qa_rows_attn_workspace_size(max_rows, ...) bytes
-    (allocated here if omitted), reusable across calls on one stream.  Returns
+    (allocated here if omitted), reusable across calls on one stream, the
+    decodes' among them if it is as large as theirs and zero at first.  Returns
     out bf16 [T,Hq,128], which may not overlap an input; rows from
     cu_seqlens[-1] on are left as they were."""
     return _done("qa_tree_attn", _fast().tree_attn(

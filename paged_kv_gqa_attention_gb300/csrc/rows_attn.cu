@@ -584,8 +584,10 @@ bool plan_of(int max_rows, int hq, int hkv, Plan *p) {
     p->block_rows = p->few ? 16 : 128;
     if (p->workers > kMaxWorkers) p->workers = kMaxWorkers;
     const size_t rows = (size_t)2 * p->workers * hkv * p->block_rows;
-    p->splits = 0;
-    p->ml = (sizeof(Split) * p->workers + 255) & ~(size_t)255;
+    // Behind the region that the decodes of either cache have their arrival counters in, which have to be zero between
+    // calls: so one workspace may serve all of them in turn.
+    p->splits = (size_t)kDecodeMaxBatch * 8 * sizeof(int32_t);
+    p->ml = p->splits + ((sizeof(Split) * p->workers + 255) & ~(size_t)255);
     p->acc = p->ml + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
     p->total = p->acc + rows * 128 * sizeof(float);
     return true;

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 
 import _rows
+import test_kvq_decode_gpu
 import workloads as wl
 from _util import bits, f64, to_dev
 
@@ -418,6 +419,31 @@ def test_chained_layers_share_a_workspace():
                 fn(*a, out, workspace=ws, stable_metadata=level, **kw)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for row in outs for x, y in zip(row, alone))
+    assert qa.qa_device_status() == 0
+
+
+@pytest.mark.parametrize("rows, kind", [([8, 3, 8], "tree"), ([40, 3, 12], "tree"), ([4, 1, 2], "cross"), ([150, 3, 64], "cross")])
+def test_workspace_shared_with_the_decodes(rows, kind):
+    """A step of one token over either cache, which counts its splits in the workspace, and drafted rows, in turn."""
+    lens = (6000, 3, 9000, 700)
+    x = wl.decode_workload(45, lens, num_pages=1100, max_pages=600)
+    d = [to_dev(x[n]) for n in ("q", "k_pages", "v_pages", "page_table", "seq_lens")]
+    w = test_kvq_decode_gpu.setup(44, lens)
+    y = [to_dev(w[n]) for n in ("q", "k_pages", "v_pages", "table", "lens")]
+    c = Case(26, rows, [900, 50, 2000], 16, 8, kind)
+    size = max(qa.qa_rows_attn_workspace_size(c.most), qa.qa_kvq_decode_workspace_size(4, 0),
+               qa.qa_decode_workspace_size(4, 9000, num_pages=1100, max_pages_per_seq=600))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    one, four, many = qa.qa_decode_attn(*d), qa.qa_kvq_decode_attn(*y), c.call()
+    c.check(many)
+    for _ in range(3):
+        got = c.call(workspace=ws, out=torch.full_like(many, 7.0), debug_checks=False)
+        assert torch.equal(got, many)
+        got = qa.qa_decode_attn(*d, torch.full_like(one, 7.0), workspace=ws)
+        assert torch.equal(got, one)
+        got = qa.qa_kvq_decode_attn(*y, torch.full_like(four, 7.0), workspace=ws)
+        assert torch.equal(got, four)
+        assert not ws[:4096 * 8 * 4].any()
     assert qa.qa_device_status() == 0
 
 
