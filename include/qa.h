@@ -682,7 +682,8 @@ qa_status qa_kvq_decode_step(const void *q, long long ldq, const void *k, const 
  * n_past is outside [0, max_pages_per_seq * 16] is skipped, rows past the
  * page-table row are not written: QA_DEVICE_BAD_LENGTH; pages outside
  * [0, num_pages): QA_DEVICE_BAD_PAGE; malformed cu_seqlens:
- * QA_DEVICE_BAD_SEGMENTS).  A row with a position outside [0, 2^18) is not
+ * QA_DEVICE_BAD_SEGMENTS, and rows of other requests may be left out too,
+ * since a row's request is found by a search over the boundaries).  A row with a position outside [0, 2^18) is not
  * written, nor is its q_out (QA_DEVICE_BAD_POSITION).  Where only the page
  * or the place in it is bad, q_out is written all the same.  No slot may be
  * written twice in a call.  Supported: head_dim 128, page_size 16,

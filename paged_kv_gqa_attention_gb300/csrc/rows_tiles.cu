@@ -45,9 +45,9 @@
 // two of 64 keys there: 44.0 and 45.1 us before that.  8 requests of 100 to 448
 // rows over 2000 to 15600 states: 224 us, where K and V are read again for each
 // 64 rows, 1.33 GB at 6.4 TB/s.  (Calls repeated on one set of inputs; where
-// these change from call to call 90.5, 37.4 and 231 us.)  Putting a job's end off until the next one's
-// first P is there costs registers in the loop: 45.5 us for the second of these
-// calls, against 39.4 at the time.
+// these change from call to call 90.5, 37.4 and 231 us.)  Putting a job's end
+// off until the next one's first P is there costs registers in the loop: 45.5
+// us for the second of these calls, against 39.4 at the time.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

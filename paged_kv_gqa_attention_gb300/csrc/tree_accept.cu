@@ -5,12 +5,12 @@
 //   path[0] = 0;  path[j + 1] = the first c with parents[c] = path[j] and
 //   draft[c] = target[path[j]];  slot n_past + j takes slot n_past + path[j]
 //
-// One CTA a request and pool (no two of which overlap).  Every CTA walks its request's tree by itself
-// (a ballot a step over at most 64 rows held two a lane), which is cheaper
-// than a launch, or a wait, between the walk and the moves.  A thread owns 16
-// bytes of a row and goes up the path: path[j] >= j, and it rises, so that a
-// slot is read before, or in the same batch of loads as, it is written, and
-// no thread waits for another.
+// One CTA a request and pool, no two of which overlap.  Every CTA walks its
+// request's tree by itself (a ballot a step over at most 64 rows held two a
+// lane), which is cheaper than a launch, or a wait, between the walk and the
+// moves.  A thread owns 16 bytes of a row and goes up the path: path[j] >= j,
+// and it rises, so that a slot is read before, or in the same batch of loads
+// as, it is written, and no thread waits for another.
 //
 // What bounds it is latency: boundaries, then tokens and parents, then page
 // ids, then rows: 3.3 us for 64 requests in four layers, 2.4 us for one, as
